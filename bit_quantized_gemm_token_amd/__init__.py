@@ -35,7 +35,8 @@ __all__ = ["Config", "W8Error", "UnsupportedShape", "Workspace", "PackedWeight",
            "config_table_size", "config_table_foreign", "tune_shape", "rank_configs",
            "profile_configs", "model_config", "moe_gemm", "moe_config", "moe_tune",
            "moe_workspace_size", "moe_linear", "moe_linear_config",
-           "pack_experts", "PackedExperts", "read_floor", "FORMATS", "MAX_M",
+           "pack_experts", "PackedExperts", "read_floor", "block_quantize", "residual_norm",
+           "block_gemm", "block_gemm_workspace_size", "grouped_gemm", "FORMATS", "MAX_M",
            "MAX_SPLIT_K", "GROUP", "ABI_VERSION"]
 
 
@@ -772,6 +773,11 @@ def algorithmic_bytes(fmt, M, N, K):
 
 
 load_default_table()
+
+
+# ------------------------------------------------- Block_FP8, any token count --
+from .block import (block_gemm, block_gemm_workspace_size, block_quantize,  # noqa: E402
+                    grouped_gemm, residual_norm)
 
 
 # -------------------------------------------------------------- measurement --

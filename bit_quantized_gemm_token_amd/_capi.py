@@ -30,7 +30,9 @@ EXPORTS = ("w8_abi_version", "w8_status_string", "w8_last_error", "w8_quantize_a
            "w8_lookup_config", "w8_tune_shape", "w8_tune_default_opts", "w8_model_config",
            "w8_rank_configs", "w8_profile_configs", "w8_moe_gemm", "w8_moe_workspace_size",
            "w8_moe_validate_config", "w8_moe_config", "w8_moe_tune", "w8_moe_linear",
-           "w8_moe_linear_config", "w8_read_floor", "w8_gemm_w8a8_noalloc", "w8_predict_us")
+           "w8_moe_linear_config", "w8_read_floor", "w8_gemm_w8a8_noalloc", "w8_predict_us",
+           "w8_block_quantize", "w8_residual_norm", "w8_block_gemm",
+           "w8_block_gemm_workspace_size", "w8_grouped_gemm")
 
 
 class Config(ctypes.Structure):
@@ -184,4 +186,19 @@ def load():
     lib.w8_moe_linear_config.argtypes = [c_int, c_int, c_int, c_int, c_int, c_int, c_int, cfgp,
                                          ctypes.POINTER(c_int)]
     lib.w8_moe_linear_config.restype = st
+    f32 = ctypes.c_float
+    lib.w8_block_quantize.argtypes = [c_int, c_int, vp, i64, vp, i64, vp, i64, f32p, vp]
+    lib.w8_block_quantize.restype = st
+    lib.w8_residual_norm.argtypes = [c_int, c_int, vp, i64, vp, i64, c_int, vp, vp, i64, f32, vp,
+                                     f32, vp, i64, vp, i64, vp, i64, f32p, vp]
+    lib.w8_residual_norm.restype = st
+    lib.w8_block_gemm_workspace_size.argtypes = [c_int, c_int, c_int, c_int,
+                                                 ctypes.POINTER(ctypes.c_size_t)]
+    lib.w8_block_gemm_workspace_size.restype = st
+    lib.w8_block_gemm.argtypes = [c_int, c_int, c_int, vp, i64, f32p, vp, i64, f32p, vp, i64, vp,
+                                  ctypes.c_size_t, vp]
+    lib.w8_block_gemm.restype = st
+    lib.w8_grouped_gemm.argtypes = [c_int, c_int, c_int, c_int, vp, i64, f32p, vp, vp, c_int, vp,
+                                    i64, i64, f32p, i64, vp, i64, vp]
+    lib.w8_grouped_gemm.restype = st
     return lib

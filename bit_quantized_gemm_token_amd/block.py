@@ -1,0 +1,246 @@
+"""Block_FP8 operators for any token count (the C-ABI's w8_block_quantize,
+w8_residual_norm, w8_block_gemm and w8_grouped_gemm).
+
+Together they make a Block_FP8 layer whose token count is not bound to the
+small-M window of gemm_w8a8 and moe_gemm: the residual update and norm between
+two blocks, straight to codes; the quantizer with the gated activation in
+front of it; the GEMM; and the GEMM per expert over ragged lists of rows.
+Like the rest of the package this module only checks and marshals arguments.
+"""
+import ctypes
+
+import torch
+
+from . import _capi
+
+GROUP = _capi.GROUP
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_CODES = torch.float8_e4m3fn
+
+
+def _groups(n):
+    return (n + GROUP - 1) // GROUP
+
+
+def _rows(t, name, dtype=None):
+    """Pointer and row stride (elements) of a 2-D device tensor with unit inner stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D tensor with unit inner stride")
+    # (a single row's stride is never used, and torch lets it be anything)
+    return t.data_ptr(), max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+
+
+def _codes(t, name):
+    p, ld = _rows(t, name)
+    if t.element_size() != 1:
+        raise TypeError(f"{name} must hold 1-byte codes")
+    return p, ld
+
+
+def _flat(t, name, dtype, n=None):
+    """Pointer of a contiguous device tensor (of n elements)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} must be a contiguous tensor of {n} elements, got shape "
+                         f"{tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _shape(t, rows, cols, name):
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
+
+
+def _aligned_codes(M, K, device):
+    """Codes [M, K] whose row stride the GEMMs take (a multiple of 16)."""
+    if K % 16 == 0:
+        return torch.empty((M, K), dtype=_CODES, device=device)
+    return torch.empty((M, (K + 15) // 16 * 16), dtype=_CODES, device=device)[:, :K]
+
+
+def block_quantize(x, gate=None, xq=None, sx=None, stream=None):
+    """E4M3FN codes [M, K] and fp32 scales [M, ceil(K/128)] of bf16 x [M, K],
+    or with gate (bf16 [M, K]) of silu(gate) * x: the gated activation in
+    front of a layer's last projection, fused into the quantizer.
+
+    Each 1 x 128 group (the last may be shorter) takes s = amax / 448 (1 for
+    an all-zero group) and codes round-to-nearest-even(x / s), as quantize_act
+    does for Block_FP8; the gated product is not rounded before.  Any M; K a
+    multiple of 8 (the GEMMs need 16); x and gate may be column slices of one
+    tensor.  A group holding a NaN or an infinity gets a non-finite scale.
+    """
+    xp, ldx = _rows(x, "x", _BF16)
+    M, K = x.shape
+    gp, ldg = None, 0
+    if gate is not None:
+        gp, ldg = _rows(gate, "gate", _BF16)
+        _shape(gate, M, K, "gate")
+    if xq is None:
+        xq = _aligned_codes(M, K, x.device)
+    else:
+        _shape(xq, M, K, "xq")
+    qp, ldq = _codes(xq, "xq")
+    if sx is None:
+        sx = torch.empty((M, _groups(K)), dtype=_F32, device=x.device)
+    sp = _flat(sx, "sx", _F32, M * _groups(K))
+    _check(_lib.w8_block_quantize(M, K, xp, ldx, gp, ldg, qp, ldq, sp, _stream(stream, x.device)))
+    return xq, sx
+
+
+def residual_norm(y, residual, weight, post_weight=None, gate=None, scale=1.0, eps=1e-6,
+                  quantize=False, h=None, out=None, stream=None):
+    """The residual update and the norm between two blocks, in one pass:
+
+        h = residual + scale * gate * N(y; post_weight)
+        z = N(h; weight),      N(v; w) = w * v / sqrt(mean(v^2) + eps)
+
+    y: bf16 [M, D], a block's output; without post_weight it is taken as it
+    is.  residual: bf16 or fp32 [M, D]; h has its type (h=residual updates it
+    in place).  weight, post_weight: bf16 [D].  gate: bf16 [D] (the same for
+    every row) or [M, D], or None for 1.
+
+    Returns (h, z) with z bf16, or with quantize=True (h, zq, sz): z's
+    Block_FP8 codes and scales, as block_quantize gives them for the unrounded
+    z.  z is computed from the unrounded h, all in fp32.  out: z, or the pair
+    (zq, sz), to write to.  Any M, 1 <= D <= 32768, any strides.
+    """
+    yp, ldy = _rows(y, "y", _BF16)
+    M, D = y.shape
+    rp, ldr = _rows(residual, "residual")
+    if residual.dtype not in (_BF16, _F32):
+        raise TypeError(f"residual must be bfloat16 or float32, got {residual.dtype}")
+    _shape(residual, M, D, "residual")
+    wp = _flat(weight, "weight", _BF16, D)
+    pp = None if post_weight is None else _flat(post_weight, "post_weight", _BF16, D)
+    gp, ldg = None, 0
+    if gate is not None:
+        if gate.dim() == 1:
+            gp = _flat(gate, "gate", _BF16, D)
+        else:
+            gp, ldg = _rows(gate, "gate", _BF16)
+            _shape(gate, M, D, "gate")
+    if h is None:
+        h = torch.empty((M, D), dtype=residual.dtype, device=y.device)
+    else:
+        _shape(h, M, D, "h")
+    hp, ldh = _rows(h, "h", residual.dtype)
+    zp = qp = sp = None
+    ldz = ldq = 0
+    if quantize:
+        zq, sz = out if out is not None else (
+            _aligned_codes(M, D, y.device),
+            torch.empty((M, _groups(D)), dtype=_F32, device=y.device))
+        _shape(zq, M, D, "zq")
+        qp, ldq = _codes(zq, "zq")
+        sp = _flat(sz, "sz", _F32, M * _groups(D))
+        result = h, zq, sz
+    else:
+        z = out if out is not None else torch.empty((M, D), dtype=_BF16, device=y.device)
+        _shape(z, M, D, "out")
+        zp, ldz = _rows(z, "out", _BF16)
+        result = h, z
+    _check(_lib.w8_residual_norm(M, D, yp, ldy, rp, ldr, residual.dtype == _F32, pp, gp, ldg,
+                                 scale, wp, eps, hp, ldh, zp, ldz, qp, ldq, sp,
+                                 _stream(stream, y.device)))
+    return result
+
+
+def block_gemm_workspace_size(M, N, K, packed=False):
+    """Bytes of workspace block_gemm needs for the shape (0 for most)."""
+    n = ctypes.c_size_t(0)
+    _check(_lib.w8_block_gemm_workspace_size(M, N, K, _layout(packed), ctypes.byref(n)))
+    return n.value
+
+
+def block_gemm(xq, sx, wq, sw, y=None, workspace=None, stream=None):
+    """Y = dequant(xq) . dequant(wq)^T as bf16 [M, N] in Block_FP8, any M.
+
+    xq, sx: codes [M, K] and scales [M, ceil(K/128)] (block_quantize,
+    residual_norm, quantize_act); wq, sw: codes [N, K] or a PackedWeight of
+    layout 1, scales [ceil(N/128), ceil(K/128)] (quantize_weight).  K a
+    multiple of 16 (packed: of 128); its last group may be shorter.
+    """
+    xp, ldq = _codes(xq, "xq")
+    M, K = xq.shape
+    if isinstance(wq, PackedWeight):
+        if wq.fmt != _capi.FORMATS["Block_FP8"] or wq.layout != 1:
+            raise ValueError("packed weights must be Block_FP8 in layout 1")
+        N, wk, wp, ldw, packed = wq.N, wq.K, wq.data.data_ptr(), 0, 1
+    else:
+        (wp, ldw), (N, wk), packed = _codes(wq, "wq"), wq.shape, 0
+    if wk != K:
+        raise ValueError(f"K mismatch: xq {tuple(xq.shape)} vs weights {(N, wk)}")
+    G = _groups(K)
+    sxp, swp = _flat(sx, "sx", _F32, M * G), _flat(sw, "sw", _F32, _groups(N) * G)
+    if y is None:
+        y = torch.empty((M, N), dtype=_BF16, device=xq.device)
+    else:
+        _shape(y, M, N, "y")
+    yp, ldy = _rows(y, "y", _BF16)
+    ws, ws_bytes = None, block_gemm_workspace_size(M, N, K, packed)
+    if ws_bytes:
+        if workspace is None:
+            workspace = _default_workspace(xq.device)
+        buf = workspace.reserve(ws_bytes, stream)
+        ws, ws_bytes = buf.data_ptr(), buf.numel()
+    _check(_lib.w8_block_gemm(M, N, K, xp, ldq, sxp, wp, ldw, swp, yp, ldy, ws, ws_bytes,
+                              _stream(stream, xq.device)))
+    return y
+
+
+def grouped_gemm(xq, sx, offsets, wq, sw, rows=None, y=None, stream=None):
+    """The Block_FP8 GEMM per expert over ragged lists of rows, any counts:
+    for entry i of expert e (offsets[e] <= i < offsets[e + 1])
+
+        Y[i] = dequant(xq[rows[i]]) . dequant(wq[e])^T      (bf16 [n_rows, N])
+
+    xq, sx: codes [T, K] and scales [T, ceil(K/128)]; offsets: int32 [E + 1]
+    on the device, ascending from 0 to the number of entries; rows: int32
+    [n_rows], the token row of each entry, or None where the entries are the
+    rows of xq in order; wq: [E, N, K] codes or PackedExperts; sw: [E,
+    ceil(N/128), ceil(K/128)].  Experts without entries read nothing.  One
+    launch, no host sync; bad offsets and rows are clamped to the arrays.
+    """
+    xp, ldq = _codes(xq, "xq")
+    T, K = xq.shape
+    if isinstance(wq, PackedExperts):
+        if wq.fmt != _capi.FORMATS["Block_FP8"]:
+            raise ValueError("experts were packed for another format")
+        E, N, wk = wq.E, wq.N, wq.K
+        wp, ldw, w_stride = wq.data.data_ptr(), 0, wq.data.stride(0)
+    else:
+        if not isinstance(wq, torch.Tensor) or not wq.is_cuda:
+            raise TypeError("wq must be a CUDA (HIP) tensor or PackedExperts")
+        if wq.dim() != 3 or wq.element_size() != 1 or wq.stride(2) != 1:
+            raise ValueError("wq must be [E, N, K] 1-byte codes with unit inner stride")
+        E, N, wk = wq.shape
+        wp, ldw, w_stride = wq.data_ptr(), wq.stride(1), wq.stride(0)
+    if wk != K:
+        raise ValueError(f"K mismatch: xq {tuple(xq.shape)} vs experts' K {wk}")
+    G = _groups(K)
+    sxp = _flat(sx, "sx", _F32, T * G)
+    per = _groups(N) * G
+    swp = _flat(sw, "sw", _F32, E * per)
+    op = _flat(offsets, "offsets", _I32, E + 1)
+    n_rows = T if rows is None else rows.numel()
+    rwp = None if rows is None else _flat(rows, "rows", _I32, n_rows)
+    if y is None:
+        y = torch.empty((n_rows, N), dtype=_BF16, device=xq.device)
+    else:
+        _shape(y, n_rows, N, "y")
+    yp, ldy = _rows(y, "y", _BF16)
+    _check(_lib.w8_grouped_gemm(E, T, N, K, xp, ldq, sxp, op, rwp, n_rows, wp, ldw, w_stride,
+                                swp, per, yp, ldy, _stream(stream, xq.device)))
+    return y
+
+
+# (the package's own helpers; __init__ imports this module after defining them)
+from . import (PackedExperts, PackedWeight, _check, _default_workspace, _layout, _lib,  # noqa: E402
+               _stream)

@@ -42,7 +42,10 @@ def _units():
              ("w8_table.cpp", ["-x", "hip"], "w8_table.o"),
              ("w8_model.cpp", ["-x", "hip"], "w8_model.o"),
              ("w8_moe.cpp", ["-x", "hip"], "w8_moe.o"),
-             ("w8_registry.cpp", ["-x", "hip"], "w8_registry.o")]
+             ("w8_registry.cpp", ["-x", "hip"], "w8_registry.o"),
+             ("w8_block_gemm.hip", [], "w8_block_gemm.o"),
+             ("w8_rows.hip", [], "w8_rows.o"),
+             ("w8_block.cpp", ["-x", "hip"], "w8_block.o")]
     # the instance file in 40 parts (the GEMM parts, the largest, first so
     # the pool stays busy; parts 4 and 5 exist for Block_FP8 only), then the
     # small units

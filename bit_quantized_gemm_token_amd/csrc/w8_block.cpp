@@ -1,0 +1,289 @@
+// C-ABI of the Block_FP8 operators for any token count: the gated quantizer,
+// the residual norm, the tiled GEMM and the per-expert (grouped) GEMM.
+// Argument checks first, then one kernel launch each; nothing here allocates,
+// frees or synchronizes.
+#include <cstdint>
+#include <string>
+
+#include "w8_block.hpp"
+#include "w8_internal.hpp"
+
+using namespace w8;
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+constexpr int kMaxK = 1 << 22;
+constexpr int kMaxN = 1 << 24;
+// rows of one call: a launch holds at most 2^32 - 1 threads, and the row
+// kernels take up to 1024 per row
+constexpr int kMaxRows = (1 << 22) - 1;
+
+int groups_of(int K) { return (K + W8_GROUP - 1) / W8_GROUP; }
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+w8_status check_rows(int M) {
+  if (M < 0 || M > kMaxRows)
+    return fail(W8_E_INVALID, "the number of rows must be in [0, " + std::to_string(kMaxRows) +
+                                  "], got " + std::to_string(M));
+  return W8_OK;
+}
+
+w8_status check_nk(int N, int K) {
+  if (N < 1 || N > kMaxN) return fail(W8_E_INVALID, "N must be in [1, 2^24]");
+  if (K < 16 || K > kMaxK || K % 16)
+    return fail(W8_E_INVALID, "K must be a multiple of 16 in [16, 2^22]");
+  return W8_OK;
+}
+
+// Operand checks shared by the dense and the grouped GEMM; *packed: the
+// weight layout ldw names.
+w8_status check_operands(int N, int K, const void* xq, int64_t ldq, const float* sx,
+                         const void* wq, int64_t ldw, const float* sw, const void* y,
+                         int64_t ldy, int* packed) {
+  if (!xq || !sx || !wq || !sw || !y) return fail(W8_E_INVALID, "null device pointer");
+  if (!aligned(xq, 16) || !aligned(wq, 16))
+    return fail(W8_E_INVALID, "xq and wq must be 16-byte aligned");
+  if (ldq < K || ldq % 16)
+    return fail(W8_E_INVALID, "ldq must be >= K and a multiple of 16");
+  if (ldw != 0 && (ldw < K || ldw % 16))
+    return fail(W8_E_INVALID, "ldw must be >= K and a multiple of 16 (row-major weights) or 0 "
+                              "(packed; the K-segmented layouts are for the small-M GEMM)");
+  *packed = ldw == 0;
+  if (*packed && K % W8_GROUP) return fail(W8_E_INVALID, "packed weights need K % 128 == 0");
+  if (ldy < N) return fail(W8_E_INVALID, "output leading dimension must be >= N");
+  if (!aligned(sx, 4) || !aligned(sw, 4) || !aligned(y, 2))
+    return fail(W8_E_INVALID, "misaligned scale or output pointer");
+  return W8_OK;
+}
+
+int vec_store(const void* y, int64_t ldy) { return aligned(y, 8) && ldy % 4 == 0; }
+
+// ------------------------------------------------------------ tile choice --
+struct Plan {
+  int tile, split_k;
+  long long tiles_m, tiles_n;
+};
+
+Plan plan_dense(int M, int N, int K) {
+  Plan p;
+  p.tile = M <= 16 ? 0 : M <= 32 ? 1 : M <= 64 ? 2 : 3;
+  if (ceil_div(M, 256) * ceil_div(N, 256) >= 192) p.tile = 4;
+  const BlockTile& t = block_tile(p.tile);
+  p.tiles_m = ceil_div(M, t.bm);
+  p.tiles_n = ceil_div(N, t.bn);
+  p.split_k = 1;
+  while (p.split_k < 16 && p.tiles_m * p.tiles_n * p.split_k < 256 &&
+         groups_of(K) / (2 * p.split_k) >= 4)
+    p.split_k *= 2;
+  if (p.tiles_m * p.tiles_n > kSplitKMaxTiles) p.split_k = 1;
+  return p;
+}
+
+size_t plan_bytes(const Plan& p) {
+  if (p.split_k == 1) return 0;
+  const BlockTile& t = block_tile(p.tile);
+  return ws_counter_bytes(0) + (size_t)(p.tiles_m * p.tiles_n) * p.split_k * t.bm * t.bn * 4;
+}
+
+w8_status check_grid(const Plan& p) {
+  const long long threads = p.tiles_m * p.tiles_n * p.split_k * block_tile(p.tile).threads;
+  if (threads > 0xFFFFFFFFLL)
+    return fail(W8_E_INVALID, "the launch's threads exceed 2^32 - 1: split the call along M or N");
+  return W8_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+w8_status w8_block_quantize(int M, int K, const void* x, int64_t ldx, const void* gate,
+                            int64_t ldg, void* xq, int64_t ldq, float* sx, w8_stream stream) {
+  w8_status st = check_rows(M);
+  if (st) return st;
+  if (K < 8 || K > kMaxK || K % 8)
+    return fail(W8_E_INVALID, "K must be a multiple of 8 in [8, 2^22]");
+  if (M == 0) return ok();
+  if (!x || !xq || !sx) return fail(W8_E_INVALID, "null device pointer");
+  if (!aligned(x, 16) || ldx % 8 || ldx < K)
+    return fail(W8_E_INVALID, "x must be 16-byte aligned with ldx >= K and ldx % 8 == 0");
+  if (gate && (!aligned(gate, 16) || ldg % 8 || ldg < K))
+    return fail(W8_E_INVALID, "gate must be 16-byte aligned with ldg >= K and ldg % 8 == 0");
+  if (!aligned(xq, 8) || ldq % 8 || ldq < K)
+    return fail(W8_E_INVALID, "xq must be 8-byte aligned with ldq >= K and ldq % 8 == 0");
+  if (!aligned(sx, 4)) return fail(W8_E_INVALID, "sx must be 4-byte aligned");
+  st = check_device();
+  if (st) return st;
+  BlockQuantArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(gate),
+                   static_cast<uint8_t*>(xq), sx, ldx, ldg, ldq, M, K};
+  const hipError_t e = launch_block_quantize(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("block_quantize launch", e));
+  return ok();
+}
+
+w8_status w8_residual_norm(int M, int D, const void* y, int64_t ldy, const void* residual,
+                           int64_t ldr, int residual_fp32, const void* post_weight,
+                           const void* gate, int64_t ldg, float scale, const void* weight,
+                           float eps, void* h, int64_t ldh, void* z, int64_t ldz, void* zq,
+                           int64_t ldq, float* sz, w8_stream stream) {
+  w8_status st = check_rows(M);
+  if (st) return st;
+  if (D < 1) return fail(W8_E_INVALID, "D must be positive");
+  if (D > kNormMaxD)
+    return fail(W8_E_UNSUPPORTED, "D=" + std::to_string(D) + " is above the row length that the "
+                                  "norm keeps in registers (" + std::to_string(kNormMaxD) +
+                                  "); use another backend");
+  if (residual_fp32 != 0 && residual_fp32 != 1)
+    return fail(W8_E_INVALID, "residual_fp32 must be 0 or 1");
+  if (!(eps >= 0.0f)) return fail(W8_E_INVALID, "eps must be >= 0");
+  if (M == 0) return ok();
+  if (!y || !residual || !weight || !h) return fail(W8_E_INVALID, "null device pointer");
+  if (!z && !zq) return fail(W8_E_INVALID, "at least one of z and zq must be given");
+  if (zq && !sz) return fail(W8_E_INVALID, "zq needs sz");
+  if (ldy < D || ldr < D || ldh < D || (gate && ldg != 0 && ldg < D) || (z && ldz < D) ||
+      (zq && ldq < D))
+    return fail(W8_E_INVALID, "leading dimensions must be >= D (gate: or 0, one row for all)");
+  const size_t ra = residual_fp32 ? 4 : 2;
+  if (!aligned(y, 2) || !aligned(residual, ra) || !aligned(h, ra) || !aligned(weight, 2) ||
+      !aligned(post_weight, 2) || !aligned(gate, 2) || !aligned(z, 2) || !aligned(sz, 4))
+    return fail(W8_E_INVALID, "every pointer must be aligned to its element type");
+  st = check_device();
+  if (st) return st;
+  NormArgs a{static_cast<const uint16_t*>(y), residual, static_cast<const uint16_t*>(gate),
+             static_cast<const uint16_t*>(post_weight), static_cast<const uint16_t*>(weight), h,
+             static_cast<uint16_t*>(z), static_cast<uint8_t*>(zq), sz, ldy, ldr, ldg, ldh, ldz,
+             ldq, M, D, residual_fp32, scale, eps};
+  const hipError_t e = launch_residual_norm(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("residual_norm launch", e));
+  return ok();
+}
+
+w8_status w8_block_gemm_workspace_size(int M, int N, int K, int packed, size_t* bytes) {
+  w8_status st = check_rows(M);
+  if (st) return st;
+  st = check_nk(N, K);
+  if (st) return st;
+  if (packed != 0 && packed != 1)
+    return fail(W8_E_INVALID, "weight layout must be 0 (row-major) or 1 (packed)");
+  if (!bytes) return fail(W8_E_INVALID, "null output pointer");
+  *bytes = M ? plan_bytes(plan_dense(M, N, K)) : 0;
+  return ok();
+}
+
+w8_status w8_block_gemm(int M, int N, int K, const void* xq, int64_t ldq, const float* sx,
+                        const void* wq, int64_t ldw, const float* sw, void* y, int64_t ldy,
+                        void* ws, size_t ws_bytes, w8_stream stream) {
+  w8_status st = check_rows(M);
+  if (st) return st;
+  st = check_nk(N, K);
+  if (st) return st;
+  if (M == 0) return ok();
+  int packed = 0;
+  st = check_operands(N, K, xq, ldq, sx, wq, ldw, sw, y, ldy, &packed);
+  if (st) return st;
+  const Plan p = plan_dense(M, N, K);
+  const size_t need = plan_bytes(p);
+  if (need > 0) {
+    if (!ws || ws_bytes < need)
+      return fail(W8_E_WORKSPACE, "workspace of " + std::to_string(need) + " bytes needed, got " +
+                                      std::to_string(ws ? ws_bytes : 0));
+    if (!aligned(ws, 16)) return fail(W8_E_INVALID, "workspace must be 16-byte aligned");
+  }
+  st = check_grid(p);
+  if (st) return st;
+  st = check_device();
+  if (st) return st;
+  BlockGemmArgs a{};
+  a.xq = static_cast<const uint8_t*>(xq);
+  a.sx = sx;
+  a.wq = static_cast<const uint8_t*>(wq);
+  a.sw = sw;
+  a.y = static_cast<uint16_t*>(y);
+  if (need > 0) {
+    a.counters = static_cast<unsigned*>(ws);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + ws_counter_bytes(0));
+  }
+  a.ldq = ldq;
+  a.ldw = ldw;
+  a.ldy = ldy;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.G = groups_of(K);
+  a.split_k = p.split_k;
+  a.vec_store = vec_store(y, ldy);
+  a.tiles_m = (int)p.tiles_m;
+  a.tiles_n = (int)p.tiles_n;
+  const hipError_t e =
+      launch_block_gemm(p.tile, false, packed, a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("block_gemm launch", e));
+  return ok();
+}
+
+w8_status w8_grouped_gemm(int E, int T, int N, int K, const void* xq, int64_t ldq,
+                          const float* sx, const int32_t* offsets, const int32_t* rows,
+                          int n_rows, const void* wq, int64_t ldw, int64_t w_stride,
+                          const float* sw, int64_t sw_stride, void* y, int64_t ldy,
+                          w8_stream stream) {
+  w8_status st = check_rows(n_rows);
+  if (st) return st;
+  st = check_nk(N, K);
+  if (st) return st;
+  if (E < 1 || E > 65536) return fail(W8_E_INVALID, "E must be in [1, 65536]");
+  if (T < 0) return fail(W8_E_INVALID, "T must be >= 0");
+  if (n_rows == 0) return ok();
+  if (T < 1) return fail(W8_E_INVALID, "routed entries need at least one token row");
+  if (!offsets) return fail(W8_E_INVALID, "null device pointer");
+  if (!rows && T < n_rows)
+    return fail(W8_E_INVALID, "without a row list entry i is row i: T must be >= n_rows");
+  int packed = 0;
+  st = check_operands(N, K, xq, ldq, sx, wq, ldw, sw, y, ldy, &packed);
+  if (st) return st;
+  if (!aligned(offsets, 4) || !aligned(rows, 4))
+    return fail(W8_E_INVALID, "offsets and rows must be 4-byte aligned");
+  const int64_t one = packed ? (int64_t)packed_weight_bytes(W8_BLOCK_FP8, N, K, 1)
+                             : (int64_t)(N - 1) * ldw + K;
+  if (w_stride % 16 || (E > 1 && w_stride < one))
+    return fail(W8_E_INVALID, "w_stride must be a multiple of 16 that holds one expert's codes");
+  if (E > 1 && sw_stride < (int64_t)groups_of(N) * groups_of(K))
+    return fail(W8_E_INVALID, "sw_stride must hold one expert's scales");
+  Plan p;
+  const long long mean = n_rows / E;
+  p.tile = mean <= 16 ? 0 : mean <= 32 ? 1 : mean <= 64 ? 2 : 3;
+  p.split_k = 1;
+  p.tiles_m = n_rows / block_tile(p.tile).bm + E;
+  p.tiles_n = ceil_div(N, block_tile(p.tile).bn);
+  st = check_grid(p);
+  if (st) return st;
+  st = check_device();
+  if (st) return st;
+  BlockGemmArgs a{};
+  a.xq = static_cast<const uint8_t*>(xq);
+  a.sx = sx;
+  a.wq = static_cast<const uint8_t*>(wq);
+  a.sw = sw;
+  a.y = static_cast<uint16_t*>(y);
+  a.ldq = ldq;
+  a.ldw = ldw;
+  a.ldy = ldy;
+  a.M = n_rows;
+  a.N = N;
+  a.K = K;
+  a.G = groups_of(K);
+  a.split_k = 1;
+  a.vec_store = vec_store(y, ldy);
+  a.tiles_m = (int)p.tiles_m;
+  a.tiles_n = (int)p.tiles_n;
+  a.offsets = offsets;
+  a.rows = rows;
+  a.w_stride = w_stride;
+  a.sw_stride = sw_stride;
+  a.n_experts = E;
+  a.xrow_max = T - 1;
+  const hipError_t e = launch_block_gemm(p.tile, true, packed, a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("grouped_gemm launch", e));
+  return ok();
+}
+
+}  // extern "C"

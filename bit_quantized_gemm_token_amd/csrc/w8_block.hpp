@@ -1,0 +1,78 @@
+// Host-side declarations of the Block_FP8 operators for any token count: the
+// argument blocks and launchers of the row operators (w8_rows.hip) and of the
+// tiled GEMM (w8_block_gemm.hip), used by their C-ABI (w8_block.cpp).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace w8 {
+
+// ------------------------------------------------------------ row kernels --
+struct BlockQuantArgs {
+  const uint16_t* x;     // bf16 [M, K]
+  const uint16_t* gate;  // bf16 [M, K], or null
+  uint8_t* xq;           // codes [M, K]
+  float* sx;             // [M, ceil(K/128)]
+  long long ldx, ldg;    // elements
+  long long ldq;         // bytes
+  long long M;
+  int K;
+};
+hipError_t launch_block_quantize(const BlockQuantArgs& a, hipStream_t s);
+
+struct NormArgs {
+  const uint16_t* y;         // bf16 [M, D]
+  const void* residual;      // bf16 or fp32 [M, D]
+  const uint16_t* gate;      // bf16 [D] (ldg 0) or [M, D], or null
+  const uint16_t* post_w;    // bf16 [D], or null
+  const uint16_t* w;         // bf16 [D]
+  void* h;                   // [M, D] of the residual's type
+  uint16_t* z;               // bf16 [M, D], or null
+  uint8_t* zq;               // codes [M, D], or null
+  float* sz;                 // [M, ceil(D/128)] with zq
+  long long ldy, ldr, ldg, ldh, ldz;  // elements
+  long long ldq;                      // bytes
+  long long M;
+  int D;
+  int residual_fp32;
+  float scale, eps;
+};
+constexpr int kNormMaxD = 32768;  // a row stays in one workgroup's registers
+hipError_t launch_residual_norm(const NormArgs& a, hipStream_t s);
+
+// ------------------------------------------------------------- tiled GEMM --
+struct BlockGemmArgs {
+  const uint8_t* xq;   // activation codes, row stride ldq bytes
+  const float* sx;     // [rows, G]
+  const uint8_t* wq;   // weight codes of expert 0
+  const float* sw;     // [ceil(N/128), G] of expert 0
+  uint16_t* y;         // bf16, row stride ldy elements
+  float* part;         // split-K partials (workspace)
+  unsigned* counters;  // split-K arrival counters (workspace)
+  long long ldq, ldw, ldy;
+  int M, N, K;
+  int G;               // ceil(K / 128): scale groups and K-steps
+  int split_k;         // power of two; 1 = whole K per workgroup
+  int vec_store;       // y and ldy allow 8-byte stores
+  int tiles_m;         // token tiles (grouped: slots, M / BM + E)
+  int tiles_n;
+  // grouped (per expert) products
+  const int* offsets;      // [E + 1] (device)
+  const int* rows;         // [M] token row of each entry (device), or null: entry i is row i
+  long long w_stride;      // bytes between two experts' weights
+  long long sw_stride;     // floats between two experts' scales
+  int n_experts;
+  int xrow_max;            // activation rows - 1
+};
+
+// A tile shape of the kernel: BM tokens x BN weight rows per workgroup.
+struct BlockTile {
+  int bm, bn, threads, lds_bytes;
+};
+constexpr int kBlockTiles = 5;
+const BlockTile& block_tile(int tile);
+hipError_t launch_block_gemm(int tile, bool grouped, bool packed, const BlockGemmArgs& a,
+                             hipStream_t s);
+
+}  // namespace w8

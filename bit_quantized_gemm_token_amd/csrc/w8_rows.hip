@@ -1,0 +1,292 @@
+// Row operators of the Block_FP8 layer for any token count: the 1 x 128
+// quantizer with the gated activation in front of it, and the residual
+// update with its norms.  Both read every input once and write every output
+// once; HBM bandwidth bounds them on many rows and launch latency on few.
+#include "w8_block.hpp"
+#include "w8_device.hpp"
+
+namespace w8 {
+namespace {
+
+// The bits of |v|: ordered like the magnitudes for finite values, infinities
+// above them and NaN above those, so an unsigned maximum keeps a NaN where
+// fmaxf would drop it.
+__device__ __forceinline__ unsigned abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+template <int CTRL>
+__device__ __forceinline__ unsigned dpp_move_u(unsigned v) {
+  return (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+
+// Maximum over aligned segments of 16 lanes.
+__device__ __forceinline__ unsigned seg16_umax(unsigned v) {
+  v = max(v, dpp_move_u<0xB1>(v));
+  v = max(v, dpp_move_u<0x4E>(v));
+  v = max(v, dpp_move_u<0x141>(v));
+  v = max(v, dpp_move_u<0x140>(v));
+  return v;
+}
+
+// Sum over the 64 lanes of a wavefront, in a fixed order.
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp_move<0xB1>(v);
+  v += dpp_move<0x4E>(v);
+  v += dpp_move<0x141>(v);
+  v += dpp_move<0x140>(v);
+  const int b = __builtin_bit_cast(int, v);
+  const float r0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 0));
+  const float r1 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 16));
+  const float r2 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 32));
+  const float r3 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 48));
+  return (r0 + r1) + (r2 + r3);
+}
+
+// fp32 -> bf16, round to nearest even; a NaN stays a NaN.
+__device__ __forceinline__ unsigned bf16_bits(float f) {
+  return abs_bits(f) > 0x7F800000u ? 0x7FC0u : (unsigned)bf16_rne(f);
+}
+
+__device__ __forceinline__ void unpack8(v4u v, float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_lo(v[i]);
+    f[2 * i + 1] = bf16_hi(v[i]);
+  }
+}
+
+// Eight values from p, of which n (any value) exist; the others read as 0.
+// The whole chunks' loads are 16 bytes at the elements' own alignment.
+__device__ __forceinline__ v4u load8_bf16(const uint16_t* p, int n) {
+  v4u v = {0u, 0u, 0u, 0u};
+  if (n >= 8) {
+    __builtin_memcpy(&v, p, 16);
+  } else {
+    for (int i = 0; i < n; ++i) v[i >> 1] |= (unsigned)p[i] << (16 * (i & 1));
+  }
+  return v;
+}
+__device__ __forceinline__ void load8_f32(const float* p, int n, float* f) {
+  if (n >= 8) {
+    __builtin_memcpy(f, p, 32);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = i < n ? p[i] : 0.0f;
+  }
+}
+__device__ __forceinline__ void store8_bf16(uint16_t* p, int n, const float* f) {
+  if (n >= 8) {
+    v4u v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = bf16_bits(f[2 * i]) | (bf16_bits(f[2 * i + 1]) << 16);
+    __builtin_memcpy(p, &v, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (uint16_t)bf16_bits(f[i]);
+  }
+}
+__device__ __forceinline__ void store8_f32(float* p, int n, const float* f) {
+  if (n >= 8) {
+    __builtin_memcpy(p, f, 32);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = f[i];
+  }
+}
+__device__ __forceinline__ void store8_codes(uint8_t* p, int n, v2u v) {
+  if (n >= 8) {
+    __builtin_memcpy(p, &v, 8);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (uint8_t)(v[i >> 2] >> (8 * (i & 3)));
+  }
+}
+
+// Codes of eight values of a 1 x 128 group whose 16 lanes call together; *s
+// is the group's scale.  A group that holds a NaN or an infinity gets a NaN
+// or infinite scale, so that it stays non-finite when dequantized.
+__device__ __forceinline__ v2u encode_group(float* f, float* s) {
+  unsigned m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(f[i]));
+  *s = act_scale<false>(__uint_as_float(seg16_umax(m)));
+  const float r = act_recip(*s);
+  if (r != 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = act_quot(f[i], *s, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = f[i] / *s;
+  }
+  return v2u{e4m3_pack4(f[0], f[1], f[2], f[3]), e4m3_pack4(f[4], f[5], f[6], f[7])};
+}
+
+// g * sigmoid(g).  exp(-g) = 2^t with t = -g log2(e) taken as a rounded
+// product and its remainder, which keeps the exponential's relative error at
+// a few 2^-24 for every g (the rounded product alone loses |t| 2^-25 of it).
+__device__ __forceinline__ float silu(float g) {
+  const float hi = g * -0x1.715476p+0f;
+  const float lo = __builtin_fmaf(g, -0x1.715476p+0f, -hi) - g * 0x1.4ae0cp-26f;
+  float e = __builtin_amdgcn_exp2f(hi);
+  // (an infinite 2^hi stays infinite: inf * lo could be inf * 0)
+  e = abs_bits(e) < 0x7F800000u ? __builtin_fmaf(e, 0x1.62e43p-1f * lo, e) : e;
+  return g * __builtin_amdgcn_rcpf(1.0f + e);
+}
+
+// ---------------------------------------------------------------- quantize --
+// 16 lanes take a group, each lane eight values; a workgroup takes 16 groups
+// and strides over the rest.
+constexpr int kQThreads = 256;
+
+template <bool GATED>
+__global__ __launch_bounds__(kQThreads) void block_quantize_kernel(BlockQuantArgs a) {
+  const int G = (a.K + kGroup - 1) / kGroup;
+  const long long total = a.M * G;
+  const int j = threadIdx.x & 15;
+  for (long long id = (long long)blockIdx.x * (kQThreads / 16) + (threadIdx.x >> 4); id < total;
+       id += (long long)gridDim.x * (kQThreads / 16)) {
+    const long long m = id / G;
+    const int k = (int)(id % G) * kGroup + 8 * j;
+    const int n = a.K - k;
+    float f[8];
+    unpack8(load8_bf16(a.x + m * a.ldx + k, n), f);
+    if (GATED) {
+      float g[8];
+      unpack8(load8_bf16(a.gate + m * a.ldg + k, n), g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= silu(g[i]);
+    }
+    float s;
+    const v2u q = encode_group(f, &s);
+    if (j == 0) a.sx[id] = s;
+    store8_codes(a.xq + m * a.ldq + k, n, q);
+  }
+}
+
+// -------------------------------------------------------------------- norm --
+// One row by T threads (64: four rows per workgroup), NC chunks of eight
+// values each, kept in registers between the two norms: every input is read
+// once.  Sums of squares are fp32, in a fixed order.
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = wave_sum(v);
+  if (T == 64) return v;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float t = 0.0f;
+#pragma unroll
+  for (int w = 0; w < T / 64; ++w) t += red[w];
+  return t;
+}
+
+template <int T, int NC, bool RF32>
+__global__ __launch_bounds__(T == 64 ? 256 : T) void residual_norm_kernel(NormArgs a) {
+  __shared__ float red[2][16];
+  const int t = T == 64 ? threadIdx.x & 63 : threadIdx.x;
+  const long long row = T == 64 ? (long long)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (T == 64 && row >= a.M) return;  // (no barrier with one wave per row)
+  const uint16_t* y = a.y + row * a.ldy;
+  const uint16_t* gate = a.gate ? a.gate + row * a.ldg : nullptr;
+  float h[NC][8], b[NC][8];
+  v4u g[NC], pw[NC], w[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int k = 8 * (t + c * T), n = a.D - k;
+    unpack8(load8_bf16(y + k, n), b[c]);
+    if (RF32)
+      load8_f32(static_cast<const float*>(a.residual) + row * a.ldr + k, n, h[c]);
+    else
+      unpack8(load8_bf16(static_cast<const uint16_t*>(a.residual) + row * a.ldr + k, n), h[c]);
+    if (gate) g[c] = load8_bf16(gate + k, n);
+    if (a.post_w) pw[c] = load8_bf16(a.post_w + k, n);
+    w[c] = load8_bf16(a.w + k, n);
+  }
+  if (a.post_w) {
+    float ss = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(b[c][i], b[c][i], ss);
+    const float r = 1.0f / sqrtf(row_sum<T>(ss, red[0]) / (float)a.D + a.eps);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      float p[8];
+      unpack8(pw[c], p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[c][i] *= r * p[i];
+    }
+  }
+  float ss = 0.0f;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    float gf[8];
+    if (gate) unpack8(g[c], gf);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (gate) b[c][i] *= gf[i];
+      h[c][i] = __builtin_fmaf(a.scale, b[c][i], h[c][i]);
+      ss = __builtin_fmaf(h[c][i], h[c][i], ss);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int k = 8 * (t + c * T), n = a.D - k;
+    if (RF32)
+      store8_f32(static_cast<float*>(a.h) + row * a.ldh + k, n, h[c]);
+    else
+      store8_bf16(static_cast<uint16_t*>(a.h) + row * a.ldh + k, n, h[c]);
+  }
+  const float r = 1.0f / sqrtf(row_sum<T>(ss, red[1]) / (float)a.D + a.eps);
+  const int G = (a.D + kGroup - 1) / kGroup;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int k = 8 * (t + c * T), n = a.D - k;
+    float wf[8];
+    unpack8(w[c], wf);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[c][i] *= r * wf[i];
+    if (a.z) store8_bf16(a.z + row * a.ldz + k, n, h[c]);
+    if (a.zq) {  // 16 consecutive lanes hold one group
+      float s;
+      const v2u q = encode_group(h[c], &s);
+      if ((t & 15) == 0 && n > 0) a.sz[row * G + k / kGroup] = s;
+      store8_codes(a.zq + row * a.ldq + k, n, q);
+    }
+  }
+}
+
+template <int T, int NC>
+hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)(T == 64 ? (a.M + 3) / 4 : a.M)), block(T == 64 ? 256 : T);
+  if (a.residual_fp32)
+    hipLaunchKernelGGL((residual_norm_kernel<T, NC, true>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((residual_norm_kernel<T, NC, false>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_block_quantize(const BlockQuantArgs& a, hipStream_t s) {
+  const long long groups = a.M * ((a.K + kGroup - 1) / kGroup);
+  const long long blocks = (groups + kQThreads / 16 - 1) / (kQThreads / 16);
+  const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20))), block(kQThreads);
+  if (a.gate)
+    hipLaunchKernelGGL(block_quantize_kernel<true>, grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL(block_quantize_kernel<false>, grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_residual_norm(const NormArgs& a, hipStream_t s) {
+  if (a.D <= 512) return launch_norm<64, 1>(a, s);
+  if (a.D <= 2048) return launch_norm<256, 1>(a, s);
+  if (a.D <= 4096) return launch_norm<256, 2>(a, s);
+  if (a.D <= 8192) return launch_norm<256, 4>(a, s);
+  if (a.D <= 16384) return launch_norm<1024, 2>(a, s);
+  return launch_norm<1024, 4>(a, s);
+}
+
+}  // namespace w8

@@ -586,6 +586,94 @@ w8_status w8_moe_linear_config(w8_fmt fmt, int E, int T, int N, int K, int max_m
 w8_status w8_moe_tune(w8_fmt fmt, int E, int T, int N, int K, int topk,
                       const w8_tune_opts *opts, w8_cfg *best, w8_tune_stats *stats);
 
+/* ------------------------------------- Block_FP8 at any token count -- */
+/* The operators of a Block_FP8 layer outside the small-M window: any number
+ * of rows (0: nothing is computed or launched, buffers may be NULL), up to
+ * 2^22 - 1 per call.  Codes are E4M3FN with one fp32 scale per 1x128 group of
+ * a row, [rows, ceil(K/128)] row-major; the last group may be shorter than
+ * 128.  Same allocation, ordering, capture and error rules as w8_gemm_w8a8.
+ * These entry points take no configuration: each picks its kernel from the
+ * sizes and alignments.                                                    */
+
+/* Codes and scales of x, or with gate != NULL of silu(gate) * x, where
+ * silu(g) = g / (1 + exp(-g)): s = amax / 448 (1 for an all-zero group),
+ * codes = round-to-nearest-even(x / s).  The gated product is fp32, not
+ * rounded before it is quantized.  One launch.
+ *   x, gate  bf16 [M, K], row strides ldx, ldg elements (device), 16-byte
+ *            aligned, strides multiples of 8 (column slices of one buffer,
+ *            for instance)
+ *   xq       codes [M, K], row stride ldq bytes, 8-byte aligned, ldq % 8 == 0
+ *            (the GEMMs below need 16)
+ *   sx       fp32 [M, ceil(K/128)]
+ * K >= 8, K % 8 == 0.  A group with a NaN or an infinity gets a non-finite
+ * scale, so it dequantizes to non-finite values.                           */
+w8_status w8_block_quantize(int M, int K, const void *x, int64_t ldx, const void *gate,
+                            int64_t ldg, void *xq, int64_t ldq, float *sx, w8_stream stream);
+
+/* The residual update and the norm between two blocks, in one pass:
+ *   b = y, or with post_weight  b = post_weight * y / sqrt(mean(y^2) + eps)
+ *   h = residual + scale * gate * b                (gate NULL: 1)
+ *   z = weight * h / sqrt(mean(h^2) + eps)
+ * per row of D elements, in fp32; h and z are rounded once, and z comes from
+ * the unrounded h.  One launch.
+ *   y            bf16 [M, D]
+ *   residual, h  bf16, or with residual_fp32 == 1 fp32, [M, D]; h may be
+ *                residual itself (same stride)
+ *   post_weight  bf16 [D] or NULL;  weight  bf16 [D]
+ *   gate         bf16 [M, D], with ldg == 0 one row [D] for every row; or NULL
+ *   z            bf16 [M, D] or NULL
+ *   zq, sz       z as codes [M, D] (row stride ldq bytes) and scales, as
+ *                w8_block_quantize gives them for the unrounded z; or NULL
+ *                (at least one of z and zq)
+ * Strides in elements, >= D; pointers aligned to their element.
+ * 1 <= D <= 32768 (above: W8_E_UNSUPPORTED), eps >= 0.                     */
+w8_status w8_residual_norm(int M, int D, const void *y, int64_t ldy, const void *residual,
+                           int64_t ldr, int residual_fp32, const void *post_weight,
+                           const void *gate, int64_t ldg, float scale, const void *weight,
+                           float eps, void *h, int64_t ldh, void *z, int64_t ldz, void *zq,
+                           int64_t ldq, float *sz, w8_stream stream);
+
+/* Y[M, N] = dequant(Xq) . dequant(Wq)^T in Block_FP8 for any M:
+ *   Y[m, n] = sum_g sx[m, g] sw[n/128, g] sum_{k in g} Xq[m, k] Wq[n, k]
+ *   xq, sx  codes, row stride ldq bytes (>= K, % 16), 16-byte aligned; scales
+ *   wq, sw  codes row-major [N, K] (ldw >= K, % 16), or ldw = 0: the packed
+ *           layout 1 of w8_pack_weight (K % 128 == 0); fp32 scales
+ *           [ceil(N/128), ceil(K/128)]
+ *   y       bf16 [M, N], row stride ldy >= N elements
+ *   ws      w8_block_gemm_workspace_size bytes with w8_gemm_w8a8's rules
+ *           (zero-filled before its first use; one workspace may serve both
+ *           entry points), NULL when the size is 0
+ * N >= 1, K >= 16, K % 16 == 0, finite codes.  Partial sums of a group come
+ * from the fp8 matrix instructions; groups are summed in fp32 in K order, so
+ * results are run-to-run deterministic.                                    */
+w8_status w8_block_gemm(int M, int N, int K, const void *xq, int64_t ldq, const float *sx,
+                        const void *wq, int64_t ldw, const float *sw, void *y, int64_t ldy,
+                        void *ws, size_t ws_bytes, w8_stream stream);
+/* Bytes of workspace (packed: the weight layout, 0 or 1). */
+w8_status w8_block_gemm_workspace_size(int M, int N, int K, int packed, size_t *bytes);
+
+/* The same product per expert over ragged lists of rows: for entry i of
+ * expert e, offsets[e] <= i < offsets[e+1],
+ *   Y[i, :] = dequant(xq[rows[i]]) . dequant(Wq_e)^T
+ * with any number of entries per expert (w8_moe_gemm holds each to 32).  One
+ * launch over all experts; the routing is read on the device, and an expert
+ * with no entry reads no weights.
+ *   xq, sx   T rows of codes and scales
+ *   offsets  int32 [E + 1] (device), ascending, offsets[0] = 0, offsets[E] =
+ *            n_rows; clamped to [0, n_rows], so bad routing reads and writes
+ *            nothing outside the buffers (entries may stay unwritten)
+ *   rows     int32 [n_rows] (device), clamped to [0, T); NULL: entry i is
+ *            row i (T >= n_rows)
+ *   wq, sw   expert e's codes at wq + e * w_stride bytes (w_stride % 16 == 0;
+ *            row-major or ldw = 0 packed), scales at sw + e * sw_stride floats
+ *   y        bf16 [n_rows, N]
+ * 1 <= E <= 65536; the rest as for w8_block_gemm.  No workspace.           */
+w8_status w8_grouped_gemm(int E, int T, int N, int K, const void *xq, int64_t ldq,
+                          const float *sx, const int32_t *offsets, const int32_t *rows,
+                          int n_rows, const void *wq, int64_t ldw, int64_t w_stride,
+                          const float *sw, int64_t sw_stride, void *y, int64_t ldy,
+                          w8_stream stream);
+
 /* -------------------------------------------------------- measurement -- */
 /* The read floor the GEMM is measured against: one kernel launch on `stream`
  * that reads `bytes` of device memory from `src` once (16-byte non-temporal
