@@ -55,17 +55,18 @@ struct Tile {
   static constexpr int NW = WM * WN, THREADS = 64 * NW;
   static constexpr int NM = BM / WM / 16, NN = BN / WN / 16;  // MFMA tiles per wave
   static_assert(BN / WN <= 128, "a wave's weight rows lie in one 128-row scale block");
-  // LDS of one stage: token codes, weight codes, token scales
+  // LDS: ST stages of token and weight codes, then two buffers of scales for
+  // eight steps each: the tokens' (32 bytes a token), then the weight blocks'
   static constexpr int X_BYTES = BM * 128, W_BYTES = BN * 128;
-  static constexpr int S_BYTES = (BM + 63) / 64 * 256;
-  static constexpr int STAGE = X_BYTES + W_BYTES + S_BYTES;
-  static constexpr int LDS = ST * STAGE;
+  static constexpr int STAGE = X_BYTES + W_BYTES;
+  static constexpr int SX_BYTES = (BM * 32 + 1023) / 1024 * 1024;
+  static constexpr int SCALES = SX_BYTES + 256;
+  static constexpr int LDS = ST * STAGE + 2 * SCALES;
   // direct-to-LDS loads of one wave per stage (a wave whose share is short
   // repeats its last piece, so that every wave counts the same loads)
   static constexpr int PX = (X_BYTES / 1024 + NW - 1) / NW;
   static constexpr int PW = (W_BYTES / 1024 + NW - 1) / NW;
-  static constexpr int PS = (S_BYTES / 256 + NW - 1) / NW;
-  static constexpr int LOADS = PX + PW + PS;
+  static constexpr int LOADS = PX + PW;
 };
 
 extern __shared__ __align__(1024) uint8_t smem[];
@@ -140,7 +141,6 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
 
   const uint8_t* px[T::PX];
   const uint8_t* pw[T::PW];
-  const float* ps[T::PS];
   auto x_row = [&](int i) -> long long {
     const int m = min(m0 + i, m1 - 1);
     if constexpr (GROUPED) {
@@ -164,12 +164,33 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
       pw[i] = wq + min(n0 + 8 * p + prow, a.N - 1) * a.ldw + 128 * (long long)ks0 + 16 * pchunk;
     }
   }
-#pragma unroll
-  for (int i = 0; i < T::PS; ++i) {
-    const int p = min(wave + i * NW, T::S_BYTES / 256 - 1);
-    ps[i] = a.sx + x_row(min(64 * p + lane, BM - 1)) * a.G + ks0;
-  }
   const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
+
+  // Token scales: 16 bytes (four steps) per lane, token 32 p + lane / 2 of
+  // piece p.  Near the end of a row the four are its last four (scale_at()
+  // knows); a row of fewer than four goes in single words.
+  const int G = a.G;
+  const float* swt = sw + (long long)(n0 / 128) * G;
+  const int sw_blocks = min((a.N + 127) / 128 - n0 / 128, (BN + 127) / 128);
+  auto scale_start = [&](int g4) { return G >= 4 ? min(g4, G - 4) : g4; };
+  auto issue_scales = [&](int c) {
+    const unsigned base = lds0 + ST * T::STAGE + (c & 1) * T::SCALES;
+    if (G >= 4) {
+      for (int p = wave; p < T::SX_BYTES / 1024; p += NW)
+        load_lds16(reinterpret_cast<const uint8_t*>(
+                       a.sx + x_row(min(32 * p + (lane >> 1), BM - 1)) * G +
+                       scale_start(8 * c + 4 * (lane & 1))),
+                   base + p * 1024);
+    } else {
+      for (int p = wave; p < T::SX_BYTES / 256; p += NW)
+        load_lds4(a.sx + x_row(min(8 * p + (lane >> 3), BM - 1)) * G + min(lane & 7, G - 1),
+                  base + p * 256);
+    }
+    if (wave == NW - 1)
+      load_lds4(swt + (long long)min((lane >> 3) & 1, sw_blocks - 1) * G +
+                    min(8 * c + (lane & 7), G - 1),
+                base + T::SX_BYTES);
+  };
 
   auto issue = [&](int k, int stage) {
     const unsigned base = lds0 + stage * T::STAGE;
@@ -186,19 +207,11 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
       load_lds16(PACKED ? pw[i] : pw[i] + adj, base + T::X_BYTES + p * 1024);
       pw[i] += PACKED ? 2048 : 128;
     }
-#pragma unroll
-    for (int i = 0; i < T::PS; ++i) {
-      const int p = min(wave + i * NW, T::S_BYTES / 256 - 1);
-      load_lds4(ps[i], base + T::X_BYTES + T::W_BYTES + p * 256);
-      ps[i] += 1;
-    }
+    // Scales of steps 8c .. 8c + 7 come with the first step that needs them:
+    // a token's scales are consecutive in memory, so taking eight steps at
+    // once fetches each cache line an eighth as often as one step would.
+    if ((k & 7) == 0 || k == ks0) issue_scales(k >> 3);
   };
-
-  // the weight block's scales: lane l holds step (multiple of 64) + l
-  const float* swr = sw + (long long)((n0 + wn * 16 * NN) / 128 < (a.N + 127) / 128
-                                          ? (n0 + wn * 16 * NN) / 128
-                                          : (a.N + 127) / 128 - 1) * a.G;
-  float swv = swr[min(ks0 + lane, k_steps - 1)];
 
   v4f acc[NN][NM];
 #pragma unroll
@@ -211,6 +224,7 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
     // (steps past the end re-load the last one into a stage nobody reads)
     if (ks0 + s < ks1) issue(ks0 + s, s);
   }
+  const int c0 = 16 * (q ^ (r & 7)), c1 = 16 * ((q + 4) ^ (r & 7));
   int stage = 0;
   for (int k = ks0; k < ks1; ++k) {
     // steps k .. k + ST - 2 are in flight, except near the end
@@ -219,28 +233,31 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
     else
       wait_stage<0>();
     if (k + ST - 1 < ks1) issue(k + ST - 1, stage == 0 ? ST - 1 : stage - 1);
-    const uint8_t* xs = smem + stage * T::STAGE + (wm * 16 * NM) * 128;
-    const uint8_t* ws = smem + stage * T::STAGE + T::X_BYTES + (wn * 16 * NN) * 128;
-    const float* ss =
-        reinterpret_cast<const float*>(smem + stage * T::STAGE + T::X_BYTES + T::W_BYTES) +
-        wm * 16 * NM + r;
-    const int c0 = 16 * (q ^ (r & 7)), c1 = 16 * ((q + 4) ^ (r & 7));
-    if (((k - ks0) & 63) == 0 && k != ks0) swv = swr[min(k + lane, k_steps - 1)];
-    const float swk = __builtin_bit_cast(
-        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, swv), (k - ks0) & 63));
+    uint8_t* xs = smem + stage * T::STAGE;
+    if (k == tail_step) {
+      // K ends inside this step: the tokens' chunks past it become zeros
+      for (int c = threadIdx.x; c < BM * (8 - tail_chunks); c += T::THREADS) {
+        const int row = c / (8 - tail_chunks), ch = tail_chunks + c % (8 - tail_chunks);
+        *reinterpret_cast<v4i*>(xs + row * 128 + 16 * (ch ^ (row & 7))) = v4i{0, 0, 0, 0};
+      }
+      wait_stage<63>();
+    }
+    const uint8_t* ws = xs + T::X_BYTES + (wn * 16 * NN) * 128;
+    xs += (wm * 16 * NM) * 128;
+    const int g4 = scale_start(k & ~3);
+    const uint8_t* ss = smem + ST * T::STAGE + ((k >> 3) & 1) * T::SCALES;
+    const float swk =
+        *reinterpret_cast<const float*>(ss + T::SX_BYTES + 32 * ((wn * 16 * NN) / 128) + 4 * (k & 7));
+    ss += (wm * 16 * NM + r) * 32 + 16 * ((k >> 2) & 1) + 4 * (k - g4);
     v8i xf[NM];
     float sc[NM];
 #pragma unroll
     for (int j = 0; j < NM; ++j) {
       const uint8_t* p = xs + (16 * j + r) * 128;
-      v4i lo = *reinterpret_cast<const v4i*>(p + c0);
-      v4i hi = *reinterpret_cast<const v4i*>(p + c1);
-      if (k == tail_step) {
-        if (q >= tail_chunks) lo = v4i{0, 0, 0, 0};
-        if (q + 4 >= tail_chunks) hi = v4i{0, 0, 0, 0};
-      }
+      const v4i lo = *reinterpret_cast<const v4i*>(p + c0);
+      const v4i hi = *reinterpret_cast<const v4i*>(p + c1);
       xf[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      sc[j] = ss[16 * j] * swk;
+      sc[j] = *reinterpret_cast<const float*>(ss + 512 * j) * swk;
     }
 #pragma unroll
     for (int i = 0; i < NN; ++i) {
