@@ -20,6 +20,8 @@ constexpr int kMaxN = 1 << 24;
 // kernels take up to 1024 per row
 constexpr int kMaxRows = (1 << 22) - 1;
 
+constexpr int64_t kMaxStride = 1 << 23;
+
 int groups_of(int K) { return (K + W8_GROUP - 1) / W8_GROUP; }
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
@@ -50,6 +52,9 @@ w8_status check_operands(int N, int K, const void* xq, int64_t ldq, const float*
   if (ldw != 0 && (ldw < K || ldw % 16))
     return fail(W8_E_INVALID, "ldw must be >= K and a multiple of 16 (row-major weights) or 0 "
                               "(packed; the K-segmented layouts are for the small-M GEMM)");
+  // (a tile's rows are addressed by 32-bit offsets from its first)
+  if (ldq > kMaxStride || ldw > kMaxStride)
+    return fail(W8_E_INVALID, "ldq and ldw must be at most 2^23");
   *packed = ldw == 0;
   if (*packed && K % W8_GROUP) return fail(W8_E_INVALID, "packed weights need K % 128 == 0");
   if (ldy < N) return fail(W8_E_INVALID, "output leading dimension must be >= N");

@@ -22,18 +22,20 @@ namespace {
 // 4 i).  M0 carries the LDS address and needs one wait state before its use.
 // Written as assembly because the compiler, which cannot tell the stages of
 // the LDS buffer apart, would wait for every load in flight before each LDS
-// read; wait_stage() below does the waiting.
+// read; wait_stage() below does the waiting, and as volatile assembly the two
+// keep their order.
+// The address is a 64-bit one per lane, or a uniform base and a 32-bit offset
+// per lane.
 __device__ __forceinline__ void load_lds16(const uint8_t* p, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(p));
+}
+__device__ __forceinline__ void load_lds16(const uint8_t* base, unsigned off, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
-               : "s"(lds), "v"(p)
-               : "memory");
+               : "s"(lds), "v"(off), "s"(base));
 }
 __device__ __forceinline__ void load_lds4(const float* p, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
-               :
-               : "s"(lds), "v"(p)
-               : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(p));
 }
 // Waits until at most N of this wave's loads are in flight and its LDS reads
 // have returned, then for the workgroup's other waves.
@@ -139,8 +141,6 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
   const int tail_step = tail_chunks ? k_steps - 1 : -1;
   const int tail_adj = 16 * (min(pchunk, max(tail_chunks, 1) - 1) - pchunk);
 
-  const uint8_t* px[T::PX];
-  const uint8_t* pw[T::PW];
   auto x_row = [&](int i) -> long long {
     const int m = min(m0 + i, m1 - 1);
     if constexpr (GROUPED) {
@@ -148,21 +148,34 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
     }
     return m;
   };
+  // Tokens: an offset from the tile's first row, or for gathered rows (which
+  // may lie more than 4 GiB apart) a pointer.  Weights: an offset from the
+  // tile's first row.  The bases advance by one step with each step's loads.
+  const uint8_t* px[T::PX];
+  unsigned ox[T::PX], ow[T::PW];
+  const uint8_t* xb = a.xq + 128LL * ks0;
+  const uint8_t* wb = wq;
+  if constexpr (!GROUPED) xb += m0 * a.ldq;
+  if constexpr (PACKED)
+    wb += ((long long)(n0 / 16) * k_steps + ks0) * 2048;
+  else
+    wb += n0 * a.ldw + 128LL * ks0;
 #pragma unroll
   for (int i = 0; i < T::PX; ++i) {
     const int p = min(wave + i * NW, T::X_BYTES / 1024 - 1);
-    px[i] = a.xq + x_row(8 * p + prow) * a.ldq + 128 * (long long)ks0 + 16 * pchunk;
+    if constexpr (GROUPED)
+      px[i] = xb + x_row(8 * p + prow) * a.ldq + 16 * pchunk;
+    else
+      ox[i] = (unsigned)(min(8 * p + prow, m1 - 1 - m0) * a.ldq + 16 * pchunk);
   }
 #pragma unroll
   for (int i = 0; i < T::PW; ++i) {
     const int p = min(wave + i * NW, T::W_BYTES / 1024 - 1);
-    if constexpr (PACKED) {
-      // fragments of 16 rows x 128 bytes, 2 KiB per K-step, in lane order
-      const int nb = min(n0 / 16 + p / 2, (a.N + 15) / 16 - 1);
-      pw[i] = wq + ((long long)nb * k_steps + ks0) * 2048 + (p & 1) * 1024 + 16 * lane;
-    } else {
-      pw[i] = wq + min(n0 + 8 * p + prow, a.N - 1) * a.ldw + 128 * (long long)ks0 + 16 * pchunk;
-    }
+    if constexpr (PACKED)  // fragments of 16 rows x 128 bytes, 2 KiB per K-step, in lane order
+      ow[i] = (unsigned)(min(p / 2, (a.N + 15) / 16 - 1 - n0 / 16) * k_steps) * 2048u +
+              (p & 1) * 1024 + 16 * lane;
+    else
+      ow[i] = (unsigned)(min(8 * p + prow, a.N - 1 - n0) * a.ldw + 16 * pchunk);
   }
   const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
 
@@ -192,24 +205,50 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
                 base + T::SX_BYTES);
   };
 
-  auto issue = [&](int k, int stage) {
-    const unsigned base = lds0 + stage * T::STAGE;
-    const int adj = k == tail_step ? tail_adj : 0;
-#pragma unroll
-    for (int i = 0; i < T::PX; ++i) {
-      const int p = min(wave + i * NW, T::X_BYTES / 1024 - 1);
-      load_lds16(px[i] + adj, base + p * 1024);
-      px[i] += 128;
+  // load n (compile time) of the wave's share of a step; wave-uniform LDS
+  // addresses
+  auto issue_one = [&](int n, unsigned base) {
+    if (n < T::PX) {
+      const unsigned lds = base + min(wave + n * NW, T::X_BYTES / 1024 - 1) * 1024;
+      if constexpr (GROUPED)
+        load_lds16(px[n], lds);
+      else
+        load_lds16(xb, ox[n], lds);
+    } else {
+      const int i = n - T::PX;
+      load_lds16(wb, ow[i],
+                 base + T::X_BYTES + min(wave + i * NW, T::W_BYTES / 1024 - 1) * 1024);
     }
+  };
+  // Before the loads of step k (in order): moves the bases on from step k - 1,
+  // and at the step that K ends inside of moves the lanes off the missing
+  // chunks.  Past the last step the bases stay, so that every step issues the
+  // same number of loads (the last ones into a stage that nobody reads).
+  // Scales of steps 8c .. 8c + 7 come with the first step that needs them: a
+  // token's scales are consecutive in memory, so taking eight steps at once
+  // fetches each cache line an eighth as often as one step would.
+  auto advance = [&](int k) {
+    if (k >= ks1) return;
+    if (k > ks0) {
+      if constexpr (GROUPED) {
 #pragma unroll
-    for (int i = 0; i < T::PW; ++i) {
-      const int p = min(wave + i * NW, T::W_BYTES / 1024 - 1);
-      load_lds16(PACKED ? pw[i] : pw[i] + adj, base + T::X_BYTES + p * 1024);
-      pw[i] += PACKED ? 2048 : 128;
+        for (int i = 0; i < T::PX; ++i) px[i] += 128;
+      } else {
+        xb += 128;
+      }
+      wb += PACKED ? 2048 : 128;
     }
-    // Scales of steps 8c .. 8c + 7 come with the first step that needs them:
-    // a token's scales are consecutive in memory, so taking eight steps at
-    // once fetches each cache line an eighth as often as one step would.
+    if (k == tail_step) {
+#pragma unroll
+      for (int i = 0; i < T::PX; ++i) {
+        if constexpr (GROUPED)
+          px[i] += tail_adj;
+        else
+          ox[i] += tail_adj;
+      }
+#pragma unroll
+      for (int i = 0; i < T::PW; ++i) ow[i] += tail_adj;
+    }
     if ((k & 7) == 0 || k == ks0) issue_scales(k >> 3);
   };
 
@@ -221,18 +260,17 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
 
 #pragma unroll
   for (int s = 0; s < ST - 1; ++s) {
-    // (steps past the end re-load the last one into a stage nobody reads)
-    if (ks0 + s < ks1) issue(ks0 + s, s);
+    advance(ks0 + s);
+#pragma unroll
+    for (int n = 0; n < T::LOADS; ++n) issue_one(n, lds0 + s * T::STAGE);
   }
   const int c0 = 16 * (q ^ (r & 7)), c1 = 16 * ((q + 4) ^ (r & 7));
   int stage = 0;
   for (int k = ks0; k < ks1; ++k) {
-    // steps k .. k + ST - 2 are in flight, except near the end
-    if (ST > 2 && k + ST - 2 < ks1)
-      wait_stage<(ST - 2) * T::LOADS>();
-    else
-      wait_stage<0>();
-    if (k + ST - 1 < ks1) issue(k + ST - 1, stage == 0 ? ST - 1 : stage - 1);
+    // steps k .. k + ST - 2 are in flight
+    wait_stage<(ST - 2) * T::LOADS>();
+    advance(k + ST - 1);
+    const unsigned next = lds0 + (stage == 0 ? ST - 1 : stage - 1) * T::STAGE;
     uint8_t* xs = smem + stage * T::STAGE;
     if (k == tail_step) {
       // K ends inside this step: the tokens' chunks past it become zeros
@@ -249,37 +287,59 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
     const float swk =
         *reinterpret_cast<const float*>(ss + T::SX_BYTES + 32 * ((wn * 16 * NN) / 128) + 4 * (k & 7));
     ss += (wm * 16 * NM + r) * 32 + 16 * ((k >> 2) & 1) + 4 * (k - g4);
-    v8i xf[NM];
+    auto frag = [&](const uint8_t* rows16, int off0, int off1) -> v8i {
+      const v4i lo = *reinterpret_cast<const v4i*>(rows16 + off0);
+      const v4i hi = *reinterpret_cast<const v4i*>(rows16 + off1);
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    auto weights = [&](int i) {
+      return PACKED ? frag(ws + i * 2048, 16 * lane, 1024 + 16 * lane)
+                    : frag(ws + i * 2048, r * 128 + c0, r * 128 + c1);
+    };
+    // Operand reads in the order of their use: the first weight tile, the
+    // tokens, then weight tiles two ahead of their MFMAs.
+    constexpr int AHEAD = NN < 3 ? NN : 3;
+    v8i wf[AHEAD], xf[NM];
     float sc[NM];
+    wf[0] = weights(0);
 #pragma unroll
-    for (int j = 0; j < NM; ++j) {
-      const uint8_t* p = xs + (16 * j + r) * 128;
-      const v4i lo = *reinterpret_cast<const v4i*>(p + c0);
-      const v4i hi = *reinterpret_cast<const v4i*>(p + c1);
-      xf[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      sc[j] = *reinterpret_cast<const float*>(ss + 512 * j) * swk;
-    }
+    for (int j = 0; j < NM; ++j) xf[j] = frag(xs + j * 2048, r * 128 + c0, r * 128 + c1);
+#pragma unroll
+    for (int j = 0; j < NM; ++j) sc[j] = *reinterpret_cast<const float*>(ss + 512 * j) * swk;
+#pragma unroll
+    for (int i = 1; i < AHEAD - 1; ++i) wf[i] = weights(i);
+    // MFMA n = (i, j) goes out while the scaled additions of MFMA n - LAG,
+    // whose result has arrived, run beside it; the scheduling barriers keep
+    // the compiler from pairing each MFMA with its own additions, which would
+    // wait out its latency every time.
+    constexpr int LAG = NN * NM < 4 ? 1 : 3;
+    v4f t[LAG + 1];
+    auto add = [&](int n) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        acc[n / NM][n % NM][u] =
+            __builtin_fmaf(t[n % (LAG + 1)][u], sc[n % NM], acc[n / NM][n % NM][u]);
+    };
 #pragma unroll
     for (int i = 0; i < NN; ++i) {
-      v4i lo, hi;
-      if constexpr (PACKED) {
-        lo = *reinterpret_cast<const v4i*>(ws + i * 2048 + 16 * lane);
-        hi = *reinterpret_cast<const v4i*>(ws + i * 2048 + 1024 + 16 * lane);
-      } else {
-        const uint8_t* p = ws + (16 * i + r) * 128;
-        lo = *reinterpret_cast<const v4i*>(p + c0);
-        hi = *reinterpret_cast<const v4i*>(p + c1);
-      }
-      const v8i wf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      if (i + AHEAD - 1 < NN) wf[(i + AHEAD - 1) % AHEAD] = weights(i + AHEAD - 1);
+      // the later step's loads are dealt over the MFMAs: issued together they
+      // would hold up every wave's MFMAs behind the memory path's queue
+#pragma unroll
+      for (int n = i * T::LOADS / NN; n < (i + 1) * T::LOADS / NN; ++n) issue_one(n, next);
 #pragma unroll
       for (int j = 0; j < NM; ++j) {
-        const v4f t = mfma_f8(wf, xf[j], v4f{0, 0, 0, 0});
-#pragma unroll
-        for (int u = 0; u < 4; ++u) acc[i][j][u] = __builtin_fmaf(t[u], sc[j], acc[i][j][u]);
+        const int n = i * NM + j;
+        t[n % (LAG + 1)] = mfma_f8(wf[i % AHEAD], xf[j], v4f{0, 0, 0, 0});
+        if (n >= LAG) add(n - LAG);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+#pragma unroll
+    for (int n = NN * NM - LAG; n < NN * NM; ++n) add(n);
     stage = stage == ST - 1 ? 0 : stage + 1;
   }
+  wait_stage<0>();  // the loads past the last step have landed before LDS is used again or freed
 
   // ---- split-K: see the protocol of the small-M GEMM's shared tiles
   // (partials written through with agent scope, acknowledged, counted; the
