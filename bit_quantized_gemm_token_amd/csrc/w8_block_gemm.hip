@@ -323,18 +323,21 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
 #pragma unroll
     for (int i = 0; i < NN; ++i) {
       if (i + AHEAD - 1 < NN) wf[(i + AHEAD - 1) % AHEAD] = weights(i + AHEAD - 1);
-      // the later step's loads are dealt over the MFMAs: issued together they
-      // would hold up every wave's MFMAs behind the memory path's queue
-#pragma unroll
-      for (int n = i * T::LOADS / NN; n < (i + 1) * T::LOADS / NN; ++n) issue_one(n, next);
 #pragma unroll
       for (int j = 0; j < NM; ++j) {
         const int n = i * NM + j;
+        // the later step's loads are dealt over the first MFMAs: all at once
+        // they would hold up the MFMAs behind the memory path's queue, and
+        // later they would arrive after the step's end (8192 x 5120 x 8192:
+        // one a MFMA 346 us, one every three 367)
+        if (n < T::LOADS) issue_one(n, next);
         t[n % (LAG + 1)] = mfma_f8(wf[i % AHEAD], xf[j], v4f{0, 0, 0, 0});
         if (n >= LAG) add(n - LAG);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
+#pragma unroll
+    for (int n = NN * NM; n < T::LOADS; ++n) issue_one(n, next);
 #pragma unroll
     for (int n = NN * NM - LAG; n < NN * NM; ++n) add(n);
     stage = stage == ST - 1 ? 0 : stage + 1;
