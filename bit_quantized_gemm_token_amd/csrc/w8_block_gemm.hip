@@ -10,6 +10,8 @@
 // (D = W X^T), so a lane's accumulators all belong to one token: the step's
 // scale is one product per token column, and a group's partial sum is added
 // as acc += partial * (sx * sw), one fp32 FMA per element per group.
+#include <type_traits>
+
 #include "w8_block.hpp"
 #include "w8_device.hpp"
 #include "w8_launch.hpp"
@@ -69,6 +71,24 @@ struct Tile {
   static constexpr int PX = (X_BYTES / 1024 + NW - 1) / NW;
   static constexpr int PW = (W_BYTES / 1024 + NW - 1) / NW;
   static constexpr int LOADS = PX + PW;
+  // The large tiles run the rotated loop (see there): H weight tiles per half
+  // step; the first H + 2 of a step are staged with its tokens, the others
+  // one step later.  In LDS a stage's weight tiles (16 rows, 2 KiB) are
+  // ordered early ones first.
+  static constexpr bool ROTATED = NN >= 4;
+  static constexpr int H = NN / 2, EARLY = ROTATED ? H + 2 : NN;
+  static constexpr int PW1 = WN * EARLY * 2 / NW;  // (exact where ROTATED)
+  static __device__ __forceinline__ constexpr int slot(int wn, int i) {
+    return i < EARLY ? wn * EARLY + i : WN * EARLY + wn * (NN - EARLY) + i - EARLY;
+  }
+  // the weight tile, counted from the workgroup's first, in slot u
+  static __device__ __forceinline__ int tile_in(int u) {
+    if (EARLY == NN) return u;
+    if (u < WN * EARLY) return u / EARLY * NN + u % EARLY;
+    constexpr int L = NN - EARLY > 0 ? NN - EARLY : 1;
+    u -= WN * EARLY;
+    return u / L * NN + EARLY + u % L;
+  }
 };
 
 extern __shared__ __align__(1024) uint8_t smem[];
@@ -138,7 +158,7 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
   // a last step that K ends inside of: chunks past K re-read the last whole
   // one, and the token operand is masked after its LDS read
   const int tail_chunks = (a.K & 127) >> 4;
-  const int tail_step = tail_chunks ? k_steps - 1 : -1;
+  const int tail_step = tail_chunks ? k_steps - 1 : -2;  // (-2: none, nor is -1 before step 0)
   const int tail_adj = 16 * (min(pchunk, max(tail_chunks, 1) - 1) - pchunk);
 
   auto x_row = [&](int i) -> long long {
@@ -171,11 +191,12 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
 #pragma unroll
   for (int i = 0; i < T::PW; ++i) {
     const int p = min(wave + i * NW, T::W_BYTES / 1024 - 1);
+    const int wt = T::tile_in(p / 2);
     if constexpr (PACKED)  // fragments of 16 rows x 128 bytes, 2 KiB per K-step, in lane order
-      ow[i] = (unsigned)(min(p / 2, (a.N + 15) / 16 - 1 - n0 / 16) * k_steps) * 2048u +
+      ow[i] = (unsigned)(min(wt, (a.N + 15) / 16 - 1 - n0 / 16) * k_steps) * 2048u +
               (p & 1) * 1024 + 16 * lane;
     else
-      ow[i] = (unsigned)(min(8 * p + prow, a.N - 1 - n0) * a.ldw + 16 * pchunk);
+      ow[i] = (unsigned)(min(16 * wt + 8 * (p & 1) + prow, a.N - 1 - n0) * a.ldw + 16 * pchunk);
   }
   const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
 
@@ -205,9 +226,11 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
                 base + T::SX_BYTES);
   };
 
-  // load n (compile time) of the wave's share of a step; wave-uniform LDS
-  // addresses
-  auto issue_one = [&](int n, unsigned base) {
+  // load n (compile time) of the wave's share of a step, into the stage at LDS
+  // address `base`; the late weight tiles (ROTATED) are the previous step's,
+  // into the stage at `late`
+  const uint8_t* wb_late = wb;
+  auto issue_one = [&](int n, unsigned base, unsigned late) {
     if (n < T::PX) {
       const unsigned lds = base + min(wave + n * NW, T::X_BYTES / 1024 - 1) * 1024;
       if constexpr (GROUPED)
@@ -216,8 +239,10 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
         load_lds16(xb, ox[n], lds);
     } else {
       const int i = n - T::PX;
-      load_lds16(wb, ow[i],
-                 base + T::X_BYTES + min(wave + i * NW, T::W_BYTES / 1024 - 1) * 1024);
+      const bool is_late = T::ROTATED && i >= T::PW1;
+      load_lds16(is_late ? wb_late : wb, ow[i],
+                 (is_late ? late : base) + T::X_BYTES +
+                     min(wave + i * NW, T::W_BYTES / 1024 - 1) * 1024);
     }
   };
   // Before the loads of step k (in order): moves the bases on from step k - 1,
@@ -228,6 +253,13 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
   // token's scales are consecutive in memory, so taking eight steps at once
   // fetches each cache line an eighth as often as one step would.
   auto advance = [&](int k) {
+    if constexpr (T::ROTATED && T::PW1 < T::PW) {
+      if (k > ks0 + 1) wb_late += PACKED ? 2048 : 128;
+      if (k - 1 == tail_step) {
+#pragma unroll
+        for (int i = T::PW1; i < T::PW; ++i) ow[i] += tail_adj;
+      }
+    }
     if (k >= ks1) return;
     if (k > ks0) {
       if constexpr (GROUPED) {
@@ -247,7 +279,7 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
           ox[i] += tail_adj;
       }
 #pragma unroll
-      for (int i = 0; i < T::PW; ++i) ow[i] += tail_adj;
+      for (int i = 0; i < (T::ROTATED ? T::PW1 : T::PW); ++i) ow[i] += tail_adj;
     }
     if ((k & 7) == 0 || k == ks0) issue_scales(k >> 3);
   };
@@ -258,89 +290,185 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
 #pragma unroll
     for (int j = 0; j < NM; ++j) acc[i][j] = v4f{0, 0, 0, 0};
 
-#pragma unroll
-  for (int s = 0; s < ST - 1; ++s) {
-    advance(ks0 + s);
-#pragma unroll
-    for (int n = 0; n < T::LOADS; ++n) issue_one(n, lds0 + s * T::STAGE);
-  }
+  // ---- LDS reads
   const int c0 = 16 * (q ^ (r & 7)), c1 = 16 * ((q + 4) ^ (r & 7));
-  int stage = 0;
-  for (int k = ks0; k < ks1; ++k) {
-    // steps k .. k + ST - 2 are in flight
-    wait_stage<(ST - 2) * T::LOADS>();
-    advance(k + ST - 1);
-    const unsigned next = lds0 + (stage == 0 ? ST - 1 : stage - 1) * T::STAGE;
-    uint8_t* xs = smem + stage * T::STAGE;
-    if (k == tail_step) {
-      // K ends inside this step: the tokens' chunks past it become zeros
-      for (int c = threadIdx.x; c < BM * (8 - tail_chunks); c += T::THREADS) {
-        const int row = c / (8 - tail_chunks), ch = tail_chunks + c % (8 - tail_chunks);
-        *reinterpret_cast<v4i*>(xs + row * 128 + 16 * (ch ^ (row & 7))) = v4i{0, 0, 0, 0};
-      }
-      wait_stage<63>();
-    }
-    const uint8_t* ws = xs + T::X_BYTES + (wn * 16 * NN) * 128;
-    xs += (wm * 16 * NM) * 128;
-    const int g4 = scale_start(k & ~3);
+  auto frag = [&](const uint8_t* p, int off0, int off1) -> v8i {
+    const v4i lo = *reinterpret_cast<const v4i*>(p + off0);
+    const v4i hi = *reinterpret_cast<const v4i*>(p + off1);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto tokens = [&](int j, int stage) {
+    return frag(smem + stage * T::STAGE + (wm * NM + j) * 2048, r * 128 + c0, r * 128 + c1);
+  };
+  auto weights = [&](int i, int stage) {
+    const uint8_t* p = smem + stage * T::STAGE + T::X_BYTES + T::slot(wn, i) * 2048;
+    return PACKED ? frag(p, 16 * lane, 1024 + 16 * lane) : frag(p, r * 128 + c0, r * 128 + c1);
+  };
+  // the tokens' scales of step k times the weight block's
+  auto scales = [&](int k, float* sc) {
     const uint8_t* ss = smem + ST * T::STAGE + ((k >> 3) & 1) * T::SCALES;
-    const float swk =
-        *reinterpret_cast<const float*>(ss + T::SX_BYTES + 32 * ((wn * 16 * NN) / 128) + 4 * (k & 7));
-    ss += (wm * 16 * NM + r) * 32 + 16 * ((k >> 2) & 1) + 4 * (k - g4);
-    auto frag = [&](const uint8_t* rows16, int off0, int off1) -> v8i {
-      const v4i lo = *reinterpret_cast<const v4i*>(rows16 + off0);
-      const v4i hi = *reinterpret_cast<const v4i*>(rows16 + off1);
-      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    };
-    auto weights = [&](int i) {
-      return PACKED ? frag(ws + i * 2048, 16 * lane, 1024 + 16 * lane)
-                    : frag(ws + i * 2048, r * 128 + c0, r * 128 + c1);
-    };
-    // Operand reads in the order of their use: the first weight tile, the
-    // tokens, then weight tiles two ahead of their MFMAs.
-    constexpr int AHEAD = NN < 3 ? NN : 3;
-    v8i wf[AHEAD], xf[NM];
-    float sc[NM];
-    wf[0] = weights(0);
-#pragma unroll
-    for (int j = 0; j < NM; ++j) xf[j] = frag(xs + j * 2048, r * 128 + c0, r * 128 + c1);
+    const float swk = *reinterpret_cast<const float*>(
+        ss + T::SX_BYTES + 32 * ((wn * 16 * NN) / 128) + 4 * (k & 7));
+    ss += (wm * 16 * NM + r) * 32 + 16 * ((k >> 2) & 1) + 4 * (k - scale_start(k & ~3));
 #pragma unroll
     for (int j = 0; j < NM; ++j) sc[j] = *reinterpret_cast<const float*>(ss + 512 * j) * swk;
-#pragma unroll
-    for (int i = 1; i < AHEAD - 1; ++i) wf[i] = weights(i);
-    // MFMA n = (i, j) goes out while the scaled additions of MFMA n - LAG,
-    // whose result has arrived, run beside it; the scheduling barriers keep
-    // the compiler from pairing each MFMA with its own additions, which would
-    // wait out its latency every time.
-    constexpr int LAG = NN * NM < 4 ? 1 : 3;
-    v4f t[LAG + 1];
-    auto add = [&](int n) {
+  };
+  // where K ends inside step k: the tokens' chunks past it become zeros
+  auto clear_tail = [&](int stage) {
+    uint8_t* xs = smem + stage * T::STAGE;
+    for (int c = threadIdx.x; c < BM * (8 - tail_chunks); c += T::THREADS) {
+      const int row = c / (8 - tail_chunks), ch = tail_chunks + c % (8 - tail_chunks);
+      *reinterpret_cast<v4i*>(xs + row * 128 + 16 * (ch ^ (row & 7))) = v4i{0, 0, 0, 0};
+    }
+    wait_stage<63>();
+  };
+
+  // MFMA n goes out while the scaled additions of MFMA n - LAG, whose result
+  // has arrived, run beside it; the scheduling barriers keep the compiler from
+  // pairing each MFMA with its own additions, which would wait out its latency
+  // every time.  A step's loads are dealt over the first MFMAs: all at once
+  // they would hold up the MFMAs behind the memory path's queue, and later
+  // they would arrive after the step's end (8192 x 5120 x 8192: one a MFMA 346
+  // us, one every three 367).
+  constexpr int LAG = NN * NM < 4 ? 1 : 3;
+  constexpr int P = NN * NM;
+  v4f t[LAG + 1];
+  if constexpr (T::ROTATED) {
+    // The loop is rotated by half a step against the staging: between two
+    // barriers the waves run the second half of step k - 1 (weight tiles H ..
+    // NN - 1) and the first half of step k.  At a barrier the registers hold
+    // the operands of the next MFMAs, and the tokens of step k replace those
+    // of step k - 1 one by one inside the interval, so that no wave waits for
+    // operand reads behind a barrier, and every load has a whole interval to
+    // arrive.  The last two weight tiles of a step run side by side, which
+    // frees the first token operand early.
+    constexpr int H = T::H, P2 = (NN - H) * NM, PJ = P2 - 2 * NM;
+    v8i wf[4], xf[NM];
+    float sc0[NM], sc1[NM];  // of steps k - 1 and k
+    auto tile_of = [](int p) constexpr {
+      return p >= P2 ? (p - P2) / NM : p < PJ ? H + p / NM : NN - 2 + (p & 1);
+    };
+    auto j_of = [](int p) constexpr {
+      return p >= P2 || p < PJ ? p % NM : (p - PJ) / 2;
+    };
+    auto add = [&](int p, const float* sc) {
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        acc[n / NM][n % NM][u] =
-            __builtin_fmaf(t[n % (LAG + 1)][u], sc[n % NM], acc[n / NM][n % NM][u]);
+        acc[tile_of(p)][j_of(p)][u] =
+            __builtin_fmaf(t[p % 4][u], sc[j_of(p)], acc[tile_of(p)][j_of(p)][u]);
     };
+    static_assert(P % 4 == 0 && NM % 4 == 0, "the ring of partial results continues over intervals");
+    auto interval = [&](auto first, auto last, int k, int stage) {
+      constexpr bool FIRST = decltype(first)::value, LAST = decltype(last)::value;
+      wait_stage<0>();
+      if (!LAST && k == tail_step) clear_tail(stage);
+      if constexpr (!LAST) advance(k + 1);
+      const unsigned here = lds0 + stage * T::STAGE, other = lds0 + (stage ^ 1) * T::STAGE;
+      if constexpr (FIRST) {
+        wf[0] = weights(0, stage);
 #pragma unroll
-    for (int i = 0; i < NN; ++i) {
-      if (i + AHEAD - 1 < NN) wf[(i + AHEAD - 1) % AHEAD] = weights(i + AHEAD - 1);
+        for (int j = 0; j < NM; ++j) xf[j] = tokens(j, stage);
+        wf[1] = weights(1, stage);
+        scales(k, sc1);
+      }
 #pragma unroll
-      for (int j = 0; j < NM; ++j) {
-        const int n = i * NM + j;
-        // the later step's loads are dealt over the first MFMAs: all at once
-        // they would hold up the MFMAs behind the memory path's queue, and
-        // later they would arrive after the step's end (8192 x 5120 x 8192:
-        // one a MFMA 346 us, one every three 367)
-        if (n < T::LOADS) issue_one(n, next);
-        t[n % (LAG + 1)] = mfma_f8(wf[i % AHEAD], xf[j], v4f{0, 0, 0, 0});
-        if (n >= LAG) add(n - LAG);
+      for (int p = FIRST ? P2 : 0; p < (LAST ? P2 : P); ++p) {
+        if constexpr (!FIRST) {
+          if (p < (NN - H - 2) * NM && p % NM == 0)  // (their slots' tiles are done)
+            wf[(H + 2 + p / NM) % 4] = weights(H + 2 + p / NM, stage ^ 1);
+          if constexpr (!LAST) {
+            if (p == PJ) {
+              scales(k, sc1);
+              wf[0] = weights(0, stage);
+            }
+            if (p == PJ + 2) wf[1] = weights(1, stage);
+          }
+        }
+        if (p >= P2 && (p - P2) % NM == 0) {
+          const int i = (p - P2) / NM + 2;
+          if (i < T::EARLY) wf[i % 4] = weights(i, stage);
+        }
+        if constexpr (!LAST) {
+          const int n = p - (FIRST ? P2 : 0);
+          if (n < T::LOADS) issue_one(n, other, here);
+        }
+        t[p % 4] = mfma_f8(wf[tile_of(p) % 4], xf[j_of(p)], v4f{0, 0, 0, 0});
+        if (!FIRST && !LAST && p >= PJ && p < P2 && (p & 1)) xf[j_of(p)] = tokens(j_of(p), stage);
+        if (p >= LAG + (FIRST ? P2 : 0))
+          add(p - LAG, p - LAG >= P2 ? sc1 : sc0);
+        else if (!FIRST)
+          add(P + p - LAG, sc0);
         __builtin_amdgcn_sched_barrier(0);
       }
+      if constexpr (LAST) {
+#pragma unroll
+        for (int p = P2 - LAG; p < P2; ++p) add(p, sc0);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NM; ++j) sc0[j] = sc1[j];
+      }
+    };
+    static_assert(P - P2 >= T::LOADS, "the first half step deals all loads");
+    typedef std::integral_constant<bool, true> Yes;
+    typedef std::integral_constant<bool, false> No;
+    advance(ks0);
+#pragma unroll
+    for (int n = 0; n < T::LOADS; ++n) issue_one(n, lds0, lds0 + T::STAGE);
+    interval(Yes{}, No{}, ks0, 0);
+    int stage = 1;
+    for (int k = ks0 + 1; k < ks1; ++k) {
+      interval(No{}, No{}, k, stage);
+      stage ^= 1;
     }
+    interval(No{}, Yes{}, ks1, stage);
+  } else {
 #pragma unroll
-    for (int n = NN * NM; n < T::LOADS; ++n) issue_one(n, next);
+    for (int s = 0; s < ST - 1; ++s) {
+      advance(ks0 + s);
 #pragma unroll
-    for (int n = NN * NM - LAG; n < NN * NM; ++n) add(n);
-    stage = stage == ST - 1 ? 0 : stage + 1;
+      for (int n = 0; n < T::LOADS; ++n) issue_one(n, lds0 + s * T::STAGE, 0);
+    }
+    int stage = 0;
+    for (int k = ks0; k < ks1; ++k) {
+      // steps k .. k + ST - 2 are in flight
+      wait_stage<(ST - 2) * T::LOADS>();
+      advance(k + ST - 1);
+      if (k == tail_step) clear_tail(stage);
+      const unsigned next = lds0 + (stage == 0 ? ST - 1 : stage - 1) * T::STAGE;
+      // operand reads in the order of their use, weight tiles two ahead
+      constexpr int AHEAD = NN < 3 ? NN : 3;
+      v8i wf[AHEAD], xf[NM];
+      float sc[NM];
+      wf[0] = weights(0, stage);
+#pragma unroll
+      for (int j = 0; j < NM; ++j) xf[j] = tokens(j, stage);
+      scales(k, sc);
+#pragma unroll
+      for (int i = 1; i < AHEAD - 1; ++i) wf[i] = weights(i, stage);
+      auto add = [&](int n) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          acc[n / NM][n % NM][u] =
+              __builtin_fmaf(t[n % (LAG + 1)][u], sc[n % NM], acc[n / NM][n % NM][u]);
+      };
+#pragma unroll
+      for (int i = 0; i < NN; ++i) {
+        if (i + AHEAD - 1 < NN) wf[(i + AHEAD - 1) % AHEAD] = weights(i + AHEAD - 1, stage);
+#pragma unroll
+        for (int j = 0; j < NM; ++j) {
+          const int n = i * NM + j;
+          if (n < T::LOADS) issue_one(n, next, 0);
+          t[n % (LAG + 1)] = mfma_f8(wf[i % AHEAD], xf[j], v4f{0, 0, 0, 0});
+          if (n >= LAG) add(n - LAG);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+#pragma unroll
+      for (int n = P; n < T::LOADS; ++n) issue_one(n, next, 0);
+#pragma unroll
+      for (int n = P - LAG; n < P; ++n) add(n);
+      stage = stage == ST - 1 ? 0 : stage + 1;
+    }
   }
   wait_stage<0>();  // the loads past the last step have landed before LDS is used again or freed
 
