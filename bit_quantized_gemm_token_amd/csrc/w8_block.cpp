@@ -63,12 +63,17 @@ w8_status check_operands(int N, int K, const void* xq, int64_t ldq, const float*
   return W8_OK;
 }
 
-int vec_store(const void* y, int64_t ldy) { return aligned(y, 8) && ldy % 4 == 0; }
+int vec_store(const void* y, int64_t ldy) {
+  return aligned(y, 16) && ldy % 8 == 0 ? 2 : aligned(y, 8) && ldy % 4 == 0 ? 1 : 0;
+}
 
 // ------------------------------------------------------------ tile choice --
+constexpr int kComputeUnits = 256;
+
 struct Plan {
   int tile, split_k;
   long long tiles_m, tiles_n;
+  long long whole, wgs;  // the largest tile's whole tiles; workgroups
 };
 
 Plan plan_dense(int M, int N, int K) {
@@ -79,10 +84,20 @@ Plan plan_dense(int M, int N, int K) {
   p.tiles_m = ceil_div(M, t.bm);
   p.tiles_n = ceil_div(N, t.bn);
   p.split_k = 1;
-  while (p.split_k < 16 && p.tiles_m * p.tiles_n * p.split_k < 256 &&
+  while (p.tile != kLargeTile && p.split_k < 16 && p.tiles_m * p.tiles_n * p.split_k < kComputeUnits &&
          groups_of(K) / (2 * p.split_k) >= 4)
     p.split_k *= 2;
-  if (p.tiles_m * p.tiles_n > kSplitKMaxTiles) p.split_k = 1;
+  const long long tiles = p.tiles_m * p.tiles_n;
+  if (tiles > kSplitKMaxTiles) p.split_k = 1;
+  p.whole = tiles;
+  p.wgs = tiles * p.split_k;
+  if (p.tile == kLargeTile) {
+    // one workgroup per compute unit at a time: the tiles of a last round that
+    // leaves at least half of them idle run as two halves each
+    const long long rest = tiles % kComputeUnits;
+    if (rest <= kComputeUnits / 2) p.whole = tiles - rest;
+    p.wgs = p.whole + 2 * (tiles - p.whole);
+  }
   return p;
 }
 
@@ -93,7 +108,7 @@ size_t plan_bytes(const Plan& p) {
 }
 
 w8_status check_grid(const Plan& p) {
-  const long long threads = p.tiles_m * p.tiles_n * p.split_k * block_tile(p.tile).threads;
+  const long long threads = p.wgs * block_tile(p.tile).threads;
   if (threads > 0xFFFFFFFFLL)
     return fail(W8_E_INVALID, "the launch's threads exceed 2^32 - 1: split the call along M or N");
   return W8_OK;
@@ -217,11 +232,12 @@ w8_status w8_block_gemm(int M, int N, int K, const void* xq, int64_t ldq, const 
   a.K = K;
   a.G = groups_of(K);
   a.split_k = p.split_k;
+  a.whole = (int)p.whole;
   a.vec_store = vec_store(y, ldy);
   a.tiles_m = (int)p.tiles_m;
   a.tiles_n = (int)p.tiles_n;
   const hipError_t e =
-      launch_block_gemm(p.tile, false, packed, a, static_cast<hipStream_t>(stream));
+      launch_block_gemm(p.tile, (unsigned)p.wgs, false, packed, a, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("block_gemm launch", e));
   return ok();
 }
@@ -256,9 +272,12 @@ w8_status w8_grouped_gemm(int E, int T, int N, int K, const void* xq, int64_t ld
   Plan p;
   const long long mean = n_rows / E;
   p.tile = mean <= 16 ? 0 : mean <= 32 ? 1 : mean <= 64 ? 2 : 3;
+  // (the largest tile addresses gathered rows by 32-bit offsets)
+  if (mean > 128 && (long long)T * ldq < (1LL << 32)) p.tile = kLargeTile;
   p.split_k = 1;
   p.tiles_m = n_rows / block_tile(p.tile).bm + E;
   p.tiles_n = ceil_div(N, block_tile(p.tile).bn);
+  p.whole = p.wgs = p.tiles_m * p.tiles_n;
   st = check_grid(p);
   if (st) return st;
   st = check_device();
@@ -286,7 +305,8 @@ w8_status w8_grouped_gemm(int E, int T, int N, int K, const void* xq, int64_t ld
   a.sw_stride = sw_stride;
   a.n_experts = E;
   a.xrow_max = T - 1;
-  const hipError_t e = launch_block_gemm(p.tile, true, packed, a, static_cast<hipStream_t>(stream));
+  const hipError_t e = launch_block_gemm(p.tile, (unsigned)p.wgs, true, packed, a,
+                                         static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("grouped_gemm launch", e));
   return ok();
 }

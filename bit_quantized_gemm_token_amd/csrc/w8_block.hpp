@@ -54,7 +54,8 @@ struct BlockGemmArgs {
   int M, N, K;
   int G;               // ceil(K / 128): scale groups and K-steps
   int split_k;         // power of two; 1 = whole K per workgroup
-  int vec_store;       // y and ldy allow 8-byte stores
+  int vec_store;       // y and ldy allow stores of 8 (1) or 16 (2) bytes
+  int whole;           // the largest tile: ids from here on are half tiles
   int tiles_m;         // token tiles (grouped: slots, M / BM + E)
   int tiles_n;
   // grouped (per expert) products
@@ -71,8 +72,9 @@ struct BlockTile {
   int bm, bn, threads, lds_bytes;
 };
 constexpr int kBlockTiles = 5;
+constexpr int kLargeTile = 4;  // runs partial rounds and short tiles at half height
 const BlockTile& block_tile(int tile);
-hipError_t launch_block_gemm(int tile, bool grouped, bool packed, const BlockGemmArgs& a,
-                             hipStream_t s);
+hipError_t launch_block_gemm(int tile, unsigned wgs, bool grouped, bool packed,
+                             const BlockGemmArgs& a, hipStream_t s);
 
 }  // namespace w8

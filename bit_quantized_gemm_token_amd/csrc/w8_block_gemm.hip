@@ -57,6 +57,7 @@ template <int BM_, int BN_, int WM_, int WN_, int ST_>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_;
   static constexpr int NW = WM * WN, THREADS = 64 * NW;
+  static constexpr bool LARGE = false;
   static constexpr int NM = BM / WM / 16, NN = BN / WN / 16;  // MFMA tiles per wave
   static_assert(BN / WN <= 128, "a wave's weight rows lie in one 128-row scale block");
   // LDS: ST stages of token and weight codes, then two buffers of scales for
@@ -93,58 +94,27 @@ struct Tile {
 
 extern __shared__ __align__(1024) uint8_t smem[];
 
+// Four fp32 values to bf16, round to nearest even (NaN stays NaN).
+typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ v2u bf16x4(v4f v) {
+  return __builtin_bit_cast(v2u, __builtin_convertvector(v, bf16x4_t));
+}
+
+// One tile: rows [m0, m1) of Y (at most BM) times weight rows n0 .. n0 + BN - 1
+// of the expert (wq, sw), over the K-steps [ks0, ks1); split and tile: which
+// part of K of which output tile this is (split_k > 1).
 template <class T, bool GROUPED, bool PACKED>
-__global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a) {
+__device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1, int n0,
+                                         const uint8_t* wq, const float* sw, int ks0, int ks1,
+                                         int split, int tile) {
   constexpr int BM = T::BM, BN = T::BN, NW = T::NW, NM = T::NM, NN = T::NN, ST = T::ST;
+  // gathered token rows by pointer, except in the largest tile, which has no
+  // registers for that (the host keeps rows more than 4 GiB apart from it)
+  constexpr bool POINTERS = GROUPED && !T::LARGE;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % T::WM, wn = wave / T::WM;
   const int r = lane & 15, q = lane >> 4;
-
-  // ---- which tile
-  int work = xcd_contiguous(blockIdx.x, gridDim.x);
-  int tm, tn, split = 0;
-  int m0, m1;  // rows of Y this tile may write: [m0, m1), at most BM
-  const uint8_t* wq = a.wq;
-  const float* sw = a.sw;
-  if constexpr (GROUPED) {
-    // Expert e owns the token slots offsets[e] / BM + e up to the next
-    // expert's: at least ceil(count / BM) of them whatever the counts are, so
-    // the host knows the number of slots without reading the offsets; the
-    // slots past an expert's last row exit here.
-    tn = work % a.tiles_n;
-    const int slot = work / a.tiles_n;
-    int e = -1;
-    for (int e0 = 0; e0 < a.n_experts; e0 += 64) {
-      bool mine = false;
-      if (e0 + lane < a.n_experts)
-        mine = min(max(a.offsets[e0 + lane], 0), a.M) / BM + e0 + lane <= slot;
-      const unsigned long long b = __ballot(mine);
-      if (b) e = e0 + 63 - __builtin_clzll(b);
-      if (~b) break;
-    }
-    if (e < 0) return;
-    e = __builtin_amdgcn_readfirstlane(e);
-    const int lo = min(max(a.offsets[e], 0), a.M), hi = min(max(a.offsets[e + 1], 0), a.M);
-    m0 = lo + (slot - lo / BM - e) * BM;
-    m1 = min(m0 + BM, hi);
-    if (m0 >= m1) return;
-    wq += (long long)e * a.w_stride;
-    sw += (long long)e * a.sw_stride;
-  } else {
-    split = work % a.split_k;
-    work /= a.split_k;
-    // bands of 8 token tiles, weight tiles inside a band in order: the ids an
-    // XCD runs at one time form a near-square patch of tiles
-    const int band = 8 * a.tiles_n;
-    const int b0 = work / band * 8;
-    const int h = min(8, a.tiles_m - b0);
-    tn = work % band / h;
-    tm = b0 + work % band % h;
-    m0 = tm * BM;
-    m1 = min(m0 + BM, a.M);
-  }
-  const int n0 = tn * BN;
 
   // ---- this wave's load addresses.  Row-major pieces are 8 rows x 128 bytes,
   // lane i holding row i / 8; the 16-byte chunk it loads is rotated by an
@@ -153,8 +123,6 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
   // products are not stored).
   const int prow = lane >> 3, pchunk = (lane & 7) ^ prow;
   const int k_steps = a.G;
-  const int ks0 = (int)((long long)k_steps * split / a.split_k);
-  const int ks1 = (int)((long long)k_steps * (split + 1) / a.split_k);
   // a last step that K ends inside of: chunks past K re-read the last whole
   // one, and the token operand is masked after its LDS read
   const int tail_chunks = (a.K & 127) >> 4;
@@ -168,8 +136,8 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
     }
     return m;
   };
-  // Tokens: an offset from the tile's first row, or for gathered rows (which
-  // may lie more than 4 GiB apart) a pointer.  Weights: an offset from the
+  // Tokens: an offset from the tile's first row, for gathered rows from the
+  // array's (which may lie more than 4 GiB apart: pointers).  Weights: an offset from the
   // tile's first row.  The bases advance by one step with each step's loads.
   const uint8_t* px[T::PX];
   unsigned ox[T::PX], ow[T::PW];
@@ -183,8 +151,10 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
 #pragma unroll
   for (int i = 0; i < T::PX; ++i) {
     const int p = min(wave + i * NW, T::X_BYTES / 1024 - 1);
-    if constexpr (GROUPED)
+    if constexpr (POINTERS)
       px[i] = xb + x_row(8 * p + prow) * a.ldq + 16 * pchunk;
+    else if constexpr (GROUPED)
+      ox[i] = (unsigned)(x_row(8 * p + prow) * a.ldq + 16 * pchunk);
     else
       ox[i] = (unsigned)(min(8 * p + prow, m1 - 1 - m0) * a.ldq + 16 * pchunk);
   }
@@ -233,7 +203,7 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
   auto issue_one = [&](int n, unsigned base, unsigned late) {
     if (n < T::PX) {
       const unsigned lds = base + min(wave + n * NW, T::X_BYTES / 1024 - 1) * 1024;
-      if constexpr (GROUPED)
+      if constexpr (POINTERS)
         load_lds16(px[n], lds);
       else
         load_lds16(xb, ox[n], lds);
@@ -262,7 +232,7 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
     }
     if (k >= ks1) return;
     if (k > ks0) {
-      if constexpr (GROUPED) {
+      if constexpr (POINTERS) {
 #pragma unroll
         for (int i = 0; i < T::PX; ++i) px[i] += 128;
       } else {
@@ -273,7 +243,7 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
     if (k == tail_step) {
 #pragma unroll
       for (int i = 0; i < T::PX; ++i) {
-        if constexpr (GROUPED)
+        if constexpr (POINTERS)
           px[i] += tail_adj;
         else
           ox[i] += tail_adj;
@@ -475,8 +445,7 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
   // ---- split-K: see the protocol of the small-M GEMM's shared tiles
   // (partials written through with agent scope, acknowledged, counted; the
   // last workgroup of the tile sums them in K order).
-  if (!GROUPED && a.split_k > 1) {
-    const int tile = work;
+  if (!GROUPED && !T::LARGE && a.split_k > 1) {
     const int bytes = a.split_k * NW * NN * NM * 1024;
     const __amdgpu_buffer_rsrc_t prs =
         coherent_rsrc(reinterpret_cast<char*>(a.part) + (long long)tile * bytes, bytes);
@@ -515,38 +484,155 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
 
   // ---- epilogue: lane (r, q) of tile (i, j) holds token 16 j + r, weight
   // rows 16 i + 4 q .. + 3
+  if constexpr (T::ROTATED) {
+    // through LDS, so that a store covers whole rows of the tile: 8-byte
+    // stores of each lane's own four would touch 16 rows at a time (256 x 256:
+    // 11700 clocks against 3000)
+    constexpr int ROW = BN * 2 + 32;
+    static_assert(BM * ROW <= T::LDS, "the output tile fits where the stages were");
 #pragma unroll
-  for (int j = 0; j < NM; ++j) {
-    const int m = m0 + (wm * NM + j) * 16 + r;
-    if (m < m1) {
-      uint16_t* yr = a.y + m * a.ldy;
+    for (int j = 0; j < NM; ++j)
 #pragma unroll
-      for (int i = 0; i < NN; ++i) {
-        const int n = n0 + (wn * NN + i) * 16 + 4 * q;
-        unsigned b[4];
+      for (int i = 0; i < NN; ++i)
+        *reinterpret_cast<v2u*>(smem + ((wm * NM + j) * 16 + r) * ROW +
+                                ((wn * NN + i) * 16 + 4 * q) * 2) = bf16x4(acc[i][j]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < (m1 - m0) * (BN / 8); c += T::THREADS) {
+      const int row = c / (BN / 8), col = c % (BN / 8) * 8, n = n0 + col;
+      const v4u v = *reinterpret_cast<const v4u*>(smem + row * ROW + col * 2);
+      uint16_t* yp = a.y + (m0 + row) * a.ldy + n;
+      if (a.vec_store == 2 && n + 8 <= a.N) {
+        *reinterpret_cast<v4u*>(yp) = v;
+      } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float f = acc[i][j][u];
-          b[u] = f != f ? 0x7FC0u : (unsigned)bf16_rne(f);
-        }
-        if (a.vec_store && n + 4 <= a.N) {
-          const v2u v = {b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
-          *reinterpret_cast<v2u*>(yr + n) = v;
-        } else {
+        for (int u = 0; u < 8; ++u)
+          if (n + u < a.N) yp[u] = (uint16_t)(v[u >> 1] >> (16 * (u & 1)));
+      }
+    }
+  } else {
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (n + u < a.N) yr[n + u] = (uint16_t)b[u];
+    for (int j = 0; j < NM; ++j) {
+      const int m = m0 + (wm * NM + j) * 16 + r;
+      if (m < m1) {
+        uint16_t* yr = a.y + m * a.ldy;
+#pragma unroll
+        for (int i = 0; i < NN; ++i) {
+          const int n = n0 + (wn * NN + i) * 16 + 4 * q;
+          const v2u v = bf16x4(acc[i][j]);
+          if (a.vec_store && n + 4 <= a.N) {
+            *reinterpret_cast<v2u*>(yr + n) = v;
+          } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (n + u < a.N) yr[n + u] = (uint16_t)(v[u >> 1] >> (16 * (u & 1)));
+          }
         }
       }
     }
   }
 }
 
+// The workgroup's part of K: steps [ks0, ks1).
+struct KRange {
+  int ks0, ks1;
+};
+__device__ __forceinline__ KRange k_range(const BlockGemmArgs& a, int split) {
+  return {(int)((long long)a.G * split / a.split_k), (int)((long long)a.G * (split + 1) / a.split_k)};
+}
+
+// Which tile a workgroup of the dense GEMM takes: bands of 8 token tiles,
+// weight tiles inside a band in order, so that the ids an XCD runs at one time
+// form a near-square patch of tiles.
+struct TilePos {
+  int tm, tn;
+};
+__device__ __forceinline__ TilePos tile_pos(const BlockGemmArgs& a, int id) {
+  const int band = 8 * a.tiles_n;
+  const int b0 = id / band * 8;
+  const int h = min(8, a.tiles_m - b0);
+  return {b0 + id % band % h, id % band / h};
+}
+
+template <class T, bool PACKED>
+__global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a) {
+  if constexpr (T::LARGE) {
+    // The tiles that fill whole rounds of the compute units run at full
+    // height; those of the last, partial round (from id a.whole on) as two
+    // halves each, so that the round takes half as long.  A tile with at most
+    // 128 rows left runs at half height too.
+    typedef typename T::Half Half;
+    int id = blockIdx.x, half = -1;
+    if (id < a.whole) {
+      id = xcd_contiguous(id, a.whole);
+    } else {
+      id = xcd_contiguous(id - a.whole, gridDim.x - a.whole);
+      half = id & 1;
+      id = a.whole + (id >> 1);
+    }
+    const TilePos t = tile_pos(a, id);
+    const int m0 = t.tm * T::BM + (half > 0 ? Half::BM : 0);
+    const int m1 = min(m0 + (half < 0 ? T::BM : Half::BM), a.M);
+    if (m0 >= m1) return;
+    if (half < 0 && m1 - m0 > Half::BM)
+      run_tile<T, false, PACKED>(a, m0, m1, t.tn * T::BN, a.wq, a.sw, 0, a.G, 0, 0);
+    else
+      run_tile<Half, false, PACKED>(a, m0, m1, t.tn * T::BN, a.wq, a.sw, 0, a.G, 0, 0);
+  } else {
+    const int work = xcd_contiguous(blockIdx.x, gridDim.x);
+    const int split = work % a.split_k, tile = work / a.split_k;
+    const TilePos t = tile_pos(a, tile);
+    const KRange k = k_range(a, split);
+    run_tile<T, false, PACKED>(a, t.tm * T::BM, min(t.tm * T::BM + T::BM, a.M), t.tn * T::BN, a.wq,
+                               a.sw, k.ks0, k.ks1, split, tile);
+  }
+}
+
+// Expert e owns the token slots offsets[e] / BM + e up to the next expert's:
+// at least ceil(count / BM) of them whatever the counts are, so the host knows
+// the number of slots without reading the offsets; the slots past an expert's
+// last row exit at once.
+template <class T, bool PACKED>
+__global__ __launch_bounds__(T::THREADS) void grouped_gemm_kernel(BlockGemmArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int work = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int n0 = work % a.tiles_n * T::BN, slot = work / a.tiles_n;
+  int e = -1;
+  for (int e0 = 0; e0 < a.n_experts; e0 += 64) {
+    bool mine = false;
+    if (e0 + lane < a.n_experts)
+      mine = min(max(a.offsets[e0 + lane], 0), a.M) / T::BM + e0 + lane <= slot;
+    const unsigned long long b = __ballot(mine);
+    if (b) e = e0 + 63 - __builtin_clzll(b);
+    if (~b) break;
+  }
+  if (e < 0) return;
+  e = __builtin_amdgcn_readfirstlane(e);
+  const int lo = min(max(a.offsets[e], 0), a.M), hi = min(max(a.offsets[e + 1], 0), a.M);
+  const int m0 = lo + (slot - lo / T::BM - e) * T::BM;
+  const int m1 = min(m0 + T::BM, hi);
+  if (m0 >= m1) return;
+  const uint8_t* wq = a.wq + (long long)e * a.w_stride;
+  const float* sw = a.sw + (long long)e * a.sw_stride;
+  if constexpr (T::LARGE) {
+    typedef typename T::Half Half;
+    if (m1 - m0 <= Half::BM) {
+      run_tile<Half, true, PACKED>(a, m0, m1, n0, wq, sw, 0, a.G, 0, 0);
+      return;
+    }
+  }
+  run_tile<T, true, PACKED>(a, m0, m1, n0, wq, sw, 0, a.G, 0, 0);
+}
+
 typedef Tile<16, 128, 1, 4, 4> T0;
 typedef Tile<32, 128, 1, 4, 4> T1;
 typedef Tile<64, 128, 1, 4, 3> T2;
 typedef Tile<128, 128, 2, 2, 2> T3;
-typedef Tile<256, 256, 4, 2, 2> T4;
+struct T4 : Tile<256, 256, 4, 2, 2> {
+  static constexpr bool LARGE = true;
+  struct Half : Tile<128, 256, 2, 4, 2> {
+    static constexpr bool LARGE = true;
+  };
+};
 
 template <class T>
 constexpr BlockTile describe() {
@@ -555,37 +641,40 @@ constexpr BlockTile describe() {
 const BlockTile kTiles[kBlockTiles] = {describe<T0>(), describe<T1>(), describe<T2>(),
                                        describe<T3>(), describe<T4>()};
 
-template <class T, bool GROUPED, bool PACKED>
-hipError_t launch(const BlockGemmArgs& a, hipStream_t s) {
+typedef void (*Kernel)(BlockGemmArgs);
+
+template <class T, Kernel K>
+hipError_t launch(unsigned wgs, const BlockGemmArgs& a, hipStream_t s) {
   // more than 64 KiB of LDS has to be asked for, once per kernel
   static const hipError_t lds = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(&block_gemm_kernel<T, GROUPED, PACKED>),
-      hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
+      reinterpret_cast<const void*>(K), hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
   if (lds != hipSuccess) return lds;
-  const unsigned wgs = (unsigned)((long long)a.tiles_m * a.tiles_n * a.split_k);
-  hipLaunchKernelGGL((block_gemm_kernel<T, GROUPED, PACKED>), dim3(wgs), dim3(T::THREADS), T::LDS,
-                     s, a);
+  hipLaunchKernelGGL(K, dim3(wgs), dim3(T::THREADS), T::LDS, s, a);
   return hipGetLastError();
 }
 
 template <class T>
-hipError_t launch_tile(bool grouped, bool packed, const BlockGemmArgs& a, hipStream_t s) {
-  if (grouped) return packed ? launch<T, true, true>(a, s) : launch<T, true, false>(a, s);
-  return packed ? launch<T, false, true>(a, s) : launch<T, false, false>(a, s);
+hipError_t launch_tile(unsigned wgs, bool grouped, bool packed, const BlockGemmArgs& a,
+                       hipStream_t s) {
+  if (grouped)
+    return packed ? launch<T, grouped_gemm_kernel<T, true>>(wgs, a, s)
+                  : launch<T, grouped_gemm_kernel<T, false>>(wgs, a, s);
+  return packed ? launch<T, block_gemm_kernel<T, true>>(wgs, a, s)
+                : launch<T, block_gemm_kernel<T, false>>(wgs, a, s);
 }
 
 }  // namespace
 
 const BlockTile& block_tile(int tile) { return kTiles[tile]; }
 
-hipError_t launch_block_gemm(int tile, bool grouped, bool packed, const BlockGemmArgs& a,
-                             hipStream_t s) {
+hipError_t launch_block_gemm(int tile, unsigned wgs, bool grouped, bool packed,
+                             const BlockGemmArgs& a, hipStream_t s) {
   switch (tile) {
-    case 0: return launch_tile<T0>(grouped, packed, a, s);
-    case 1: return launch_tile<T1>(grouped, packed, a, s);
-    case 2: return launch_tile<T2>(grouped, packed, a, s);
-    case 3: return launch_tile<T3>(grouped, packed, a, s);
-    default: return launch_tile<T4>(grouped, packed, a, s);
+    case 0: return launch_tile<T0>(wgs, grouped, packed, a, s);
+    case 1: return launch_tile<T1>(wgs, grouped, packed, a, s);
+    case 2: return launch_tile<T2>(wgs, grouped, packed, a, s);
+    case 3: return launch_tile<T3>(wgs, grouped, packed, a, s);
+    default: return launch_tile<T4>(wgs, grouped, packed, a, s);
   }
 }
 
