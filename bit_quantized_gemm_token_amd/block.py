@@ -22,39 +22,53 @@ def _groups(n):
     return (n + GROUP - 1) // GROUP
 
 
+# One call's checks run before every launch of a few microseconds, so the
+# helpers below keep to the cheap attributes and build messages only on error.
+def _not_rows(t, name, dtype):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if dtype is not None and t.dtype != dtype:
+        return TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return ValueError(f"{name} must be a 2-D tensor with unit inner stride")
+
+
 def _rows(t, name, dtype=None):
     """Pointer and row stride (elements) of a 2-D device tensor with unit inner stride."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be a 2-D tensor with unit inner stride")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or (dtype is not None and
+                                                            t.dtype is not dtype):
+        raise _not_rows(t, name, dtype)
+    st = t.stride()
+    if len(st) != 2:
+        raise _not_rows(t, name, dtype)
+    ld, one = st
+    rows, cols = t.shape
+    if one != 1 and cols > 1:
+        raise _not_rows(t, name, dtype)
     # (a single row's stride is never used, and torch lets it be anything)
-    return t.data_ptr(), max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+    return t.data_ptr(), (ld if rows > 1 or ld >= cols else cols)
 
 
 def _codes(t, name):
-    p, ld = _rows(t, name)
+    p_ld = _rows(t, name)
     if t.element_size() != 1:
         raise TypeError(f"{name} must hold 1-byte codes")
-    return p, ld
+    return p_ld
 
 
-def _flat(t, name, dtype, n=None):
-    """Pointer of a contiguous device tensor (of n elements)."""
+def _flat(t, name, dtype, n):
+    """Pointer of a contiguous device tensor of n elements."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous() or (n is not None and t.numel() != n):
+    if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of {n} elements, got shape "
                          f"{tuple(t.shape)}")
     return t.data_ptr()
 
 
 def _shape(t, rows, cols, name):
-    if tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
 
 
@@ -63,6 +77,17 @@ def _aligned_codes(M, K, device):
     if K % 16 == 0:
         return torch.empty((M, K), dtype=_CODES, device=device)
     return torch.empty((M, (K + 15) // 16 * 16), dtype=_CODES, device=device)[:, :K]
+
+
+# The current stream's handle without building a Stream object for it (2 us of
+# a call), where this torch has the function.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(stream, device):
+    if stream is None and _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return _stream(stream, device)
 
 
 def block_quantize(x, gate=None, xq=None, sx=None, stream=None):
@@ -90,7 +115,7 @@ def block_quantize(x, gate=None, xq=None, sx=None, stream=None):
     if sx is None:
         sx = torch.empty((M, _groups(K)), dtype=_F32, device=x.device)
     sp = _flat(sx, "sx", _F32, M * _groups(K))
-    _check(_lib.w8_block_quantize(M, K, xp, ldx, gp, ldg, qp, ldq, sp, _stream(stream, x.device)))
+    _check(_lib.w8_block_quantize(M, K, xp, ldx, gp, ldg, qp, ldq, sp, _on(stream, x.device)))
     return xq, sx
 
 
@@ -148,7 +173,7 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, scale=1.0, e
         result = h, z
     _check(_lib.w8_residual_norm(M, D, yp, ldy, rp, ldr, residual.dtype == _F32, pp, gp, ldg,
                                  scale, wp, eps, hp, ldh, zp, ldz, qp, ldq, sp,
-                                 _stream(stream, y.device)))
+                                 _on(stream, y.device)))
     return result
 
 
@@ -191,7 +216,7 @@ def block_gemm(xq, sx, wq, sw, y=None, workspace=None, stream=None):
         buf = workspace.reserve(ws_bytes, stream)
         ws, ws_bytes = buf.data_ptr(), buf.numel()
     _check(_lib.w8_block_gemm(M, N, K, xp, ldq, sxp, wp, ldw, swp, yp, ldy, ws, ws_bytes,
-                              _stream(stream, xq.device)))
+                              _on(stream, xq.device)))
     return y
 
 
@@ -237,7 +262,7 @@ def grouped_gemm(xq, sx, offsets, wq, sw, rows=None, y=None, stream=None):
         _shape(y, n_rows, N, "y")
     yp, ldy = _rows(y, "y", _BF16)
     _check(_lib.w8_grouped_gemm(E, T, N, K, xp, ldq, sxp, op, rwp, n_rows, wp, ldw, w_stride,
-                                swp, per, yp, ldy, _stream(stream, xq.device)))
+                                swp, per, yp, ldy, _on(stream, xq.device)))
     return y
 
 
