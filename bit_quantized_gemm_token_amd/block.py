@@ -16,6 +16,7 @@ from . import _capi
 GROUP = _capi.GROUP
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _CODES = torch.float8_e4m3fn
+_E_WORKSPACE = 3
 
 
 def _groups(n):
@@ -209,14 +210,20 @@ def block_gemm(xq, sx, wq, sw, y=None, workspace=None, stream=None):
     else:
         _shape(y, M, N, "y")
     yp, ldy = _rows(y, "y", _BF16)
-    ws, ws_bytes = None, block_gemm_workspace_size(M, N, K, packed)
-    if ws_bytes:
-        if workspace is None:
-            workspace = _default_workspace(xq.device)
-        buf = workspace.reserve(ws_bytes, stream)
-        ws, ws_bytes = buf.data_ptr(), buf.numel()
-    _check(_lib.w8_block_gemm(M, N, K, xp, ldq, sxp, wp, ldw, swp, yp, ldy, ws, ws_bytes,
-                              _on(stream, xq.device)))
+    if workspace is None:
+        workspace = _default_workspace(xq.device)
+    s = _on(stream, xq.device)
+    # what the workspace holds is enough for most calls: its size is asked for
+    # only when the library says it is not
+    buf = workspace.buf
+    for retry in (True, False):
+        status = _lib.w8_block_gemm(M, N, K, xp, ldq, sxp, wp, ldw, swp, yp, ldy,
+                                    None if buf is None else buf.data_ptr(),
+                                    0 if buf is None else buf.numel(), s)
+        if status != _E_WORKSPACE or not retry:
+            break
+        buf = workspace.reserve(block_gemm_workspace_size(M, N, K, packed), stream)
+    _check(status)
     return y
 
 

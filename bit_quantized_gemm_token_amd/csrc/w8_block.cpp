@@ -76,28 +76,109 @@ struct Plan {
   long long whole, wgs;  // the largest tile's whole tiles; workgroups
 };
 
-Plan plan_dense(int M, int N, int K) {
-  Plan p;
-  p.tile = M <= 16 ? 0 : M <= 32 ? 1 : M <= 64 ? 2 : 3;
-  if (ceil_div(M, 256) * ceil_div(N, 256) >= 192) p.tile = 4;
+// Microseconds of a launch with `n` workgroups (output tiles times split_k) of
+// `steps` K-steps each.  Measured on the five smaller tiles over 32 shapes
+// (20 <= M <= 8192) and every split_k of 1 .. 8, and fitted: a launch costs
+// 4; a step costs what the memory path takes for its bytes, with one or two
+// workgroups on a compute unit; split K costs its hand-off and the partials'
+// traffic.  The fastest of the estimates was within 1% of the fastest
+// measured, on average (10% at worst).
+struct TileCost {
+  int resident;       // workgroups of a compute unit
+  double step1, step2;  // us a step, one or two of them resident
+  double round;       // us a round beside the steps (the tiles that fill a unit)
+};
+constexpr TileCost kTileCost[kBlockTiles] = {
+    {2, 0.30, 0.55, 0}, {2, 0.36, 0.88, 0}, {2, 0.315, 0.53, 0},
+    {2, 0.45, 0.76, 0}, {1, 0.59, 0.59, 2}, {1, 1.65, 1.65, 7}};
+constexpr double kHalfStep = 0.97;    // the largest tile at half height
+constexpr double kWeightBytesPerUs = 4.5e6;
+
+double estimate(const Plan& p, int N, int K) {
+  const TileCost& c = kTileCost[p.tile];
   const BlockTile& t = block_tile(p.tile);
-  p.tiles_m = ceil_div(M, t.bm);
-  p.tiles_n = ceil_div(N, t.bn);
-  p.split_k = 1;
-  while (p.tile != kLargeTile && p.split_k < 16 && p.tiles_m * p.tiles_n * p.split_k < kComputeUnits &&
-         groups_of(K) / (2 * p.split_k) >= 4)
-    p.split_k *= 2;
-  const long long tiles = p.tiles_m * p.tiles_n;
-  if (tiles > kSplitKMaxTiles) p.split_k = 1;
-  p.whole = tiles;
-  p.wgs = tiles * p.split_k;
-  if (p.tile == kLargeTile) {
-    // one workgroup per compute unit at a time: the tiles of a last round that
-    // leaves at least half of them idle run as two halves each
-    const long long rest = tiles % kComputeUnits;
-    if (rest <= kComputeUnits / 2) p.whole = tiles - rest;
-    p.wgs = p.whole + 2 * (tiles - p.whole);
+  const int G = groups_of(K);
+  const long long tiles = p.tiles_m * p.tiles_n, n = tiles * p.split_k;
+  if (p.tile == kLargeTile)
+    return (double)ceil_div(p.whole, kComputeUnits) * (G * c.step1 + c.round) +
+           (p.whole < tiles ? G * kHalfStep + c.round : 0);
+  const double steps = (double)ceil_div(G, p.split_k);
+  const long long cap = (long long)kComputeUnits * c.resident;
+  double loop = (double)(n / cap) * (steps * c.step2 + c.round);
+  if (n % cap) loop += steps * (n % cap <= kComputeUnits ? c.step1 : c.step2) + c.round;
+  const double weights = (double)N * K / kWeightBytesPerUs;
+  double us = 4 + (loop > weights ? loop : weights);
+  if (p.split_k > 1) us += 0.9 + 0.43e-6 * (double)n * t.bm * t.bn * 4;
+  return us;
+}
+
+Plan plan_dense(int M, int N, int K) {
+  Plan best{};
+  double best_us = 0;
+  for (int tile = 0; tile < kBlockTiles; ++tile) {
+    Plan p;
+    p.tile = tile;
+    const BlockTile& t = block_tile(tile);
+    p.tiles_m = ceil_div(M, t.bm);
+    p.tiles_n = ceil_div(N, t.bn);
+    const long long tiles = p.tiles_m * p.tiles_n;
+    p.whole = tiles;
+    if (tile == kLargeTile) {
+      // one workgroup per compute unit at a time: the tiles of a last round
+      // that leaves at least half of them idle run as two halves each
+      const long long rest = tiles % kComputeUnits;
+      if (rest <= kComputeUnits / 2) p.whole = tiles - rest;
+    }
+    // (a workgroup keeps two steps at least, and the arrival counters hold
+    // kSplitKMaxTiles tiles)
+    for (p.split_k = 1; p.split_k <= 16; p.split_k *= 2) {
+      if (p.split_k > 1 && (tile == kLargeTile || tiles > kSplitKMaxTiles ||
+                            groups_of(K) < 2 * p.split_k || tiles * p.split_k > 2 * kComputeUnits))
+        break;
+      p.wgs = tile == kLargeTile ? p.whole + 2 * (tiles - p.whole) : tiles * p.split_k;
+      const double us = estimate(p, N, K);
+      if (!best.wgs || us < best_us) {
+        best = p;
+        best_us = us;
+      }
+    }
   }
+  return best;
+}
+
+// Up to W8_MAX_M tokens run on the small-M GEMM, whose waves stream the
+// weights into registers: 1 x 4608 x 7168 10.3 us against 12.1 on the best of
+// the tiles here, 32 x 4608 x 7168 14.1 against 14.3, 16 x 1000 x 2048 4.9
+// against 6.0.  (It needs whole groups.)
+bool use_small_m(int M, int K) { return M <= W8_MAX_M && K % W8_GROUP == 0; }
+
+// The counts per expert are on the device, so their mean picks the tile: up to
+// 8 rows the weights' bytes are all that counts and the smallest tile streams
+// them best (128 experts of 1536 x 2048, 64 rows: 34.8 us, with the 64-row
+// tile 36.4, the largest 49.0); up to 64 the 64-row tile (4096 rows of
+// 2048 x 768: 51 us, 69 and 59); above, the largest, which runs short tiles at
+// half height (32768 rows of 1536 x 2048: 179 us, 64-row tile 235, 128-row
+// 218), unless it has too few tiles for the compute units (2000 rows, 8
+// experts of 1000 x 1008: 24 us, 128-row tile 11).
+Plan plan_grouped(int E, int T, int N, int64_t ldq, int n_rows) {
+  const long long mean = n_rows / E, experts = n_rows < E ? n_rows : E;
+  Plan p{};
+  const auto take = [&](int tile) {
+    p.tile = tile;
+    p.tiles_m = n_rows / block_tile(tile).bm + experts;
+    p.tiles_n = ceil_div(N, block_tile(tile).bn);
+  };
+  if (mean <= 8) {
+    take(0);
+  } else if (mean <= 64) {
+    take(3);
+  } else {
+    take(kLargeTile);
+    // (the largest tile addresses gathered rows by 32-bit offsets)
+    if (p.tiles_m * p.tiles_n < 3 * kComputeUnits / 4 || (long long)T * ldq >= (1LL << 32)) take(4);
+  }
+  p.split_k = 1;
+  p.whole = p.wgs = p.tiles_m * p.tiles_n;
   return p;
 }
 
@@ -187,6 +268,8 @@ w8_status w8_block_gemm_workspace_size(int M, int N, int K, int packed, size_t* 
   if (packed != 0 && packed != 1)
     return fail(W8_E_INVALID, "weight layout must be 0 (row-major) or 1 (packed)");
   if (!bytes) return fail(W8_E_INVALID, "null output pointer");
+  if (M && use_small_m(M, K))
+    return w8_workspace_size(W8_BLOCK_FP8, W8_OP_GEMM, M, N, K, packed, nullptr, bytes);
   *bytes = M ? plan_bytes(plan_dense(M, N, K)) : 0;
   return ok();
 }
@@ -202,6 +285,9 @@ w8_status w8_block_gemm(int M, int N, int K, const void* xq, int64_t ldq, const 
   int packed = 0;
   st = check_operands(N, K, xq, ldq, sx, wq, ldw, sw, y, ldy, &packed);
   if (st) return st;
+  if (use_small_m(M, K))
+    return w8_gemm_w8a8(W8_BLOCK_FP8, M, N, K, xq, ldq, sx, wq, ldw, sw, y, ldy, nullptr, ws,
+                        ws_bytes, stream);
   const Plan p = plan_dense(M, N, K);
   const size_t need = plan_bytes(p);
   if (need > 0) {
@@ -237,7 +323,7 @@ w8_status w8_block_gemm(int M, int N, int K, const void* xq, int64_t ldq, const 
   a.tiles_m = (int)p.tiles_m;
   a.tiles_n = (int)p.tiles_n;
   const hipError_t e =
-      launch_block_gemm(p.tile, (unsigned)p.wgs, false, packed, a, static_cast<hipStream_t>(stream));
+      launch_block_gemm(p.tile, (unsigned)p.wgs, packed, a, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("block_gemm launch", e));
   return ok();
 }
@@ -269,15 +355,7 @@ w8_status w8_grouped_gemm(int E, int T, int N, int K, const void* xq, int64_t ld
     return fail(W8_E_INVALID, "w_stride must be a multiple of 16 that holds one expert's codes");
   if (E > 1 && sw_stride < (int64_t)groups_of(N) * groups_of(K))
     return fail(W8_E_INVALID, "sw_stride must hold one expert's scales");
-  Plan p;
-  const long long mean = n_rows / E;
-  p.tile = mean <= 16 ? 0 : mean <= 32 ? 1 : mean <= 64 ? 2 : 3;
-  // (the largest tile addresses gathered rows by 32-bit offsets)
-  if (mean > 128 && (long long)T * ldq < (1LL << 32)) p.tile = kLargeTile;
-  p.split_k = 1;
-  p.tiles_m = n_rows / block_tile(p.tile).bm + E;
-  p.tiles_n = ceil_div(N, block_tile(p.tile).bn);
-  p.whole = p.wgs = p.tiles_m * p.tiles_n;
+  const Plan p = plan_grouped(E, T, N, ldq, n_rows);
   st = check_grid(p);
   if (st) return st;
   st = check_device();
@@ -305,8 +383,8 @@ w8_status w8_grouped_gemm(int E, int T, int N, int K, const void* xq, int64_t ld
   a.sw_stride = sw_stride;
   a.n_experts = E;
   a.xrow_max = T - 1;
-  const hipError_t e = launch_block_gemm(p.tile, (unsigned)p.wgs, true, packed, a,
-                                         static_cast<hipStream_t>(stream));
+  const hipError_t e =
+      launch_grouped_gemm(p.tile, (unsigned)p.wgs, packed, a, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("grouped_gemm launch", e));
   return ok();
 }

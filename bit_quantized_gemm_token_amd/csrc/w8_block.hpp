@@ -56,7 +56,7 @@ struct BlockGemmArgs {
   int split_k;         // power of two; 1 = whole K per workgroup
   int vec_store;       // y and ldy allow stores of 8 (1) or 16 (2) bytes
   int whole;           // the largest tile: ids from here on are half tiles
-  int tiles_m;         // token tiles (grouped: slots, M / BM + E)
+  int tiles_m;         // token tiles (grouped: slots, M / BM + min(E, M))
   int tiles_n;
   // grouped (per expert) products
   const int* offsets;      // [E + 1] (device)
@@ -71,10 +71,13 @@ struct BlockGemmArgs {
 struct BlockTile {
   int bm, bn, threads, lds_bytes;
 };
-constexpr int kBlockTiles = 5;
-constexpr int kLargeTile = 4;  // runs partial rounds and short tiles at half height
+constexpr int kBlockTiles = 6;
+constexpr int kLargeTile = 5;  // runs partial rounds and short tiles at half height
 const BlockTile& block_tile(int tile);
-hipError_t launch_block_gemm(int tile, unsigned wgs, bool grouped, bool packed,
-                             const BlockGemmArgs& a, hipStream_t s);
+hipError_t launch_block_gemm(int tile, unsigned wgs, bool packed, const BlockGemmArgs& a,
+                             hipStream_t s);
+// (tiles 0, 3, 4 and 5)
+hipError_t launch_grouped_gemm(int tile, unsigned wgs, bool packed, const BlockGemmArgs& a,
+                               hipStream_t s);
 
 }  // namespace w8

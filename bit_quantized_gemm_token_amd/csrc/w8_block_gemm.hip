@@ -76,7 +76,7 @@ struct Tile {
   // step; the first H + 2 of a step are staged with its tokens, the others
   // one step later.  In LDS a stage's weight tiles (16 rows, 2 KiB) are
   // ordered early ones first.
-  static constexpr bool ROTATED = NN >= 4;
+  static constexpr bool ROTATED = NN >= 4 && ST == 2;
   static constexpr int H = NN / 2, EARLY = ROTATED ? H + 2 : NN;
   static constexpr int PW1 = WN * EARLY * 2 / NW;  // (exact where ROTATED)
   static __device__ __forceinline__ constexpr int slot(int wn, int i) {
@@ -359,8 +359,9 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
           if (i < T::EARLY) wf[i % 4] = weights(i, stage);
         }
         if constexpr (!LAST) {
-          const int n = p - (FIRST ? P2 : 0);
-          if (n < T::LOADS) issue_one(n, other, here);
+          // (every other MFMA where a whole step is left to deal them)
+          const int n = p - (FIRST ? P2 : 0), gap = FIRST || P < 32 ? 1 : 2;
+          if (n % gap == 0 && n / gap < T::LOADS) issue_one(n / gap, other, here);
         }
         t[p % 4] = mfma_f8(wf[tile_of(p) % 4], xf[j_of(p)], v4f{0, 0, 0, 0});
         if (!FIRST && !LAST && p >= PJ && p < P2 && (p & 1)) xf[j_of(p)] = tokens(j_of(p), stage);
@@ -392,6 +393,9 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
     }
     interval(No{}, Yes{}, ks1, stage);
   } else {
+    // (Reading the operands of the next step ahead of this one's MFMAs, in a
+    // second register set, measured 2-5% slower on these tiles: what bounds
+    // them is the memory path, 24 bytes a clock and compute unit.)
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s) {
       advance(ks0 + s);
@@ -471,20 +475,37 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
     __syncthreads();
     if (!*flag) return;
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    // slots in batches whose loads are all in flight together, added in slot
+    // order (a batch of the tile's 4 NN NM registers a slot, 64 at most)
+    constexpr int Q = NN * NM >= 16 ? 1 : 16 / (NN * NM);
 #pragma unroll
-    for (int i = 0; i < NN; ++i) {
+    for (int i = 0; i < NN; ++i)
 #pragma unroll
       for (int j = 0; j < NM; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-      for (int s = 0; s < a.split_k; ++s)
+    for (int s0 = 0; s0 < a.split_k; s0 += Q) {
+      v4i v[Q][NN][NM];
 #pragma unroll
-        for (int j = 0; j < NM; ++j)
-          acc[i][j] += __builtin_bit_cast(v4f, coherent_load16(prs, foff(s, i, j)));
+      for (int s = 0; s < Q; ++s)
+        if (s0 + s < a.split_k) {
+#pragma unroll
+          for (int i = 0; i < NN; ++i)
+#pragma unroll
+            for (int j = 0; j < NM; ++j) v[s][i][j] = coherent_load16(prs, foff(s0 + s, i, j));
+        }
+#pragma unroll
+      for (int s = 0; s < Q; ++s)
+        if (s0 + s < a.split_k) {
+#pragma unroll
+          for (int i = 0; i < NN; ++i)
+#pragma unroll
+            for (int j = 0; j < NM; ++j) acc[i][j] += __builtin_bit_cast(v4f, v[s][i][j]);
+        }
     }
   }
 
   // ---- epilogue: lane (r, q) of tile (i, j) holds token 16 j + r, weight
   // rows 16 i + 4 q .. + 3
-  if constexpr (T::ROTATED) {
+  if constexpr (BM * BN >= 128 * 128) {
     // through LDS, so that a store covers whole rows of the tile: 8-byte
     // stores of each lane's own four would touch 16 rows at a time (256 x 256:
     // 11700 clocks against 3000)
@@ -537,7 +558,8 @@ struct KRange {
   int ks0, ks1;
 };
 __device__ __forceinline__ KRange k_range(const BlockGemmArgs& a, int split) {
-  return {(int)((long long)a.G * split / a.split_k), (int)((long long)a.G * (split + 1) / a.split_k)};
+  const int shift = __builtin_ctz(a.split_k);
+  return {(int)((long long)a.G * split >> shift), (int)((long long)a.G * (split + 1) >> shift)};
 }
 
 // Which tile a workgroup of the dense GEMM takes: bands of 8 token tiles,
@@ -547,6 +569,7 @@ struct TilePos {
   int tm, tn;
 };
 __device__ __forceinline__ TilePos tile_pos(const BlockGemmArgs& a, int id) {
+  if (a.tiles_m == 1) return {0, id};
   const int band = 8 * a.tiles_n;
   const int b0 = id / band * 8;
   const int h = min(8, a.tiles_m - b0);
@@ -579,7 +602,7 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
       run_tile<Half, false, PACKED>(a, m0, m1, t.tn * T::BN, a.wq, a.sw, 0, a.G, 0, 0);
   } else {
     const int work = xcd_contiguous(blockIdx.x, gridDim.x);
-    const int split = work % a.split_k, tile = work / a.split_k;
+    const int split = work & (a.split_k - 1), tile = work >> __builtin_ctz(a.split_k);
     const TilePos t = tile_pos(a, tile);
     const KRange k = k_range(a, split);
     run_tile<T, false, PACKED>(a, t.tm * T::BM, min(t.tm * T::BM + T::BM, a.M), t.tn * T::BN, a.wq,
@@ -587,30 +610,57 @@ __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a)
   }
 }
 
-// Expert e owns the token slots offsets[e] / BM + e up to the next expert's:
-// at least ceil(count / BM) of them whatever the counts are, so the host knows
-// the number of slots without reading the offsets; the slots past an expert's
-// last row exit at once.
+// Inclusive sum over the lanes of a wavefront: within rows of 16 lanes by
+// shifts, then the rows' totals passed on (gfx9 DPP row_shr and row_bcast).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+
+// Expert e has ceil(count / BM) token tiles; slot s is the s-th of them over
+// all experts, found by every wave from the offsets.  The launch holds the
+// most slots that n_rows entries can need, M / BM + min(E, M); those past the
+// last tile exit at once.
 template <class T, bool PACKED>
 __global__ __launch_bounds__(T::THREADS) void grouped_gemm_kernel(BlockGemmArgs a) {
   const int lane = threadIdx.x & 63;
-  const int work = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int n0 = work % a.tiles_n * T::BN, slot = work / a.tiles_n;
-  int e = -1;
+  // entries and tiles of expert e0 + lane
+  int lo = 0, hi = 0;
+  auto tiles_of = [&](int e0) {
+    const int i = min(e0 + lane, a.n_experts - 1);
+    lo = min(max(a.offsets[i], 0), a.M);
+    hi = min(max(a.offsets[i + 1], 0), a.M);
+    return e0 + lane < a.n_experts ? (max(hi - lo, 0) + T::BM - 1) / T::BM : 0;
+  };
+  // the XCDs share the tiles there are, not the slots of the launch
+  int total = 0;
+  for (int e0 = 0; e0 < a.n_experts; e0 += 64)
+    total += __builtin_amdgcn_readlane(wave_scan(tiles_of(e0)), 63);
+  if ((long long)blockIdx.x >= (long long)total * a.tiles_n) return;
+  const int work = xcd_contiguous(blockIdx.x, total * a.tiles_n);
+  const int n0 = work % a.tiles_n * T::BN;
+  int slot = work / a.tiles_n, e = -1;
   for (int e0 = 0; e0 < a.n_experts; e0 += 64) {
-    bool mine = false;
-    if (e0 + lane < a.n_experts)
-      mine = min(max(a.offsets[e0 + lane], 0), a.M) / T::BM + e0 + lane <= slot;
-    const unsigned long long b = __ballot(mine);
-    if (b) e = e0 + 63 - __builtin_clzll(b);
-    if (~b) break;
+    const int tiles = tiles_of(e0);
+    const int sum = wave_scan(tiles);
+    const unsigned long long past = __ballot(sum > slot);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      e = e0 + l;
+      lo = __builtin_amdgcn_readlane(lo, l);
+      hi = __builtin_amdgcn_readlane(hi, l);
+      slot -= __builtin_amdgcn_readlane(sum - tiles, l);
+      break;
+    }
+    slot -= __builtin_amdgcn_readlane(sum, 63);
   }
   if (e < 0) return;
-  e = __builtin_amdgcn_readfirstlane(e);
-  const int lo = min(max(a.offsets[e], 0), a.M), hi = min(max(a.offsets[e + 1], 0), a.M);
-  const int m0 = lo + (slot - lo / T::BM - e) * T::BM;
-  const int m1 = min(m0 + T::BM, hi);
-  if (m0 >= m1) return;
+  const int m0 = lo + slot * T::BM, m1 = min(m0 + T::BM, hi);
   const uint8_t* wq = a.wq + (long long)e * a.w_stride;
   const float* sw = a.sw + (long long)e * a.sw_stride;
   if constexpr (T::LARGE) {
@@ -625,13 +675,15 @@ __global__ __launch_bounds__(T::THREADS) void grouped_gemm_kernel(BlockGemmArgs 
 
 typedef Tile<16, 128, 1, 4, 4> T0;
 typedef Tile<32, 128, 1, 4, 4> T1;
-typedef Tile<64, 128, 1, 4, 3> T2;
-typedef Tile<128, 128, 2, 2, 2> T3;
-struct T4 : Tile<256, 256, 4, 2, 2> {
+typedef Tile<64, 64, 2, 2, 4> T2;
+typedef Tile<64, 128, 2, 4, 3> T3;
+typedef Tile<128, 128, 4, 2, 4> T4;
+struct T5 : Tile<256, 256, 4, 2, 2> {
   static constexpr bool LARGE = true;
-  struct Half : Tile<128, 256, 2, 4, 2> {
+  struct Half : Tile<128, 256, 4, 2, 3> {
     static constexpr bool LARGE = true;
   };
+  static constexpr int LDS = Half::LDS > Tile::LDS ? Half::LDS : Tile::LDS;
 };
 
 template <class T>
@@ -639,7 +691,8 @@ constexpr BlockTile describe() {
   return BlockTile{T::BM, T::BN, T::THREADS, T::LDS};
 }
 const BlockTile kTiles[kBlockTiles] = {describe<T0>(), describe<T1>(), describe<T2>(),
-                                       describe<T3>(), describe<T4>()};
+                                       describe<T3>(), describe<T4>(),
+                                       describe<T5>()};
 
 typedef void (*Kernel)(BlockGemmArgs);
 
@@ -654,27 +707,39 @@ hipError_t launch(unsigned wgs, const BlockGemmArgs& a, hipStream_t s) {
 }
 
 template <class T>
-hipError_t launch_tile(unsigned wgs, bool grouped, bool packed, const BlockGemmArgs& a,
-                       hipStream_t s) {
-  if (grouped)
-    return packed ? launch<T, grouped_gemm_kernel<T, true>>(wgs, a, s)
-                  : launch<T, grouped_gemm_kernel<T, false>>(wgs, a, s);
+hipError_t launch_dense(unsigned wgs, bool packed, const BlockGemmArgs& a, hipStream_t s) {
   return packed ? launch<T, block_gemm_kernel<T, true>>(wgs, a, s)
                 : launch<T, block_gemm_kernel<T, false>>(wgs, a, s);
+}
+template <class T>
+hipError_t launch_grouped(unsigned wgs, bool packed, const BlockGemmArgs& a, hipStream_t s) {
+  return packed ? launch<T, grouped_gemm_kernel<T, true>>(wgs, a, s)
+                : launch<T, grouped_gemm_kernel<T, false>>(wgs, a, s);
 }
 
 }  // namespace
 
 const BlockTile& block_tile(int tile) { return kTiles[tile]; }
 
-hipError_t launch_block_gemm(int tile, unsigned wgs, bool grouped, bool packed,
-                             const BlockGemmArgs& a, hipStream_t s) {
+hipError_t launch_block_gemm(int tile, unsigned wgs, bool packed, const BlockGemmArgs& a,
+                             hipStream_t s) {
   switch (tile) {
-    case 0: return launch_tile<T0>(wgs, grouped, packed, a, s);
-    case 1: return launch_tile<T1>(wgs, grouped, packed, a, s);
-    case 2: return launch_tile<T2>(wgs, grouped, packed, a, s);
-    case 3: return launch_tile<T3>(wgs, grouped, packed, a, s);
-    default: return launch_tile<T4>(wgs, grouped, packed, a, s);
+    case 0: return launch_dense<T0>(wgs, packed, a, s);
+    case 1: return launch_dense<T1>(wgs, packed, a, s);
+    case 2: return launch_dense<T2>(wgs, packed, a, s);
+    case 3: return launch_dense<T3>(wgs, packed, a, s);
+    case 4: return launch_dense<T4>(wgs, packed, a, s);
+    default: return launch_dense<T5>(wgs, packed, a, s);
+  }
+}
+
+hipError_t launch_grouped_gemm(int tile, unsigned wgs, bool packed, const BlockGemmArgs& a,
+                               hipStream_t s) {
+  switch (tile) {
+    case 0: return launch_grouped<T0>(wgs, packed, a, s);
+    case 3: return launch_grouped<T3>(wgs, packed, a, s);
+    case 4: return launch_grouped<T4>(wgs, packed, a, s);
+    default: return launch_grouped<T5>(wgs, packed, a, s);
   }
 }
 
