@@ -205,6 +205,8 @@ w8_status w8_block_quantize(int M, int K, const void* x, int64_t ldx, const void
   if (st) return st;
   if (K < 8 || K > kMaxK || K % 8)
     return fail(W8_E_INVALID, "K must be a multiple of 8 in [8, 2^22]");
+  if ((long long)M * groups_of(K) >= (1LL << 31))
+    return fail(W8_E_INVALID, "the groups (M x ceil(K / 128)) must be fewer than 2^31");
   if (M == 0) return ok();
   if (!x || !xq || !sx) return fail(W8_E_INVALID, "null device pointer");
   if (!aligned(x, 16) || ldx % 8 || ldx < K)
@@ -217,7 +219,8 @@ w8_status w8_block_quantize(int M, int K, const void* x, int64_t ldx, const void
   st = check_device();
   if (st) return st;
   BlockQuantArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(gate),
-                   static_cast<uint8_t*>(xq), sx, ldx, ldg, ldq, M, K};
+                   static_cast<uint8_t*>(xq), sx, ldx, ldg, ldq, K, (unsigned)groups_of(K),
+                   (unsigned)M * (unsigned)groups_of(K), 0, 0};
   const hipError_t e = launch_block_quantize(a, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("block_quantize launch", e));
   return ok();

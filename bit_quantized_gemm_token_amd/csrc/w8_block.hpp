@@ -16,10 +16,12 @@ struct BlockQuantArgs {
   float* sx;             // [M, ceil(K/128)]
   long long ldx, ldg;    // elements
   long long ldq;         // bytes
-  long long M;
   int K;
+  unsigned G, groups;    // groups of a row and of all rows (below 2^31)
+  unsigned magic;        // (set by the launcher) id / G as a multiplication
+  int shift;
 };
-hipError_t launch_block_quantize(const BlockQuantArgs& a, hipStream_t s);
+hipError_t launch_block_quantize(BlockQuantArgs a, hipStream_t s);
 
 struct NormArgs {
   const uint16_t* y;         // bf16 [M, D]

@@ -123,16 +123,20 @@ __device__ __forceinline__ v2u encode_group(float* f, float* s) {
   return v2u{e4m3_pack4(f[0], f[1], f[2], f[3]), e4m3_pack4(f[4], f[5], f[6], f[7])};
 }
 
-// g * sigmoid(g).  exp(-g) = 2^t with t = -g log2(e) taken as a rounded
-// product and its remainder, which keeps the exponential's relative error at
-// a few 2^-24 for every g (the rounded product alone loses |t| 2^-25 of it).
+// g * sigmoid(g) = g / d, d = 1 + exp(-g).  exp(-g) = 2^t with t = -g log2(e)
+// taken as a rounded product and its remainder, which keeps the exponential's
+// relative error at a few 2^-24 for every g (the rounded product alone loses
+// |t| 2^-25 of it); the quotient from the reciprocal with one correction.
 __device__ __forceinline__ float silu(float g) {
   const float hi = g * -0x1.715476p+0f;
   const float lo = __builtin_fmaf(g, -0x1.715476p+0f, -hi) - g * 0x1.4ae0cp-26f;
-  float e = __builtin_amdgcn_exp2f(hi);
-  // (an infinite 2^hi stays infinite: inf * lo could be inf * 0)
-  e = abs_bits(e) < 0x7F800000u ? __builtin_fmaf(e, 0x1.62e43p-1f * lo, e) : e;
-  return g * __builtin_amdgcn_rcpf(1.0f + e);
+  const float e = __builtin_amdgcn_exp2f(hi);
+  const float d = 1.0f + __builtin_fmaf(e, 0x1.62e43p-1f * lo, e);
+  const float r = __builtin_amdgcn_rcpf(d);
+  const float q = g * r;
+  const float s = __builtin_fmaf(__builtin_fmaf(-q, d, g), r, q);
+  // (an infinite 2^hi makes inf * lo and the correction NaN: the quotient is 0)
+  return abs_bits(e) < 0x7F800000u ? s : g * 0.0f;
 }
 
 // ---------------------------------------------------------------- quantize --
@@ -142,13 +146,13 @@ constexpr int kQThreads = 256;
 
 template <bool GATED>
 __global__ __launch_bounds__(kQThreads) void block_quantize_kernel(BlockQuantArgs a) {
-  const int G = (a.K + kGroup - 1) / kGroup;
-  const long long total = a.M * G;
   const int j = threadIdx.x & 15;
-  for (long long id = (long long)blockIdx.x * (kQThreads / 16) + (threadIdx.x >> 4); id < total;
-       id += (long long)gridDim.x * (kQThreads / 16)) {
-    const long long m = id / G;
-    const int k = (int)(id % G) * kGroup + 8 * j;
+  for (unsigned id = blockIdx.x * (kQThreads / 16) + (threadIdx.x >> 4); id < a.groups;
+       id += gridDim.x * (kQThreads / 16)) {
+    // (groups < 2^31: the quotient by a multiplication, exact for such ids)
+    const unsigned row = a.shift < 0 ? id : __umulhi(id, a.magic) >> a.shift;
+    const long long m = row;
+    const int k = (int)(id - row * a.G) * kGroup + 8 * j;
     const int n = a.K - k;
     float f[8];
     unpack8(load8_bf16(a.x + m * a.ldx + k, n), f);
@@ -166,27 +170,28 @@ __global__ __launch_bounds__(kQThreads) void block_quantize_kernel(BlockQuantArg
 }
 
 // -------------------------------------------------------------------- norm --
-// One row by T threads (64: four rows per workgroup), NC chunks of eight
-// values each, kept in registers between the two norms: every input is read
-// once.  Sums of squares are fp32, in a fixed order.
-template <int T>
+// One row by the waves of a workgroup (ONE_WAVE: four rows, a wave each), NC
+// chunks of eight values a lane, kept in registers between the two norms, so
+// that every input is read once.  Sums of squares are fp32, in a fixed order.
+template <bool ONE_WAVE>
 __device__ __forceinline__ float row_sum(float v, float* red) {
   v = wave_sum(v);
-  if (T == 64) return v;
+  if (ONE_WAVE) return v;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
   float t = 0.0f;
-#pragma unroll
-  for (int w = 0; w < T / 64; ++w) t += red[w];
+  for (unsigned w = 0; w < blockDim.x / 64; ++w) t += red[w];
   return t;
 }
 
-template <int T, int NC, bool RF32>
-__global__ __launch_bounds__(T == 64 ? 256 : T) void residual_norm_kernel(NormArgs a) {
+template <bool ONE_WAVE, int NC, bool RF32>
+__global__ __launch_bounds__(ONE_WAVE ? 256 : 1024) void residual_norm_kernel(NormArgs a) {
   __shared__ float red[2][16];
-  const int t = T == 64 ? threadIdx.x & 63 : threadIdx.x;
-  const long long row = T == 64 ? (long long)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-  if (T == 64 && row >= a.M) return;  // (no barrier with one wave per row)
+  const int T = ONE_WAVE ? 64 : blockDim.x;
+  const int t = ONE_WAVE ? threadIdx.x & 63 : threadIdx.x;
+  const long long row =
+      ONE_WAVE ? (long long)blockIdx.x * 4 + (threadIdx.x >> 6) : (long long)blockIdx.x;
+  if (ONE_WAVE && row >= a.M) return;  // (no barrier with one wave per row)
   const uint16_t* y = a.y + row * a.ldy;
   const uint16_t* gate = a.gate ? a.gate + row * a.ldg : nullptr;
   float h[NC][8], b[NC][8];
@@ -209,7 +214,7 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void residual_norm_kernel(NormAr
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(b[c][i], b[c][i], ss);
-    const float r = 1.0f / sqrtf(row_sum<T>(ss, red[0]) / (float)a.D + a.eps);
+    const float r = 1.0f / sqrtf(row_sum<ONE_WAVE>(ss, red[0]) / (float)a.D + a.eps);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       float p[8];
@@ -238,7 +243,7 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void residual_norm_kernel(NormAr
     else
       store8_bf16(static_cast<uint16_t*>(a.h) + row * a.ldh + k, n, h[c]);
   }
-  const float r = 1.0f / sqrtf(row_sum<T>(ss, red[1]) / (float)a.D + a.eps);
+  const float r = 1.0f / sqrtf(row_sum<ONE_WAVE>(ss, red[1]) / (float)a.D + a.eps);
   const int G = (a.D + kGroup - 1) / kGroup;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
@@ -257,21 +262,30 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void residual_norm_kernel(NormAr
   }
 }
 
-template <int T, int NC>
+template <bool ONE_WAVE, int NC>
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(T == 64 ? (a.M + 3) / 4 : a.M)), block(T == 64 ? 256 : T);
+  // as many waves as the row has chunks for
+  const unsigned threads = ONE_WAVE ? 256u : (unsigned)((a.D + 512 * NC - 1) / (512 * NC)) * 64u;
+  const dim3 grid((unsigned)(ONE_WAVE ? (a.M + 3) / 4 : a.M)), block(threads);
   if (a.residual_fp32)
-    hipLaunchKernelGGL((residual_norm_kernel<T, NC, true>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((residual_norm_kernel<ONE_WAVE, NC, true>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((residual_norm_kernel<T, NC, false>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((residual_norm_kernel<ONE_WAVE, NC, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_block_quantize(const BlockQuantArgs& a, hipStream_t s) {
-  const long long groups = a.M * ((a.K + kGroup - 1) / kGroup);
-  const long long blocks = (groups + kQThreads / 16 - 1) / (kQThreads / 16);
+hipError_t launch_block_quantize(BlockQuantArgs a, hipStream_t s) {
+  // id / G = umulhi(id, magic) >> shift for id < 2^31, with magic the
+  // reciprocal 2^(32 + shift) / G rounded up, 2^shift < G <= 2^(shift + 1)
+  a.shift = -1;
+  if (a.G > 1) {
+    a.shift = 0;
+    while ((2u << a.shift) < a.G) ++a.shift;
+    a.magic = (unsigned)(((1ull << (32 + a.shift)) + a.G - 1) / a.G);
+  }
+  const long long blocks = ((long long)a.groups + kQThreads / 16 - 1) / (kQThreads / 16);
   const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20))), block(kQThreads);
   if (a.gate)
     hipLaunchKernelGGL(block_quantize_kernel<true>, grid, block, 0, s, a);
@@ -281,12 +295,15 @@ hipError_t launch_block_quantize(const BlockQuantArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_residual_norm(const NormArgs& a, hipStream_t s) {
-  if (a.D <= 512) return launch_norm<64, 1>(a, s);
-  if (a.D <= 2048) return launch_norm<256, 1>(a, s);
-  if (a.D <= 4096) return launch_norm<256, 2>(a, s);
-  if (a.D <= 8192) return launch_norm<256, 4>(a, s);
-  if (a.D <= 16384) return launch_norm<1024, 2>(a, s);
-  return launch_norm<1024, 4>(a, s);
+  // One chunk a lane has the shortest chain of a single row (1 x 7168: 4.1 us,
+  // four chunks 5.3) and the most loads in flight on fp32 residuals (8192 x
+  // 5120: 115 us, two chunks 124, four 160); many long bf16 rows move too few
+  // bytes a lane that way (8192 x 5120: 65.6 us, two chunks 58.1).
+  if (a.D <= 512) return launch_norm<true, 1>(a, s);
+  if (a.D <= 8192 && (a.residual_fp32 || a.M < 512 || a.D <= 4096))
+    return launch_norm<false, 1>(a, s);
+  if (a.D <= 16384) return launch_norm<false, 2>(a, s);
+  return launch_norm<false, 4>(a, s);
 }
 
 }  // namespace w8

@@ -211,3 +211,36 @@ def test_grouped_strided_experts(w8):
     buf[:, :96, :272] = c.wq
     wq = codes_on_device(buf)[:, :96, :272]
     c.check(w8.grouped_gemm(c.dev[0], c.dev[1], c.dev[2], wq, c.dev[4], rows=c.drows))
+
+
+# ------------------------------------------------------- past 32-bit offsets --
+def test_output_past_32_bit_offsets(w8):
+    """An output of more than 2^32 bytes: its last rows and columns."""
+    M, N, K = 66000, 33000, 128
+    c = Gemm(16, N, K)
+    x, s = c.dev[0].view(torch.uint8).repeat(M // 16, 1), c.dev[1].repeat(M // 16, 1)
+    y = w8.block_gemm(x, s, c.dev[2], c.dev[3])
+    assert y.shape == (M, N)
+    assert_product(y[-16:], c.x, c.w)
+    assert_product(y[32768:32784], c.x, c.w)
+
+
+def test_weights_and_tokens_past_32_bit_offsets(w8):
+    """Weight rows and gathered token rows more than 2^32 bytes from the first."""
+    K, far = 8192, 540000
+    c = Gemm(300, 256, K)
+    big = torch.zeros(far, K, dtype=torch.uint8, device=DEV)
+    scales = torch.ones(far, K // 128, device=DEV)
+    big[-300:], scales[-300:] = c.dev[0].view(torch.uint8), c.dev[1]
+    rows = torch.arange(far - 300, far, dtype=torch.int32, device=DEV)
+    offsets = torch.tensor([0, 300], dtype=torch.int32, device=DEV)
+    y = w8.grouped_gemm(big, scales, offsets, c.dev[2][None], c.dev[3][None], rows=rows)
+    assert_product(y, c.x, c.w, "tokens")
+    del scales
+    # the same codes as weights, the last 256 rows of 540000
+    big[-256:] = c.dev[2].view(torch.uint8)
+    sw = torch.ones(far // 128 + 1, K // 128, device=DEV)
+    sw[-3:] = c.dev[3][0]  # (the last rows start inside a scale block)
+    y = w8.block_gemm(c.dev[0][:40], c.dev[1][:40], big, sw)
+    w = dequant_blocks(c.wq, np.repeat(c.sw[:1], 2, axis=0))
+    assert_product(y[:, -256:], c.x[:40], w, "weights")

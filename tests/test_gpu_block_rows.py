@@ -179,3 +179,20 @@ def test_norm_nan_stays_in_its_row(w8):
     assert torch.isnan(gz[2]).all() and torch.isnan(gh[2, 17])
     keep = [0, 1, 3, 4]
     near(gz[keep], z[keep], dz[keep] + 2.0 ** -8 * 1.01 * np.abs(z[keep]), "z")
+
+
+def test_rows_past_32_bit_offsets(w8):
+    """Rows whose elements and codes lie more than 2^32 bytes from the first:
+    the same results as on their own."""
+    M, K = 70000, 65536
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV)
+    x[-3:] = torch.randn(3, K, device=DEV).bfloat16()
+    q, s = w8.block_quantize(x)
+    q0, s0 = w8.block_quantize(x[-3:].contiguous())
+    assert torch.equal(q[-3:].view(torch.uint8), q0.view(torch.uint8)) and torch.equal(s[-3:], s0)
+    del q, s
+    x = x.view(-1, 16384)
+    w = torch.ones(16384, dtype=torch.bfloat16, device=DEV)
+    h, z = w8.residual_norm(x, x, w)
+    h0, z0 = w8.residual_norm(x[-12:].contiguous(), x[-12:].contiguous(), w)
+    assert torch.equal(h[-12:], h0) and torch.equal(z[-12:], z0)
