@@ -73,11 +73,16 @@ def _shape(t, rows, cols, name):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
 
 
+# (empty_strided and empty_like cost the host about half of what empty does)
+def _dense(rows, cols, dtype, device):
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
 def _aligned_codes(M, K, device):
     """Codes [M, K] whose row stride the GEMMs take (a multiple of 16)."""
     if K % 16 == 0:
-        return torch.empty((M, K), dtype=_CODES, device=device)
-    return torch.empty((M, (K + 15) // 16 * 16), dtype=_CODES, device=device)[:, :K]
+        return torch.empty_strided((M, K), (K, 1), dtype=_CODES, device=device)
+    return _dense(M, (K + 15) // 16 * 16, _CODES, device)[:, :K]
 
 
 # The current stream's handle without building a Stream object for it (2 us of
@@ -114,7 +119,7 @@ def block_quantize(x, gate=None, xq=None, sx=None, stream=None):
         _shape(xq, M, K, "xq")
     qp, ldq = _codes(xq, "xq")
     if sx is None:
-        sx = torch.empty((M, _groups(K)), dtype=_F32, device=x.device)
+        sx = _dense(M, _groups(K), _F32, x.device)
     sp = _flat(sx, "sx", _F32, M * _groups(K))
     _check(_lib.w8_block_quantize(M, K, xp, ldx, gp, ldg, qp, ldq, sp, _on(stream, x.device)))
     return xq, sx
@@ -153,7 +158,7 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, scale=1.0, e
             gp, ldg = _rows(gate, "gate", _BF16)
             _shape(gate, M, D, "gate")
     if h is None:
-        h = torch.empty((M, D), dtype=residual.dtype, device=y.device)
+        h = torch.empty_like(residual)
     else:
         _shape(h, M, D, "h")
     hp, ldh = _rows(h, "h", residual.dtype)
@@ -161,14 +166,13 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, scale=1.0, e
     ldz = ldq = 0
     if quantize:
         zq, sz = out if out is not None else (
-            _aligned_codes(M, D, y.device),
-            torch.empty((M, _groups(D)), dtype=_F32, device=y.device))
+            _aligned_codes(M, D, y.device), _dense(M, _groups(D), _F32, y.device))
         _shape(zq, M, D, "zq")
         qp, ldq = _codes(zq, "zq")
         sp = _flat(sz, "sz", _F32, M * _groups(D))
         result = h, zq, sz
     else:
-        z = out if out is not None else torch.empty((M, D), dtype=_BF16, device=y.device)
+        z = out if out is not None else torch.empty_like(y)
         _shape(z, M, D, "out")
         zp, ldz = _rows(z, "out", _BF16)
         result = h, z
@@ -206,7 +210,7 @@ def block_gemm(xq, sx, wq, sw, y=None, workspace=None, stream=None):
     G = _groups(K)
     sxp, swp = _flat(sx, "sx", _F32, M * G), _flat(sw, "sw", _F32, _groups(N) * G)
     if y is None:
-        y = torch.empty((M, N), dtype=_BF16, device=xq.device)
+        y = _dense(M, N, _BF16, xq.device)
     else:
         _shape(y, M, N, "y")
     yp, ldy = _rows(y, "y", _BF16)
@@ -264,7 +268,7 @@ def grouped_gemm(xq, sx, offsets, wq, sw, rows=None, y=None, stream=None):
     n_rows = T if rows is None else rows.numel()
     rwp = None if rows is None else _flat(rows, "rows", _I32, n_rows)
     if y is None:
-        y = torch.empty((n_rows, N), dtype=_BF16, device=xq.device)
+        y = _dense(n_rows, N, _BF16, xq.device)
     else:
         _shape(y, n_rows, N, "y")
     yp, ldy = _rows(y, "y", _BF16)
