@@ -74,6 +74,7 @@ struct Plan {
   int tile, split_k;
   long long tiles_m, tiles_n;
   long long whole, wgs;  // the largest tile's whole tiles; workgroups
+  int parts;             // the largest tile: pieces of each other tile
 };
 
 // Microseconds of a launch with `n` workgroups (output tiles times split_k) of
@@ -91,7 +92,7 @@ struct TileCost {
 constexpr TileCost kTileCost[kBlockTiles] = {
     {2, 0.30, 0.55, 0}, {2, 0.36, 0.88, 0}, {2, 0.315, 0.53, 0},
     {2, 0.45, 0.76, 0}, {1, 0.59, 0.59, 2}, {1, 1.65, 1.65, 7}};
-constexpr double kHalfStep = 0.97;    // the largest tile at half height
+constexpr double kHalfStep = 0.97, kQuarterStep = 0.59;  // pieces of the largest tile
 constexpr double kWeightBytesPerUs = 4.5e6;
 
 double estimate(const Plan& p, int N, int K) {
@@ -101,7 +102,7 @@ double estimate(const Plan& p, int N, int K) {
   const long long tiles = p.tiles_m * p.tiles_n, n = tiles * p.split_k;
   if (p.tile == kLargeTile)
     return (double)ceil_div(p.whole, kComputeUnits) * (G * c.step1 + c.round) +
-           (p.whole < tiles ? G * kHalfStep + c.round : 0);
+           (p.whole < tiles ? G * (p.parts == 4 ? kQuarterStep : kHalfStep) + c.round : 0);
   const double steps = (double)ceil_div(G, p.split_k);
   const long long cap = (long long)kComputeUnits * c.resident;
   double loop = (double)(n / cap) * (steps * c.step2 + c.round);
@@ -116,7 +117,7 @@ Plan plan_dense(int M, int N, int K) {
   Plan best{};
   double best_us = 0;
   for (int tile = 0; tile < kBlockTiles; ++tile) {
-    Plan p;
+    Plan p{};
     p.tile = tile;
     const BlockTile& t = block_tile(tile);
     p.tiles_m = ceil_div(M, t.bm);
@@ -124,10 +125,12 @@ Plan plan_dense(int M, int N, int K) {
     const long long tiles = p.tiles_m * p.tiles_n;
     p.whole = tiles;
     if (tile == kLargeTile) {
-      // one workgroup per compute unit at a time: the tiles of a last round
-      // that leaves at least half of them idle run as two halves each
+      // one workgroup per compute unit: the tiles of a last round that leaves
+      // at least half of them idle run as two halves each, or where three
+      // quarters would idle as four quarters
       const long long rest = tiles % kComputeUnits;
       if (rest <= kComputeUnits / 2) p.whole = tiles - rest;
+      p.parts = rest <= kComputeUnits / 4 ? 4 : 2;
     }
     // (a workgroup keeps two steps at least, and the arrival counters hold
     // kSplitKMaxTiles tiles)
@@ -135,7 +138,7 @@ Plan plan_dense(int M, int N, int K) {
       if (p.split_k > 1 && (tile == kLargeTile || tiles > kSplitKMaxTiles ||
                             groups_of(K) < 2 * p.split_k || tiles * p.split_k > 2 * kComputeUnits))
         break;
-      p.wgs = tile == kLargeTile ? p.whole + 2 * (tiles - p.whole) : tiles * p.split_k;
+      p.wgs = tile == kLargeTile ? p.whole + p.parts * (tiles - p.whole) : tiles * p.split_k;
       const double us = estimate(p, N, K);
       if (!best.wgs || us < best_us) {
         best = p;
@@ -322,6 +325,7 @@ w8_status w8_block_gemm(int M, int N, int K, const void* xq, int64_t ldq, const 
   a.G = groups_of(K);
   a.split_k = p.split_k;
   a.whole = (int)p.whole;
+  a.parts = p.parts;
   a.vec_store = vec_store(y, ldy);
   a.tiles_m = (int)p.tiles_m;
   a.tiles_n = (int)p.tiles_n;

@@ -57,7 +57,7 @@ struct BlockGemmArgs {
   int G;               // ceil(K / 128): scale groups and K-steps
   int split_k;         // power of two; 1 = whole K per workgroup
   int vec_store;       // y and ldy allow stores of 8 (1) or 16 (2) bytes
-  int whole;           // the largest tile: ids from here on are half tiles
+  int whole, parts;    // the largest tile: ids from `whole` on run in parts (2 or 4)
   int tiles_m;         // token tiles (grouped: slots, M / BM + min(E, M))
   int tiles_n;
   // grouped (per expert) products

@@ -518,16 +518,31 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
         *reinterpret_cast<v2u*>(smem + ((wm * NM + j) * 16 + r) * ROW +
                                 ((wn * NN + i) * 16 + 4 * q) * 2) = bf16x4(acc[i][j]);
     __syncthreads();
-    for (int c = threadIdx.x; c < (m1 - m0) * (BN / 8); c += T::THREADS) {
-      const int row = c / (BN / 8), col = c % (BN / 8) * 8, n = n0 + col;
-      const v4u v = *reinterpret_cast<const v4u*>(smem + row * ROW + col * 2);
-      uint16_t* yp = a.y + (m0 + row) * a.ldy + n;
-      if (a.vec_store == 2 && n + 8 <= a.N) {
-        *reinterpret_cast<v4u*>(yp) = v;
-      } else {
+    // (a thread's column is the same every time: THREADS is a multiple of the
+    // chunks of a row; the reads of a batch are in flight together)
+    constexpr int CHUNKS = BN / 8, STEP = T::THREADS / CHUNKS;
+    constexpr int BATCH = BM / STEP < 8 ? BM / STEP : 8;
+    static_assert(T::THREADS % CHUNKS == 0 && BM % (STEP * BATCH) == 0, "whole batches");
+    const int col = threadIdx.x % CHUNKS * 8, n = n0 + col;
+    uint16_t* yp = a.y + (long long)m0 * a.ldy + n;
+    const bool whole = a.vec_store == 2 && n + 8 <= a.N;
+    for (int r0 = threadIdx.x / CHUNKS; r0 < m1 - m0; r0 += STEP * BATCH) {
+      v4u v[BATCH];
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-          if (n + u < a.N) yp[u] = (uint16_t)(v[u >> 1] >> (16 * (u & 1)));
+      for (int b = 0; b < BATCH; ++b)
+        v[b] = *reinterpret_cast<const v4u*>(smem + (r0 + b * STEP) * ROW + col * 2);
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) {
+        const int row = r0 + b * STEP;
+        if (row >= m1 - m0) break;
+        uint16_t* p = yp + row * a.ldy;
+        if (whole) {
+          *reinterpret_cast<v4u*>(p) = v[b];
+        } else {
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (n + u < a.N) p[u] = (uint16_t)(v[b][u >> 1] >> (16 * (u & 1)));
+        }
       }
     }
   } else {
@@ -579,27 +594,32 @@ __device__ __forceinline__ TilePos tile_pos(const BlockGemmArgs& a, int id) {
 template <class T, bool PACKED>
 __global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a) {
   if constexpr (T::LARGE) {
-    // The tiles that fill whole rounds of the compute units run at full
-    // height; those of the last, partial round (from id a.whole on) as two
-    // halves each, so that the round takes half as long.  A tile with at most
-    // 128 rows left runs at half height too.
+    // The tiles that fill whole rounds of the compute units run at full size;
+    // those of the last, partial round (from id a.whole on) as two halves or
+    // four quarters each (a.parts), so that the round gets shorter.  A tile
+    // with at most 128 rows left runs at half height too.
     typedef typename T::Half Half;
-    int id = blockIdx.x, half = -1;
-    if (id < a.whole) {
+    typedef typename T::Quarter Quarter;
+    int id = blockIdx.x, part = 0;
+    const bool whole = id < a.whole;
+    if (whole) {
       id = xcd_contiguous(id, a.whole);
     } else {
       id = xcd_contiguous(id - a.whole, gridDim.x - a.whole);
-      half = id & 1;
-      id = a.whole + (id >> 1);
+      part = id & (a.parts - 1);
+      id = a.whole + (id >> (a.parts >> 1));
     }
     const TilePos t = tile_pos(a, id);
-    const int m0 = t.tm * T::BM + (half > 0 ? Half::BM : 0);
-    const int m1 = min(m0 + (half < 0 ? T::BM : Half::BM), a.M);
-    if (m0 >= m1) return;
-    if (half < 0 && m1 - m0 > Half::BM)
-      run_tile<T, false, PACKED>(a, m0, m1, t.tn * T::BN, a.wq, a.sw, 0, a.G, 0, 0);
+    const int m0 = t.tm * T::BM + (part & 1) * Half::BM;
+    const int m1 = min(m0 + (whole ? T::BM : Half::BM), a.M);
+    const int n0 = t.tn * T::BN + (part >> 1) * Quarter::BN;
+    if (m0 >= m1 || n0 >= a.N) return;
+    if (whole && m1 - m0 > Half::BM)
+      run_tile<T, false, PACKED>(a, m0, m1, n0, a.wq, a.sw, 0, a.G, 0, 0);
+    else if (whole || a.parts == 2)
+      run_tile<Half, false, PACKED>(a, m0, m1, n0, a.wq, a.sw, 0, a.G, 0, 0);
     else
-      run_tile<Half, false, PACKED>(a, m0, m1, t.tn * T::BN, a.wq, a.sw, 0, a.G, 0, 0);
+      run_tile<Quarter, false, PACKED>(a, m0, m1, n0, a.wq, a.sw, 0, a.G, 0, 0);
   } else {
     const int work = xcd_contiguous(blockIdx.x, gridDim.x);
     const int split = work & (a.split_k - 1), tile = work >> __builtin_ctz(a.split_k);
@@ -629,32 +649,48 @@ __device__ __forceinline__ int wave_scan(int v) {
 template <class T, bool PACKED>
 __global__ __launch_bounds__(T::THREADS) void grouped_gemm_kernel(BlockGemmArgs a) {
   const int lane = threadIdx.x & 63;
-  // entries and tiles of expert e0 + lane
-  int lo = 0, hi = 0;
-  auto tiles_of = [&](int e0) {
-    const int i = min(e0 + lane, a.n_experts - 1);
-    lo = min(max(a.offsets[i], 0), a.M);
-    hi = min(max(a.offsets[i + 1], 0), a.M);
-    return e0 + lane < a.n_experts ? (max(hi - lo, 0) + T::BM - 1) / T::BM : 0;
+  // Lane l holds experts e0 + 4 l .. + 3 of 256 at a time: the tiles of each,
+  // and their running sum over the lanes.
+  int off[5], tiles[4], sum = 0;
+  auto scan = [&](int e0) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+      off[i] = min(max(a.offsets[min(e0 + 4 * lane + i, a.n_experts)], 0), a.M);
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      tiles[i] = (max(off[i + 1] - off[i], 0) + T::BM - 1) / T::BM;
+      mine += tiles[i];
+    }
+    sum = wave_scan(mine);
   };
   // the XCDs share the tiles there are, not the slots of the launch
   int total = 0;
-  for (int e0 = 0; e0 < a.n_experts; e0 += 64)
-    total += __builtin_amdgcn_readlane(wave_scan(tiles_of(e0)), 63);
+  for (int e0 = 0; e0 < a.n_experts; e0 += 256) {
+    scan(e0);
+    total += __builtin_amdgcn_readlane(sum, 63);
+  }
   if ((long long)blockIdx.x >= (long long)total * a.tiles_n) return;
   const int work = xcd_contiguous(blockIdx.x, total * a.tiles_n);
   const int n0 = work % a.tiles_n * T::BN;
-  int slot = work / a.tiles_n, e = -1;
-  for (int e0 = 0; e0 < a.n_experts; e0 += 64) {
-    const int tiles = tiles_of(e0);
-    const int sum = wave_scan(tiles);
+  int slot = work / a.tiles_n, e = -1, lo = 0, hi = 0;
+  for (int e0 = 0; e0 < a.n_experts; e0 += 256) {
+    if (a.n_experts > 256) scan(e0);
     const unsigned long long past = __ballot(sum > slot);
     if (past) {
       const int l = __builtin_ctzll(past);
-      e = e0 + l;
-      lo = __builtin_amdgcn_readlane(lo, l);
-      hi = __builtin_amdgcn_readlane(hi, l);
-      slot -= __builtin_amdgcn_readlane(sum - tiles, l);
+      slot -= l ? __builtin_amdgcn_readlane(sum, l - 1) : 0;
+      // which of the lane's four
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = __builtin_amdgcn_readlane(tiles[i], l);
+        if (e < 0 && slot < t) {
+          e = e0 + 4 * l + i;
+          lo = __builtin_amdgcn_readlane(off[i], l);
+          hi = __builtin_amdgcn_readlane(off[i + 1], l);
+        }
+        if (e < 0) slot -= t;
+      }
       break;
     }
     slot -= __builtin_amdgcn_readlane(sum, 63);
@@ -683,7 +719,11 @@ struct T5 : Tile<256, 256, 4, 2, 2> {
   struct Half : Tile<128, 256, 4, 2, 3> {
     static constexpr bool LARGE = true;
   };
+  struct Quarter : Tile<128, 128, 4, 2, 4> {
+    static constexpr bool LARGE = true;
+  };
   static constexpr int LDS = Half::LDS > Tile::LDS ? Half::LDS : Tile::LDS;
+  static_assert(Quarter::LDS <= LDS, "");
 };
 
 template <class T>

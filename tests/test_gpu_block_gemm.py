@@ -47,12 +47,14 @@ def test_product(w8, M, N, K):
         assert_product(w8.block_gemm(c.dev[0], c.dev[1], wp, c.dev[3]), c.x, c.w, "packed")
 
 
-@pytest.mark.parametrize("M,N,K", [(3900, 3200, 640), (8200, 1600, 272)])
+@pytest.mark.parametrize("M,N,K", [(3900, 3200, 640), (8200, 1600, 272), (5000, 3600, 1040),
+                                   (5000, 4500, 1040)])
 def test_product_many_tiles(w8, M, N, K):
-    """Enough tiles to run several per compute unit; checked on sampled rows."""
+    """Enough tiles to run several per compute unit, with last rounds that run
+    in halves and quarters of a tile; checked on sampled rows."""
     c = Gemm(M, N, K)
     y = w8.block_gemm(*c.dev)
-    rows = np.unique(np.r_[0, M - 1, np.random.default_rng(1).integers(0, M, 200)])
+    rows = np.unique(np.r_[0, M - 1, np.random.default_rng(1).integers(0, M, 300)])
     assert_product(y[torch.from_numpy(rows).to(DEV)], c.x[rows], c.w)
 
 
