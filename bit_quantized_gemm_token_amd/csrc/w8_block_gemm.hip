@@ -170,21 +170,21 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
   }
   const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
 
-  // Token scales: 16 bytes (four steps) per lane, token 32 p + lane / 2 of
-  // piece p.  Near the end of a row the four are its last four (scale_at()
+  // Token scales: 16 bytes (four steps) per lane, token 32 w + lane / 2 by
+  // wave w.  Near the end of a row the four are its last four (scales()
   // knows); a row of fewer than four goes in single words.
   const int G = a.G;
   const float* swt = sw + (long long)(n0 / 128) * G;
   const int sw_blocks = min((a.N + 127) / 128 - n0 / 128, (BN + 127) / 128);
+  static_assert(T::SX_BYTES / 1024 <= NW, "a wave loads one piece of the token scales");
+  const float* sxt = a.sx + x_row(min(32 * wave + (lane >> 1), BM - 1)) * G;
   auto scale_start = [&](int g4) { return G >= 4 ? min(g4, G - 4) : g4; };
   auto issue_scales = [&](int c) {
     const unsigned base = lds0 + ST * T::STAGE + (c & 1) * T::SCALES;
     if (G >= 4) {
-      for (int p = wave; p < T::SX_BYTES / 1024; p += NW)
-        load_lds16(reinterpret_cast<const uint8_t*>(
-                       a.sx + x_row(min(32 * p + (lane >> 1), BM - 1)) * G +
-                       scale_start(8 * c + 4 * (lane & 1))),
-                   base + p * 1024);
+      if (wave < T::SX_BYTES / 1024)
+        load_lds16(reinterpret_cast<const uint8_t*>(sxt + scale_start(8 * c + 4 * (lane & 1))),
+                   base + wave * 1024);
     } else {
       for (int p = wave; p < T::SX_BYTES / 256; p += NW)
         load_lds4(a.sx + x_row(min(8 * p + (lane >> 3), BM - 1)) * G + min(lane & 7, G - 1),
