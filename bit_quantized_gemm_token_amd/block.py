@@ -126,7 +126,7 @@ def block_quantize(x, gate=None, xq=None, sx=None, stream=None):
 
 
 def residual_norm(y, residual, weight, post_weight=None, gate=None, scale=1.0, eps=1e-6,
-                  quantize=False, h=None, out=None, stream=None):
+                  quantize=False, with_z=False, h=None, out=None, stream=None):
     """The residual update and the norm between two blocks, in one pass:
 
         h = residual + scale * gate * N(y; post_weight)
@@ -139,8 +139,10 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, scale=1.0, e
 
     Returns (h, z) with z bf16, or with quantize=True (h, zq, sz): z's
     Block_FP8 codes and scales, as block_quantize gives them for the unrounded
-    z.  z is computed from the unrounded h, all in fp32.  out: z, or the pair
-    (zq, sz), to write to.  Any M, 1 <= D <= 32768, any strides.
+    z; with_z=True then adds z itself, (h, zq, sz, z), for a consumer beside
+    the quantized ones (a router).  z is computed from the unrounded h, all in
+    fp32.  out: z, or the pair (zq, sz), to write to.  Any M, 1 <= D <= 32768,
+    any strides.
     """
     yp, ldy = _rows(y, "y", _BF16)
     M, D = y.shape
@@ -171,6 +173,10 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, scale=1.0, e
         qp, ldq = _codes(zq, "zq")
         sp = _flat(sz, "sz", _F32, M * _groups(D))
         result = h, zq, sz
+        if with_z:
+            z = torch.empty_like(y)
+            zp, ldz = _rows(z, "z", _BF16)
+            result = h, zq, sz, z
     else:
         z = out if out is not None else torch.empty_like(y)
         _shape(z, M, D, "out")

@@ -27,13 +27,17 @@ namespace {
 // read; wait_stage() below does the waiting, and as volatile assembly the two
 // keep their order.
 // The address is a 64-bit one per lane, or a uniform base and a 32-bit offset
-// per lane.
+// per lane.  The base is copied by a scalar move on the way: a load may not
+// read a scalar register within five wait states of a vector instruction's
+// write to it, which the compiler does not watch in assembly (and the move is
+// M0's wait state too).
 __device__ __forceinline__ void load_lds16(const uint8_t* p, unsigned lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(p));
 }
 __device__ __forceinline__ void load_lds16(const uint8_t* base, unsigned off, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :
+  const uint8_t* copy;
+  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
+               : "=&s"(copy)
                : "s"(lds), "v"(off), "s"(base));
 }
 __device__ __forceinline__ void load_lds4(const float* p, unsigned lds) {
@@ -124,7 +128,7 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
   const int prow = lane >> 3, pchunk = (lane & 7) ^ prow;
   const int k_steps = a.G;
   // a last step that K ends inside of: chunks past K re-read the last whole
-  // one, and the token operand is masked after its LDS read
+  // one, and the tokens' are cleared in LDS (clear_tail)
   const int tail_chunks = (a.K & 127) >> 4;
   const int tail_step = tail_chunks ? k_steps - 1 : -2;  // (-2: none, nor is -1 before step 0)
   const int tail_adj = 16 * (min(pchunk, max(tail_chunks, 1) - 1) - pchunk);
@@ -137,8 +141,9 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
     return m;
   };
   // Tokens: an offset from the tile's first row, for gathered rows from the
-  // array's (which may lie more than 4 GiB apart: pointers).  Weights: an offset from the
-  // tile's first row.  The bases advance by one step with each step's loads.
+  // array's (which may lie more than 4 GiB apart: pointers).  Weights: an
+  // offset from the tile's first row.  The bases advance by one step with each
+  // step's loads.
   const uint8_t* px[T::PX];
   unsigned ox[T::PX], ow[T::PW];
   const uint8_t* xb = a.xq + 128LL * ks0;
@@ -296,10 +301,11 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
   // MFMA n goes out while the scaled additions of MFMA n - LAG, whose result
   // has arrived, run beside it; the scheduling barriers keep the compiler from
   // pairing each MFMA with its own additions, which would wait out its latency
-  // every time.  A step's loads are dealt over the first MFMAs: all at once
+  // every time.  A step's loads are dealt over its first MFMAs: all at once
   // they would hold up the MFMAs behind the memory path's queue, and later
-  // they would arrive after the step's end (8192 x 5120 x 8192: one a MFMA 346
-  // us, one every three 367).
+  // they would arrive after the step's end (8192 x 5120 x 8192 on the largest
+  // tile: one load every two MFMAs 300 us, one a MFMA 307, one every three
+  // 304 to 311).
   constexpr int LAG = NN * NM < 4 ? 1 : 3;
   constexpr int P = NN * NM;
   v4f t[LAG + 1];
@@ -360,7 +366,7 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
         }
         if constexpr (!LAST) {
           // (every other MFMA where a whole step is left to deal them)
-          const int n = p - (FIRST ? P2 : 0), gap = FIRST || P < 32 ? 1 : 2;
+          const int n = p - (FIRST ? P2 : 0), gap = FIRST ? 1 : 2;
           if (n % gap == 0 && n / gap < T::LOADS) issue_one(n / gap, other, here);
         }
         t[p % 4] = mfma_f8(wf[tile_of(p) % 4], xf[j_of(p)], v4f{0, 0, 0, 0});
@@ -379,7 +385,7 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
         for (int j = 0; j < NM; ++j) sc0[j] = sc1[j];
       }
     };
-    static_assert(P - P2 >= T::LOADS, "the first half step deals all loads");
+    static_assert(P - P2 >= T::LOADS && P >= 2 * T::LOADS, "an interval deals all loads");
     typedef std::integral_constant<bool, true> Yes;
     typedef std::integral_constant<bool, false> No;
     advance(ks0);

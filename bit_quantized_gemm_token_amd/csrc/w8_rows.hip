@@ -195,7 +195,11 @@ __global__ __launch_bounds__(ONE_WAVE ? 256 : 1024) void residual_norm_kernel(No
   const uint16_t* y = a.y + row * a.ldy;
   const uint16_t* gate = a.gate ? a.gate + row * a.ldg : nullptr;
   float h[NC][8], b[NC][8];
-  v4u g[NC], pw[NC], w[NC];
+  // the factors too are loaded up front, where there are registers for that
+  // (four chunks a lane: at their use, from L2 for all rows but the first)
+  constexpr bool EARLY = NC < 4;
+  constexpr int NF = EARLY ? NC : 1;
+  v4u g[NF], pw[NF], w[NF];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int k = 8 * (t + c * T), n = a.D - k;
@@ -204,10 +208,17 @@ __global__ __launch_bounds__(ONE_WAVE ? 256 : 1024) void residual_norm_kernel(No
       load8_f32(static_cast<const float*>(a.residual) + row * a.ldr + k, n, h[c]);
     else
       unpack8(load8_bf16(static_cast<const uint16_t*>(a.residual) + row * a.ldr + k, n), h[c]);
-    if (gate) g[c] = load8_bf16(gate + k, n);
-    if (a.post_w) pw[c] = load8_bf16(a.post_w + k, n);
-    w[c] = load8_bf16(a.w + k, n);
+    if constexpr (EARLY) {
+      if (gate) g[c] = load8_bf16(gate + k, n);
+      if (a.post_w) pw[c] = load8_bf16(a.post_w + k, n);
+      w[c] = load8_bf16(a.w + k, n);
+    }
   }
+  auto factor = [&](const v4u* held, const uint16_t* p, int c) {
+    if constexpr (EARLY) return held[c];
+    const int k = 8 * (t + c * T);
+    return load8_bf16(p + k, a.D - k);
+  };
   if (a.post_w) {
     float ss = 0.0f;
 #pragma unroll
@@ -218,7 +229,7 @@ __global__ __launch_bounds__(ONE_WAVE ? 256 : 1024) void residual_norm_kernel(No
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       float p[8];
-      unpack8(pw[c], p);
+      unpack8(factor(pw, a.post_w, c), p);
 #pragma unroll
       for (int i = 0; i < 8; ++i) b[c][i] *= r * p[i];
     }
@@ -227,7 +238,7 @@ __global__ __launch_bounds__(ONE_WAVE ? 256 : 1024) void residual_norm_kernel(No
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     float gf[8];
-    if (gate) unpack8(g[c], gf);
+    if (gate) unpack8(factor(g, gate, c), gf);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (gate) b[c][i] *= gf[i];
@@ -249,7 +260,7 @@ __global__ __launch_bounds__(ONE_WAVE ? 256 : 1024) void residual_norm_kernel(No
   for (int c = 0; c < NC; ++c) {
     const int k = 8 * (t + c * T), n = a.D - k;
     float wf[8];
-    unpack8(w[c], wf);
+    unpack8(factor(w, a.w, c), wf);
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[c][i] *= r * wf[i];
     if (a.z) store8_bf16(a.z + row * a.ldz + k, n, h[c]);

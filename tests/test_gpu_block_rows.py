@@ -138,6 +138,10 @@ def test_residual_norm(w8, M, D, rdtype, post, gate):
     gh2, zq, sz = w8.residual_norm(y, r, w, scale=0.7, eps=1e-6, quantize=True, **kw)
     assert torch.equal(gh2, gh)
     assert_codes(zq, sz, z, dz, "codes")
+    gh3, zq3, sz3, gz3 = w8.residual_norm(y, r, w, scale=0.7, eps=1e-6, quantize=True,
+                                          with_z=True, **kw)
+    assert torch.equal(gh3, gh) and torch.equal(gz3, gz) and torch.equal(sz3, sz)
+    assert torch.equal(zq3.view(torch.uint8), zq.view(torch.uint8))
 
 
 def test_in_place_and_strides(w8):
