@@ -63,13 +63,7 @@ w8_status check_operands(int N, int K, const void* xq, int64_t ldq, const float*
   return W8_OK;
 }
 
-int vec_store(const void* y, int64_t ldy) {
-  return aligned(y, 16) && ldy % 8 == 0 ? 2 : aligned(y, 8) && ldy % 4 == 0 ? 1 : 0;
-}
-
 // ------------------------------------------------------------ tile choice --
-constexpr int kComputeUnits = 256;
-
 struct Plan {
   int tile, split_k;
   long long tiles_m, tiles_n;
@@ -78,21 +72,24 @@ struct Plan {
 };
 
 // Microseconds of a launch with `n` workgroups (output tiles times split_k) of
-// `steps` K-steps each.  Measured on the five smaller tiles over 32 shapes
-// (20 <= M <= 8192) and every split_k of 1 .. 8, and fitted: a launch costs
-// 4; a step costs what the memory path takes for its bytes, with one or two
-// workgroups on a compute unit; split K costs its hand-off and the partials'
-// traffic.  The fastest of the estimates was within 1% of the fastest
-// measured, on average (10% at worst).
+// `steps` K-steps each, fitted to 129 random shapes (20 <= M <= 8192, 256 <= N,
+// K <= 8192) measured on every tile and every split_k of 1 .. 16: a step costs
+// what the memory path takes for its bytes, with one or two workgroups on a
+// compute unit; a round of workgroups costs its start and its output beside
+// the steps; split K costs its hand-off and the partials' traffic.  The
+// fastest of the estimates was within 1% of the fastest measured, on average
+// (15% at worst).
 struct TileCost {
-  int resident;       // workgroups of a compute unit
+  int resident;         // workgroups of a compute unit
   double step1, step2;  // us a step, one or two of them resident
-  double round;       // us a round beside the steps (the tiles that fill a unit)
+  double round;         // us a round beside the steps
 };
+constexpr double kLaunch = 1.3;
 constexpr TileCost kTileCost[kBlockTiles] = {
-    {2, 0.30, 0.55, 0}, {2, 0.36, 0.88, 0}, {2, 0.315, 0.53, 0},
-    {2, 0.45, 0.76, 0}, {1, 0.59, 0.59, 2}, {1, 1.65, 1.65, 7}};
-constexpr double kHalfStep = 0.97, kQuarterStep = 0.59;  // pieces of the largest tile
+    {2, 0.33, 0.57, 1.9}, {2, 0.35, 0.91, 2.3}, {2, 0.35, 0.55, 1.9},
+    {2, 0.44, 0.81, 2.5}, {1, 0.56, 0.56, 2.9}, {1, 1.33, 1.33, 7.7}};
+// pieces of the largest tile
+constexpr double kHalfStep = 0.95, kQuarterStep = 0.53, kPieceRound = 3.2;
 constexpr double kWeightBytesPerUs = 4.5e6;
 
 double estimate(const Plan& p, int N, int K) {
@@ -101,15 +98,15 @@ double estimate(const Plan& p, int N, int K) {
   const int G = groups_of(K);
   const long long tiles = p.tiles_m * p.tiles_n, n = tiles * p.split_k;
   if (p.tile == kLargeTile)
-    return (double)ceil_div(p.whole, kComputeUnits) * (G * c.step1 + c.round) +
-           (p.whole < tiles ? G * (p.parts == 4 ? kQuarterStep : kHalfStep) + c.round : 0);
+    return kLaunch + (double)ceil_div(p.whole, kComputeUnits) * (G * c.step1 + c.round) +
+           (p.whole < tiles ? G * (p.parts == 4 ? kQuarterStep : kHalfStep) + kPieceRound : 0);
   const double steps = (double)ceil_div(G, p.split_k);
   const long long cap = (long long)kComputeUnits * c.resident;
   double loop = (double)(n / cap) * (steps * c.step2 + c.round);
   if (n % cap) loop += steps * (n % cap <= kComputeUnits ? c.step1 : c.step2) + c.round;
   const double weights = (double)N * K / kWeightBytesPerUs;
-  double us = 4 + (loop > weights ? loop : weights);
-  if (p.split_k > 1) us += 0.9 + 0.43e-6 * (double)n * t.bm * t.bn * 4;
+  double us = kLaunch + (loop > weights ? loop : weights);
+  if (p.split_k > 1) us += 1.1 + 0.40e-6 * (double)n * t.bm * t.bn * 4;
   return us;
 }
 
@@ -125,12 +122,8 @@ Plan plan_dense(int M, int N, int K) {
     const long long tiles = p.tiles_m * p.tiles_n;
     p.whole = tiles;
     if (tile == kLargeTile) {
-      // one workgroup per compute unit: the tiles of a last round that leaves
-      // at least half of them idle run as two halves each, or where three
-      // quarters would idle as four quarters
-      const long long rest = tiles % kComputeUnits;
-      if (rest <= kComputeUnits / 2) p.whole = tiles - rest;
-      p.parts = rest <= kComputeUnits / 4 ? 4 : 2;
+      p.parts = last_round_parts(tiles);
+      if (p.parts > 1) p.whole = tiles - tiles % kComputeUnits;
     }
     // (a workgroup keeps two steps at least, and the arrival counters hold
     // kSplitKMaxTiles tiles)
@@ -160,9 +153,13 @@ bool use_small_m(int M, int K) { return M <= W8_MAX_M && K % W8_GROUP == 0; }
 // them best (128 experts of 1536 x 2048, 64 rows: 34.8 us, with the 64-row
 // tile 36.4, the largest 49.0); up to 64 the 64-row tile (4096 rows of
 // 2048 x 768: 51 us, 69 and 59); above, the largest, which runs short tiles at
-// half height (32768 rows of 1536 x 2048: 179 us, 64-row tile 235, 128-row
-// 218), unless it has too few tiles for the compute units (2000 rows, 8
-// experts of 1000 x 1008: 24 us, 128-row tile 11).
+// half height (32768 rows of 1536 x 2048: 163 us, 64-row tile 235, 128-row
+// 218), unless it has few tiles for the compute units even in pieces (8 experts
+// of 623 x 848, 5184 rows, 84 tiles: 13.5 us, 128-row tile 10.9; of 268 x 1216,
+// 13320 rows, 120 tiles: 18.1 us and 22.7).  Where a smaller tile still
+// leaves every workgroup a compute unit to itself, its steps are shorter at no
+// cost (16 experts of 260 x 448, 3942 rows: 64-row tile 6.5 us, 128-row 7.9; 8
+// experts of 384 x 1152, 380 rows: 16-row tile 7.0, 64-row 8.4).
 Plan plan_grouped(int E, int T, int N, int64_t ldq, int n_rows) {
   const long long mean = n_rows / E, experts = n_rows < E ? n_rows : E;
   Plan p{};
@@ -171,6 +168,11 @@ Plan plan_grouped(int E, int T, int N, int64_t ldq, int n_rows) {
     p.tiles_m = n_rows / block_tile(tile).bm + experts;
     p.tiles_n = ceil_div(N, block_tile(tile).bn);
   };
+  // (half a tile an expert is what partial tiles add on average)
+  const auto fits = [&](int tile) {
+    return (n_rows / block_tile(tile).bm + experts / 2) * ceil_div(N, block_tile(tile).bn) <=
+           kComputeUnits;
+  };
   if (mean <= 8) {
     take(0);
   } else if (mean <= 64) {
@@ -178,10 +180,13 @@ Plan plan_grouped(int E, int T, int N, int64_t ldq, int n_rows) {
   } else {
     take(kLargeTile);
     // (the largest tile addresses gathered rows by 32-bit offsets)
-    if (p.tiles_m * p.tiles_n < 3 * kComputeUnits / 4 || (long long)T * ldq >= (1LL << 32)) take(4);
+    if (p.tiles_m * p.tiles_n < 3 * kComputeUnits / 8 || (long long)T * ldq >= (1LL << 32)) take(4);
   }
+  if (p.tile == 4 && fits(3)) take(3);
+  if (p.tile == 3 && fits(0)) take(0);
   p.split_k = 1;
   p.whole = p.wgs = p.tiles_m * p.tiles_n;
+  if (p.tile == kLargeTile) p.wgs += kGroupedPieces;
   return p;
 }
 
@@ -326,7 +331,6 @@ w8_status w8_block_gemm(int M, int N, int K, const void* xq, int64_t ldq, const 
   a.split_k = p.split_k;
   a.whole = (int)p.whole;
   a.parts = p.parts;
-  a.vec_store = vec_store(y, ldy);
   a.tiles_m = (int)p.tiles_m;
   a.tiles_n = (int)p.tiles_n;
   const hipError_t e =
@@ -381,7 +385,6 @@ w8_status w8_grouped_gemm(int E, int T, int N, int K, const void* xq, int64_t ld
   a.K = K;
   a.G = groups_of(K);
   a.split_k = 1;
-  a.vec_store = vec_store(y, ldy);
   a.tiles_m = (int)p.tiles_m;
   a.tiles_n = (int)p.tiles_n;
   a.offsets = offsets;

@@ -56,8 +56,7 @@ struct BlockGemmArgs {
   int M, N, K;
   int G;               // ceil(K / 128): scale groups and K-steps
   int split_k;         // power of two; 1 = whole K per workgroup
-  int vec_store;       // y and ldy allow stores of 8 (1) or 16 (2) bytes
-  int whole, parts;    // the largest tile: ids from `whole` on run in parts (2 or 4)
+  int whole, parts;    // the largest tile: ids from `whole` on run in parts (2 or 4, 1: none do)
   int tiles_m;         // token tiles (grouped: slots, M / BM + min(E, M))
   int tiles_n;
   // grouped (per expert) products
@@ -74,7 +73,16 @@ struct BlockTile {
   int bm, bn, threads, lds_bytes;
 };
 constexpr int kBlockTiles = 6;
-constexpr int kLargeTile = 5;  // runs partial rounds and short tiles at half height
+constexpr int kLargeTile = 5;  // runs a last, partial round in pieces, short tiles at half height
+constexpr int kComputeUnits = 256;
+// The largest tile takes a compute unit to itself.  The tiles of a last round
+// that leaves at least half of the units idle run as two halves each, or where
+// three quarters would idle as four quarters.
+__host__ __device__ constexpr int last_round_parts(long long tiles) {
+  const int rest = (int)(tiles % kComputeUnits);
+  return rest == 0 || rest > kComputeUnits / 2 ? 1 : rest <= kComputeUnits / 4 ? 4 : 2;
+}
+constexpr int kGroupedPieces = 3 * kComputeUnits / 4;  // at most this many more than tiles
 const BlockTile& block_tile(int tile);
 hipError_t launch_block_gemm(int tile, unsigned wgs, bool packed, const BlockGemmArgs& a,
                              hipStream_t s);

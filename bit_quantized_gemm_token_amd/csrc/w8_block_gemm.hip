@@ -98,6 +98,12 @@ struct Tile {
 
 extern __shared__ __align__(1024) uint8_t smem[];
 
+// Vectors in memory at any address of a bf16 value: global stores need no more
+// alignment than that, so rows of any length and leading dimension are written
+// the same way.
+typedef v4u v4u_any __attribute__((aligned(2)));
+typedef v2u v2u_any __attribute__((aligned(2)));
+
 // Four fp32 values to bf16, round to nearest even (NaN stays NaN).
 typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ v2u bf16x4(v4f v) {
@@ -531,7 +537,7 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
     static_assert(T::THREADS % CHUNKS == 0 && BM % (STEP * BATCH) == 0, "whole batches");
     const int col = threadIdx.x % CHUNKS * 8, n = n0 + col;
     uint16_t* yp = a.y + (long long)m0 * a.ldy + n;
-    const bool whole = a.vec_store == 2 && n + 8 <= a.N;
+    const bool whole = n + 8 <= a.N;
     for (int r0 = threadIdx.x / CHUNKS; r0 < m1 - m0; r0 += STEP * BATCH) {
       v4u v[BATCH];
 #pragma unroll
@@ -546,9 +552,9 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
           // (the largest tile's outputs would push the operands out of L2:
           // non-temporal, 8192 x 5120 x 8192 301 -> 295 us)
           if constexpr (T::LARGE)
-            __builtin_nontemporal_store(v[b], reinterpret_cast<v4u*>(p));
+            __builtin_nontemporal_store(v[b], reinterpret_cast<v4u_any*>(p));
           else
-            *reinterpret_cast<v4u*>(p) = v[b];
+            *reinterpret_cast<v4u_any*>(p) = v[b];
         } else {
 #pragma unroll
           for (int u = 0; u < 8; ++u)
@@ -566,8 +572,8 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
         for (int i = 0; i < NN; ++i) {
           const int n = n0 + (wn * NN + i) * 16 + 4 * q;
           const v2u v = bf16x4(acc[i][j]);
-          if (a.vec_store && n + 4 <= a.N) {
-            *reinterpret_cast<v2u*>(yr + n) = v;
+          if (n + 4 <= a.N) {
+            *reinterpret_cast<v2u_any*>(yr + n) = v;
           } else {
 #pragma unroll
             for (int u = 0; u < 4; ++u)
@@ -676,15 +682,33 @@ __global__ __launch_bounds__(T::THREADS) void grouped_gemm_kernel(BlockGemmArgs 
     }
     sum = wave_scan(mine);
   };
-  // the XCDs share the tiles there are, not the slots of the launch
+  // the XCDs share the tiles there are, not the slots of the launch (which
+  // bound them, whatever the offsets hold)
   int total = 0;
   for (int e0 = 0; e0 < a.n_experts; e0 += 256) {
     scan(e0);
-    total += __builtin_amdgcn_readlane(sum, 63);
+    total = min(total + __builtin_amdgcn_readlane(sum, 63), a.tiles_m);
   }
-  if ((long long)blockIdx.x >= (long long)total * a.tiles_n) return;
-  const int work = xcd_contiguous(blockIdx.x, total * a.tiles_n);
-  const int n0 = work % a.tiles_n * T::BN;
+  total *= a.tiles_n;
+  int work = blockIdx.x, part = 0, parts = 1, whole = total;
+  if constexpr (T::LARGE) {
+    // a last, partial round in pieces, as in the dense kernel (the launch holds
+    // kGroupedPieces workgroups more than slots for them)
+    parts = last_round_parts(total);
+    whole = parts > 1 ? total / kComputeUnits * kComputeUnits : total;
+  }
+  if (work < whole) {
+    work = xcd_contiguous(work, whole);
+    parts = 1;
+  } else {
+    work -= whole;
+    const int pieces = (total - whole) * parts;
+    if (work >= pieces) return;
+    work = xcd_contiguous(work, pieces);
+    part = work & (parts - 1);
+    work = whole + (work >> (parts >> 1));
+  }
+  int n0 = work % a.tiles_n * T::BN;
   int slot = work / a.tiles_n, e = -1, lo = 0, hi = 0;
   for (int e0 = 0; e0 < a.n_experts; e0 += 256) {
     if (a.n_experts > 256) scan(e0);
@@ -708,11 +732,22 @@ __global__ __launch_bounds__(T::THREADS) void grouped_gemm_kernel(BlockGemmArgs 
     slot -= __builtin_amdgcn_readlane(sum, 63);
   }
   if (e < 0) return;
-  const int m0 = lo + slot * T::BM, m1 = min(m0 + T::BM, hi);
+  int m0 = lo + slot * T::BM, m1 = min(m0 + T::BM, hi);
   const uint8_t* wq = a.wq + (long long)e * a.w_stride;
   const float* sw = a.sw + (long long)e * a.sw_stride;
   if constexpr (T::LARGE) {
     typedef typename T::Half Half;
+    typedef typename T::Quarter Quarter;
+    if (parts > 1) {
+      m0 += (part & 1) * Half::BM;
+      m1 = min(m0 + Half::BM, m1);
+      n0 += (part >> 1) * Quarter::BN;
+      if (m0 >= m1 || n0 >= a.N) return;
+    }
+    if (parts == 4) {
+      run_tile<Quarter, true, PACKED>(a, m0, m1, n0, wq, sw, 0, a.G, 0, 0);
+      return;
+    }
     if (m1 - m0 <= Half::BM) {
       run_tile<Half, true, PACKED>(a, m0, m1, n0, wq, sw, 0, a.G, 0, 0);
       return;
