@@ -98,6 +98,15 @@ struct Tile {
 
 extern __shared__ __align__(1024) uint8_t smem[];
 
+// As wait_stage() with the loads of n more steps (at most N) left in flight.
+template <class T, int N>
+__device__ __forceinline__ void wait_steps(int n) {
+  if constexpr (N > 0) {
+    if (n < N) return wait_steps<T, N - 1>(n);
+  }
+  wait_stage<N * T::LOADS>();
+}
+
 // Vectors in memory at any address of a bf16 value: global stores need no more
 // alignment than that, so rows of any length and leading dimension are written
 // the same way.
@@ -228,8 +237,8 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
   };
   // Before the loads of step k (in order): moves the bases on from step k - 1,
   // and at the step that K ends inside of moves the lanes off the missing
-  // chunks.  Past the last step the bases stay, so that every step issues the
-  // same number of loads (the last ones into a stage that nobody reads).
+  // chunks.  (ROTATED: past the last step the bases stay, and its loads go into
+  // a stage that nobody reads.)
   // Scales of steps 8c .. 8c + 7 come with the first step that needs them: a
   // token's scales are consecutive in memory, so taking eight steps at once
   // fetches each cache line an eighth as often as one step would.
@@ -315,6 +324,8 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
   constexpr int LAG = NN * NM < 4 ? 1 : 3;
   constexpr int P = NN * NM;
   v4f t[LAG + 1];
+  typedef std::integral_constant<bool, true> Yes;
+  typedef std::integral_constant<bool, false> No;
   if constexpr (T::ROTATED) {
     // The loop is rotated by half a step against the staging: between two
     // barriers the waves run the second half of step k - 1 (weight tiles H ..
@@ -392,8 +403,6 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
       }
     };
     static_assert(P - P2 >= T::LOADS && P >= 2 * T::LOADS, "an interval deals all loads");
-    typedef std::integral_constant<bool, true> Yes;
-    typedef std::integral_constant<bool, false> No;
     advance(ks0);
 #pragma unroll
     for (int n = 0; n < T::LOADS; ++n) issue_one(n, lds0, lds0 + T::STAGE);
@@ -410,15 +419,15 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
     // them is the memory path, 24 bytes a clock and compute unit.)
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s) {
+      if (ks0 + s >= ks1) break;
       advance(ks0 + s);
 #pragma unroll
       for (int n = 0; n < T::LOADS; ++n) issue_one(n, lds0 + s * T::STAGE, 0);
     }
-    int stage = 0;
-    for (int k = ks0; k < ks1; ++k) {
-      // steps k .. k + ST - 2 are in flight
-      wait_stage<(ST - 2) * T::LOADS>();
-      advance(k + ST - 1);
+    // step k in `stage`; ISSUE: with the loads of step k + ST - 1
+    auto step = [&](auto issue, int k, int stage) {
+      constexpr bool ISSUE = decltype(issue)::value;
+      if constexpr (ISSUE) advance(k + ST - 1);
       if (k == tail_step) clear_tail(stage);
       const unsigned next = lds0 + (stage == 0 ? ST - 1 : stage - 1) * T::STAGE;
       // operand reads in the order of their use, weight tiles two ahead
@@ -443,16 +452,29 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
 #pragma unroll
         for (int j = 0; j < NM; ++j) {
           const int n = i * NM + j;
-          if (n < T::LOADS) issue_one(n, next, 0);
+          if (ISSUE && n < T::LOADS) issue_one(n, next, 0);
           t[n % (LAG + 1)] = mfma_f8(wf[i % AHEAD], xf[j], v4f{0, 0, 0, 0});
           if (n >= LAG) add(n - LAG);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
+      if constexpr (ISSUE) {
 #pragma unroll
-      for (int n = P; n < T::LOADS; ++n) issue_one(n, next, 0);
+        for (int n = P; n < T::LOADS; ++n) issue_one(n, next, 0);
+      }
 #pragma unroll
       for (int n = P - LAG; n < P; ++n) add(n);
+    };
+    int k = ks0, stage = 0;
+    for (; k < ks1 - (ST - 1); ++k) {
+      // steps k .. k + ST - 2 are in flight
+      wait_stage<(ST - 2) * T::LOADS>();
+      step(Yes{}, k, stage);
+      stage = stage == ST - 1 ? 0 : stage + 1;
+    }
+    for (; k < ks1; ++k) {
+      wait_steps<T, ST - 2>(ks1 - 1 - k);
+      step(No{}, k, stage);
       stage = stage == ST - 1 ? 0 : stage + 1;
     }
   }
@@ -803,7 +825,6 @@ hipError_t launch_grouped(unsigned wgs, bool packed, const BlockGemmArgs& a, hip
   return packed ? launch<T, grouped_gemm_kernel<T, true>>(wgs, a, s)
                 : launch<T, grouped_gemm_kernel<T, false>>(wgs, a, s);
 }
-
 }  // namespace
 
 const BlockTile& block_tile(int tile) { return kTiles[tile]; }
