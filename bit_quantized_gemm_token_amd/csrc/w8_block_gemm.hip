@@ -10,7 +10,9 @@
 // (D = W X^T), so a lane's accumulators all belong to one token: the step's
 // scale is one product per token column, and a group's partial sum is added
 // as acc += partial * (sx * sw), one fp32 FMA per element per group.
+#include <climits>
 #include <type_traits>
+#include <utility>
 
 #include "w8_block.hpp"
 #include "w8_device.hpp"
@@ -62,6 +64,8 @@ struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_;
   static constexpr int NW = WM * WN, THREADS = 64 * NW;
   static constexpr bool LARGE = false;
+  // waves of a SIMD: two workgroups on a compute unit where LDS holds them
+  static constexpr int WAVES = ST * (BM + BN) * 128 < 80 * 1024 ? NW / 2 : 2;
   static constexpr int NM = BM / WM / 16, NN = BN / WN / 16;  // MFMA tiles per wave
   static_assert(BN / WN <= 128, "a wave's weight rows lie in one 128-row scale block");
   // LDS: ST stages of token and weight codes, then two buffers of scales for
@@ -105,6 +109,12 @@ __device__ __forceinline__ void wait_steps(int n) {
     if (n < N) return wait_steps<T, N - 1>(n);
   }
   wait_stage<N * T::LOADS>();
+}
+
+// f(0), f(1), ... as compile-time constants.
+template <int... I, class F>
+__device__ __forceinline__ void for_each_number(std::integer_sequence<int, I...>, F&& f) {
+  (f(std::integral_constant<int, I>{}), ...);
 }
 
 // Vectors in memory at any address of a bf16 value: global stores need no more
@@ -235,6 +245,15 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
                      min(wave + i * NW, T::W_BYTES / 1024 - 1) * 1024);
     }
   };
+  auto advance_bases = [&] {
+    if constexpr (POINTERS) {
+#pragma unroll
+      for (int i = 0; i < T::PX; ++i) px[i] += 128;
+    } else {
+      xb += 128;
+    }
+    wb += PACKED ? 2048 : 128;
+  };
   // Before the loads of step k (in order): moves the bases on from step k - 1,
   // and at the step that K ends inside of moves the lanes off the missing
   // chunks.  (ROTATED: past the last step the bases stay, and its loads go into
@@ -251,15 +270,7 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
       }
     }
     if (k >= ks1) return;
-    if (k > ks0) {
-      if constexpr (POINTERS) {
-#pragma unroll
-        for (int i = 0; i < T::PX; ++i) px[i] += 128;
-      } else {
-        xb += 128;
-      }
-      wb += PACKED ? 2048 : 128;
-    }
+    if (k > ks0) advance_bases();
     if (k == tail_step) {
 #pragma unroll
       for (int i = 0; i < T::PX; ++i) {
@@ -294,14 +305,17 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
     const uint8_t* p = smem + stage * T::STAGE + T::X_BYTES + T::slot(wn, i) * 2048;
     return PACKED ? frag(p, 16 * lane, 1024 + 16 * lane) : frag(p, r * 128 + c0, r * 128 + c1);
   };
-  // the tokens' scales of step k times the weight block's
+  // the tokens' scales of step k times the weight block's (a row's last four
+  // scales lie `last_shift` bytes on where G is no multiple of four)
+  const int last_four = G >= 4 && G % 4 ? G & ~3 : INT_MAX, last_shift = 4 * (4 - G % 4);
+  const uint8_t* ssx = smem + ST * T::STAGE + (wm * 16 * NM + r) * 32;
+  const uint8_t* ssw = smem + ST * T::STAGE + T::SX_BYTES + 32 * ((wn * 16 * NN) / 128);
   auto scales = [&](int k, float* sc) {
-    const uint8_t* ss = smem + ST * T::STAGE + ((k >> 3) & 1) * T::SCALES;
-    const float swk = *reinterpret_cast<const float*>(
-        ss + T::SX_BYTES + 32 * ((wn * 16 * NN) / 128) + 4 * (k & 7));
-    ss += (wm * 16 * NM + r) * 32 + 16 * ((k >> 2) & 1) + 4 * (k - scale_start(k & ~3));
+    const int o = (k & 8 ? T::SCALES : 0) + 4 * (k & 7);
+    const float swk = *reinterpret_cast<const float*>(ssw + o);
+    const uint8_t* sx = ssx + (o + (k >= last_four ? last_shift : 0));
 #pragma unroll
-    for (int j = 0; j < NM; ++j) sc[j] = *reinterpret_cast<const float*>(ss + 512 * j) * swk;
+    for (int j = 0; j < NM; ++j) sc[j] = *reinterpret_cast<const float*>(sx + 512 * j) * swk;
   };
   // where K ends inside step k: the tokens' chunks past it become zeros
   auto clear_tail = [&](int stage) {
@@ -414,69 +428,107 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
     }
     interval(No{}, Yes{}, ks1, stage);
   } else {
-    // (Reading the operands of the next step ahead of this one's MFMAs, in a
-    // second register set, measured 2-5% slower on these tiles: what bounds
-    // them is the memory path, 24 bytes a clock and compute unit.)
+    // Operands are read one step ahead, into a second register set, between
+    // the MFMAs: past the barrier of step k every wave holds that step's
+    // operands, its stage is loaded with step k + ST, and step k + 1 is read.
+    // What bounds these tiles is the instructions of a wave, one in four
+    // clocks, beside the MFMAs; so the steps run in groups whose stages and
+    // register sets are constants.
+    constexpr int GROUP = ST % 2 ? 2 * ST : ST, F = NM + NN;
+    static_assert(ST + GROUP + 1 <= 10, "no scales land on those still to be read");
+    static_assert(P % (LAG + 1) == 0, "the ring of partial results continues over steps");
+    v8i wf[2][NN], xf[2][NM];
+    float sc[2][NM];
+    auto read = [&](int f, int stage, int set) {  // fragment f, in the order of use
+      if (f == 0)
+        wf[set][0] = weights(0, stage);
+      else if (f <= NM)
+        xf[set][f - 1] = tokens(f - 1, stage);
+      else
+        wf[set][f - NM] = weights(f - NM, stage);
+    };
+    auto add = [&](int n, int set) {
 #pragma unroll
-    for (int s = 0; s < ST - 1; ++s) {
+      for (int u = 0; u < 4; ++u)
+        acc[n / NM][n % NM][u] =
+            __builtin_fmaf(t[n % (LAG + 1)][u], sc[set][n % NM], acc[n / NM][n % NM][u]);
+    };
+    auto issue_step = [&](int stage) {
+#pragma unroll
+      for (int n = 0; n < T::LOADS; ++n) issue_one(n, lds0 + stage * T::STAGE, 0);
+    };
+#pragma unroll
+    for (int s = 0; s < ST; ++s) {
       if (ks0 + s >= ks1) break;
       advance(ks0 + s);
-#pragma unroll
-      for (int n = 0; n < T::LOADS; ++n) issue_one(n, lds0 + s * T::STAGE, 0);
+      issue_step(s);
     }
-    // step k in `stage`; ISSUE: with the loads of step k + ST - 1
-    auto step = [&](auto issue, int k, int stage) {
-      constexpr bool ISSUE = decltype(issue)::value;
-      if constexpr (ISSUE) advance(k + ST - 1);
-      if (k == tail_step) clear_tail(stage);
-      const unsigned next = lds0 + (stage == 0 ? ST - 1 : stage - 1) * T::STAGE;
-      // operand reads in the order of their use, weight tiles two ahead
-      constexpr int AHEAD = NN < 3 ? NN : 3;
-      v8i wf[AHEAD], xf[NM];
-      float sc[NM];
-      wf[0] = weights(0, stage);
+    wait_steps<T, ST - 1>(ks1 - 1 - ks0);
+    if (ks0 == tail_step) clear_tail(0);
 #pragma unroll
-      for (int j = 0; j < NM; ++j) xf[j] = tokens(j, stage);
-      scales(k, sc);
+    for (int f = 0; f < F; ++f) read(f, 0, 0);
+    scales(ks0, sc[0]);
 #pragma unroll
-      for (int i = 1; i < AHEAD - 1; ++i) wf[i] = weights(i, stage);
-      auto add = [&](int n) {
+    for (int j = 0; j < NM; ++j) sc[1][j] = 0.0f;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          acc[n / NM][n % NM][u] =
-              __builtin_fmaf(t[n % (LAG + 1)][u], sc[n % NM], acc[n / NM][n % NM][u]);
-      };
+    for (int n = 0; n < LAG + 1; ++n) t[n] = v4f{0, 0, 0, 0};
+    int k = ks0;
+    // Groups that load whole steps only.  The additions of a step's last MFMAs
+    // run beside the next step's first (before the first step: of zeros).
+    for (const int end = min(ks1, tail_step >= 0 ? tail_step : ks1) - (ST + GROUP); k <= end;
+         k += GROUP) {
 #pragma unroll
-      for (int i = 0; i < NN; ++i) {
-        if (i + AHEAD - 1 < NN) wf[(i + AHEAD - 1) % AHEAD] = weights(i + AHEAD - 1, stage);
+      for (int s = 0; s < GROUP; ++s) {
+        const int stage = s % ST, set = s % 2;
+        wait_stage<(ST - 2) * T::LOADS>();  // steps k + s + 2 .. k + s + ST - 1 are in flight
+        // the scales that the group's loads come to need
+        if (s == 0 && ((k + ST - 1) & 8) != ((k + ST + GROUP - 1) & 8))
+          issue_scales((k + ST + GROUP - 1) >> 3);
+        advance_bases();
 #pragma unroll
-        for (int j = 0; j < NM; ++j) {
-          const int n = i * NM + j;
-          if (ISSUE && n < T::LOADS) issue_one(n, next, 0);
-          t[n % (LAG + 1)] = mfma_f8(wf[i % AHEAD], xf[j], v4f{0, 0, 0, 0});
-          if (n >= LAG) add(n - LAG);
+        for (int n = 0; n < P; ++n) {
+#pragma unroll
+          for (int l = n * T::LOADS / P; l < (n + 1) * T::LOADS / P; ++l)
+            issue_one(l, lds0 + stage * T::STAGE, 0);
+#pragma unroll
+          for (int f = n * F / P; f < (n + 1) * F / P; ++f) read(f, (s + 1) % ST, set ^ 1);
+          t[n % (LAG + 1)] = mfma_f8(wf[set][n / NM], xf[set][n % NM], v4f{0, 0, 0, 0});
+          if (n >= LAG)
+            add(n - LAG, set);
+          else
+            add(P + n - LAG, set ^ 1);
+          if (n == LAG) scales(k + s + 1, sc[set ^ 1]);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
-      if constexpr (ISSUE) {
+    }
 #pragma unroll
-        for (int n = P; n < T::LOADS; ++n) issue_one(n, next, 0);
+    for (int n = P - LAG; n < P; ++n) add(n, 1);
+    // the steps that are left, at most ST + GROUP
+    auto step = [&](auto number) {
+      if (k >= ks1) return;
+      constexpr int s = decltype(number)::value, stage = s % ST, next = (s + 1) % ST, set = s % 2;
+      if (k + 1 < ks1) wait_steps<T, ST - 2>(min(ks1 - 2 - k, ST - 2));
+      if (k + ST < ks1) {
+        advance(k + ST);
+        issue_step(stage);
       }
+      if (k + 1 == tail_step) clear_tail(next);
+      // (past the last step these read what nobody uses)
 #pragma unroll
-      for (int n = P - LAG; n < P; ++n) add(n);
+      for (int n = 0; n < P; ++n) {
+#pragma unroll
+        for (int f = n * F / P; f < (n + 1) * F / P; ++f) read(f, next, set ^ 1);
+        t[n % (LAG + 1)] = mfma_f8(wf[set][n / NM], xf[set][n % NM], v4f{0, 0, 0, 0});
+        if (n >= LAG) add(n - LAG, set);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      scales(k + 1, sc[set ^ 1]);
+#pragma unroll
+      for (int n = P - LAG; n < P; ++n) add(n, set);
+      ++k;
     };
-    int k = ks0, stage = 0;
-    for (; k < ks1 - (ST - 1); ++k) {
-      // steps k .. k + ST - 2 are in flight
-      wait_stage<(ST - 2) * T::LOADS>();
-      step(Yes{}, k, stage);
-      stage = stage == ST - 1 ? 0 : stage + 1;
-    }
-    for (; k < ks1; ++k) {
-      wait_steps<T, ST - 2>(ks1 - 1 - k);
-      step(No{}, k, stage);
-      stage = stage == ST - 1 ? 0 : stage + 1;
-    }
+    for_each_number(std::make_integer_sequence<int, ST + GROUP>{}, step);
   }
   wait_stage<0>();  // the loads past the last step have landed before LDS is used again or freed
 
@@ -632,7 +684,7 @@ __device__ __forceinline__ TilePos tile_pos(const BlockGemmArgs& a, int id) {
 }
 
 template <class T, bool PACKED>
-__global__ __launch_bounds__(T::THREADS) void block_gemm_kernel(BlockGemmArgs a) {
+__global__ __launch_bounds__(T::THREADS, T::WAVES) void block_gemm_kernel(BlockGemmArgs a) {
   if constexpr (T::LARGE) {
     // The tiles that fill whole rounds of the compute units run at full size;
     // those of the last, partial round (from id a.whole on) as two halves or
@@ -687,7 +739,7 @@ __device__ __forceinline__ int wave_scan(int v) {
 // most slots that n_rows entries can need, M / BM + min(E, M); those past the
 // last tile exit at once.
 template <class T, bool PACKED>
-__global__ __launch_bounds__(T::THREADS) void grouped_gemm_kernel(BlockGemmArgs a) {
+__global__ __launch_bounds__(T::THREADS, T::WAVES) void grouped_gemm_kernel(BlockGemmArgs a) {
   const int lane = threadIdx.x & 63;
   // Lane l holds experts e0 + 4 l .. + 3 of 256 at a time: the tiles of each,
   // and their running sum over the lanes.
@@ -785,7 +837,7 @@ typedef Tile<64, 128, 2, 4, 3> T3;
 typedef Tile<128, 128, 4, 2, 4> T4;
 struct T5 : Tile<256, 256, 4, 2, 2> {
   static constexpr bool LARGE = true;
-  struct Half : Tile<128, 256, 4, 2, 3> {
+  struct Half : Tile<128, 256, 2, 4, 2> {
     static constexpr bool LARGE = true;
   };
   struct Quarter : Tile<128, 128, 4, 2, 4> {
