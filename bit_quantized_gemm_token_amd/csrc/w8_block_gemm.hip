@@ -84,8 +84,9 @@ struct Tile {
   // step; the first H + 2 of a step are staged with its tokens, the others
   // one step later.  In LDS a stage's weight tiles (16 rows, 2 KiB) are
   // ordered early ones first.
-  static constexpr bool ROTATED = NN >= 4 && ST == 2;
+  static constexpr bool ROTATED = NN * NM >= 16;
   static constexpr int H = NN / 2, EARLY = ROTATED ? H + 2 : NN;
+  static_assert(!ROTATED || EARLY == NN || ST == 2, "late weight tiles follow one step behind");
   static constexpr int PW1 = WN * EARLY * 2 / NW;  // (exact where ROTATED)
   static __device__ __forceinline__ constexpr int slot(int wn, int i) {
     return i < EARLY ? wn * EARLY + i : WN * EARLY + wn * (NN - EARLY) + i - EARLY;
@@ -367,10 +368,11 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
     static_assert(P % 4 == 0 && NM % 4 == 0, "the ring of partial results continues over intervals");
     auto interval = [&](auto first, auto last, int k, int stage) {
       constexpr bool FIRST = decltype(first)::value, LAST = decltype(last)::value;
-      wait_stage<0>();
+      wait_stage<(ST - 2) * T::LOADS>();
       if (!LAST && k == tail_step) clear_tail(stage);
-      if constexpr (!LAST) advance(k + 1);
-      const unsigned here = lds0 + stage * T::STAGE, other = lds0 + (stage ^ 1) * T::STAGE;
+      if constexpr (!LAST) advance(k + ST - 1);
+      const int before = stage == 0 ? ST - 1 : stage - 1;  // the stage of step k - 1
+      const unsigned here = lds0 + stage * T::STAGE, other = lds0 + before * T::STAGE;
       if constexpr (FIRST) {
         wf[0] = weights(0, stage);
 #pragma unroll
@@ -382,7 +384,7 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
       for (int p = FIRST ? P2 : 0; p < (LAST ? P2 : P); ++p) {
         if constexpr (!FIRST) {
           if (p < (NN - H - 2) * NM && p % NM == 0)  // (their slots' tiles are done)
-            wf[(H + 2 + p / NM) % 4] = weights(H + 2 + p / NM, stage ^ 1);
+            wf[(H + 2 + p / NM) % 4] = weights(H + 2 + p / NM, before);
           if constexpr (!LAST) {
             if (p == PJ) {
               scales(k, sc1);
@@ -417,14 +419,18 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
       }
     };
     static_assert(P - P2 >= T::LOADS && P >= 2 * T::LOADS, "an interval deals all loads");
-    advance(ks0);
 #pragma unroll
-    for (int n = 0; n < T::LOADS; ++n) issue_one(n, lds0, lds0 + T::STAGE);
+    for (int s = 0; s < ST - 1; ++s) {
+      advance(ks0 + s);
+#pragma unroll
+      for (int n = 0; n < T::LOADS; ++n)
+        issue_one(n, lds0 + s * T::STAGE, lds0 + (s + 1) * T::STAGE);
+    }
     interval(Yes{}, No{}, ks0, 0);
     int stage = 1;
     for (int k = ks0 + 1; k < ks1; ++k) {
       interval(No{}, No{}, k, stage);
-      stage ^= 1;
+      stage = stage == ST - 1 ? 0 : stage + 1;
     }
     interval(No{}, Yes{}, ks1, stage);
   } else {
@@ -837,7 +843,7 @@ typedef Tile<64, 128, 2, 4, 3> T3;
 typedef Tile<128, 128, 4, 2, 4> T4;
 struct T5 : Tile<256, 256, 4, 2, 2> {
   static constexpr bool LARGE = true;
-  struct Half : Tile<128, 256, 2, 4, 2> {
+  struct Half : Tile<128, 256, 2, 4, 3> {
     static constexpr bool LARGE = true;
   };
   struct Quarter : Tile<128, 128, 4, 2, 4> {
