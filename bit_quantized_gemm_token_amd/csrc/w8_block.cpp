@@ -78,18 +78,20 @@ struct Plan {
 // compute unit; a round of workgroups costs its start and its output beside
 // the steps; split K costs its hand-off and the partials' traffic.  The
 // fastest of the estimates was within 1% of the fastest measured, on average
-// (15% at worst).
+// (7% at worst).
 struct TileCost {
   int resident;         // workgroups of a compute unit
   double step1, step2;  // us a step, one or two of them resident
   double round;         // us a round beside the steps
 };
-constexpr double kLaunch = 1.3;
-constexpr TileCost kTileCost[kBlockTiles] = {
-    {2, 0.33, 0.57, 1.9}, {2, 0.35, 0.91, 2.3}, {2, 0.35, 0.55, 1.9},
-    {2, 0.44, 0.81, 2.5}, {1, 0.56, 0.56, 2.9}, {1, 1.33, 1.33, 7.7}};
+constexpr double kLaunch = 1.7;
+constexpr TileCost kTileCost[kBlockTiles] = {{2, 0.26, 0.50, 1.5},
+                                             {2, 0.23, 0.465, 2.0},
+                                             {2, 0.36, 0.725, 2.5},
+                                             {1, 0.47, 0.47, 3.15},
+                                             {1, 1.305, 1.305, 7.4}};
 // pieces of the largest tile
-constexpr double kHalfStep = 0.95, kQuarterStep = 0.53, kPieceRound = 3.2;
+constexpr double kHalfStep = 0.89, kQuarterStep = 0.456, kPieceRound = 3.3;
 constexpr double kWeightBytesPerUs = 4.5e6;
 
 double estimate(const Plan& p, int N, int K) {
@@ -106,7 +108,7 @@ double estimate(const Plan& p, int N, int K) {
   if (n % cap) loop += steps * (n % cap <= kComputeUnits ? c.step1 : c.step2) + c.round;
   const double weights = (double)N * K / kWeightBytesPerUs;
   double us = kLaunch + (loop > weights ? loop : weights);
-  if (p.split_k > 1) us += 1.1 + 0.40e-6 * (double)n * t.bm * t.bn * 4;
+  if (p.split_k > 1) us += 1.1 + 0.38e-6 * (double)n * t.bm * t.bn * 4;
   return us;
 }
 
@@ -153,37 +155,39 @@ bool use_small_m(int M, int K) { return M <= W8_MAX_M && K % W8_GROUP == 0; }
 // them best (128 experts of 1536 x 2048, 64 rows: 34.8 us, with the 64-row
 // tile 36.4, the largest 49.0); up to 64 the 64-row tile (4096 rows of
 // 2048 x 768: 51 us, 69 and 59); above, the largest, which runs short tiles at
-// half height (32768 rows of 1536 x 2048: 163 us, 64-row tile 235, 128-row
-// 218), unless it has few tiles for the compute units even in pieces (8 experts
-// of 623 x 848, 5184 rows, 84 tiles: 13.5 us, 128-row tile 10.9; of 268 x 1216,
-// 13320 rows, 120 tiles: 18.1 us and 22.7).  Where a smaller tile still
-// leaves every workgroup a compute unit to itself, its steps are shorter at no
-// cost (16 experts of 260 x 448, 3942 rows: 64-row tile 6.5 us, 128-row 7.9; 8
-// experts of 384 x 1152, 380 rows: 16-row tile 7.0, 64-row 8.4).
-Plan plan_grouped(int E, int T, int N, int64_t ldq, int n_rows) {
+// half height (32768 rows of 1536 x 2048: 164 us, 64-row tile 227, 128-row
+// 214), unless it has few tiles for the compute units even in pieces (8 experts
+// of 623 x 848, 5184 rows, 84 tiles: 12.9 us, 128-row tile 10.8; of 268 x 1216,
+// 13320 rows, 120 tiles: 17.6 us and 22.4).  Where a smaller tile's
+// workgroups all run at once still, its shorter steps win (64-row tile, one
+// workgroup a compute unit, 16 experts of 260 x 448, 3942 rows: 6.4 us, 128-row
+// 8.0; 16-row tile, two a unit where K is short, 60 experts of 512 x 512, 1588
+// rows: 6.5, 64-row 7.1; of 420 x 1072, 805 rows: 11.6 and 9.9).
+Plan plan_grouped(int E, int T, int N, int K, int64_t ldq, int n_rows) {
   const long long mean = n_rows / E, experts = n_rows < E ? n_rows : E;
   Plan p{};
-  const auto take = [&](int tile) {
+  const auto take = [&](BlockTileId tile) {
     p.tile = tile;
     p.tiles_m = n_rows / block_tile(tile).bm + experts;
     p.tiles_n = ceil_div(N, block_tile(tile).bn);
   };
   // (half a tile an expert is what partial tiles add on average)
-  const auto fits = [&](int tile) {
-    return (n_rows / block_tile(tile).bm + experts / 2) * ceil_div(N, block_tile(tile).bn) <=
-           kComputeUnits;
+  const auto fits = [&](BlockTileId tile, int wgs) {
+    return (n_rows / block_tile(tile).bm + experts / 2) * ceil_div(N, block_tile(tile).bn) <= wgs;
   };
   if (mean <= 8) {
-    take(0);
+    take(kTile16x128);
   } else if (mean <= 64) {
-    take(3);
+    take(kTile64x128);
   } else {
-    take(kLargeTile);
+    take(kTile256x256);
     // (the largest tile addresses gathered rows by 32-bit offsets)
-    if (p.tiles_m * p.tiles_n < 3 * kComputeUnits / 8 || (long long)T * ldq >= (1LL << 32)) take(4);
+    if (p.tiles_m * p.tiles_n < 3 * kComputeUnits / 8 || (long long)T * ldq >= (1LL << 32))
+      take(kTile128x128);
   }
-  if (p.tile == 4 && fits(3)) take(3);
-  if (p.tile == 3 && fits(0)) take(0);
+  if (p.tile == kTile128x128 && fits(kTile64x128, kComputeUnits)) take(kTile64x128);
+  const int run = groups_of(K) <= 6 ? 2 * kComputeUnits : kComputeUnits;
+  if (p.tile == kTile64x128 && fits(kTile16x128, run)) take(kTile16x128);
   p.split_k = 1;
   p.whole = p.wgs = p.tiles_m * p.tiles_n;
   if (p.tile == kLargeTile) p.wgs += kGroupedPieces;
@@ -366,7 +370,7 @@ w8_status w8_grouped_gemm(int E, int T, int N, int K, const void* xq, int64_t ld
     return fail(W8_E_INVALID, "w_stride must be a multiple of 16 that holds one expert's codes");
   if (E > 1 && sw_stride < (int64_t)groups_of(N) * groups_of(K))
     return fail(W8_E_INVALID, "sw_stride must hold one expert's scales");
-  const Plan p = plan_grouped(E, T, N, ldq, n_rows);
+  const Plan p = plan_grouped(E, T, N, K, ldq, n_rows);
   st = check_grid(p);
   if (st) return st;
   st = check_device();

@@ -72,8 +72,11 @@ struct BlockGemmArgs {
 struct BlockTile {
   int bm, bn, threads, lds_bytes;
 };
-constexpr int kBlockTiles = 6;
-constexpr int kLargeTile = 5;  // runs a last, partial round in pieces, short tiles at half height
+// The tiles, by tokens x weight rows.  The largest runs a last, partial round
+// in pieces and (grouped) short tiles at half height; kTile64x64 is not built
+// for the grouped product.
+enum BlockTileId { kTile16x128, kTile64x64, kTile64x128, kTile128x128, kTile256x256, kBlockTiles };
+constexpr int kLargeTile = kTile256x256;
 constexpr int kComputeUnits = 256;
 // The largest tile takes a compute unit to itself.  The tiles of a last round
 // that leaves at least half of the units idle run as two halves each, or where

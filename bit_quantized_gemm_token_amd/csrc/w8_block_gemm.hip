@@ -837,11 +837,10 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES) void grouped_gemm_kernel(Bloc
 }
 
 typedef Tile<16, 128, 1, 4, 4> T0;
-typedef Tile<32, 128, 1, 4, 4> T1;
-typedef Tile<64, 64, 2, 2, 4> T2;
-typedef Tile<64, 128, 2, 4, 3> T3;
-typedef Tile<128, 128, 4, 2, 4> T4;
-struct T5 : Tile<256, 256, 4, 2, 2> {
+typedef Tile<64, 64, 2, 2, 4> T1;
+typedef Tile<64, 128, 2, 4, 3> T2;
+typedef Tile<128, 128, 4, 2, 4> T3;
+struct T4 : Tile<256, 256, 4, 2, 2> {
   static constexpr bool LARGE = true;
   struct Half : Tile<128, 256, 2, 4, 3> {
     static constexpr bool LARGE = true;
@@ -858,8 +857,7 @@ constexpr BlockTile describe() {
   return BlockTile{T::BM, T::BN, T::THREADS, T::LDS};
 }
 const BlockTile kTiles[kBlockTiles] = {describe<T0>(), describe<T1>(), describe<T2>(),
-                                       describe<T3>(), describe<T4>(),
-                                       describe<T5>()};
+                                       describe<T3>(), describe<T4>()};
 
 typedef void (*Kernel)(BlockGemmArgs);
 
@@ -890,22 +888,21 @@ const BlockTile& block_tile(int tile) { return kTiles[tile]; }
 hipError_t launch_block_gemm(int tile, unsigned wgs, bool packed, const BlockGemmArgs& a,
                              hipStream_t s) {
   switch (tile) {
-    case 0: return launch_dense<T0>(wgs, packed, a, s);
-    case 1: return launch_dense<T1>(wgs, packed, a, s);
-    case 2: return launch_dense<T2>(wgs, packed, a, s);
-    case 3: return launch_dense<T3>(wgs, packed, a, s);
-    case 4: return launch_dense<T4>(wgs, packed, a, s);
-    default: return launch_dense<T5>(wgs, packed, a, s);
+    case kTile16x128: return launch_dense<T0>(wgs, packed, a, s);
+    case kTile64x64: return launch_dense<T1>(wgs, packed, a, s);
+    case kTile64x128: return launch_dense<T2>(wgs, packed, a, s);
+    case kTile128x128: return launch_dense<T3>(wgs, packed, a, s);
+    default: return launch_dense<T4>(wgs, packed, a, s);
   }
 }
 
 hipError_t launch_grouped_gemm(int tile, unsigned wgs, bool packed, const BlockGemmArgs& a,
                                hipStream_t s) {
   switch (tile) {
-    case 0: return launch_grouped<T0>(wgs, packed, a, s);
-    case 3: return launch_grouped<T3>(wgs, packed, a, s);
-    case 4: return launch_grouped<T4>(wgs, packed, a, s);
-    default: return launch_grouped<T5>(wgs, packed, a, s);
+    case kTile16x128: return launch_grouped<T0>(wgs, packed, a, s);
+    case kTile64x128: return launch_grouped<T2>(wgs, packed, a, s);
+    case kTile128x128: return launch_grouped<T3>(wgs, packed, a, s);
+    default: return launch_grouped<T4>(wgs, packed, a, s);
   }
 }
 
