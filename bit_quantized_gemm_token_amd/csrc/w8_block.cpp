@@ -144,11 +144,20 @@ Plan plan_dense(int M, int N, int K) {
   return best;
 }
 
-// Up to W8_MAX_M tokens run on the small-M GEMM, whose waves stream the
-// weights into registers: 1 x 4608 x 7168 10.3 us against 12.1 on the best of
-// the tiles here, 32 x 4608 x 7168 14.1 against 14.3, 16 x 1000 x 2048 4.9
-// against 6.0.  (It needs whole groups.)
-bool use_small_m(int M, int K) { return M <= W8_MAX_M && K % W8_GROUP == 0; }
+// Up to W8_MAX_M tokens the small-M GEMM, whose waves stream the weights into
+// registers, has the shorter start, and the tiles, whose loads do not wait for
+// registers, the higher rate: the larger the weights and M, the better for the
+// tiles (on its untuned configurations 1 x 2048 x 2048 4.1 us, tiles 5.2; 16 x
+// 4096 x 4096 7.9 and 7.7; 24 x 4096 x 4096 9.7 and 7.8; 24 x 896 x 512 3.5 and
+// 4.0; 1 x 4608 x 7168 12.5 and 9.8; 16 x 5120 x 8192 19.0 and 11.7).  Packed
+// weights, which it reads in whole lines, move the border (1 x 5120 x 8192 10.8
+// and 12.2; 8 x 5120 x 8192 12.4 and 11.7).  It needs whole groups.
+bool use_small_m(int M, int N, int K, bool packed) {
+  if (M > W8_MAX_M || K % W8_GROUP) return false;
+  const long long weights = (long long)N * K;
+  if (M > W8_MAX_M / 2) return weights < 1 << 22;
+  return weights < 24 << 20 || (packed && M < 8);
+}
 
 // The counts per expert are on the device, so their mean picks the tile: up to
 // 8 rows the weights' bytes are all that counts and the smallest tile streams
@@ -283,7 +292,7 @@ w8_status w8_block_gemm_workspace_size(int M, int N, int K, int packed, size_t* 
   if (packed != 0 && packed != 1)
     return fail(W8_E_INVALID, "weight layout must be 0 (row-major) or 1 (packed)");
   if (!bytes) return fail(W8_E_INVALID, "null output pointer");
-  if (M && use_small_m(M, K))
+  if (M && use_small_m(M, N, K, packed))
     return w8_workspace_size(W8_BLOCK_FP8, W8_OP_GEMM, M, N, K, packed, nullptr, bytes);
   *bytes = M ? plan_bytes(plan_dense(M, N, K)) : 0;
   return ok();
@@ -300,7 +309,7 @@ w8_status w8_block_gemm(int M, int N, int K, const void* xq, int64_t ldq, const 
   int packed = 0;
   st = check_operands(N, K, xq, ldq, sx, wq, ldw, sw, y, ldy, &packed);
   if (st) return st;
-  if (use_small_m(M, K))
+  if (use_small_m(M, N, K, packed))
     return w8_gemm_w8a8(W8_BLOCK_FP8, M, N, K, xq, ldq, sx, wq, ldw, sw, y, ldy, nullptr, ws,
                         ws_bytes, stream);
   const Plan p = plan_dense(M, N, K);

@@ -3,6 +3,9 @@
  *
  *     Y[M, N] = dequant(Xq)[M, K] . dequant(Wq)[N, K]^T,   1 <= M <= 32
  *
+ * and, for the Block_FP8 format, the operators of a layer at any token count
+ * (w8_block_gemm, w8_grouped_gemm, w8_residual_norm, w8_block_quantize).
+ *
  * The method: ai-radar.it, "Helion nel backend vLLM: un solo GEMM, tuning per
  * forma e guadagni fino al 10%".
  *   - paragraph 1: the three 8-bit formats FP8_Dynamic, W8A8_INT8, Block_FP8;
@@ -605,8 +608,9 @@ w8_status w8_moe_tune(w8_fmt fmt, int E, int T, int N, int K, int topk,
  *   xq       codes [M, K], row stride ldq bytes, 8-byte aligned, ldq % 8 == 0
  *            (the GEMMs below need 16)
  *   sx       fp32 [M, ceil(K/128)]
- * K >= 8, K % 8 == 0.  A group with a NaN or an infinity gets a non-finite
- * scale, so it dequantizes to non-finite values.                           */
+ * 8 <= K <= 2^22, K % 8 == 0, M * ceil(K/128) < 2^31.  A group with a NaN or
+ * an infinity gets a non-finite scale, so it dequantizes to non-finite
+ * values.                                                                  */
 w8_status w8_block_quantize(int M, int K, const void *x, int64_t ldx, const void *gate,
                             int64_t ldg, void *xq, int64_t ldq, float *sx, w8_stream stream);
 
@@ -643,9 +647,12 @@ w8_status w8_residual_norm(int M, int D, const void *y, int64_t ldy, const void 
  *   ws      w8_block_gemm_workspace_size bytes with w8_gemm_w8a8's rules
  *           (zero-filled before its first use; one workspace may serve both
  *           entry points), NULL when the size is 0
- * N >= 1, K >= 16, K % 16 == 0, finite codes.  Partial sums of a group come
- * from the fp8 matrix instructions; groups are summed in fp32 in K order, so
- * results are run-to-run deterministic.                                    */
+ * 1 <= N <= 2^24, 16 <= K <= 2^22, K % 16 == 0; ldq and ldw at most 2^23;
+ * finite codes (w8_gemm_w8a8's condition).  Partial sums of a group come from
+ * the fp8 matrix instructions; groups are summed in fp32 in K order, within
+ * each part of a split K and then over the parts, so results are run-to-run
+ * deterministic.  Up to W8_MAX_M tokens on weights below a few tens of MiB run
+ * w8_gemm_w8a8's kernel (and configuration table) where K % 128 == 0.       */
 w8_status w8_block_gemm(int M, int N, int K, const void *xq, int64_t ldq, const float *sx,
                         const void *wq, int64_t ldw, const float *sw, void *y, int64_t ldy,
                         void *ws, size_t ws_bytes, w8_stream stream);

@@ -125,3 +125,14 @@ def test_binding_refuses_host_tensors(w8):
         w8.block_gemm(q, s, q, s)
     with pytest.raises(TypeError, match="HIP"):
         w8.grouped_gemm(q, s, torch.zeros(2, dtype=torch.int32), q[None], s[None])
+
+
+def test_strides_and_groups_limits(lib):
+    """Beyond what the kernels' 32-bit offsets address."""
+    for kw in (dict(ldq=(1 << 23) + 16), dict(ldw=(1 << 23) + 16)):
+        assert call(lib.w8_block_gemm, GEMM, **kw) == INVALID
+        assert call(lib.w8_grouped_gemm, GROUPED, w_stride=1 << 40, **kw) == INVALID
+        assert b"2^23" in lib.w8_last_error()
+    long = dict(M=1 << 17, K=1 << 21, ldx=1 << 21, ldg=1 << 21, ldq=1 << 21)
+    assert call(lib.w8_block_quantize, QUANT, **long) == INVALID
+    assert b"2^31" in lib.w8_last_error()
