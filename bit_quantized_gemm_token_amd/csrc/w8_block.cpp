@@ -73,12 +73,11 @@ struct Plan {
 
 // Microseconds of a launch with `n` workgroups (output tiles times split_k) of
 // `steps` K-steps each, fitted to 129 random shapes (20 <= M <= 8192, 256 <= N,
-// K <= 8192) measured on every tile and every split_k of 1 .. 16: a step costs
-// what the memory path takes for its bytes, with one or two workgroups on a
-// compute unit; a round of workgroups costs its start and its output beside
-// the steps; split K costs its hand-off and the partials' traffic.  The
-// fastest of the estimates was within 1% of the fastest measured, on average
-// (7% at worst).
+// K <= 8192) measured on every tile and every split_k of 1 .. 16: a step has
+// one time with one workgroup on a compute unit and one with two; a round of
+// workgroups costs its start and its output beside the steps; split K costs its
+// hand-off and the partials' traffic.  The fastest of the estimates was within
+// 1% of the fastest measured, on average (7% at worst).
 struct TileCost {
   int resident;         // workgroups of a compute unit
   double step1, step2;  // us a step, one or two of them resident

