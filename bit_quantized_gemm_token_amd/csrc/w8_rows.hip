@@ -105,20 +105,23 @@ __device__ __forceinline__ void store8_codes(uint8_t* p, int n, v2u v) {
 }
 
 // Codes of eight values of a 1 x 128 group whose 16 lanes call together; *s
-// is the group's scale.  A group that holds a NaN or an infinity gets a NaN
-// or infinite scale, so that it stays non-finite when dequantized.
-__device__ __forceinline__ v2u encode_group(float* f, float* s) {
+// is the scale of the group times `factor` (1 for zeros).  A group that holds a
+// NaN or an infinity gets a NaN or infinite scale, so that it stays non-finite
+// when dequantized.
+__device__ __forceinline__ v2u encode_group(float* f, float* scale, float factor = 1.0f) {
   unsigned m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, abs_bits(f[i]));
-  *s = act_scale<false>(__uint_as_float(seg16_umax(m)));
-  const float r = act_recip(*s);
+  m = seg16_umax(m);
+  const float s = act_scale<false>(__uint_as_float(m));
+  *scale = m ? s * factor : 1.0f;
+  const float r = act_recip(s);
   if (r != 0.0f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = act_quot(f[i], *s, r);
+    for (int i = 0; i < 8; ++i) f[i] = act_quot(f[i], s, r);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = f[i] / *s;
+    for (int i = 0; i < 8; ++i) f[i] = f[i] / s;
   }
   return v2u{e4m3_pack4(f[0], f[1], f[2], f[3]), e4m3_pack4(f[4], f[5], f[6], f[7])};
 }
@@ -266,12 +269,19 @@ __global__ __launch_bounds__(ONE_WAVE ? 256 : 1024) void residual_norm_kernel(No
     const int k = 8 * (t + c * T), n = a.D - k;
     float wf[8];
     unpack8(factor(w, a.w, c), wf);
+    // (the row's factor r leaves the codes alone and goes into the scale: one
+    // rounding less a code)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[c][i] *= r * wf[i];
-    if (a.z) store8_bf16(a.z + row * a.ldz + k, n, h[c]);
+    for (int i = 0; i < 8; ++i) h[c][i] *= wf[i];
+    if (a.z) {
+      float z[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = h[c][i] * r;
+      store8_bf16(a.z + row * a.ldz + k, n, z);
+    }
     if (a.zq) {  // 16 consecutive lanes hold one group
       float s;
-      const v2u q = encode_group(h[c], &s);
+      const v2u q = encode_group(h[c], &s, r);
       if ((t & 15) == 0 && n > 0) a.sz[row * G + k / kGroup] = s;
       store8_codes(a.zq + row * a.ldq + k, n, q);
     }
