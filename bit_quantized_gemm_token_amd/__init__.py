@@ -1,7 +1,10 @@
 """Small-M 8-bit quantized linear-layer GEMM for MI355X (gfx950).
 
     Y[M, N] = dequant(Xq) . dequant(Wq)^T,  1 <= M <= 32,
-    formats FP8_Dynamic, W8A8_INT8 and Block_FP8.
+    formats FP8_Dynamic, W8A8_INT8 and Block_FP8;
+
+and the operators of a Block_FP8 layer at any token count: block_gemm,
+grouped_gemm, residual_norm and block_quantize.
 
 Python face of the C-ABI in include/w8gemm.h (libw8gemm.so, built in-tree).
 This module only marshals arguments: it takes torch tensors for device memory
