@@ -73,16 +73,20 @@ def _shape(t, rows, cols, name):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
 
 
-# (empty_strided and empty_like cost the host about half of what empty does)
-def _dense(rows, cols, dtype, device):
-    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+# Outputs that the caller did not give: the tensor, its pointer and row stride,
+# which need no checks.  (empty_strided costs the host about half of what empty
+# does.)
+def _new(rows, cols, dtype, device):
+    t = torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+    return t, t.data_ptr(), cols
 
 
-def _aligned_codes(M, K, device):
+def _new_codes(M, K, device):
     """Codes [M, K] whose row stride the GEMMs take (a multiple of 16)."""
-    if K % 16 == 0:
-        return torch.empty_strided((M, K), (K, 1), dtype=_CODES, device=device)
-    return _dense(M, (K + 15) // 16 * 16, _CODES, device)[:, :K]
+    ld = (K + 15) // 16 * 16
+    t = torch.empty_strided((M, ld), (ld, 1), dtype=_CODES, device=device)
+    p = t.data_ptr()
+    return (t if ld == K else t[:, :K]), p, ld
 
 
 # The current stream's handle without building a Stream object for it (2 us of
@@ -114,13 +118,14 @@ def block_quantize(x, gate=None, xq=None, sx=None, stream=None):
         gp, ldg = _rows(gate, "gate", _BF16)
         _shape(gate, M, K, "gate")
     if xq is None:
-        xq = _aligned_codes(M, K, x.device)
+        xq, qp, ldq = _new_codes(M, K, x.device)
     else:
         _shape(xq, M, K, "xq")
-    qp, ldq = _codes(xq, "xq")
+        qp, ldq = _codes(xq, "xq")
     if sx is None:
-        sx = _dense(M, _groups(K), _F32, x.device)
-    sp = _flat(sx, "sx", _F32, M * _groups(K))
+        sx, sp, _ = _new(M, _groups(K), _F32, x.device)
+    else:
+        sp = _flat(sx, "sx", _F32, M * _groups(K))
     _check(_lib.w8_block_quantize(M, K, xp, ldx, gp, ldg, qp, ldq, sp, _on(stream, x.device)))
     return xq, sx
 
@@ -160,27 +165,32 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, scale=1.0, e
             gp, ldg = _rows(gate, "gate", _BF16)
             _shape(gate, M, D, "gate")
     if h is None:
-        h = torch.empty_like(residual)
+        h, hp, ldh = _new(M, D, residual.dtype, y.device)
     else:
         _shape(h, M, D, "h")
-    hp, ldh = _rows(h, "h", residual.dtype)
+        hp, ldh = _rows(h, "h", residual.dtype)
     zp = qp = sp = None
     ldz = ldq = 0
     if quantize:
-        zq, sz = out if out is not None else (
-            _aligned_codes(M, D, y.device), _dense(M, _groups(D), _F32, y.device))
-        _shape(zq, M, D, "zq")
-        qp, ldq = _codes(zq, "zq")
-        sp = _flat(sz, "sz", _F32, M * _groups(D))
+        if out is None:
+            zq, qp, ldq = _new_codes(M, D, y.device)
+            sz, sp, _ = _new(M, _groups(D), _F32, y.device)
+        else:
+            zq, sz = out
+            _shape(zq, M, D, "zq")
+            qp, ldq = _codes(zq, "zq")
+            sp = _flat(sz, "sz", _F32, M * _groups(D))
         result = h, zq, sz
         if with_z:
-            z = torch.empty_like(y)
-            zp, ldz = _rows(z, "z", _BF16)
+            z, zp, ldz = _new(M, D, _BF16, y.device)
             result = h, zq, sz, z
     else:
-        z = out if out is not None else torch.empty_like(y)
-        _shape(z, M, D, "out")
-        zp, ldz = _rows(z, "out", _BF16)
+        if out is None:
+            z, zp, ldz = _new(M, D, _BF16, y.device)
+        else:
+            z = out
+            _shape(z, M, D, "out")
+            zp, ldz = _rows(z, "out", _BF16)
         result = h, z
     _check(_lib.w8_residual_norm(M, D, yp, ldy, rp, ldr, residual.dtype == _F32, pp, gp, ldg,
                                  scale, wp, eps, hp, ldh, zp, ldz, qp, ldq, sp,
@@ -216,10 +226,10 @@ def block_gemm(xq, sx, wq, sw, y=None, workspace=None, stream=None):
     G = _groups(K)
     sxp, swp = _flat(sx, "sx", _F32, M * G), _flat(sw, "sw", _F32, _groups(N) * G)
     if y is None:
-        y = _dense(M, N, _BF16, xq.device)
+        y, yp, ldy = _new(M, N, _BF16, xq.device)
     else:
         _shape(y, M, N, "y")
-    yp, ldy = _rows(y, "y", _BF16)
+        yp, ldy = _rows(y, "y", _BF16)
     if workspace is None:
         workspace = _default_workspace(xq.device)
     s = _on(stream, xq.device)
@@ -274,10 +284,10 @@ def grouped_gemm(xq, sx, offsets, wq, sw, rows=None, y=None, stream=None):
     n_rows = T if rows is None else rows.numel()
     rwp = None if rows is None else _flat(rows, "rows", _I32, n_rows)
     if y is None:
-        y = _dense(n_rows, N, _BF16, xq.device)
+        y, yp, ldy = _new(n_rows, N, _BF16, xq.device)
     else:
         _shape(y, n_rows, N, "y")
-    yp, ldy = _rows(y, "y", _BF16)
+        yp, ldy = _rows(y, "y", _BF16)
     _check(_lib.w8_grouped_gemm(E, T, N, K, xp, ldq, sxp, op, rwp, n_rows, wp, ldw, w_stride,
                                 swp, per, yp, ldy, _on(stream, xq.device)))
     return y
