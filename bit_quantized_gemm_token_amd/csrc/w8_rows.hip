@@ -59,7 +59,7 @@ __device__ __forceinline__ void unpack8(v4u v, float* f) {
 // Eight values of a row of D from element k on, 16 bytes a load at the
 // elements' own alignment.  Past D - 8 the row's last eight are loaded, so that
 // no load waits for a condition, and trim8() moves them into place (a load for
-// each element of a short chunk took 2235 x 1871 from 13 to 20 us).
+// each element of a short chunk took 2235 x 1871 from 12 to 20 us).
 __device__ __forceinline__ v4u load8_bf16(const uint16_t* row, int k, int D) {
   v4u v;
   __builtin_memcpy(&v, row + min(k, D - 8), 16);
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(kQThreads) void block_quantize_kernel(BlockQuantArg
 // chunks of eight values a lane, kept in registers between the two norms, so
 // that every input is read once.  Sums of squares are fp32, in a fixed order.
 // Bound by HBM on many rows (8192 x 5120, fp32 residual, post norm, gate rows:
-// 115 us, 5.1 TB/s) and on one by its chain of load, sum, sum and store (1 x
+// 111 us, 5.3 TB/s) and on one by its chain of load, sum, sum and store (1 x
 // 7168 to codes: 3.9 us).
 template <bool ONE_WAVE>
 __device__ __forceinline__ float row_sum(float v, float* red) {
@@ -402,12 +402,13 @@ hipError_t launch_block_quantize(BlockQuantArgs a, hipStream_t s) {
 }
 
 hipError_t launch_residual_norm(const NormArgs& a, hipStream_t s) {
-  // One chunk a lane has the shortest chain of a single row (1 x 7168: 4.1 us,
-  // four chunks 5.3) and the most loads in flight on fp32 residuals (8192 x
-  // 5120: 115 us, two chunks 124, four 160); many long bf16 rows move too few
-  // bytes a lane that way (8192 x 5120: 65.6 us, two chunks 58.1).
+  // One chunk a lane has the shortest chain of a single row (1 x 7168: 4.0 us,
+  // two chunks 4.2, four 5.5) and the most loads in flight on fp32 residuals
+  // (8192 x 5120: 111.0 us, 112.1, 122.9); many long bf16 rows move too few
+  // bytes a lane that way (8192 x 5120: 63.1 us, 57.2, 63.6; 8192 x 2048: 27.3,
+  // 25.9, 30.6).
   if (a.D <= 512) return launch_norm<true, 1>(a, s);
-  if (a.D <= 8192 && (a.residual_fp32 || a.M < 512 || a.D <= 4096))
+  if (a.D <= 8192 && (a.residual_fp32 || a.M < 512 || a.D < 2048))
     return launch_norm<false, 1>(a, s);
   if (a.D <= 16384) return launch_norm<false, 2>(a, s);
   return launch_norm<false, 4>(a, s);
