@@ -171,6 +171,16 @@ def test_grouped(w8, counts, N, K, T):
         c.check(w8.grouped_gemm(xq, sx, off, experts, sw, rows=c.drows))
 
 
+@pytest.mark.parametrize("counts,N,K", [
+    ([1100, 1030, 1279, 991], 1280, 144),         # one round, all of it in halves
+    ([3400, 3329, 3300, 3571], 1280, 128),        # a full round and a rest in quarters
+    ([2600, 2000, 2305, 1, 0, 2561], 1800, 272),  # a full round and a rest in halves
+    ([600, 0, 0, 0, 0, 0, 0, 0], 2560, 256)])     # one round, all of it in quarters
+def test_grouped_last_round_in_pieces(w8, counts, N, K):
+    c = Grouped(counts, N, K, 600)
+    c.check(w8.grouped_gemm(*c.dev, rows=c.drows))
+
+
 def test_grouped_equals_dense_per_expert(w8):
     """Bit for bit: with four groups K is not split, and every tile shape adds
     the groups in the same order."""

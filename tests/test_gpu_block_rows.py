@@ -144,6 +144,23 @@ def test_residual_norm(w8, M, D, rdtype, post, gate):
     assert torch.equal(zq3.view(torch.uint8), zq.view(torch.uint8))
 
 
+@pytest.mark.parametrize("M,D", [(3, 8), (5, 9), (2, 15), (600, 2057), (530, 5003), (3, 9001),
+                                 (2, 20007)])
+@pytest.mark.parametrize("rdtype,post,gate", [("bf16", False, "none"), ("fp32", True, "token")])
+def test_residual_norm_short_last_chunk(w8, M, D, rdtype, post, gate):
+    test_residual_norm(w8, M, D, rdtype, post, gate)
+
+
+@pytest.mark.parametrize("D", [520, 1003, 2051])
+def test_in_place_without_post_norm(w8, D):
+    """No barrier stands between a row's loads and the stores of h over them."""
+    y, r, w, kw, h, z, dh, dz = norm_case(700, D, "fp32", False, "none")
+    gh, gz = w8.residual_norm(y, r, w, scale=0.7, eps=1e-6, h=r, **kw)
+    assert gh is r
+    near(gh, h, dh + 2.0 ** -24 * 1.01 * np.abs(h) + 1e-38, "h")
+    near(gz, z, dz + 2.0 ** -8 * 1.01 * np.abs(z) + 1e-38, "z")
+
+
 def test_in_place_and_strides(w8):
     """h written over the residual, rows inside wider buffers whose other
     columns stay, odd strides."""
