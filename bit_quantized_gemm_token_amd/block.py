@@ -100,6 +100,17 @@ def _on(stream, device):
     return _stream(stream, device)
 
 
+# The package's default workspaces, by device index.
+_shared = {}
+
+
+def _shared_workspace(device):
+    w = _shared.get(device.index)
+    if w is None:
+        w = _shared[device.index] = _default_workspace(device)
+    return w
+
+
 def block_quantize(x, gate=None, xq=None, sx=None, stream=None):
     """E4M3FN codes [M, K] and fp32 scales [M, ceil(K/128)] of bf16 x [M, K],
     or with gate (bf16 [M, K]) of silu(gate) * x: the gated activation in
@@ -231,7 +242,7 @@ def block_gemm(xq, sx, wq, sw, y=None, workspace=None, stream=None):
         _shape(y, M, N, "y")
         yp, ldy = _rows(y, "y", _BF16)
     if workspace is None:
-        workspace = _default_workspace(xq.device)
+        workspace = _shared_workspace(xq.device)
     s = _on(stream, xq.device)
     # what the workspace holds is enough for most calls: its size is asked for
     # only when the library says it is not

@@ -8,6 +8,15 @@
 
 namespace w8 {
 
+// One kernel of one argument block, without the call configuration that the
+// launch syntax pushes and pops (0.1 us of a call on the host).
+template <class Args>
+inline hipError_t launch_kernel(void (*kernel)(Args), dim3 grid, dim3 block, size_t lds,
+                                hipStream_t s, Args args) {
+  void* list[] = {&args};
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, list, lds, s);
+}
+
 // ------------------------------------------------------------ row kernels --
 struct BlockQuantArgs {
   const uint16_t* x;     // bf16 [M, K]

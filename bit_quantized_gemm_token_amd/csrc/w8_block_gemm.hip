@@ -879,8 +879,7 @@ hipError_t launch(unsigned wgs, const BlockGemmArgs& a, hipStream_t s) {
   static const hipError_t lds = hipFuncSetAttribute(
       reinterpret_cast<const void*>(K), hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
   if (lds != hipSuccess) return lds;
-  hipLaunchKernelGGL(K, dim3(wgs), dim3(T::THREADS), T::LDS, s, a);
-  return hipGetLastError();
+  return launch_kernel(K, dim3(wgs), dim3(T::THREADS), T::LDS, s, a);
 }
 
 template <class T>

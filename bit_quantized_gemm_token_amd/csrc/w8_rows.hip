@@ -377,8 +377,7 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
                                                 : residual_norm_kernel<ONE_WAVE, NC, false, true>
                       : a.residual_fp32 ? residual_norm_kernel<ONE_WAVE, NC, true, false>
                                         : residual_norm_kernel<ONE_WAVE, NC, false, false>;
-  hipLaunchKernelGGL(kernel, grid, block, 0, s, a);
-  return hipGetLastError();
+  return launch_kernel(kernel, grid, block, 0, s, a);
 }
 
 }  // namespace
@@ -394,11 +393,8 @@ hipError_t launch_block_quantize(BlockQuantArgs a, hipStream_t s) {
   }
   const long long blocks = ((long long)a.groups + kQThreads / 16 - 1) / (kQThreads / 16);
   const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20))), block(kQThreads);
-  if (a.gate)
-    hipLaunchKernelGGL(block_quantize_kernel<true>, grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL(block_quantize_kernel<false>, grid, block, 0, s, a);
-  return hipGetLastError();
+  return launch_kernel(a.gate ? block_quantize_kernel<true> : block_quantize_kernel<false>, grid,
+                       block, 0, s, a);
 }
 
 hipError_t launch_residual_norm(const NormArgs& a, hipStream_t s) {
