@@ -18,6 +18,7 @@
 // by the weights (7 us at a copy's rate), the hand-off of split K and the
 // start; 128 experts, top 8, of 1536 x 2048: 8 tokens 33.6 us, 4.8 TB/s, by the
 // weights' bytes; 4096 tokens 160 us, 1.3 PFLOP/s, as the dense tiles.
+#include <atomic>
 #include <climits>
 #include <type_traits>
 #include <utility>
@@ -875,10 +876,18 @@ typedef void (*Kernel)(BlockGemmArgs);
 
 template <class T, Kernel K>
 hipError_t launch(unsigned wgs, const BlockGemmArgs& a, hipStream_t s) {
-  // more than 64 KiB of LDS has to be asked for, once per kernel
-  static const hipError_t lds = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(K), hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
-  if (lds != hipSuccess) return lds;
+  // more than 64 KiB of LDS has to be asked for, once per kernel and device
+  // (the caller has checked that the device's number is below 64)
+  static std::atomic<unsigned long long> asked{0};
+  int device = 0;
+  hipError_t e = hipGetDevice(&device);
+  if (e != hipSuccess) return e;
+  if (!(asked.load(std::memory_order_relaxed) >> device & 1)) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(K),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
+    if (e != hipSuccess) return e;
+    asked.fetch_or(1ull << device, std::memory_order_relaxed);
+  }
   return launch_kernel(K, dim3(wgs), dim3(T::THREADS), T::LDS, s, a);
 }
 
