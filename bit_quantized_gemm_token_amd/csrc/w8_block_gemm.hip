@@ -26,40 +26,10 @@
 #include "w8_block.hpp"
 #include "w8_device.hpp"
 #include "w8_launch.hpp"
+#include "w8_lds.hpp"
 
 namespace w8 {
 namespace {
-
-// ------------------------------------------------------------ LDS traffic --
-// Direct-to-LDS loads: lane i's 16 (or 4) bytes go to LDS byte lds + 16 i (or
-// 4 i).  M0 carries the LDS address and needs one wait state before its use.
-// Written as assembly because the compiler, which cannot tell the stages of
-// the LDS buffer apart, would wait for every load in flight before each LDS
-// read; wait_stage() below does the waiting, and as volatile assembly the two
-// keep their order.
-// The address is a 64-bit one per lane, or a uniform base and a 32-bit offset
-// per lane.  The base is copied by a scalar move on the way: a load may not
-// read a scalar register within five wait states of a vector instruction's
-// write to it, which the compiler does not watch in assembly (and the move is
-// M0's wait state too).
-__device__ __forceinline__ void load_lds16(const uint8_t* p, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(p));
-}
-__device__ __forceinline__ void load_lds16(const uint8_t* base, unsigned off, unsigned lds) {
-  const uint8_t* copy;
-  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
-               : "=&s"(copy)
-               : "s"(lds), "v"(off), "s"(base));
-}
-__device__ __forceinline__ void load_lds4(const float* p, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(p));
-}
-// Waits until at most N of this wave's loads are in flight and its LDS reads
-// have returned, then for the workgroup's other waves.
-template <int N>
-__device__ __forceinline__ void wait_stage() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
-}
 
 // blockIdx -> work id such that each XCD (workgroups are dealt to the 8 XCDs
 // in turn) runs one contiguous range of ids and its L2 sees neighbours.
@@ -428,11 +398,13 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
       }
     };
     static_assert(P - P2 >= T::LOADS && P >= 2 * T::LOADS, "an interval deals all loads");
+    // (no late weight tiles here: there is no step before the first, and where
+    // K ends inside that one their offsets still point past the rows' ends)
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s) {
       advance(ks0 + s);
 #pragma unroll
-      for (int n = 0; n < T::LOADS; ++n)
+      for (int n = 0; n < T::PX + T::PW1; ++n)
         issue_one(n, lds0 + s * T::STAGE, lds0 + (s + 1) * T::STAGE);
     }
     interval(Yes{}, No{}, ks0, 0);
