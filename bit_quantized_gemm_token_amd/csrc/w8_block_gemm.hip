@@ -540,7 +540,9 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
     __builtin_amdgcn_s_waitcnt(0);
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __syncthreads();
-    int* flag = reinterpret_cast<int*>(smem);
+    // (past the output tile, which the first waves write below while others
+    // may not have read the flag yet)
+    int* flag = reinterpret_cast<int*>(smem + T::LDS - 16);
     if (threadIdx.x == 0) {
       const unsigned inc = 256u / (unsigned)a.split_k;
       const unsigned prev = __hip_atomic_fetch_add(a.counters + (long long)tile * kCounterWords,
@@ -585,7 +587,7 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
     // stores of each lane's own four would touch 16 rows at a time (all
     // outputs of a 256 x 256 round take 8500 clocks, the rate of the writes)
     constexpr int ROW = BN * 2 + 32;
-    static_assert(BM * ROW <= T::LDS, "the output tile fits where the stages were");
+    static_assert(BM * ROW <= T::LDS - 16, "the output tile fits where the stages were");
 #pragma unroll
     for (int j = 0; j < NM; ++j)
 #pragma unroll

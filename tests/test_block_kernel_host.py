@@ -80,6 +80,19 @@ def test_split(lib, tile, M, N, split_k):
     check(lib, tile, M, N, 1424, split_k=split_k, orders=ORDERS[::3])
 
 
+def test_split_flag_outlives_the_output_tile(lib):
+    """Wavefronts that run ahead after the split's hand-off must not overwrite
+    what the others have yet to read: with a tile whose first outputs are zero
+    (four weight rows of zeros) all outputs are still stored."""
+    c = inputs(130, 140, 1408)
+    c[2][:4] = 0
+    for tile in ("64x128", "128x128"):
+        for descending, late in ORDERS:
+            y, faults, text = host.run(lib, tile, *c, split_k=2, descending=descending, late=late)
+            assert faults == 0, text
+            assert_near(y, dequant_rows(*c[:2]), dequant_blocks(*c[2:]), tile)
+
+
 @pytest.mark.parametrize("K", range(16, 128, 16))
 @pytest.mark.parametrize("parts", [1, 2, 4])
 def test_single_short_step_reads_inside(lib, K, parts):
