@@ -299,6 +299,17 @@ class Workspace:
         return ctypes.c_void_p(buf.data_ptr()), buf.numel()
 
 
+def _weight_stride(ld, rows, K):
+    """Row stride of row-major weight codes.  The library takes a stride of 0
+    or less for a packed layout, so rows that share memory (expand()) are
+    refused; a single row's stride, which torch lets be anything, is K."""
+    if ld >= K:
+        return ld
+    if rows > 1:
+        raise ValueError(f"the weights' row stride must be at least K = {K}, got {ld}")
+    return K
+
+
 def _weights(f, wq):
     """(N, K, ldw, device tensor, layout) of row-major codes or a PackedWeight
     (ldw 0 for layout 1, -T for the K-segmented layouts)."""
@@ -309,7 +320,7 @@ def _weights(f, wq):
     if wq.element_size() != 1:
         raise TypeError("wq must hold 1-byte codes")
     N, wk = wq.shape
-    return N, wk, _row_major(wq, "wq") * wq.element_size(), wq, 0
+    return N, wk, _weight_stride(_row_major(wq, "wq"), N, wk), wq, 0
 
 
 def _gemm(entry, fmt, xq, sx, wq, sw, out, cfg, workspace, stream):
@@ -438,7 +449,8 @@ def _experts(f, wq):
     if wq.dim() != 3 or wq.element_size() != 1 or wq.stride(2) != 1:
         raise ValueError("wq must be [E, N, K] 1-byte codes with unit inner stride")
     E, N, K = wq.shape
-    return E, N, K, wq.stride(1), wq.stride(0), _dev_ptr(wq, "wq"), False
+    ldw = _weight_stride(wq.stride(1), N, K)
+    return E, N, K, ldw, wq.stride(0), _dev_ptr(wq, "wq"), False
 
 
 def moe_config(fmt, E, T, N, K, max_m=32, packed=False):

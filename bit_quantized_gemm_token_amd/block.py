@@ -232,6 +232,7 @@ def block_gemm(xq, sx, wq, sw, y=None, workspace=None, stream=None):
         N, wk, wp, ldw, packed = wq.N, wq.K, wq.data.data_ptr(), 0, 1
     else:
         (wp, ldw), (N, wk), packed = _codes(wq, "wq"), wq.shape, 0
+        ldw = _weight_stride(ldw, N, wk)
     if wk != K:
         raise ValueError(f"K mismatch: xq {tuple(xq.shape)} vs weights {(N, wk)}")
     G = _groups(K)
@@ -284,7 +285,7 @@ def grouped_gemm(xq, sx, offsets, wq, sw, rows=None, y=None, stream=None):
         if wq.dim() != 3 or wq.element_size() != 1 or wq.stride(2) != 1:
             raise ValueError("wq must be [E, N, K] 1-byte codes with unit inner stride")
         E, N, wk = wq.shape
-        wp, ldw, w_stride = wq.data_ptr(), wq.stride(1), wq.stride(0)
+        wp, ldw, w_stride = wq.data_ptr(), _weight_stride(wq.stride(1), N, wk), wq.stride(0)
     if wk != K:
         raise ValueError(f"K mismatch: xq {tuple(xq.shape)} vs experts' K {wk}")
     G = _groups(K)
@@ -306,4 +307,4 @@ def grouped_gemm(xq, sx, offsets, wq, sw, rows=None, y=None, stream=None):
 
 # (the package's own helpers; __init__ imports this module after defining them)
 from . import (PackedExperts, PackedWeight, _check, _default_workspace, _layout, _lib,  # noqa: E402
-               _stream)
+               _stream, _weight_stride)
