@@ -70,10 +70,22 @@ def _fmt(fmt):
     return int(fmt)
 
 
-def _stream(stream, device):
+# The current stream's handle without building a Stream object for it (2 us of
+# a call), where this torch has the function.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _handle(stream, device):
+    """The handle of `stream` (a torch stream or a handle; None: the current stream)."""
     if stream is None:
+        if _raw_stream is not None and device.index is not None:
+            return _raw_stream(device.index)
         stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _stream(stream, device):
+    return ctypes.c_void_p(_handle(stream, device))
 
 
 def _dev_ptr(t, name, dtype=None):
@@ -248,7 +260,8 @@ class Workspace:
     Zero-filled when (re)allocated; the GEMM leaves its arrival counters at
     multiples of 256 after each call (which is all a call needs of them), so
     one Workspace can serve any sequence of calls on one stream
-    (calls that overlap on several streams race).
+    (calls that overlap on several streams race: each stream needs its own,
+    as calls without a workspace argument have it).
 
     Under HIP graph capture the workspace cannot grow: the fill would be
     recorded into the graph and a buffer given back to the allocator could
@@ -256,7 +269,11 @@ class Workspace:
     beforehand (Workspace(device, nbytes), or call reserve() before the
     capture).  A buffer that a larger one replaces is kept alive for the
     Workspace's lifetime, because a graph captured earlier may still use it;
-    release_retired() drops those once no such graph remains.
+    release_retired() drops those once no such graph remains.  A call that is
+    captured without a workspace argument on a stream without one of its own
+    takes the largest that eager calls on the device have sized; replays must
+    then not overlap the calls of that stream, so a graph replayed beside
+    other work needs a Workspace of its own.
     """
 
     def __init__(self, device=None, nbytes=0):
@@ -337,7 +354,7 @@ def _gemm(entry, fmt, xq, sx, wq, sw, out, cfg, workspace, stream):
     _check_scales(sw, _weight_scales(f, N, K), "sw")
     _check_out(out, M, N, "out")
     if workspace is None:
-        workspace = _default_workspace(xq.device)
+        workspace = _default_workspace(xq.device, stream)
     ws_ptr, ws_bytes = workspace.for_call(f, M, N, K, cfg, packed, "gemm", stream)
     _check(entry(f, M, N, K, _dev_ptr(xq, "xq"), ldq, _dev_ptr(sx, "sx", torch.float32),
                  _dev_ptr(wptr, "wq"), ldw, _dev_ptr(sw, "sw", torch.float32),
@@ -346,14 +363,27 @@ def _gemm(entry, fmt, xq, sx, wq, sw, out, cfg, workspace, stream):
     return out
 
 
+# The package's own workspaces, for calls that are given none: one for each
+# (device index, stream handle), because calls that share one must not overlap.
 _workspaces = {}
 
 
-def _default_workspace(device):
-    key = str(device)
-    if key not in _workspaces:
-        _workspaces[key] = Workspace(device)
-    return _workspaces[key]
+def _default_workspace(device, stream=None):
+    return _workspace_of(device, _handle(stream, device))
+
+
+def _workspace_of(device, handle):
+    w = _workspaces.get((device.index, handle))
+    if w is None:
+        if torch.cuda.is_current_stream_capturing():
+            # nothing may be allocated here, and a graph is replayed on any
+            # stream: the largest that eager calls on this device have sized
+            held = [v for (index, _), v in _workspaces.items()
+                    if index == device.index and v.buf is not None]
+            if held:
+                return max(held, key=lambda v: v.buf.numel())
+        w = _workspaces.setdefault((device.index, handle), Workspace(device))
+    return w
 
 
 def gemm_w8a8(fmt, xq, sx, wq, sw, cfg=None, y=None, workspace=None, stream=None):
@@ -409,7 +439,7 @@ def linear(fmt, x, wq, sw, cfg=None, y=None, workspace=None, stream=None, fused=
     _check_out(y, M, N, "y")
     _check_scales(sw, _weight_scales(f, N, K), "sw")
     if workspace is None:
-        workspace = _default_workspace(x.device)
+        workspace = _default_workspace(x.device, stream)
     ws_ptr, ws_bytes = workspace.for_call(f, M, N, K, cfg, packed, "linear", stream)
     _check(_lib.w8_linear(f, M, N, K, _dev_ptr(x, "x"), ldx, _dev_ptr(wptr, "wq"), ldw,
                           _dev_ptr(sw, "sw", torch.float32), _dev_ptr(y, "y"), _row_major(y, "y"),
@@ -522,7 +552,7 @@ def moe_gemm(fmt, xq, sx, offsets, rows, wq, sw, max_m=32, cfg=None, y=None, wor
     elif y.shape[0] < rows.numel() or y.shape[1] != N:
         raise ValueError(f"y must be [{rows.numel()}, {N}]")
     if workspace is None:
-        workspace = _default_workspace(xq.device)
+        workspace = _default_workspace(xq.device, stream)
     need = moe_workspace_size(f, E, T, N, K, max_m, cfg, packed)
     ws_ptr, ws_bytes = (None, 0)
     if need:
@@ -567,7 +597,7 @@ def moe_linear(fmt, x, offsets, rows, wq, sw, max_m=32, cfg=None, y=None, worksp
     if cfg is None:
         cfg = moe_linear_config(f, E, T, N, K, max_m, packed)[0]
     if workspace is None:
-        workspace = _default_workspace(x.device)
+        workspace = _default_workspace(x.device, stream)
     need = moe_workspace_size(f, E, T, N, K, max_m, cfg, packed)
     ws_ptr, ws_bytes = (None, 0)
     if need:

@@ -89,28 +89,6 @@ def _new_codes(M, K, device):
     return (t if ld == K else t[:, :K]), p, ld
 
 
-# The current stream's handle without building a Stream object for it (2 us of
-# a call), where this torch has the function.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _on(stream, device):
-    if stream is None and _raw_stream is not None and device.index is not None:
-        return _raw_stream(device.index)
-    return _stream(stream, device)
-
-
-# The package's default workspaces, by device index.
-_shared = {}
-
-
-def _shared_workspace(device):
-    w = _shared.get(device.index)
-    if w is None:
-        w = _shared[device.index] = _default_workspace(device)
-    return w
-
-
 def block_quantize(x, gate=None, xq=None, sx=None, stream=None):
     """E4M3FN codes [M, K] and fp32 scales [M, ceil(K/128)] of bf16 x [M, K],
     or with gate (bf16 [M, K]) of silu(gate) * x: the gated activation in
@@ -137,7 +115,7 @@ def block_quantize(x, gate=None, xq=None, sx=None, stream=None):
         sx, sp, _ = _new(M, _groups(K), _F32, x.device)
     else:
         sp = _flat(sx, "sx", _F32, M * _groups(K))
-    _check(_lib.w8_block_quantize(M, K, xp, ldx, gp, ldg, qp, ldq, sp, _on(stream, x.device)))
+    _check(_lib.w8_block_quantize(M, K, xp, ldx, gp, ldg, qp, ldq, sp, _handle(stream, x.device)))
     return xq, sx
 
 
@@ -205,7 +183,7 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, scale=1.0, e
         result = h, z
     _check(_lib.w8_residual_norm(M, D, yp, ldy, rp, ldr, residual.dtype == _F32, pp, gp, ldg,
                                  scale, wp, eps, hp, ldh, zp, ldz, qp, ldq, sp,
-                                 _on(stream, y.device)))
+                                 _handle(stream, y.device)))
     return result
 
 
@@ -223,6 +201,10 @@ def block_gemm(xq, sx, wq, sw, y=None, workspace=None, stream=None):
     residual_norm, quantize_act); wq, sw: codes [N, K] or a PackedWeight of
     layout 1, scales [ceil(N/128), ceil(K/128)] (quantize_weight).  K a
     multiple of 16 (packed: of 128); its last group may be shorter.
+
+    workspace: a Workspace of the stream's own (calls that overlap must not
+    share one), for shapes that block_gemm_workspace_size gives bytes for;
+    None takes the package's for the stream.
     """
     xp, ldq = _codes(xq, "xq")
     M, K = xq.shape
@@ -242,9 +224,9 @@ def block_gemm(xq, sx, wq, sw, y=None, workspace=None, stream=None):
     else:
         _shape(y, M, N, "y")
         yp, ldy = _rows(y, "y", _BF16)
+    s = _handle(stream, xq.device)
     if workspace is None:
-        workspace = _shared_workspace(xq.device)
-    s = _on(stream, xq.device)
+        workspace = _workspace_of(xq.device, s)
     # what the workspace holds is enough for most calls: its size is asked for
     # only when the library says it is not
     buf = workspace.buf
@@ -301,10 +283,10 @@ def grouped_gemm(xq, sx, offsets, wq, sw, rows=None, y=None, stream=None):
         _shape(y, n_rows, N, "y")
         yp, ldy = _rows(y, "y", _BF16)
     _check(_lib.w8_grouped_gemm(E, T, N, K, xp, ldq, sxp, op, rwp, n_rows, wp, ldw, w_stride,
-                                swp, per, yp, ldy, _on(stream, xq.device)))
+                                swp, per, yp, ldy, _handle(stream, xq.device)))
     return y
 
 
 # (the package's own helpers; __init__ imports this module after defining them)
-from . import (PackedExperts, PackedWeight, _check, _default_workspace, _layout, _lib,  # noqa: E402
-               _stream, _weight_stride)
+from . import (PackedExperts, PackedWeight, _check, _handle, _layout, _lib,  # noqa: E402
+               _weight_stride, _workspace_of)
