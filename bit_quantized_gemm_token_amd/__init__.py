@@ -6,6 +6,11 @@
 and the operators of a Block_FP8 layer at any token count: block_gemm,
 grouped_gemm, residual_norm and block_quantize.
 
+Kernels run on torch's current stream, or on a call's `stream` (a torch stream
+or a handle).  There the caller orders the stream after whatever writes the
+call's inputs, and keeps or records them (Tensor.record_stream) until it has
+read them; outputs that the call makes are allocated for that stream.
+
 Python face of the C-ABI in include/w8gemm.h (libw8gemm.so, built in-tree).
 This module only marshals arguments: it takes torch tensors for device memory
 and the current HIP stream, checks dtypes and layouts, and calls the library;
@@ -88,6 +93,31 @@ def _stream(stream, device):
     return ctypes.c_void_p(_handle(stream, device))
 
 
+def _on_stream(stream, device):
+    """Makes `stream` (a torch stream or a handle) the current one."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """An output for a kernel on `stream` (None: the current one)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _allocate(stream, device, lambda: torch.empty(shape, dtype=dtype, device=device))
+
+
+def _allocate(stream, device, factory):
+    """factory()'s tensor for a kernel on `stream`: memory of that stream's, because
+    another's may still be in use by what was queued there before, and kept for
+    what the current stream does with it before the tensor goes."""
+    current = torch.cuda.current_stream(device)
+    with _on_stream(stream, device):
+        t = factory()
+    t.record_stream(current)
+    return t
+
+
 def _dev_ptr(t, name, dtype=None):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
@@ -157,10 +187,10 @@ def quantize_act(fmt, x, xq=None, sx=None, stream=None):
     ldx = _row_major(x, "x")
     M, K = x.shape
     if xq is None:
-        xq = torch.empty((M, K), dtype=_codes_dtype(f), device=x.device)
+        xq = _empty((M, K), _codes_dtype(f), x.device, stream)
     if sx is None:
         shape = (M, K // GROUP) if f == FORMATS["Block_FP8"] else (M,)
-        sx = torch.empty(shape, dtype=torch.float32, device=x.device)
+        sx = _empty(shape, torch.float32, x.device, stream)
     _check_out(xq, M, K, "xq")
     if xq.element_size() != 1:
         raise TypeError("xq must hold 1-byte codes")
@@ -181,11 +211,11 @@ def quantize_weight(fmt, w, wq=None, sw=None, stream=None):
     ldw = _row_major(w, "w")
     N, K = w.shape
     if wq is None:
-        wq = torch.empty((N, K), dtype=torch.float8_e4m3fn, device=w.device)
+        wq = _empty((N, K), torch.float8_e4m3fn, w.device, stream)
     if sw is None:
         shape = ((N + GROUP - 1) // GROUP, (K + GROUP - 1) // GROUP) \
             if f == FORMATS["Block_FP8"] else (N,)
-        sw = torch.empty(shape, dtype=torch.float32, device=w.device)
+        sw = _empty(shape, torch.float32, w.device, stream)
     ldq = _row_major(wq, "wq")
     _check(_lib.w8_quantize_weight(f, N, K, _dev_ptr(w, "w", torch.float32), ldw,
                                    _dev_ptr(wq, "wq"), ldq * wq.element_size(),
@@ -240,7 +270,7 @@ def pack_weight(fmt, wq, stream=None, layout=1):
     lay = _layout(layout)
     ldw = _row_major(wq, "wq") * wq.element_size()
     N, K = wq.shape
-    out = torch.empty(packed_weight_size(f, N, K, lay), dtype=torch.uint8, device=wq.device)
+    out = _empty(packed_weight_size(f, N, K, lay), torch.uint8, wq.device, stream)
     _check(_lib.w8_pack_weight(f, N, K, _dev_ptr(wq, "wq"), ldw, _dev_ptr(out, "out"), lay,
                                _stream(stream, wq.device)))
     return PackedWeight(f, N, K, out, lay)
@@ -295,9 +325,7 @@ class Workspace:
         if self.buf is not None:
             self._retired.append(self.buf)
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        if not isinstance(s, torch.cuda.Stream):
-            s = torch.cuda.ExternalStream(int(s), device=self.device)
-        with torch.cuda.stream(s):
+        with _on_stream(s, self.device):
             buf = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=self.device)
             buf.zero_()
         self.buf = buf
@@ -395,7 +423,7 @@ def gemm_w8a8(fmt, xq, sx, wq, sw, cfg=None, y=None, workspace=None, stream=None
     """
     M, N = xq.shape[0], wq.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+        y = _empty((M, N), torch.bfloat16, xq.device, stream)
     elif y.dtype != torch.bfloat16:
         raise TypeError("y must be bfloat16")
     return _gemm(_lib.w8_gemm_w8a8, fmt, xq, sx, wq, sw, y, cfg, workspace, stream)
@@ -406,7 +434,7 @@ def gemm_w8a8_acc(fmt, xq, sx, wq, sw, cfg=None, out=None, workspace=None, strea
     M, N = xq.shape[0], wq.shape[0]
     dt = torch.int32 if _fmt(fmt) == FORMATS["W8A8_INT8"] else torch.float32
     if out is None:
-        out = torch.empty((M, N), dtype=dt, device=xq.device)
+        out = _empty((M, N), dt, xq.device, stream)
     elif out.dtype != dt:
         raise TypeError(f"out must be {dt}")
     return _gemm(_lib.w8_gemm_w8a8_acc, fmt, xq, sx, wq, sw, out, cfg, workspace, stream)
@@ -433,7 +461,7 @@ def linear(fmt, x, wq, sw, cfg=None, y=None, workspace=None, stream=None, fused=
     if wk != K:
         raise ValueError(f"K mismatch: x {tuple(x.shape)} vs weights {(N, wk)}")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _empty((M, N), torch.bfloat16, x.device, stream)
     elif y.dtype != torch.bfloat16:
         raise TypeError("y must be bfloat16")
     _check_out(y, M, N, "y")
@@ -462,7 +490,7 @@ def pack_experts(fmt, wq, stream=None):
     """Pack row-major expert codes [E, N, K] (offline, on the GPU)."""
     f = _fmt(fmt)
     E, N, K = wq.shape
-    out = torch.empty((E, packed_weight_size(f, N, K)), dtype=torch.uint8, device=wq.device)
+    out = _empty((E, packed_weight_size(f, N, K)), torch.uint8, wq.device, stream)
     for e in range(E):
         w = wq[e]
         _check(_lib.w8_pack_weight(f, N, K, _dev_ptr(w, "wq"), _row_major(w, "wq"),
@@ -546,7 +574,7 @@ def moe_gemm(fmt, xq, sx, offsets, rows, wq, sw, max_m=32, cfg=None, y=None, wor
         raise ValueError(f"sw must be a contiguous [E, {_weight_scales(f, N, K)}] tensor")
     _check_scales(sx, _act_scales(f, T, K), "sx")
     if y is None:
-        y = torch.empty((rows.numel(), N), dtype=torch.bfloat16, device=xq.device)
+        y = _empty((rows.numel(), N), torch.bfloat16, xq.device, stream)
     elif y.dtype != torch.bfloat16:
         raise TypeError("y must be bfloat16")
     elif y.shape[0] < rows.numel() or y.shape[1] != N:
@@ -589,7 +617,7 @@ def moe_linear(fmt, x, offsets, rows, wq, sw, max_m=32, cfg=None, y=None, worksp
     if sw.shape[0] != E or not sw.is_contiguous() or sw.numel() != E * _weight_scales(f, N, K):
         raise ValueError(f"sw must be a contiguous [E, {_weight_scales(f, N, K)}] tensor")
     if y is None:
-        y = torch.empty((rows.numel(), N), dtype=torch.bfloat16, device=x.device)
+        y = _empty((rows.numel(), N), torch.bfloat16, x.device, stream)
     elif y.dtype != torch.bfloat16:
         raise TypeError("y must be bfloat16")
     elif y.shape[0] < rows.numel() or y.shape[1] != N:

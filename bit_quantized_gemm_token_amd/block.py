@@ -74,18 +74,19 @@ def _shape(t, rows, cols, name):
 
 
 # Outputs that the caller did not give: the tensor, its pointer and row stride,
-# which need no checks.  (empty_strided costs the host about half of what empty
-# does.)
-def _new(rows, cols, dtype, device):
-    t = torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+# which need no checks; allocated for the stream that the kernel runs on.
+# (empty_strided costs the host about half of what empty does.)
+def _new(rows, cols, dtype, device, stream):
+    if stream is not None:
+        t = _allocate(stream, device, lambda: _new(rows, cols, dtype, device, None)[0])
+    else:
+        t = torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
     return t, t.data_ptr(), cols
 
 
-def _new_codes(M, K, device):
+def _new_codes(M, K, device, stream):
     """Codes [M, K] whose row stride the GEMMs take (a multiple of 16)."""
-    ld = (K + 15) // 16 * 16
-    t = torch.empty_strided((M, ld), (ld, 1), dtype=_CODES, device=device)
-    p = t.data_ptr()
+    t, p, ld = _new(M, (K + 15) // 16 * 16, _CODES, device, stream)
     return (t if ld == K else t[:, :K]), p, ld
 
 
@@ -107,12 +108,12 @@ def block_quantize(x, gate=None, xq=None, sx=None, stream=None):
         gp, ldg = _rows(gate, "gate", _BF16)
         _shape(gate, M, K, "gate")
     if xq is None:
-        xq, qp, ldq = _new_codes(M, K, x.device)
+        xq, qp, ldq = _new_codes(M, K, x.device, stream)
     else:
         _shape(xq, M, K, "xq")
         qp, ldq = _codes(xq, "xq")
     if sx is None:
-        sx, sp, _ = _new(M, _groups(K), _F32, x.device)
+        sx, sp, _ = _new(M, _groups(K), _F32, x.device, stream)
     else:
         sp = _flat(sx, "sx", _F32, M * _groups(K))
     _check(_lib.w8_block_quantize(M, K, xp, ldx, gp, ldg, qp, ldq, sp, _handle(stream, x.device)))
@@ -154,7 +155,7 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, scale=1.0, e
             gp, ldg = _rows(gate, "gate", _BF16)
             _shape(gate, M, D, "gate")
     if h is None:
-        h, hp, ldh = _new(M, D, residual.dtype, y.device)
+        h, hp, ldh = _new(M, D, residual.dtype, y.device, stream)
     else:
         _shape(h, M, D, "h")
         hp, ldh = _rows(h, "h", residual.dtype)
@@ -162,8 +163,8 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, scale=1.0, e
     ldz = ldq = 0
     if quantize:
         if out is None:
-            zq, qp, ldq = _new_codes(M, D, y.device)
-            sz, sp, _ = _new(M, _groups(D), _F32, y.device)
+            zq, qp, ldq = _new_codes(M, D, y.device, stream)
+            sz, sp, _ = _new(M, _groups(D), _F32, y.device, stream)
         else:
             zq, sz = out
             _shape(zq, M, D, "zq")
@@ -171,11 +172,11 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, scale=1.0, e
             sp = _flat(sz, "sz", _F32, M * _groups(D))
         result = h, zq, sz
         if with_z:
-            z, zp, ldz = _new(M, D, _BF16, y.device)
+            z, zp, ldz = _new(M, D, _BF16, y.device, stream)
             result = h, zq, sz, z
     else:
         if out is None:
-            z, zp, ldz = _new(M, D, _BF16, y.device)
+            z, zp, ldz = _new(M, D, _BF16, y.device, stream)
         else:
             z = out
             _shape(z, M, D, "out")
@@ -220,7 +221,7 @@ def block_gemm(xq, sx, wq, sw, y=None, workspace=None, stream=None):
     G = _groups(K)
     sxp, swp = _flat(sx, "sx", _F32, M * G), _flat(sw, "sw", _F32, _groups(N) * G)
     if y is None:
-        y, yp, ldy = _new(M, N, _BF16, xq.device)
+        y, yp, ldy = _new(M, N, _BF16, xq.device, stream)
     else:
         _shape(y, M, N, "y")
         yp, ldy = _rows(y, "y", _BF16)
@@ -278,7 +279,7 @@ def grouped_gemm(xq, sx, offsets, wq, sw, rows=None, y=None, stream=None):
     n_rows = T if rows is None else rows.numel()
     rwp = None if rows is None else _flat(rows, "rows", _I32, n_rows)
     if y is None:
-        y, yp, ldy = _new(n_rows, N, _BF16, xq.device)
+        y, yp, ldy = _new(n_rows, N, _BF16, xq.device, stream)
     else:
         _shape(y, n_rows, N, "y")
         yp, ldy = _rows(y, "y", _BF16)
@@ -288,5 +289,5 @@ def grouped_gemm(xq, sx, offsets, wq, sw, rows=None, y=None, stream=None):
 
 
 # (the package's own helpers; __init__ imports this module after defining them)
-from . import (PackedExperts, PackedWeight, _check, _handle, _layout, _lib,  # noqa: E402
+from . import (PackedExperts, PackedWeight, _allocate, _check, _handle, _layout, _lib,  # noqa: E402
                _weight_stride, _workspace_of)

@@ -59,3 +59,41 @@ def test_capture_without_a_workspace_after_eager_calls(w8):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, eager) and torch.equal(w8.block_gemm(*args), eager)
+
+
+def _later_fill(like):
+    """Frees a tensor of this size and type while the current stream has yet to
+    write it: the allocator gives its memory to the stream's next tensor."""
+    t = torch.empty_like(like)
+    torch.cuda._sleep(100_000_000)
+    t.fill_(float("nan"))
+
+
+def test_default_stream_as_a_handle(w8):
+    args = gemm_inputs(200, 512, 512)
+    want = w8.block_gemm(*args)
+    assert torch.equal(w8.block_gemm(*args, stream=0), want)
+
+
+@pytest.mark.parametrize("given", ["stream", "handle"])
+def test_outputs_belong_to_the_stream_they_are_written_on(w8, given):
+    """What the current stream still has to do cannot reach them."""
+    st = torch.cuda.Stream()
+    stream = st if given == "stream" else st.cuda_stream
+    args = gemm_inputs(200, 512, 512)
+    x = torch.randn(200, 512, device=DEV).bfloat16()
+    w = torch.ones(512, dtype=torch.bfloat16, device=DEV)
+    off = torch.tensor([0, 200], dtype=torch.int32, device=DEV)
+    experts = args[2].view(torch.uint8)[None].view(torch.float8_e4m3fn)
+    calls = [lambda **kw: w8.block_gemm(*args, **kw),
+             lambda **kw: w8.grouped_gemm(*args[:2], off, experts, args[3][None], **kw),
+             lambda **kw: w8.residual_norm(x, x, w, **kw)[1],
+             lambda **kw: w8.block_quantize(x, **kw)[1],
+             lambda **kw: w8.linear("Block_FP8", x[:8], *args[2:], **kw)]
+    for i, call in enumerate(calls):
+        want = call()
+        torch.cuda.synchronize()
+        _later_fill(want)
+        got = call(stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), i
