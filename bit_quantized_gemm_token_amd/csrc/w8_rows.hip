@@ -178,8 +178,13 @@ __device__ __forceinline__ float silu(float g) {
   const float r = __builtin_amdgcn_rcpf(d);
   const float q = g * r;
   const float s = __builtin_fmaf(__builtin_fmaf(-q, d, g), r, q);
-  // (an infinite 2^hi makes inf * lo and the correction NaN: the quotient is 0)
-  return abs_bits(e) < 0x7F800000u ? s : g * 0.0f;
+  if (hi > 126.0f) {
+    // d is 2^hi to every bit and its reciprocal, below 2^-126, would come out
+    // as 0: g 2^-hi, the power with 64 more in its exponent
+    const float p = __builtin_amdgcn_exp2f(64.0f - hi);
+    return p == 0.0f ? g * 0.0f : g * __builtin_fmaf(p, -0x1.62e43p-1f * lo, p) * 0x1p-64f;
+  }
+  return s;
 }
 
 // ---------------------------------------------------------------- quantize --
