@@ -354,8 +354,6 @@ __global__ __launch_bounds__(ONE_WAVE ? 256 : 1024) void residual_norm_kernel(No
     const int k = 8 * (t + c * T), n = a.D - k;
     float wf[8];
     unpack8(factor(w, a.w, c), wf);
-    // (the row's factor r leaves the codes alone and goes into the scale: one
-    // rounding less a code)
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[c][i] *= wf[i];
     if (a.z) {
@@ -365,8 +363,16 @@ __global__ __launch_bounds__(ONE_WAVE ? 256 : 1024) void residual_norm_kernel(No
       store8_bf16(a.z + row * a.ldz + k, n, z);
     }
     if (a.zq) {  // 16 consecutive lanes hold one group
+      // The row's factor r leaves the codes alone and goes into the scale (one
+      // rounding less a code), unless it is 0, infinite or NaN: then it decides
+      // what the values are, zeros among them.
+      const bool apart = r > 0.0f && r < __builtin_inff();
+      if (!apart) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[c][i] *= r;
+      }
       float s;
-      const v2u q = encode_group(h[c], &s, r);
+      const v2u q = encode_group(h[c], &s, apart ? r : 1.0f);
       if ((t & 15) == 0 && n > 0) a.sz[row * G + k / kGroup] = s;
       store8_codes(a.zq + row * a.ldq + k, n, q);
     }
