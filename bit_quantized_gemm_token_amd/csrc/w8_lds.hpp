@@ -5,6 +5,11 @@
 
 namespace w8 {
 
+// (the compiler says of M0 below that it keeps no value there across such a
+// statement, which is what naming it is for)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+
 // Direct-to-LDS loads: lane i's 16 (or 4) bytes go to LDS byte lds + 16 i (or
 // 4 i).  M0 carries the LDS address and needs one wait state before its use.
 // Written as assembly because the compiler, which cannot tell the stages of
@@ -17,17 +22,26 @@ namespace w8 {
 // write to it, which the compiler does not watch in assembly (and the move is
 // M0's wait state too).
 __device__ __forceinline__ void load_lds16(const uint8_t* p, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(p));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(lds), "v"(p)
+               : "m0");
 }
 __device__ __forceinline__ void load_lds16(const uint8_t* base, unsigned off, unsigned lds) {
   const uint8_t* copy;
   asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
                : "=&s"(copy)
-               : "s"(lds), "v"(off), "s"(base));
+               : "s"(lds), "v"(off), "s"(base)
+               : "m0");
 }
 __device__ __forceinline__ void load_lds4(const float* p, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(p));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :
+               : "s"(lds), "v"(p)
+               : "m0");
 }
+#pragma clang diagnostic pop
+
 // Waits until at most N of this wave's loads are in flight and its LDS reads
 // have returned, then for the workgroup's other waves.
 template <int N>
