@@ -96,9 +96,9 @@ __host__ __device__ constexpr int last_round_parts(long long tiles) {
 }
 constexpr int kGroupedPieces = 3 * kComputeUnits / 4;  // at most this many more than tiles
 const BlockTile& block_tile(int tile);
+// (hipErrorInvalidValue for a tile that is not built)
 hipError_t launch_block_gemm(int tile, unsigned wgs, bool packed, const BlockGemmArgs& a,
                              hipStream_t s);
-// (tiles 0, 3, 4 and 5)
 hipError_t launch_grouped_gemm(int tile, unsigned wgs, bool packed, const BlockGemmArgs& a,
                                hipStream_t s);
 

@@ -886,7 +886,8 @@ hipError_t launch_block_gemm(int tile, unsigned wgs, bool packed, const BlockGem
     case kTile64x64: return launch_dense<T1>(wgs, packed, a, s);
     case kTile64x128: return launch_dense<T2>(wgs, packed, a, s);
     case kTile128x128: return launch_dense<T3>(wgs, packed, a, s);
-    default: return launch_dense<T4>(wgs, packed, a, s);
+    case kTile256x256: return launch_dense<T4>(wgs, packed, a, s);
+    default: return hipErrorInvalidValue;
   }
 }
 
@@ -896,7 +897,8 @@ hipError_t launch_grouped_gemm(int tile, unsigned wgs, bool packed, const BlockG
     case kTile16x128: return launch_grouped<T0>(wgs, packed, a, s);
     case kTile64x128: return launch_grouped<T2>(wgs, packed, a, s);
     case kTile128x128: return launch_grouped<T3>(wgs, packed, a, s);
-    default: return launch_grouped<T4>(wgs, packed, a, s);
+    case kTile256x256: return launch_grouped<T4>(wgs, packed, a, s);
+    default: return hipErrorInvalidValue;
   }
 }
 

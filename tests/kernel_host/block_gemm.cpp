@@ -77,3 +77,9 @@ extern "C" long long emu_gemm(const EmuGemm* e) {
 }
 extern "C" const char* emu_text() { return emu::m().text.c_str(); }
 extern "C" long long emu_loads() { return emu::m().loads; }
+// The library's launchers: what they say to a tile.
+extern "C" int emu_launch(int tile, int grouped, int packed) {
+  const w8::BlockGemmArgs a{};
+  return grouped ? w8::launch_grouped_gemm(tile, 1, packed, a, nullptr)
+                 : w8::launch_block_gemm(tile, 1, packed, a, nullptr);
+}

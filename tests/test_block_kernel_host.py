@@ -119,3 +119,14 @@ def test_a_read_past_the_end_is_seen(lib):
     for tile in host.TILES:
         c = inputs(130, 256, 256)
         assert host.run(lib, tile, *c, hide=16, parts=1)[1] > 0, tile
+
+
+def test_launchers_refuse_tiles_that_are_not_built(lib):
+    """(another tile's kernel on this one's grid would compute something else)"""
+    ids = {name: t[0] for name, t in host.TILES.items()}
+    for packed in (0, 1):
+        for id_ in ids.values():
+            assert lib.emu_launch(id_, 0, packed) == 0
+            assert lib.emu_launch(id_, 1, packed) == (1 if id_ == ids["64x64"] else 0)
+        for id_ in (-1, len(ids)):
+            assert lib.emu_launch(id_, 0, packed) == 1 and lib.emu_launch(id_, 1, packed) == 1
