@@ -44,8 +44,8 @@ __all__ = ["Config", "W8Error", "UnsupportedShape", "Workspace", "PackedWeight",
            "profile_configs", "model_config", "moe_gemm", "moe_config", "moe_tune",
            "moe_workspace_size", "moe_linear", "moe_linear_config",
            "pack_experts", "PackedExperts", "read_floor", "block_quantize", "residual_norm",
-           "block_gemm", "block_gemm_workspace_size", "grouped_gemm", "FORMATS", "MAX_M",
-           "MAX_SPLIT_K", "GROUP", "ABI_VERSION"]
+           "block_gemm", "block_gemm_workspace_size", "block_gemm_plan", "grouped_gemm",
+           "grouped_gemm_plan", "FORMATS", "MAX_M", "MAX_SPLIT_K", "GROUP", "ABI_VERSION"]
 
 
 class W8Error(RuntimeError):
@@ -849,8 +849,8 @@ load_default_table()
 
 
 # ------------------------------------------------- Block_FP8, any token count --
-from .block import (block_gemm, block_gemm_workspace_size, block_quantize,  # noqa: E402
-                    grouped_gemm, residual_norm)
+from .block import (block_gemm, block_gemm_plan, block_gemm_workspace_size,  # noqa: E402
+                    block_quantize, grouped_gemm, grouped_gemm_plan, residual_norm)
 
 
 # -------------------------------------------------------------- measurement --

@@ -32,7 +32,8 @@ EXPORTS = ("w8_abi_version", "w8_status_string", "w8_last_error", "w8_quantize_a
            "w8_moe_validate_config", "w8_moe_config", "w8_moe_tune", "w8_moe_linear",
            "w8_moe_linear_config", "w8_read_floor", "w8_gemm_w8a8_noalloc", "w8_predict_us",
            "w8_block_quantize", "w8_residual_norm", "w8_block_gemm",
-           "w8_block_gemm_workspace_size", "w8_grouped_gemm")
+           "w8_block_gemm_workspace_size", "w8_block_gemm_plan", "w8_grouped_gemm",
+           "w8_grouped_gemm_plan")
 
 
 class Config(ctypes.Structure):
@@ -81,6 +82,15 @@ class TuneStats(ctypes.Structure):
                 ("default_us_bank2", ctypes.c_double), ("best_gbps", ctypes.c_double),
                 ("tune_seconds", ctypes.c_double), ("best_us_bank2_min", ctypes.c_double),
                 ("best_us_bank2_p90", ctypes.c_double)]
+
+    def as_dict(self):
+        return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class BlockPlan(ctypes.Structure):
+    _fields_ = [("tile_m", ctypes.c_int32), ("tile_n", ctypes.c_int32),
+                ("split_k", ctypes.c_int32), ("parts", ctypes.c_int32),
+                ("workgroups", ctypes.c_int64)]
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_}
@@ -201,4 +211,9 @@ def load():
     lib.w8_grouped_gemm.argtypes = [c_int, c_int, c_int, c_int, vp, i64, f32p, vp, vp, c_int, vp,
                                     i64, i64, f32p, i64, vp, i64, vp]
     lib.w8_grouped_gemm.restype = st
+    planp = ctypes.POINTER(BlockPlan)
+    lib.w8_block_gemm_plan.argtypes = [c_int, c_int, c_int, c_int, planp]
+    lib.w8_block_gemm_plan.restype = st
+    lib.w8_grouped_gemm_plan.argtypes = [c_int, c_int, c_int, c_int, i64, c_int, planp]
+    lib.w8_grouped_gemm_plan.restype = st
     return lib

@@ -195,6 +195,24 @@ def block_gemm_workspace_size(M, N, K, packed=False):
     return n.value
 
 
+def block_gemm_plan(M, N, K, packed=False):
+    """What block_gemm runs for the shape: tile_m x tile_n (tokens x weight
+    rows of a workgroup; 0 x 0 where the small-M GEMM runs), split_k, parts
+    (pieces of each tile in the last, partial round) and workgroups.  Host only."""
+    p = _capi.BlockPlan()
+    _check(_lib.w8_block_gemm_plan(M, N, K, _layout(packed), ctypes.byref(p)))
+    return p.as_dict()
+
+
+def grouped_gemm_plan(E, T, N, K, n_rows=None, ldq=None):
+    """What grouped_gemm runs for n_rows entries (default T) of E experts on T
+    token rows of stride ldq (default K), as block_gemm_plan says it."""
+    p = _capi.BlockPlan()
+    _check(_lib.w8_grouped_gemm_plan(E, T, N, K, K if ldq is None else ldq,
+                                     T if n_rows is None else n_rows, ctypes.byref(p)))
+    return p.as_dict()
+
+
 def block_gemm(xq, sx, wq, sw, y=None, workspace=None, stream=None):
     """Y = dequant(xq) . dequant(wq)^T as bf16 [M, N] in Block_FP8, any M.
 

@@ -39,6 +39,26 @@ w8_status check_nk(int N, int K) {
   return W8_OK;
 }
 
+w8_status check_ldq(int K, int64_t ldq) {
+  if (ldq < K || ldq % 16)
+    return fail(W8_E_INVALID, "ldq must be >= K and a multiple of 16");
+  // (a tile's rows are addressed by 32-bit offsets from its first)
+  if (ldq > kMaxStride) return fail(W8_E_INVALID, "ldq must be at most 2^23");
+  return W8_OK;
+}
+
+w8_status check_layout(int packed) {
+  if (packed != 0 && packed != 1)
+    return fail(W8_E_INVALID, "weight layout must be 0 (row-major) or 1 (packed)");
+  return W8_OK;
+}
+
+w8_status check_experts(int E, int T) {
+  if (E < 1 || E > 65536) return fail(W8_E_INVALID, "E must be in [1, 65536]");
+  if (T < 0) return fail(W8_E_INVALID, "T must be >= 0");
+  return W8_OK;
+}
+
 // Operand checks shared by the dense and the grouped GEMM; *packed: the
 // weight layout ldw names.
 w8_status check_operands(int N, int K, const void* xq, int64_t ldq, const float* sx,
@@ -47,14 +67,12 @@ w8_status check_operands(int N, int K, const void* xq, int64_t ldq, const float*
   if (!xq || !sx || !wq || !sw || !y) return fail(W8_E_INVALID, "null device pointer");
   if (!aligned(xq, 16) || !aligned(wq, 16))
     return fail(W8_E_INVALID, "xq and wq must be 16-byte aligned");
-  if (ldq < K || ldq % 16)
-    return fail(W8_E_INVALID, "ldq must be >= K and a multiple of 16");
+  const w8_status st = check_ldq(K, ldq);
+  if (st) return st;
   if (ldw != 0 && (ldw < K || ldw % 16))
     return fail(W8_E_INVALID, "ldw must be >= K and a multiple of 16 (row-major weights) or 0 "
                               "(packed; the K-segmented layouts are for the small-M GEMM)");
-  // (a tile's rows are addressed by 32-bit offsets from its first)
-  if (ldq > kMaxStride || ldw > kMaxStride)
-    return fail(W8_E_INVALID, "ldq and ldw must be at most 2^23");
+  if (ldw > kMaxStride) return fail(W8_E_INVALID, "ldw must be at most 2^23");
   *packed = ldw == 0;
   if (*packed && K % W8_GROUP) return fail(W8_E_INVALID, "packed weights need K % 128 == 0");
   if (ldy < N) return fail(W8_E_INVALID, "output leading dimension must be >= N");
@@ -196,7 +214,7 @@ Plan plan_grouped(int E, int T, int N, int K, int64_t ldq, int n_rows) {
   if (p.tile == kTile128x128 && fits(kTile64x128, kComputeUnits)) take(kTile64x128);
   const int run = groups_of(K) <= 6 ? 2 * kComputeUnits : kComputeUnits;
   if (p.tile == kTile64x128 && fits(kTile16x128, run)) take(kTile16x128);
-  p.split_k = 1;
+  p.split_k = p.parts = 1;
   p.whole = p.wgs = p.tiles_m * p.tiles_n;
   if (p.tile == kLargeTile) p.wgs += kGroupedPieces;
   return p;
@@ -206,6 +224,11 @@ size_t plan_bytes(const Plan& p) {
   if (p.split_k == 1) return 0;
   const BlockTile& t = block_tile(p.tile);
   return ws_counter_bytes(0) + (size_t)(p.tiles_m * p.tiles_n) * p.split_k * t.bm * t.bn * 4;
+}
+
+w8_block_plan describe(const Plan& p) {
+  const BlockTile& t = block_tile(p.tile);
+  return {t.bm, t.bn, p.split_k, p.tile == kLargeTile ? p.parts : 1, p.wgs};
 }
 
 w8_status check_grid(const Plan& p) {
@@ -288,12 +311,26 @@ w8_status w8_block_gemm_workspace_size(int M, int N, int K, int packed, size_t* 
   if (st) return st;
   st = check_nk(N, K);
   if (st) return st;
-  if (packed != 0 && packed != 1)
-    return fail(W8_E_INVALID, "weight layout must be 0 (row-major) or 1 (packed)");
+  st = check_layout(packed);
+  if (st) return st;
   if (!bytes) return fail(W8_E_INVALID, "null output pointer");
   if (M && use_small_m(M, N, K, packed))
     return w8_workspace_size(W8_BLOCK_FP8, W8_OP_GEMM, M, N, K, packed, nullptr, bytes);
   *bytes = M ? plan_bytes(plan_dense(M, N, K)) : 0;
+  return ok();
+}
+
+w8_status w8_block_gemm_plan(int M, int N, int K, int packed, w8_block_plan* plan) {
+  w8_status st = check_rows(M);
+  if (st) return st;
+  st = check_nk(N, K);
+  if (st) return st;
+  st = check_layout(packed);
+  if (st) return st;
+  if (packed && K % W8_GROUP) return fail(W8_E_INVALID, "packed weights need K % 128 == 0");
+  if (!plan) return fail(W8_E_INVALID, "null output pointer");
+  *plan = w8_block_plan{0, 0, 1, 1, 0};
+  if (M && !use_small_m(M, N, K, packed)) *plan = describe(plan_dense(M, N, K));
   return ok();
 }
 
@@ -351,6 +388,22 @@ w8_status w8_block_gemm(int M, int N, int K, const void* xq, int64_t ldq, const 
   return ok();
 }
 
+w8_status w8_grouped_gemm_plan(int E, int T, int N, int K, int64_t ldq, int n_rows,
+                               w8_block_plan* plan) {
+  w8_status st = check_rows(n_rows);
+  if (st) return st;
+  st = check_nk(N, K);
+  if (st) return st;
+  st = check_experts(E, T);
+  if (st) return st;
+  st = check_ldq(K, ldq);
+  if (st) return st;
+  if (!plan) return fail(W8_E_INVALID, "null output pointer");
+  *plan = w8_block_plan{0, 0, 1, 1, 0};
+  if (n_rows) *plan = describe(plan_grouped(E, T, N, K, ldq, n_rows));
+  return ok();
+}
+
 w8_status w8_grouped_gemm(int E, int T, int N, int K, const void* xq, int64_t ldq,
                           const float* sx, const int32_t* offsets, const int32_t* rows,
                           int n_rows, const void* wq, int64_t ldw, int64_t w_stride,
@@ -360,8 +413,8 @@ w8_status w8_grouped_gemm(int E, int T, int N, int K, const void* xq, int64_t ld
   if (st) return st;
   st = check_nk(N, K);
   if (st) return st;
-  if (E < 1 || E > 65536) return fail(W8_E_INVALID, "E must be in [1, 65536]");
-  if (T < 0) return fail(W8_E_INVALID, "T must be >= 0");
+  st = check_experts(E, T);
+  if (st) return st;
   if (n_rows == 0) return ok();
   if (T < 1) return fail(W8_E_INVALID, "routed entries need at least one token row");
   if (!offsets) return fail(W8_E_INVALID, "null device pointer");

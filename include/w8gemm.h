@@ -659,6 +659,18 @@ w8_status w8_block_gemm(int M, int N, int K, const void *xq, int64_t ldq, const 
 /* Bytes of workspace (packed: the weight layout, 0 or 1). */
 w8_status w8_block_gemm_workspace_size(int M, int N, int K, int packed, size_t *bytes);
 
+/* What a call runs.  Host only; no device is touched. */
+typedef struct w8_block_plan {
+    int32_t tile_m, tile_n; /* tokens x weight rows of a workgroup's tile; 0, 0:
+                               w8_gemm_w8a8's kernel, or nothing (no rows) */
+    int32_t split_k;        /* workgroups that share a tile's K */
+    int32_t parts;          /* 2 or 4: the tiles of a last, partial round over
+                               the GPU run in so many pieces each; 1: none do */
+    int64_t workgroups;     /* of the launch (grouped: the most that any offsets
+                               need; those without work end at once) */
+} w8_block_plan;
+w8_status w8_block_gemm_plan(int M, int N, int K, int packed, w8_block_plan *plan);
+
 /* The same product per expert over ragged lists of rows: for entry i of
  * expert e, offsets[e] <= i < offsets[e+1],
  *   Y[i, :] = dequant(xq[rows[i]]) . dequant(Wq_e)^T
@@ -680,6 +692,10 @@ w8_status w8_grouped_gemm(int E, int T, int N, int K, const void *xq, int64_t ld
                           int n_rows, const void *wq, int64_t ldw, int64_t w_stride,
                           const float *sw, int64_t sw_stride, void *y, int64_t ldy,
                           w8_stream stream);
+/* What a call runs (parts: 1; the kernel finds the last round's pieces from
+ * the offsets). */
+w8_status w8_grouped_gemm_plan(int E, int T, int N, int K, int64_t ldq, int n_rows,
+                               w8_block_plan *plan);
 
 /* -------------------------------------------------------- measurement -- */
 /* The read floor the GEMM is measured against: one kernel launch on `stream`
