@@ -9,15 +9,20 @@
 // MFMA operands from LDS.  MFMA operand A is the weights and B the tokens
 // (D = W X^T), so a lane's accumulators all belong to one token: the step's
 // scale is one product per token column, and a group's partial sum is added
-// as acc += partial * (sx * sw), one fp32 FMA per element per group.
+// as acc += partial * (sx * sw), one fp32 FMA per element per group.  The
+// instruction itself rounds a group's sum: by 2^-16 of the result in the root
+// mean square, unbiased, at most 2^-16 of the sum of |products| (measured, 2^17
+// results), so about 1% of the bf16 outputs lie one step beside the rounded
+// exact one; the fp32 sum over the groups adds nothing to that.
 //
-// Measured, and what bounds it: 8192 x 5120 x 8192 281 us, 2.45 PFLOP/s, by
-// power (the clock falls to 1.7 .. 2.0 GHz) and the direct-to-LDS loads beside
-// the MFMAs; 4096 x 5120 x 2048 46 us, 1.87 PFLOP/s, by the start and the output
-// of a tile, which nothing on the compute unit overlaps; 48 x 4608 x 7168 12 us
-// by the weights (7 us at a copy's rate), the hand-off of split K and the
-// start; 128 experts, top 8, of 1536 x 2048: 8 tokens 33.6 us, 4.8 TB/s, by the
-// weights' bytes; 4096 tokens 160 us, 1.3 PFLOP/s, as the dense tiles.
+// Measured, and what bounds it: 8192 x 5120 x 8192 284 to 300 us, 2.3 to 2.4
+// PFLOP/s, by power (0.555 M clocks at 1.7 .. 2.0 GHz) and the direct-to-LDS
+// loads beside the MFMAs; 4096 x 5120 x 2048 46 us, 1.87 PFLOP/s, by the start
+// and the output of a tile, which nothing on the compute unit overlaps; 48 x
+// 4608 x 7168 12 us by the weights (5 us at the rate of reads, 7 at a copy's),
+// the hand-off of split K and the start; 128 experts, top 8, of 1536 x 2048: 8
+// tokens 33.5 us, 4.9 TB/s, by the weights' bytes; 4096 tokens 158 to 182 us
+// (0.333 M clocks at 1.85 .. 2.1 GHz), 1.3 PFLOP/s, as the dense tiles.
 #include <atomic>
 #include <climits>
 #include <type_traits>

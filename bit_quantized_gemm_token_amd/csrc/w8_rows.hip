@@ -190,8 +190,8 @@ __device__ __forceinline__ float silu(float g) {
 // ---------------------------------------------------------------- quantize --
 // 16 lanes take a group, each lane eight values; a workgroup takes 16 groups
 // and strides over the rest.  Bound by HBM on many rows (32768 x 768 gated:
-// 27 us, 4.7 TB/s; a copy reaches 4.8) and by the launch on few (33 x 2048:
-// 2.5 us).
+// 27.6 us, 4.6 TB/s; a copy reaches 4.8) and by the launch on few (33 x 2048:
+// 2.6 us).
 constexpr int kQThreads = 256;
 
 template <bool GATED>

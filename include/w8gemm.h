@@ -630,7 +630,10 @@ w8_status w8_block_quantize(int M, int K, const void *x, int64_t ldx, const void
  *                w8_block_quantize gives them for the unrounded z; or NULL
  *                (at least one of z and zq)
  * Strides in elements, >= D; pointers aligned to their element.
- * 1 <= D <= 32768 (above: W8_E_UNSUPPORTED), eps >= 0.                     */
+ * 1 <= D <= 32768 (above: W8_E_UNSUPPORTED), eps >= 0.  The sums of squares
+ * are fp32: a row with squares past its range gets z = 0, as the finite values
+ * beside an infinity do.  Where the root is 0 (eps = 0, a row of zeros) or NaN,
+ * all of the row's z is NaN, and so is every scale.                        */
 w8_status w8_residual_norm(int M, int D, const void *y, int64_t ldy, const void *residual,
                            int64_t ldr, int residual_fp32, const void *post_weight,
                            const void *gate, int64_t ldg, float scale, const void *weight,
@@ -649,9 +652,10 @@ w8_status w8_residual_norm(int M, int D, const void *y, int64_t ldy, const void 
  *           entry points), NULL when the size is 0
  * 1 <= N <= 2^24, 16 <= K <= 2^22, K % 16 == 0; ldq and ldw at most 2^23;
  * finite codes (w8_gemm_w8a8's condition).  Partial sums of a group come from
- * the fp8 matrix instructions; groups are summed in fp32 in K order, within
- * each part of a split K and then over the parts, so results are run-to-run
- * deterministic.  Up to W8_MAX_M tokens on weights below a few tens of MiB run
+ * the fp8 matrix instructions, which round them (2^-16 of the sum in the root
+ * mean square); groups are summed in fp32 in K order, within each part of a
+ * split K and then over the parts, so results are run-to-run deterministic.
+ * Calls that overlap on several streams need a workspace each.  Up to W8_MAX_M tokens on weights below a few tens of MiB run
  * w8_gemm_w8a8's kernel (and configuration table) where K % 128 == 0.       */
 w8_status w8_block_gemm(int M, int N, int K, const void *xq, int64_t ldq, const float *sx,
                         const void *wq, int64_t ldw, const float *sw, void *y, int64_t ldy,
