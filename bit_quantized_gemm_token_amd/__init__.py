@@ -300,10 +300,10 @@ class Workspace:
     capture).  A buffer that a larger one replaces is kept alive for the
     Workspace's lifetime, because a graph captured earlier may still use it;
     release_retired() drops those once no such graph remains.  A call that is
-    captured without a workspace argument on a stream without one of its own
-    takes the largest that eager calls on the device have sized; replays must
-    then not overlap the calls of that stream, so a graph replayed beside
-    other work needs a Workspace of its own.
+    captured without a workspace argument takes its stream's if that is large
+    enough, else the largest that eager calls on the device have sized;
+    replays must then not overlap the calls of that stream, so a graph
+    replayed beside other work needs a Workspace of its own.
     """
 
     def __init__(self, device=None, nbytes=0):
@@ -403,15 +403,23 @@ def _default_workspace(device, stream=None):
 def _workspace_of(device, handle):
     w = _workspaces.get((device.index, handle))
     if w is None:
-        if torch.cuda.is_current_stream_capturing():
-            # nothing may be allocated here, and a graph is replayed on any
-            # stream: the largest that eager calls on this device have sized
-            held = [v for (index, _), v in _workspaces.items()
-                    if index == device.index and v.buf is not None]
-            if held:
-                return max(held, key=lambda v: v.buf.numel())
-        w = _workspaces.setdefault((device.index, handle), Workspace(device))
+        w = _workspaces.setdefault((device.index, handle), _StreamWorkspace(device))
     return w
+
+
+class _StreamWorkspace(Workspace):
+    """A stream's own.  Under capture, where it cannot grow, it lends the
+    largest that eager calls on the device have sized (a graph is captured on
+    one stream and replayed on any)."""
+
+    def reserve(self, nbytes, stream=None):
+        if ((self.buf is None or self.buf.numel() < nbytes)
+                and torch.cuda.is_current_stream_capturing()):
+            held = [w.buf for w in list(_workspaces.values())
+                    if w.device == self.device and w.buf is not None and w.buf.numel() >= nbytes]
+            if held:
+                return max(held, key=torch.Tensor.numel)
+        return super().reserve(nbytes, stream)
 
 
 def gemm_w8a8(fmt, xq, sx, wq, sw, cfg=None, y=None, workspace=None, stream=None):

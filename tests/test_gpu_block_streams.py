@@ -97,3 +97,23 @@ def test_outputs_belong_to_the_stream_they_are_written_on(w8, given):
         got = call(stream=stream)
         torch.cuda.synchronize()
         assert torch.equal(got, want), i
+
+
+def test_capture_on_a_stream_whose_workspace_is_too_small(w8):
+    """What eager calls on another stream have sized is enough for it."""
+    args, few = gemm_inputs(100, 1024, 8192), gemm_inputs(40, 256, 1024)
+    assert w8.block_gemm_workspace_size(100, 1024, 8192) > \
+        w8.block_gemm_workspace_size(40, 256, 1024) > 0
+    st = torch.cuda.Stream()
+    w8.block_gemm(*few, stream=st)
+    eager = w8.block_gemm(*args)
+    y = torch.empty_like(eager)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        w8.block_gemm(*args, y=y)
+    for _ in range(4):
+        y.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, eager) and torch.equal(w8.block_gemm(*args), eager)

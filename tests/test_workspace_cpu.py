@@ -23,18 +23,17 @@ def test_each_stream_has_its_own(w8):
 
 
 def test_a_capture_takes_one_that_is_there(w8, monkeypatch):
-    """On a stream without one: the largest on the device; none of another
-    device's, and one without memory where there is none to take (whose growth
-    the Workspace then refuses)."""
-    for i, (stream, nbytes) in enumerate(((0x1000, 256), (0x2000, 4096), (0x3000, 1024))):
+    """Where the stream's own is missing or too small: the largest on the
+    device, none of another device's; and where there is none that is large
+    enough the Workspace refuses to grow."""
+    for stream, nbytes in ((0x1000, 256), (0x2000, 4096), (0x3000, 1024)):
         w8._default_workspace(DEV, stream).buf = torch.zeros(nbytes, dtype=torch.uint8)
     w8._default_workspace(torch.device("cuda:1"), 0x2000).buf = torch.zeros(8192, dtype=torch.uint8)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
-    assert w8._default_workspace(DEV, 0x9000).buf.numel() == 4096
-    assert w8._default_workspace(DEV, 0x3000).buf.numel() == 1024  # the stream's own
-    empty = w8._default_workspace(torch.device("cuda:2"), 0x9000)
-    assert empty.buf is None
-    with pytest.raises(RuntimeError, match="capture"):
-        empty.reserve(1024)
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
-    assert w8._default_workspace(DEV, 0x9000).buf is None  # (not kept for the stream)
+    new, small = w8._default_workspace(DEV, 0x9000), w8._default_workspace(DEV, 0x3000)
+    assert new.reserve(512).numel() == 4096 and small.reserve(2048).numel() == 4096
+    assert small.reserve(1024).numel() == 1024  # its own
+    for w in (new, small, w8._default_workspace(torch.device("cuda:2"), 0x9000)):
+        with pytest.raises(RuntimeError, match="capture"):
+            w.reserve(8192)
+    assert new.buf is None and small.buf.numel() == 1024  # (what was lent is not kept)
