@@ -3,8 +3,11 @@
     Y[M, N] = dequant(Xq) . dequant(Wq)^T,  1 <= M <= 32,
     formats FP8_Dynamic, W8A8_INT8 and Block_FP8;
 
-and the operators of a Block_FP8 layer at any token count: block_gemm,
-grouped_gemm, residual_norm and block_quantize.
+the operators of a Block_FP8 layer at any token count (block_gemm,
+grouped_gemm, residual_norm, block_quantize), the quantizer and GEMM of the
+other two formats at any token count (token_quantize, token_gemm), and the MoE
+layer around the grouped products (moe_route, moe_combine; moe_layer for a few
+tokens as a whole).
 
 Kernels run on torch's current stream, or on a call's `stream` (a torch stream
 or a handle).  There the caller orders the stream after whatever writes the
@@ -45,7 +48,9 @@ __all__ = ["Config", "W8Error", "UnsupportedShape", "Workspace", "PackedWeight",
            "moe_workspace_size", "moe_linear", "moe_linear_config",
            "pack_experts", "PackedExperts", "read_floor", "block_quantize", "residual_norm",
            "block_gemm", "block_gemm_workspace_size", "block_gemm_plan", "grouped_gemm",
-           "grouped_gemm_plan", "FORMATS", "MAX_M", "MAX_SPLIT_K", "GROUP", "ABI_VERSION"]
+           "grouped_gemm_plan", "token_quantize", "token_gemm", "token_gemm_workspace_size",
+           "token_gemm_plan", "moe_route", "moe_route_workspace_size", "moe_combine", "moe_layer",
+           "moe_layer_workspace_size", "FORMATS", "MAX_M", "MAX_SPLIT_K", "GROUP", "ABI_VERSION"]
 
 
 class W8Error(RuntimeError):
@@ -859,6 +864,13 @@ load_default_table()
 # ------------------------------------------------- Block_FP8, any token count --
 from .block import (block_gemm, block_gemm_plan, block_gemm_workspace_size,  # noqa: E402
                     block_quantize, grouped_gemm, grouped_gemm_plan, residual_norm)
+
+
+# ------------------------- token-scaled formats at any token count, MoE layer --
+from .tokens import (token_gemm, token_gemm_plan, token_gemm_workspace_size,  # noqa: E402
+                     token_quantize)
+from .moe import (moe_combine, moe_layer, moe_layer_workspace_size, moe_route,  # noqa: E402
+                  moe_route_workspace_size)
 
 
 # -------------------------------------------------------------- measurement --

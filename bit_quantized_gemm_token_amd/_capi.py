@@ -33,7 +33,10 @@ EXPORTS = ("w8_abi_version", "w8_status_string", "w8_last_error", "w8_quantize_a
            "w8_moe_linear_config", "w8_read_floor", "w8_gemm_w8a8_noalloc", "w8_predict_us",
            "w8_block_quantize", "w8_residual_norm", "w8_block_gemm",
            "w8_block_gemm_workspace_size", "w8_block_gemm_plan", "w8_grouped_gemm",
-           "w8_grouped_gemm_plan")
+           "w8_grouped_gemm_plan", "w8_token_quantize", "w8_token_gemm",
+           "w8_token_gemm_workspace_size", "w8_token_gemm_plan", "w8_moe_route",
+           "w8_moe_route_workspace_size", "w8_moe_combine", "w8_moe_layer",
+           "w8_moe_layer_workspace_size")
 
 
 class Config(ctypes.Structure):
@@ -216,4 +219,29 @@ def load():
     lib.w8_block_gemm_plan.restype = st
     lib.w8_grouped_gemm_plan.argtypes = [c_int, c_int, c_int, c_int, i64, c_int, planp]
     lib.w8_grouped_gemm_plan.restype = st
+    sizep = ctypes.POINTER(ctypes.c_size_t)
+    lib.w8_token_quantize.argtypes = [c_int, c_int, c_int, vp, i64, vp, i64, c_int, vp, i64, f32p,
+                                      vp]
+    lib.w8_token_quantize.restype = st
+    lib.w8_token_gemm_workspace_size.argtypes = [c_int, c_int, c_int, c_int, c_int, sizep]
+    lib.w8_token_gemm_workspace_size.restype = st
+    lib.w8_token_gemm_plan.argtypes = [c_int, c_int, c_int, c_int, c_int, planp]
+    lib.w8_token_gemm_plan.restype = st
+    lib.w8_token_gemm.argtypes = [c_int, c_int, c_int, c_int, vp, i64, f32p, vp, i64, f32p, vp,
+                                  i64, vp, ctypes.c_size_t, vp]
+    lib.w8_token_gemm.restype = st
+    lib.w8_moe_route_workspace_size.argtypes = [c_int, c_int, c_int, sizep]
+    lib.w8_moe_route_workspace_size.restype = st
+    lib.w8_moe_route.argtypes = [c_int, c_int, c_int, vp, i64, c_int, c_int, f32, vp, f32p, vp, vp,
+                                 vp, vp, ctypes.c_size_t, vp]
+    lib.w8_moe_route.restype = st
+    lib.w8_moe_combine.argtypes = [c_int, c_int, c_int, vp, i64, c_int, f32p, vp, vp, i64, vp, i64,
+                                   vp]
+    lib.w8_moe_combine.restype = st
+    lib.w8_moe_layer_workspace_size.argtypes = [c_int, c_int, c_int, c_int, sizep]
+    lib.w8_moe_layer_workspace_size.restype = st
+    lib.w8_moe_layer.argtypes = [c_int, c_int, c_int, c_int, c_int, c_int, vp, i64, f32p, vp, f32p,
+                                 vp, i64, i64, f32p, i64, vp, i64, i64, f32p, i64, vp, i64, vp,
+                                 ctypes.c_size_t, vp]
+    lib.w8_moe_layer.restype = st
     return lib

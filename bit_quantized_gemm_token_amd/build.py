@@ -45,6 +45,9 @@ def _units():
              ("w8_registry.cpp", ["-x", "hip"], "w8_registry.o"),
              ("w8_block_gemm.hip", [], "w8_block_gemm.o"),
              ("w8_rows.hip", [], "w8_rows.o"),
+             ("w8_route.hip", [], "w8_route.o"),
+             ("w8_moe_layer.hip", [], "w8_moe_layer.o"),
+             ("w8_route.cpp", ["-x", "hip"], "w8_route_capi.o"),
              ("w8_block.cpp", ["-x", "hip"], "w8_block.o")]
     # the instance file in 40 parts (the GEMM parts, the largest, first so
     # the pool stays busy; parts 4 and 5 exist for Block_FP8 only), then the

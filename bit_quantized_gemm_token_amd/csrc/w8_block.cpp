@@ -1,5 +1,6 @@
-// C-ABI of the Block_FP8 operators for any token count: the gated quantizer,
-// the residual norm, the tiled GEMM and the per-expert (grouped) GEMM.
+// C-ABI of the operators for any token count: Block_FP8's gated quantizer,
+// residual norm, tiled GEMM and per-expert (grouped) GEMM, and the quantizer
+// and tiled GEMM of the formats with one scale per token and output channel.
 // Argument checks first, then one kernel launch each; nothing here allocates,
 // frees or synchronizes.
 #include <cstdint>
@@ -36,6 +37,30 @@ w8_status check_nk(int N, int K) {
   if (N < 1 || N > kMaxN) return fail(W8_E_INVALID, "N must be in [1, 2^24]");
   if (K < 16 || K > kMaxK || K % 16)
     return fail(W8_E_INVALID, "K must be a multiple of 16 in [16, 2^22]");
+  return W8_OK;
+}
+
+// The formats with one scale per token and per output channel.
+w8_status check_token_format(int fmt) {
+  if (fmt != W8_FP8_DYNAMIC && fmt != W8_W8A8_INT8)
+    return fail(W8_E_INVALID, "the format must be FP8_Dynamic or W8A8_INT8 (Block_FP8 has entry "
+                              "points of its own), got " + std::to_string(fmt));
+  return W8_OK;
+}
+
+// int8: sums of K products of any two codes, 2^14 at most each, stay in int32
+constexpr int kMaxKInt8 = (1 << 17) - 16;
+
+w8_status check_token_shape(int fmt, int M, int N, int K) {
+  w8_status st = check_token_format(fmt);
+  if (st) return st;
+  st = check_rows(M);
+  if (st) return st;
+  st = check_nk(N, K);
+  if (st) return st;
+  if (fmt == W8_W8A8_INT8 && K > kMaxKInt8)
+    return fail(W8_E_INVALID, "W8A8_INT8: K must be at most " + std::to_string(kMaxKInt8) +
+                                  ", where any codes' sums stay in int32");
   return W8_OK;
 }
 
@@ -173,8 +198,8 @@ Plan plan_dense(int M, int N, int K) {
 // 4.0; 1 x 4608 x 7168 12.5 and 9.8; 16 x 5120 x 8192 19.0 and 11.7).  Packed
 // weights, which it reads in whole lines, move the border (1 x 5120 x 8192 10.8
 // and 12.2; 8 x 5120 x 8192 12.4 and 11.7).  It needs whole groups.
-bool use_small_m(int M, int N, int K, bool packed) {
-  if (M > W8_MAX_M || K % W8_GROUP) return false;
+bool use_small_m(int fmt, int M, int N, int K, bool packed) {
+  if (M > W8_MAX_M || (fmt == W8_BLOCK_FP8 && K % W8_GROUP)) return false;
   const long long weights = (long long)N * K;
   if (M > W8_MAX_M / 2) return weights < 1 << 22;
   return weights < 24 << 20 || (packed && M < 8);
@@ -242,19 +267,14 @@ w8_status check_grid(const Plan& p) {
   return W8_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-w8_status w8_block_quantize(int M, int K, const void* x, int64_t ldx, const void* gate,
-                            int64_t ldg, void* xq, int64_t ldq, float* sx, w8_stream stream) {
-  w8_status st = check_rows(M);
+// Arguments of a quantizer (M == 0 needs no buffers).
+w8_status check_quantize(int M, int K, const void* x, int64_t ldx, const void* gate, int64_t ldg,
+                         const void* xq, int64_t ldq, const float* sx) {
+  const w8_status st = check_rows(M);
   if (st) return st;
   if (K < 8 || K > kMaxK || K % 8)
     return fail(W8_E_INVALID, "K must be a multiple of 8 in [8, 2^22]");
-  if ((long long)M * groups_of(K) >= (1LL << 31))
-    return fail(W8_E_INVALID, "the groups (M x ceil(K / 128)) must be fewer than 2^31");
-  if (M == 0) return ok();
+  if (M == 0) return W8_OK;
   if (!x || !xq || !sx) return fail(W8_E_INVALID, "null device pointer");
   if (!aligned(x, 16) || ldx % 8 || ldx < K)
     return fail(W8_E_INVALID, "x must be 16-byte aligned with ldx >= K and ldx % 8 == 0");
@@ -263,6 +283,72 @@ w8_status w8_block_quantize(int M, int K, const void* x, int64_t ldx, const void
   if (!aligned(xq, 8) || ldq % 8 || ldq < K)
     return fail(W8_E_INVALID, "xq must be 8-byte aligned with ldq >= K and ldq % 8 == 0");
   if (!aligned(sx, 4)) return fail(W8_E_INVALID, "sx must be 4-byte aligned");
+  return W8_OK;
+}
+
+// The dense GEMM of any format, its shape checked and M > 0.
+w8_status dense_gemm(int fmt, int M, int N, int K, const void* xq, int64_t ldq, const float* sx,
+                     const void* wq, int64_t ldw, const float* sw, void* y, int64_t ldy, void* ws,
+                     size_t ws_bytes, w8_stream stream) {
+  int packed = 0;
+  w8_status st = check_operands(N, K, xq, ldq, sx, wq, ldw, sw, y, ldy, &packed);
+  if (st) return st;
+  if (use_small_m(fmt, M, N, K, packed))
+    return w8_gemm_w8a8((w8_fmt)fmt, M, N, K, xq, ldq, sx, wq, ldw, sw, y, ldy, nullptr, ws,
+                        ws_bytes, stream);
+  const Plan p = plan_dense(M, N, K);
+  const size_t need = plan_bytes(p);
+  if (need > 0) {
+    if (!ws || ws_bytes < need)
+      return fail(W8_E_WORKSPACE, "workspace of " + std::to_string(need) + " bytes needed, got " +
+                                      std::to_string(ws ? ws_bytes : 0));
+    if (!aligned(ws, 16)) return fail(W8_E_INVALID, "workspace must be 16-byte aligned");
+  }
+  st = check_grid(p);
+  if (st) return st;
+  st = check_device();
+  if (st) return st;
+  BlockGemmArgs a{};
+  a.xq = static_cast<const uint8_t*>(xq);
+  a.sx = sx;
+  a.wq = static_cast<const uint8_t*>(wq);
+  a.sw = sw;
+  a.y = static_cast<uint16_t*>(y);
+  if (need > 0) {
+    a.counters = static_cast<unsigned*>(ws);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + ws_counter_bytes(0));
+  }
+  a.ldq = ldq;
+  a.ldw = ldw;
+  a.ldy = ldy;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.G = groups_of(K);
+  a.split_k = p.split_k;
+  a.whole = (int)p.whole;
+  a.parts = p.parts;
+  a.tiles_m = (int)p.tiles_m;
+  a.tiles_n = (int)p.tiles_n;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipError_t e = fmt == W8_BLOCK_FP8
+                           ? launch_block_gemm(p.tile, (unsigned)p.wgs, packed, a, s)
+                           : launch_token_gemm(fmt, p.tile, (unsigned)p.wgs, packed, a, s);
+  if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("tiled GEMM launch", e));
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+w8_status w8_block_quantize(int M, int K, const void* x, int64_t ldx, const void* gate,
+                            int64_t ldg, void* xq, int64_t ldq, float* sx, w8_stream stream) {
+  w8_status st = check_quantize(M, K, x, ldx, gate, ldg, xq, ldq, sx);
+  if (st) return st;
+  if ((long long)M * groups_of(K) >= (1LL << 31))
+    return fail(W8_E_INVALID, "the groups (M x ceil(K / 128)) must be fewer than 2^31");
+  if (M == 0) return ok();
   st = check_device();
   if (st) return st;
   BlockQuantArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(gate),
@@ -318,7 +404,7 @@ w8_status w8_block_gemm_workspace_size(int M, int N, int K, int packed, size_t* 
   st = check_layout(packed);
   if (st) return st;
   if (!bytes) return fail(W8_E_INVALID, "null output pointer");
-  if (M && use_small_m(M, N, K, packed))
+  if (M && use_small_m(W8_BLOCK_FP8, M, N, K, packed))
     return w8_workspace_size(W8_BLOCK_FP8, W8_OP_GEMM, M, N, K, packed, nullptr, bytes);
   *bytes = M ? plan_bytes(plan_dense(M, N, K)) : 0;
   return ok();
@@ -334,7 +420,7 @@ w8_status w8_block_gemm_plan(int M, int N, int K, int packed, w8_block_plan* pla
   if (packed && K % W8_GROUP) return fail(W8_E_INVALID, "packed weights need K % 128 == 0");
   if (!plan) return fail(W8_E_INVALID, "null output pointer");
   *plan = w8_block_plan{0, 0, 1, 1, 0};
-  if (M && !use_small_m(M, N, K, packed)) *plan = describe(plan_dense(M, N, K));
+  if (M && !use_small_m(W8_BLOCK_FP8, M, N, K, packed)) *plan = describe(plan_dense(M, N, K));
   return ok();
 }
 
@@ -346,49 +432,62 @@ w8_status w8_block_gemm(int M, int N, int K, const void* xq, int64_t ldq, const 
   st = check_nk(N, K);
   if (st) return st;
   if (M == 0) return ok();
-  int packed = 0;
-  st = check_operands(N, K, xq, ldq, sx, wq, ldw, sw, y, ldy, &packed);
+  return dense_gemm(W8_BLOCK_FP8, M, N, K, xq, ldq, sx, wq, ldw, sw, y, ldy, ws, ws_bytes, stream);
+}
+
+w8_status w8_token_gemm_workspace_size(w8_fmt fmt_in, int M, int N, int K, int packed,
+                                       size_t* bytes) {
+  const int fmt = raw_enum(fmt_in);
+  w8_status st = check_token_shape(fmt, M, N, K);
   if (st) return st;
-  if (use_small_m(M, N, K, packed))
-    return w8_gemm_w8a8(W8_BLOCK_FP8, M, N, K, xq, ldq, sx, wq, ldw, sw, y, ldy, nullptr, ws,
-                        ws_bytes, stream);
-  const Plan p = plan_dense(M, N, K);
-  const size_t need = plan_bytes(p);
-  if (need > 0) {
-    if (!ws || ws_bytes < need)
-      return fail(W8_E_WORKSPACE, "workspace of " + std::to_string(need) + " bytes needed, got " +
-                                      std::to_string(ws ? ws_bytes : 0));
-    if (!aligned(ws, 16)) return fail(W8_E_INVALID, "workspace must be 16-byte aligned");
-  }
-  st = check_grid(p);
+  st = check_layout(packed);
   if (st) return st;
+  if (!bytes) return fail(W8_E_INVALID, "null output pointer");
+  if (M && use_small_m(fmt, M, N, K, packed))
+    return w8_workspace_size((w8_fmt)fmt, W8_OP_GEMM, M, N, K, packed, nullptr, bytes);
+  *bytes = M ? plan_bytes(plan_dense(M, N, K)) : 0;
+  return ok();
+}
+
+w8_status w8_token_gemm_plan(w8_fmt fmt_in, int M, int N, int K, int packed, w8_block_plan* plan) {
+  const int fmt = raw_enum(fmt_in);
+  w8_status st = check_token_shape(fmt, M, N, K);
+  if (st) return st;
+  st = check_layout(packed);
+  if (st) return st;
+  if (packed && K % W8_GROUP) return fail(W8_E_INVALID, "packed weights need K % 128 == 0");
+  if (!plan) return fail(W8_E_INVALID, "null output pointer");
+  *plan = w8_block_plan{0, 0, 1, 1, 0};
+  if (M && !use_small_m(fmt, M, N, K, packed)) *plan = describe(plan_dense(M, N, K));
+  return ok();
+}
+
+w8_status w8_token_gemm(w8_fmt fmt_in, int M, int N, int K, const void* xq, int64_t ldq,
+                        const float* sx, const void* wq, int64_t ldw, const float* sw, void* y,
+                        int64_t ldy, void* ws, size_t ws_bytes, w8_stream stream) {
+  const int fmt = raw_enum(fmt_in);
+  const w8_status st = check_token_shape(fmt, M, N, K);
+  if (st) return st;
+  if (M == 0) return ok();
+  return dense_gemm(fmt, M, N, K, xq, ldq, sx, wq, ldw, sw, y, ldy, ws, ws_bytes, stream);
+}
+
+w8_status w8_token_quantize(w8_fmt fmt_in, int M, int K, const void* x, int64_t ldx,
+                            const void* gate, int64_t ldg, int reciprocal, void* xq, int64_t ldq,
+                            float* sx, w8_stream stream) {
+  const int fmt = raw_enum(fmt_in);
+  w8_status st = check_token_format(fmt);
+  if (st) return st;
+  if (reciprocal != 0 && reciprocal != 1) return fail(W8_E_INVALID, "reciprocal must be 0 or 1");
+  st = check_quantize(M, K, x, ldx, gate, ldg, xq, ldq, sx);
+  if (st) return st;
+  if (M == 0) return ok();
   st = check_device();
   if (st) return st;
-  BlockGemmArgs a{};
-  a.xq = static_cast<const uint8_t*>(xq);
-  a.sx = sx;
-  a.wq = static_cast<const uint8_t*>(wq);
-  a.sw = sw;
-  a.y = static_cast<uint16_t*>(y);
-  if (need > 0) {
-    a.counters = static_cast<unsigned*>(ws);
-    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + ws_counter_bytes(0));
-  }
-  a.ldq = ldq;
-  a.ldw = ldw;
-  a.ldy = ldy;
-  a.M = M;
-  a.N = N;
-  a.K = K;
-  a.G = groups_of(K);
-  a.split_k = p.split_k;
-  a.whole = (int)p.whole;
-  a.parts = p.parts;
-  a.tiles_m = (int)p.tiles_m;
-  a.tiles_n = (int)p.tiles_n;
-  const hipError_t e =
-      launch_block_gemm(p.tile, (unsigned)p.wgs, packed, a, static_cast<hipStream_t>(stream));
-  if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("block_gemm launch", e));
+  const TokenQuantArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(gate),
+                         static_cast<uint8_t*>(xq), sx, ldx, ldg, ldq, M, K, reciprocal};
+  const hipError_t e = launch_token_quantize(fmt, a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("token_quantize launch", e));
   return ok();
 }
 

@@ -1,4 +1,4 @@
-// Host-side declarations of the Block_FP8 operators for any token count: the
+// Host-side declarations of the operators for any token count: the
 // argument blocks and launchers of the row operators (w8_rows.hip) and of the
 // tiled GEMM (w8_block_gemm.hip), used by their C-ABI (w8_block.cpp).
 #pragma once
@@ -32,6 +32,19 @@ struct BlockQuantArgs {
 };
 hipError_t launch_block_quantize(BlockQuantArgs a, hipStream_t s);
 
+struct TokenQuantArgs {
+  const uint16_t* x;     // bf16 [M, K]
+  const uint16_t* gate;  // bf16 [M, K], or null
+  uint8_t* xq;           // codes [M, K]
+  float* sx;             // [M]
+  long long ldx, ldg;    // elements
+  long long ldq;         // bytes
+  long long M;
+  int K;
+  int reciprocal;        // scales by a product with 1 / Qmax
+};
+hipError_t launch_token_quantize(int fmt, const TokenQuantArgs& a, hipStream_t s);
+
 struct NormArgs {
   const uint16_t* y;         // bf16 [M, D]
   const void* residual;      // bf16 or fp32 [M, D]
@@ -55,15 +68,15 @@ hipError_t launch_residual_norm(const NormArgs& a, hipStream_t s);
 // ------------------------------------------------------------- tiled GEMM --
 struct BlockGemmArgs {
   const uint8_t* xq;   // activation codes, row stride ldq bytes
-  const float* sx;     // [rows, G]
+  const float* sx;     // [rows, G] (token-scaled formats: [rows])
   const uint8_t* wq;   // weight codes of expert 0
-  const float* sw;     // [ceil(N/128), G] of expert 0
+  const float* sw;     // [ceil(N/128), G] of expert 0 (token-scaled formats: [N])
   uint16_t* y;         // bf16, row stride ldy elements
   float* part;         // split-K partials (workspace)
   unsigned* counters;  // split-K arrival counters (workspace)
   long long ldq, ldw, ldy;
   int M, N, K;
-  int G;               // ceil(K / 128): scale groups and K-steps
+  int G;               // ceil(K / 128): K-steps, and Block_FP8's scale groups
   int split_k;         // power of two; 1 = whole K per workgroup
   int whole, parts;    // the largest tile: ids from `whole` on run in parts (2 or 4, 1: none do)
   int tiles_m;         // token tiles (grouped: slots, M / BM + min(E, M))
@@ -98,6 +111,9 @@ constexpr int kGroupedPieces = 3 * kComputeUnits / 4;  // at most this many more
 const BlockTile& block_tile(int tile);
 // (hipErrorInvalidValue for a tile that is not built)
 hipError_t launch_block_gemm(int tile, unsigned wgs, bool packed, const BlockGemmArgs& a,
+                             hipStream_t s);
+// (FP8_Dynamic or W8A8_INT8)
+hipError_t launch_token_gemm(int fmt, int tile, unsigned wgs, bool packed, const BlockGemmArgs& a,
                              hipStream_t s);
 hipError_t launch_grouped_gemm(int tile, unsigned wgs, bool packed, const BlockGemmArgs& a,
                                hipStream_t s);

@@ -64,6 +64,9 @@ struct Tile {
   static constexpr int PX = (X_BYTES / 1024 + NW - 1) / NW;
   static constexpr int PW = (W_BYTES / 1024 + NW - 1) / NW;
   static constexpr int LOADS = PX + PW;
+  // the token-scaled formats: the tile's scales, one a token and one a weight
+  // row, in whole loads of 64
+  static constexpr int TOKEN_SCALES = (BM + BN + 63) / 64 * 256;
   // The large tiles run the rotated loop (see there): H weight tiles per half
   // step; the first H + 2 of a step are staged with its tokens, the others
   // one step later.  In LDS a stage's weight tiles (16 rows, 2 KiB) are
@@ -117,11 +120,13 @@ __device__ __forceinline__ v2u bf16x4(v4f v) {
 // One tile: rows [m0, m1) of Y (at most BM) times weight rows n0 .. n0 + BN - 1
 // of the expert (wq, sw), over the K-steps [ks0, ks1); split and tile: which
 // part of K of which output tile this is (split_k > 1).
-template <class T, bool GROUPED, bool PACKED>
+template <class T, int FMT, bool GROUPED, bool PACKED>
 __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1, int n0,
                                          const uint8_t* wq, const float* sw, int ks0, int ks1,
                                          int split, int tile) {
   constexpr int BM = T::BM, BN = T::BN, NW = T::NW, NM = T::NM, NN = T::NN, ST = T::ST;
+  constexpr bool BLOCK = FMT == BLOCK_FP8;
+  typedef std::conditional_t<FMT == W8A8_INT8, v4i, v4f> Acc;
   // gathered token rows by pointer, except in the largest tile, which has no
   // registers for that (the host keeps rows more than 4 GiB apart from it)
   constexpr bool POINTERS = GROUPED && !T::LARGE;
@@ -185,14 +190,26 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
   }
   const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem;
 
-  // Token scales: 16 bytes (four steps) per lane, token 32 w + lane / 2 by
+  // The token-scaled formats' scales: all of the tile's, once, at the end of
+  // LDS, where neither the stages nor the output tile reach.
+  constexpr int SCALES_AT = T::LDS - 16 - T::TOKEN_SCALES;
+  if constexpr (!BLOCK) {
+    static_assert(SCALES_AT >= ST * T::STAGE, "the scales lie past the stages");
+    for (int p = wave; p < T::TOKEN_SCALES / 256; p += NW) {
+      const int c = 64 * p + lane;
+      load_lds4(c < BM ? a.sx + x_row(c) : sw + min(n0 + c - BM, a.N - 1),
+                lds0 + SCALES_AT + 256 * p);
+    }
+  }
+
+  // Block_FP8, token scales: 16 bytes (four steps) per lane, token 32 w + lane / 2 by
   // wave w.  Near the end of a row the four are its last four (scales()
   // knows); a row of fewer than four goes in single words.
   const int G = a.G;
-  const float* swt = sw + (long long)(n0 / 128) * G;
+  const float* swt = BLOCK ? sw + (long long)(n0 / 128) * G : nullptr;
   const int sw_blocks = min((a.N + 127) / 128 - n0 / 128, (BN + 127) / 128);
   static_assert(T::SX_BYTES / 1024 <= NW, "a wave loads one piece of the token scales");
-  const float* sxt = a.sx + x_row(min(32 * wave + (lane >> 1), BM - 1)) * G;
+  const float* sxt = BLOCK ? a.sx + x_row(min(32 * wave + (lane >> 1), BM - 1)) * G : nullptr;
   auto scale_start = [&](int g4) { return G >= 4 ? min(g4, G - 4) : g4; };
   auto issue_scales = [&](int c) {
     const unsigned base = lds0 + ST * T::STAGE + (c & 1) * T::SCALES;
@@ -267,14 +284,14 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
 #pragma unroll
       for (int i = 0; i < (T::ROTATED ? T::PW1 : T::PW); ++i) ow[i] += tail_adj;
     }
-    if ((k & 7) == 0 || k == ks0) issue_scales(k >> 3);
+    if (BLOCK && ((k & 7) == 0 || k == ks0)) issue_scales(k >> 3);
   };
 
-  v4f acc[NN][NM];
+  Acc acc[NN][NM];
 #pragma unroll
   for (int i = 0; i < NN; ++i)
 #pragma unroll
-    for (int j = 0; j < NM; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+    for (int j = 0; j < NM; ++j) acc[i][j] = Acc{0, 0, 0, 0};
 
   // ---- LDS reads
   const int c0 = 16 * (q ^ (r & 7)), c1 = 16 * ((q + 4) ^ (r & 7));
@@ -296,6 +313,7 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
   const uint8_t* ssx = smem + ST * T::STAGE + (wm * 16 * NM + r) * 32;
   const uint8_t* ssw = smem + ST * T::STAGE + T::SX_BYTES + 32 * ((wn * 16 * NN) / 128);
   auto scales = [&](int k, float* sc) {
+    if constexpr (!BLOCK) return;
     const int o = (k & 8 ? T::SCALES : 0) + 4 * (k & 7);
     const float swk = *reinterpret_cast<const float*>(ssw + o);
     const uint8_t* sx = ssx + (o + (k >= last_four ? last_shift : 0));
@@ -323,6 +341,17 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
   constexpr int LAG = NN * NM < 4 ? 1 : 3;
   constexpr int P = NN * NM;
   v4f t[LAG + 1];
+  // the token-scaled formats: products go straight into the accumulators
+  auto multiply = [&](Acc& c, v8i w, v8i x) {
+    if constexpr (FMT == W8A8_INT8) {
+      c = mfma_i8(__builtin_shufflevector(w, w, 0, 1, 2, 3), __builtin_shufflevector(x, x, 0, 1, 2, 3),
+                  c);
+      c = mfma_i8(__builtin_shufflevector(w, w, 4, 5, 6, 7), __builtin_shufflevector(x, x, 4, 5, 6, 7),
+                  c);
+    } else {
+      c = mfma_f8(w, x, c);
+    }
+  };
   typedef std::integral_constant<bool, true> Yes;
   typedef std::integral_constant<bool, false> No;
   if constexpr (T::ROTATED) {
@@ -343,7 +372,7 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
     auto j_of = [](int p) constexpr {
       return p >= P2 || p < PJ ? p % NM : (p - PJ) / 2;
     };
-    auto add = [&](int p, const float* sc) {
+    [[maybe_unused]] auto add = [&](int p, const float* sc) {
 #pragma unroll
       for (int u = 0; u < 4; ++u)
         acc[tile_of(p)][j_of(p)][u] =
@@ -386,15 +415,21 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
           const int n = p - (FIRST ? P2 : 0), gap = FIRST ? 1 : 2;
           if (n % gap == 0 && n / gap < T::LOADS) issue_one(n / gap, other, here);
         }
-        t[p % 4] = mfma_f8(wf[tile_of(p) % 4], xf[j_of(p)], v4f{0, 0, 0, 0});
+        if constexpr (BLOCK)
+          t[p % 4] = mfma_f8(wf[tile_of(p) % 4], xf[j_of(p)], v4f{0, 0, 0, 0});
+        else
+          multiply(acc[tile_of(p)][j_of(p)], wf[tile_of(p) % 4], xf[j_of(p)]);
         if (!FIRST && !LAST && p >= PJ && p < P2 && (p & 1)) xf[j_of(p)] = tokens(j_of(p), stage);
-        if (p >= LAG + (FIRST ? P2 : 0))
-          add(p - LAG, p - LAG >= P2 ? sc1 : sc0);
-        else if (!FIRST)
-          add(P + p - LAG, sc0);
+        if constexpr (BLOCK) {
+          if (p >= LAG + (FIRST ? P2 : 0))
+            add(p - LAG, p - LAG >= P2 ? sc1 : sc0);
+          else if (!FIRST)
+            add(P + p - LAG, sc0);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
-      if constexpr (LAST) {
+      if constexpr (!BLOCK) {
+      } else if constexpr (LAST) {
 #pragma unroll
         for (int p = P2 - LAG; p < P2; ++p) add(p, sc0);
       } else {
@@ -441,7 +476,7 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
       else
         wf[set][f - NM] = weights(f - NM, stage);
     };
-    auto add = [&](int n, int set) {
+    [[maybe_unused]] auto add = [&](int n, int set) {
 #pragma unroll
       for (int u = 0; u < 4; ++u)
         acc[n / NM][n % NM][u] =
@@ -476,7 +511,7 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
         const int stage = s % ST, set = s % 2;
         wait_stage<(ST - 2) * T::LOADS>();  // steps k + s + 2 .. k + s + ST - 1 are in flight
         // the scales that the group's loads come to need
-        if (s == 0 && ((k + ST - 1) & 8) != ((k + ST + GROUP - 1) & 8))
+        if (BLOCK && s == 0 && ((k + ST - 1) & 8) != ((k + ST + GROUP - 1) & 8))
           issue_scales((k + ST + GROUP - 1) >> 3);
         advance_bases();
 #pragma unroll
@@ -486,18 +521,24 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
             issue_one(l, lds0 + stage * T::STAGE, 0);
 #pragma unroll
           for (int f = n * F / P; f < (n + 1) * F / P; ++f) read(f, (s + 1) % ST, set ^ 1);
-          t[n % (LAG + 1)] = mfma_f8(wf[set][n / NM], xf[set][n % NM], v4f{0, 0, 0, 0});
-          if (n >= LAG)
-            add(n - LAG, set);
-          else
-            add(P + n - LAG, set ^ 1);
-          if (n == LAG) scales(k + s + 1, sc[set ^ 1]);
+          if constexpr (BLOCK) {
+            t[n % (LAG + 1)] = mfma_f8(wf[set][n / NM], xf[set][n % NM], v4f{0, 0, 0, 0});
+            if (n >= LAG)
+              add(n - LAG, set);
+            else
+              add(P + n - LAG, set ^ 1);
+            if (n == LAG) scales(k + s + 1, sc[set ^ 1]);
+          } else {
+            multiply(acc[n / NM][n % NM], wf[set][n / NM], xf[set][n % NM]);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
+    if constexpr (BLOCK) {
 #pragma unroll
-    for (int n = P - LAG; n < P; ++n) add(n, 1);
+      for (int n = P - LAG; n < P; ++n) add(n, 1);
+    }
     // the steps that are left, at most ST + GROUP
     auto step = [&](auto number) {
       if (k >= ks1) return;
@@ -513,13 +554,19 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
       for (int n = 0; n < P; ++n) {
 #pragma unroll
         for (int f = n * F / P; f < (n + 1) * F / P; ++f) read(f, next, set ^ 1);
-        t[n % (LAG + 1)] = mfma_f8(wf[set][n / NM], xf[set][n % NM], v4f{0, 0, 0, 0});
-        if (n >= LAG) add(n - LAG, set);
+        if constexpr (BLOCK) {
+          t[n % (LAG + 1)] = mfma_f8(wf[set][n / NM], xf[set][n % NM], v4f{0, 0, 0, 0});
+          if (n >= LAG) add(n - LAG, set);
+        } else {
+          multiply(acc[n / NM][n % NM], wf[set][n / NM], xf[set][n % NM]);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
       scales(k + 1, sc[set ^ 1]);
+      if constexpr (BLOCK) {
 #pragma unroll
-      for (int n = P - LAG; n < P; ++n) add(n, set);
+        for (int n = P - LAG; n < P; ++n) add(n, set);
+      }
       ++k;
     };
     for_each_number(std::make_integer_sequence<int, ST + GROUP>{}, step);
@@ -563,7 +610,7 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
 #pragma unroll
     for (int i = 0; i < NN; ++i)
 #pragma unroll
-      for (int j = 0; j < NM; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+      for (int j = 0; j < NM; ++j) acc[i][j] = Acc{0, 0, 0, 0};
     for (int s0 = 0; s0 < a.split_k; s0 += Q) {
       v4i v[Q][NN][NM];
 #pragma unroll
@@ -580,25 +627,46 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
 #pragma unroll
           for (int i = 0; i < NN; ++i)
 #pragma unroll
-            for (int j = 0; j < NM; ++j) acc[i][j] += __builtin_bit_cast(v4f, v[s][i][j]);
+            for (int j = 0; j < NM; ++j) acc[i][j] += __builtin_bit_cast(Acc, v[s][i][j]);
         }
     }
   }
 
   // ---- epilogue: lane (r, q) of tile (i, j) holds token 16 j + r, weight
   // rows 16 i + 4 q .. + 3
+  float sxv[NM];
+  v4f swv[NN];
+  if constexpr (!BLOCK) {
+    const float* sc = reinterpret_cast<const float*>(smem + SCALES_AT);
+#pragma unroll
+    for (int j = 0; j < NM; ++j) sxv[j] = sc[(wm * NM + j) * 16 + r];
+#pragma unroll
+    for (int i = 0; i < NN; ++i)
+      swv[i] = *reinterpret_cast<const v4f*>(sc + BM + (wn * NN + i) * 16 + 4 * q);
+  }
+  auto output = [&](int i, int j) -> v2u {
+    if constexpr (BLOCK) {
+      return bf16x4(acc[i][j]);
+    } else {
+      v4f v;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = (float)acc[i][j][u] * sxv[j] * swv[i][u];
+      return bf16x4(v);
+    }
+  };
   if constexpr (BM * BN >= 128 * 128) {
     // through LDS, so that a store covers whole rows of the tile: 8-byte
     // stores of each lane's own four would touch 16 rows at a time (all
     // outputs of a 256 x 256 round take 8500 clocks, the rate of the writes)
     constexpr int ROW = BN * 2 + 32;
-    static_assert(BM * ROW <= T::LDS - 16, "the output tile fits where the stages were");
+    static_assert(BM * ROW <= (BLOCK ? T::LDS - 16 : SCALES_AT),
+                  "the output tile fits where the stages were");
 #pragma unroll
     for (int j = 0; j < NM; ++j)
 #pragma unroll
       for (int i = 0; i < NN; ++i)
         *reinterpret_cast<v2u*>(smem + ((wm * NM + j) * 16 + r) * ROW +
-                                ((wn * NN + i) * 16 + 4 * q) * 2) = bf16x4(acc[i][j]);
+                                ((wn * NN + i) * 16 + 4 * q) * 2) = output(i, j);
     __syncthreads();
     // (a thread's column is the same every time: THREADS is a multiple of the
     // chunks of a row; the reads of a batch are in flight together)
@@ -641,7 +709,7 @@ __device__ __forceinline__ void run_tile(const BlockGemmArgs& a, int m0, int m1,
 #pragma unroll
         for (int i = 0; i < NN; ++i) {
           const int n = n0 + (wn * NN + i) * 16 + 4 * q;
-          const v2u v = bf16x4(acc[i][j]);
+          const v2u v = output(i, j);
           if (n + 4 <= a.N) {
             *reinterpret_cast<v2u_any*>(yr + n) = v;
           } else {
@@ -679,7 +747,7 @@ __device__ __forceinline__ TilePos tile_pos(const BlockGemmArgs& a, int id) {
   return {b0 + id % band % h, id % band / h};
 }
 
-template <class T, bool PACKED>
+template <class T, bool PACKED, int FMT = BLOCK_FP8>
 __global__ __launch_bounds__(T::THREADS, T::WAVES) void block_gemm_kernel(BlockGemmArgs a) {
   if constexpr (T::LARGE) {
     // The tiles that fill whole rounds of the compute units run at full size;
@@ -703,31 +771,19 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES) void block_gemm_kernel(BlockG
     const int n0 = t.tn * T::BN + (part >> 1) * Quarter::BN;
     if (m0 >= m1 || n0 >= a.N) return;
     if (whole && m1 - m0 > Half::BM)
-      run_tile<T, false, PACKED>(a, m0, m1, n0, a.wq, a.sw, 0, a.G, 0, 0);
+      run_tile<T, FMT, false, PACKED>(a, m0, m1, n0, a.wq, a.sw, 0, a.G, 0, 0);
     else if (whole || a.parts == 2)
-      run_tile<Half, false, PACKED>(a, m0, m1, n0, a.wq, a.sw, 0, a.G, 0, 0);
+      run_tile<Half, FMT, false, PACKED>(a, m0, m1, n0, a.wq, a.sw, 0, a.G, 0, 0);
     else
-      run_tile<Quarter, false, PACKED>(a, m0, m1, n0, a.wq, a.sw, 0, a.G, 0, 0);
+      run_tile<Quarter, FMT, false, PACKED>(a, m0, m1, n0, a.wq, a.sw, 0, a.G, 0, 0);
   } else {
     const int work = xcd_contiguous(blockIdx.x, gridDim.x);
     const int split = work & (a.split_k - 1), tile = work >> __builtin_ctz(a.split_k);
     const TilePos t = tile_pos(a, tile);
     const KRange k = k_range(a, split);
-    run_tile<T, false, PACKED>(a, t.tm * T::BM, min(t.tm * T::BM + T::BM, a.M), t.tn * T::BN, a.wq,
+    run_tile<T, FMT, false, PACKED>(a, t.tm * T::BM, min(t.tm * T::BM + T::BM, a.M), t.tn * T::BN, a.wq,
                                a.sw, k.ks0, k.ks1, split, tile);
   }
-}
-
-// Inclusive sum over the lanes of a wavefront: within rows of 16 lanes by
-// shifts, then the rows' totals passed on (gfx9 DPP row_shr and row_bcast).
-__device__ __forceinline__ int wave_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
-  return v;
 }
 
 // Expert e has ceil(count / BM) token tiles; slot s is the s-th of them over
@@ -815,15 +871,15 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES) void grouped_gemm_kernel(Bloc
       if (m0 >= m1 || n0 >= a.N) return;
     }
     if (parts == 4) {
-      run_tile<Quarter, true, PACKED>(a, m0, m1, n0, wq, sw, 0, a.G, 0, 0);
+      run_tile<Quarter, BLOCK_FP8, true, PACKED>(a, m0, m1, n0, wq, sw, 0, a.G, 0, 0);
       return;
     }
     if (m1 - m0 <= Half::BM) {
-      run_tile<Half, true, PACKED>(a, m0, m1, n0, wq, sw, 0, a.G, 0, 0);
+      run_tile<Half, BLOCK_FP8, true, PACKED>(a, m0, m1, n0, wq, sw, 0, a.G, 0, 0);
       return;
     }
   }
-  run_tile<T, true, PACKED>(a, m0, m1, n0, wq, sw, 0, a.G, 0, 0);
+  run_tile<T, BLOCK_FP8, true, PACKED>(a, m0, m1, n0, wq, sw, 0, a.G, 0, 0);
 }
 
 // The small tiles leave a compute unit room for two workgroups; stages that
@@ -870,10 +926,22 @@ hipError_t launch(unsigned wgs, const BlockGemmArgs& a, hipStream_t s) {
   return launch_kernel(K, dim3(wgs), dim3(T::THREADS), T::LDS, s, a);
 }
 
-template <class T>
+template <int FMT, class T>
 hipError_t launch_dense(unsigned wgs, bool packed, const BlockGemmArgs& a, hipStream_t s) {
-  return packed ? launch<T, block_gemm_kernel<T, true>>(wgs, a, s)
-                : launch<T, block_gemm_kernel<T, false>>(wgs, a, s);
+  return packed ? launch<T, block_gemm_kernel<T, true, FMT>>(wgs, a, s)
+                : launch<T, block_gemm_kernel<T, false, FMT>>(wgs, a, s);
+}
+template <int FMT>
+hipError_t launch_dense_tile(int tile, unsigned wgs, bool packed, const BlockGemmArgs& a,
+                             hipStream_t s) {
+  switch (tile) {
+    case kTile16x128: return launch_dense<FMT, T0>(wgs, packed, a, s);
+    case kTile64x64: return launch_dense<FMT, T1>(wgs, packed, a, s);
+    case kTile64x128: return launch_dense<FMT, T2>(wgs, packed, a, s);
+    case kTile128x128: return launch_dense<FMT, T3>(wgs, packed, a, s);
+    case kTile256x256: return launch_dense<FMT, T4>(wgs, packed, a, s);
+    default: return hipErrorInvalidValue;
+  }
 }
 template <class T>
 hipError_t launch_grouped(unsigned wgs, bool packed, const BlockGemmArgs& a, hipStream_t s) {
@@ -886,14 +954,13 @@ const BlockTile& block_tile(int tile) { return kTiles[tile]; }
 
 hipError_t launch_block_gemm(int tile, unsigned wgs, bool packed, const BlockGemmArgs& a,
                              hipStream_t s) {
-  switch (tile) {
-    case kTile16x128: return launch_dense<T0>(wgs, packed, a, s);
-    case kTile64x64: return launch_dense<T1>(wgs, packed, a, s);
-    case kTile64x128: return launch_dense<T2>(wgs, packed, a, s);
-    case kTile128x128: return launch_dense<T3>(wgs, packed, a, s);
-    case kTile256x256: return launch_dense<T4>(wgs, packed, a, s);
-    default: return hipErrorInvalidValue;
-  }
+  return launch_dense_tile<BLOCK_FP8>(tile, wgs, packed, a, s);
+}
+
+hipError_t launch_token_gemm(int fmt, int tile, unsigned wgs, bool packed, const BlockGemmArgs& a,
+                             hipStream_t s) {
+  return fmt == W8A8_INT8 ? launch_dense_tile<W8A8_INT8>(tile, wgs, packed, a, s)
+                          : launch_dense_tile<FP8_DYNAMIC>(tile, wgs, packed, a, s);
 }
 
 hipError_t launch_grouped_gemm(int tile, unsigned wgs, bool packed, const BlockGemmArgs& a,

@@ -152,6 +152,18 @@ __device__ __forceinline__ float wave_max(float v) {
   return fmaxf(fmaxf(r0, r1), fmaxf(r2, r3));
 }
 
+// Inclusive sum over the lanes of a wavefront: within rows of 16 lanes by
+// shifts, then the rows' totals passed on (gfx9 DPP row_shr and row_bcast).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+
 // ------------------------------------------------- device-coherent I/O --
 // Buffer loads and stores of 16 bytes a lane with the agent-scope cache
 // policy (SC1): the same bits the compiler sets on agent-scope atomic loads

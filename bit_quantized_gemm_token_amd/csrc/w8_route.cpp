@@ -1,0 +1,271 @@
+// C-ABI of the MoE operators around the grouped products: the routing, the
+// combination of the experts' outputs and the whole layer of a few tokens.
+// Argument checks first, then one or two kernel launches; nothing here
+// allocates, frees or synchronizes.
+#include <algorithm>
+#include <cstdint>
+#include <string>
+
+#include "w8_internal.hpp"
+#include "w8_route.hpp"
+
+using namespace w8;
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+constexpr int kMaxRows = (1 << 22) - 1;  // (as the other operators for any token count)
+constexpr int kMaxColumns = 1 << 20;     // of a combined row
+constexpr int kMaxWidth = 1 << 16;       // D and I of the layer: 32-bit offsets of its partials
+constexpr int kRouteBlocks = 2048;       // workgroups of the routing's first launch
+
+w8_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (!ws || have < need)
+    return fail(W8_E_WORKSPACE, "workspace of " + std::to_string(need) + " bytes needed, got " +
+                                    std::to_string(ws ? have : 0));
+  if (!aligned(ws, 16)) return fail(W8_E_INVALID, "workspace must be 16-byte aligned");
+  return W8_OK;
+}
+
+w8_status check_route(int T, int E, int topk) {
+  if (T < 0 || T > kMaxRows)
+    return fail(W8_E_INVALID, "T must be in [0, " + std::to_string(kMaxRows) + "], got " +
+                                  std::to_string(T));
+  if (E < 1 || E > kMaxExperts)
+    return fail(W8_E_INVALID, "E must be in [1, " + std::to_string(kMaxExperts) + "], got " +
+                                  std::to_string(E));
+  if (topk < 1 || topk > kMaxTopk || topk > E)
+    return fail(W8_E_INVALID, "topk must be in [1, " + std::to_string(std::min(kMaxTopk, E)) +
+                                  "] (at most E), got " + std::to_string(topk));
+  return W8_OK;
+}
+
+// Passes of at most kRoutePass entries, as many to a workgroup as keep the
+// workgroups, whose counts the second launch reads, to kRouteBlocks.
+void plan_route(RouteArgs* a) {
+  a->tokens = kRoutePass / a->topk;
+  const long long passes = ceil_div(a->T, a->tokens);
+  a->passes = (int)ceil_div(passes, kRouteBlocks);
+  a->blocks = (int)ceil_div(passes, a->passes);
+}
+
+size_t route_bytes(const RouteArgs& a) {
+  return a.blocks > 1 ? ws_counter_bytes(0) + (size_t)a.blocks * a.E * 4 : 0;
+}
+
+// The layer's workspace (byte offsets): the counter region that every
+// operation keeps, then its arrays.
+struct LayerWs {
+  size_t h, hmax, part, total;
+};
+LayerWs layer_ws(int T, int topk, int D, int I) {
+  const size_t n = (size_t)T * topk;
+  LayerWs w;
+  w.h = ws_counter_bytes(0);
+  w.hmax = w.h + round256(n * I * 4);
+  w.part = w.hmax + round256(n * (I / 16) * 4);
+  w.total = w.part + round256(n * D * 4);
+  return w;
+}
+
+w8_status check_layer(int fmt, int E, int T, int topk, int D, int I) {
+  if (fmt < 0 || fmt > 2) return fail(W8_E_INVALID, "unknown format " + std::to_string(fmt));
+  if (T < 0) return fail(W8_E_INVALID, "T must be >= 0");
+  if (T > kLayerTokens)
+    return fail(W8_E_UNSUPPORTED, "T=" + std::to_string(T) + " is above the few tokens the layer "
+                                  "takes (" + std::to_string(kLayerTokens) + "); use the grouped "
+                                  "products");
+  if (E < 1 || E > kMaxExperts)
+    return fail(W8_E_INVALID, "E must be in [1, " + std::to_string(kMaxExperts) + "], got " +
+                                  std::to_string(E));
+  if (topk < 1 || topk > kMaxTopk)
+    return fail(W8_E_INVALID, "topk must be in [1, " + std::to_string(kMaxTopk) + "], got " +
+                                  std::to_string(topk));
+  const int unit = fmt == W8_BLOCK_FP8 ? W8_GROUP : 16;
+  if (D < unit || D > kMaxWidth || D % unit || I < unit || I > kMaxWidth || I % unit)
+    return fail(W8_E_INVALID, "D and I must be multiples of " + std::to_string(unit) + " up to " +
+                                  std::to_string(kMaxWidth));
+  return W8_OK;
+}
+
+// One of the layer's weights: [E, N, K] codes and their scales.
+w8_status check_experts(int fmt, int E, int N, int K, const void* w, int64_t ldw,
+                        int64_t w_stride, const float* s, int64_t s_stride) {
+  if (!w || !s) return fail(W8_E_INVALID, "null device pointer");
+  if (!aligned(w, 16) || !aligned(s, 4)) return fail(W8_E_INVALID, "misaligned weights or scales");
+  if (ldw != 0 && (ldw < K || ldw % 16))
+    return fail(W8_E_INVALID, "ldw must be >= K and a multiple of 16 (row-major) or 0 (packed)");
+  const int64_t one = ldw == 0 ? (int64_t)packed_weight_bytes(fmt, N, K, 1)
+                               : (int64_t)(N - 1) * ldw + K;
+  if (w_stride % 16 || (E > 1 && w_stride < one))
+    return fail(W8_E_INVALID, "the experts' stride must be a multiple of 16 that holds one's codes");
+  const int64_t scales = fmt == W8_BLOCK_FP8 ? (int64_t)(N / W8_GROUP) * (K / W8_GROUP) : N;
+  if (E > 1 && s_stride < scales)
+    return fail(W8_E_INVALID, "the scales' stride must hold one expert's");
+  return W8_OK;
+}
+
+// Columns of I whose codes a workgroup of the layer's second kernel holds in
+// LDS, beside 64 KiB less what the kernel needs itself: whole 128s.
+int layer_chunk(int T, int I) {
+  const int per_row = 56 * 1024 / T - 16;  // (codes, 16 bytes of padding, Block_FP8's scales)
+  const int most = per_row * 32 / 33 / W8_GROUP * W8_GROUP;
+  return std::min(most, (I + W8_GROUP - 1) / W8_GROUP * W8_GROUP);
+}
+
+}  // namespace
+
+extern "C" {
+
+w8_status w8_moe_route_workspace_size(int T, int E, int topk, size_t* bytes) {
+  const w8_status st = check_route(T, E, topk);
+  if (st) return st;
+  if (!bytes) return fail(W8_E_INVALID, "null output pointer");
+  RouteArgs a{};
+  a.T = T;
+  a.E = E;
+  a.topk = topk;
+  *bytes = 0;
+  if (T) {
+    plan_route(&a);
+    *bytes = route_bytes(a);
+  }
+  return ok();
+}
+
+w8_status w8_moe_route(int T, int E, int topk, const void* logits, int64_t ldl, int logits_fp32,
+                       int renormalize, float scale, int32_t* experts, float* weights,
+                       int32_t* offsets, int32_t* rows, int32_t* slots, void* ws, size_t ws_bytes,
+                       w8_stream stream) {
+  w8_status st = check_route(T, E, topk);
+  if (st) return st;
+  if ((logits_fp32 != 0 && logits_fp32 != 1) || (renormalize != 0 && renormalize != 1))
+    return fail(W8_E_INVALID, "logits_fp32 and renormalize must be 0 or 1");
+  if (T == 0 && !offsets) return ok();
+  if (T && (!logits || !experts || !weights)) return fail(W8_E_INVALID, "null device pointer");
+  if (T && !offsets != !rows) return fail(W8_E_INVALID, "offsets, rows and slots go together");
+  if (T && !offsets != !slots) return fail(W8_E_INVALID, "offsets, rows and slots go together");
+  if (ldl < E) return fail(W8_E_INVALID, "ldl must be >= E");
+  if (!aligned(logits, logits_fp32 ? 4 : 2) || !aligned(experts, 4) || !aligned(weights, 4) ||
+      !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(slots, 4))
+    return fail(W8_E_INVALID, "every pointer must be aligned to its element type");
+  RouteArgs a{logits, !logits_fp32, ldl, T, E, topk, renormalize, scale, experts, weights, offsets,
+              rows, slots, 0, 0, 0, nullptr};
+  a.blocks = 1;  // (no tokens: the offsets alone)
+  if (T) plan_route(&a);
+  const size_t need = offsets ? route_bytes(a) : 0;
+  if (need > 0) {
+    st = check_workspace(ws, ws_bytes, need);
+    if (st) return st;
+    a.counts = reinterpret_cast<int*>(static_cast<char*>(ws) + ws_counter_bytes(0));
+  }
+  st = check_device();
+  if (st) return st;
+  const hipError_t e = launch_route(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("moe_route launch", e));
+  return ok();
+}
+
+w8_status w8_moe_combine(int T, int topk, int D, const void* y, int64_t ldy, int n_rows,
+                         const float* weights, const int32_t* slots, const void* base, int64_t ldb,
+                         void* out, int64_t ldo, w8_stream stream) {
+  if (T < 0 || T > kMaxRows)
+    return fail(W8_E_INVALID, "T must be in [0, " + std::to_string(kMaxRows) + "], got " +
+                                  std::to_string(T));
+  if (topk < 1 || topk > kMaxTopk)
+    return fail(W8_E_INVALID, "topk must be in [1, " + std::to_string(kMaxTopk) + "], got " +
+                                  std::to_string(topk));
+  if (D < 1 || D > kMaxColumns) return fail(W8_E_INVALID, "D must be in [1, 2^20]");
+  if (n_rows < 0) return fail(W8_E_INVALID, "n_rows must be >= 0");
+  if (T == 0) return ok();
+  if (!weights || !slots || !out || (n_rows && !y)) return fail(W8_E_INVALID, "null device pointer");
+  if ((n_rows && ldy < D) || (base && ldb < D) || ldo < D)
+    return fail(W8_E_INVALID, "leading dimensions must be >= D");
+  if (!aligned(y, 2) || !aligned(base, 2) || !aligned(out, 2) || !aligned(weights, 4) ||
+      !aligned(slots, 4))
+    return fail(W8_E_INVALID, "every pointer must be aligned to its element type");
+  // (a workgroup of 256 threads for at most 2048 columns of a token)
+  if (T * ceil_div(D, 2048) * 256 > 0xFFFFFFFFLL)
+    return fail(W8_E_INVALID, "the launch's threads exceed 2^32 - 1: split the call along T");
+  const w8_status st = check_device();
+  if (st) return st;
+  const CombineArgs a{static_cast<const uint16_t*>(y), weights, slots,
+                      static_cast<const uint16_t*>(base), static_cast<uint16_t*>(out), ldy, ldb,
+                      ldo, T, D, topk, n_rows};
+  const hipError_t e = launch_combine(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("moe_combine launch", e));
+  return ok();
+}
+
+w8_status w8_moe_layer_workspace_size(int T, int topk, int D, int I, size_t* bytes) {
+  const w8_status st = check_layer(W8_FP8_DYNAMIC, 1, T, topk, D, I);
+  if (st) return st;
+  if (!bytes) return fail(W8_E_INVALID, "null output pointer");
+  *bytes = T ? layer_ws(T, topk, D, I).total : 0;
+  return ok();
+}
+
+w8_status w8_moe_layer(w8_fmt fmt_in, int E, int T, int topk, int D, int I, const void* xq,
+                       int64_t ldq, const float* sx, const int32_t* experts, const float* weights,
+                       const void* w1, int64_t ldw1, int64_t w1_stride, const float* s1,
+                       int64_t s1_stride, const void* w2, int64_t ldw2, int64_t w2_stride,
+                       const float* s2, int64_t s2_stride, void* y, int64_t ldy, void* ws,
+                       size_t ws_bytes, w8_stream stream) {
+  const int fmt = raw_enum(fmt_in);
+  w8_status st = check_layer(fmt, E, T, topk, D, I);
+  if (st) return st;
+  if (T == 0) return ok();
+  if (!xq || !sx || !experts || !weights || !y) return fail(W8_E_INVALID, "null device pointer");
+  if (!aligned(xq, 16) || ldq < D || ldq % 16)
+    return fail(W8_E_INVALID, "xq must be 16-byte aligned with ldq >= D and ldq % 16 == 0");
+  if (ldy < D) return fail(W8_E_INVALID, "output leading dimension must be >= D");
+  if (!aligned(sx, 4) || !aligned(experts, 4) || !aligned(weights, 4) || !aligned(y, 2))
+    return fail(W8_E_INVALID, "every pointer must be aligned to its element type");
+  st = check_experts(fmt, E, 2 * I, D, w1, ldw1, w1_stride, s1, s1_stride);
+  if (st) return st;
+  st = check_experts(fmt, E, D, I, w2, ldw2, w2_stride, s2, s2_stride);
+  if (st) return st;
+  const LayerWs w = layer_ws(T, topk, D, I);
+  st = check_workspace(ws, ws_bytes, w.total);
+  if (st) return st;
+  st = check_device();
+  if (st) return st;
+  char* p = static_cast<char*>(ws);
+  MoeLayerArgs a{};
+  a.xq = static_cast<const uint8_t*>(xq);
+  a.sx = sx;
+  a.experts = experts;
+  a.weights = weights;
+  a.w1 = static_cast<const uint8_t*>(w1);
+  a.s1 = s1;
+  a.w2 = static_cast<const uint8_t*>(w2);
+  a.s2 = s2;
+  a.y = static_cast<uint16_t*>(y);
+  a.h = reinterpret_cast<float*>(p + w.h);
+  a.hmax = reinterpret_cast<float*>(p + w.hmax);
+  a.part = reinterpret_cast<float*>(p + w.part);
+  a.counters = static_cast<unsigned*>(ws);
+  a.ldq = ldq;
+  a.ldw1 = ldw1;
+  a.ldw2 = ldw2;
+  a.ldy = ldy;
+  a.w1_stride = w1_stride;
+  a.w2_stride = w2_stride;
+  a.s1_stride = s1_stride;
+  a.s2_stride = s2_stride;
+  a.E = E;
+  a.T = T;
+  a.topk = topk;
+  a.D = D;
+  a.I = I;
+  a.chunk = layer_chunk(T, I);
+  const hipError_t e =
+      launch_moe_layer(fmt, ldw1 == 0, ldw2 == 0, a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("moe_layer launch", e));
+  return ok();
+}
+
+}  // extern "C"

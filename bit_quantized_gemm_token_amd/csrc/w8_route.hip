@@ -1,0 +1,276 @@
+// MoE routing: each token's top-k experts and their weights from the router's
+// logits, and the lists per expert that the grouped products take.
+//
+// The chosen are the k largest logits, ties to the lowest expert; -inf and NaN
+// are never chosen.  The entries (token, choice) in order, sorted by expert
+// with their order kept, are the lists: an entry's place is its expert's
+// offset, plus the entries of that expert in front of it.  Those are counted
+// within a pass of up to 256 entries, over the passes of a workgroup and, in a
+// second launch, over the workgroups: whole numbers in a fixed order, so the
+// lists are the same every time.
+#include "w8_block.hpp"
+#include "w8_device.hpp"
+#include "w8_route.hpp"
+#include "w8_values.hpp"
+
+namespace w8 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kNone = 0x7FFFFFFF;
+
+__device__ __forceinline__ unsigned seg16_umin(unsigned v) {
+  v = min(v, dpp_move_u<0xB1>(v));
+  v = min(v, dpp_move_u<0x4E>(v));
+  v = min(v, dpp_move_u<0x141>(v));
+  v = min(v, dpp_move_u<0x140>(v));
+  return v;
+}
+// Over the L lanes (16 or 64) that share a token.
+template <int L>
+__device__ __forceinline__ unsigned lanes_umax(unsigned v) {
+  return L == 16 ? seg16_umax(v) : wave_umax(v);
+}
+template <int L>
+__device__ __forceinline__ unsigned lanes_umin(unsigned v) {
+  v = seg16_umin(v);
+  if (L == 16) return v;
+  const unsigned r0 = __builtin_amdgcn_readlane((int)v, 0);
+  const unsigned r1 = __builtin_amdgcn_readlane((int)v, 16);
+  const unsigned r2 = __builtin_amdgcn_readlane((int)v, 32);
+  const unsigned r3 = __builtin_amdgcn_readlane((int)v, 48);
+  return min(min(r0, r1), min(r2, r3));
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  v += dpp_move<0xB1>(v);
+  v += dpp_move<0x4E>(v);
+  v += dpp_move<0x141>(v);
+  v += dpp_move<0x140>(v);
+  if (L == 16) return v;
+  const int b = __builtin_bit_cast(int, v);
+  const float r0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 0));
+  const float r1 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 16));
+  const float r2 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 32));
+  const float r3 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 48));
+  return (r0 + r1) + (r2 + r3);
+}
+
+// Unsigned keys in the order of the logits; 0: never chosen (-inf, NaN).  The
+// two zeros are one.
+__device__ __forceinline__ unsigned key_of(float l) {
+  if (!(l > -__builtin_inff())) return 0u;
+  const unsigned u = __float_as_uint(l == 0.0f ? 0.0f : l);
+  return u >> 31 ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float logit_of(unsigned key) {
+  return __uint_as_float(key >> 31 ? key & 0x7FFFFFFFu : ~key);
+}
+
+// exp(l - top), 1 at the top itself (where that is +inf too)
+__device__ __forceinline__ float over_top(float l, float top) {
+  return l == top ? 1.0f : expf(l - top);
+}
+
+// The place of each expert's first entry: an exclusive sum over count[0 .. E),
+// by one workgroup; at[E] is the sum of all.  (at may be count.)
+__device__ __forceinline__ void place_experts(const int* count, int* at, int E) {
+  // the first wave, 16 experts a lane (E <= 1024)
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    const int per = (E + 63) / 64;
+    int mine = 0;
+    for (int i = 0; i < per; ++i) mine += lane * per + i < E ? count[lane * per + i] : 0;
+    const int upto = wave_scan(mine);
+    int sum = upto - mine;
+    for (int i = 0; i < per; ++i) {
+      const int e = lane * per + i;
+      if (e < E) {
+        const int c = count[e];
+        at[e] = sum;
+        sum += c;
+      }
+    }
+    if (lane == 63) at[E] = upto;
+  }
+}
+
+// L lanes take a token, PER logits each (E <= L * PER).
+template <int L, int PER, typename Logit>
+__global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
+  __shared__ int ids[kRoutePass];
+  __shared__ float vals[kRoutePass];
+  __shared__ float sums[kRoutePass];         // (not renormalized) of all experts, by token
+  __shared__ int count[kMaxExperts + 1];     // entries of each expert in the passes so far
+  const int sub = threadIdx.x % L, group = threadIdx.x / L;
+  const bool lists = a.offsets != nullptr;
+  if (a.T == 0) {  // (lists of nothing)
+    for (int e = threadIdx.x; e <= a.E; e += kThreads) a.offsets[e] = 0;
+    return;
+  }
+  for (int e = threadIdx.x; e < a.E; e += kThreads) count[e] = 0;
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const long long t0 = ((long long)blockIdx.x * a.passes + pass) * a.tokens;
+    if (t0 >= a.T) break;
+    const int nt = (int)min((long long)a.tokens, a.T - t0);
+    for (int t = group; t < nt; t += kThreads / L) {
+      const Logit* row = static_cast<const Logit*>(a.logits) + (t0 + t) * a.ldl;
+      unsigned key[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int e = i * L + sub;
+        if constexpr (sizeof(Logit) == 2)
+          key[i] = e < a.E ? key_of(bf16_lo(row[e])) : 0u;
+        else
+          key[i] = e < a.E ? key_of(row[e]) : 0u;
+      }
+      float top = 0.0f, all = 0.0f;
+      for (int j = 0; j < a.topk; ++j) {
+        unsigned best = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) best = max(best, key[i]);
+        best = lanes_umax<L>(best);
+        unsigned e = kNone;
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i) e = key[i] == best ? (unsigned)(i * L + sub) : e;
+        e = lanes_umin<L>(e);
+        const float l = logit_of(best);
+        if (j == 0) {
+          top = l;
+          if (!a.renormalize) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) all += key[i] ? over_top(logit_of(key[i]), top) : 0.0f;
+            all = lanes_sum<L>(all);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = (unsigned)(i * L + sub) == e ? 0u : key[i];
+        if (sub == 0) {
+          ids[t * a.topk + j] = best ? (int)e : -1;
+          vals[t * a.topk + j] = best ? over_top(l, top) : 0.0f;
+        }
+      }
+      if (sub == 0) sums[t] = all;
+    }
+    __syncthreads();
+    // an entry a thread
+    const int n = nt * a.topk, i = threadIdx.x;
+    const long long at = t0 * a.topk + i;
+    int id = -1, rank = 0;
+    if (i < n) {
+      const int t = i / a.topk;
+      float sum = sums[t];
+      if (a.renormalize) {
+        sum = 0.0f;
+        for (int j = 0; j < a.topk; ++j) sum += vals[t * a.topk + j];
+      }
+      id = ids[i];
+      a.experts[at] = id;
+      a.weights[at] = id >= 0 ? a.scale * (vals[i] / sum) : 0.0f;
+      if (lists && id >= 0) {
+        rank = count[id];
+        for (int b = 0; b < i; ++b) rank += ids[b] == id;
+      }
+    }
+    if (!lists) {
+      __syncthreads();
+      continue;
+    }
+    __syncthreads();
+    if (id >= 0) atomicAdd(&count[id], 1);
+    __syncthreads();
+    if (a.blocks > 1) {
+      if (i < n) a.slots[at] = id >= 0 ? rank : -1;
+      continue;
+    }
+    // (one workgroup has one pass)
+    place_experts(count, count, a.E);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= a.E; e += kThreads) a.offsets[e] = count[e];
+    if (i < n) {
+      a.slots[at] = id >= 0 ? count[id] + rank : -1;
+      if (id >= 0) a.rows[count[id] + rank] = i / a.topk;
+      if (i >= count[a.E]) a.rows[i] = 0;
+    }
+  }
+  if (lists && a.blocks > 1) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kThreads)
+      a.counts[(long long)blockIdx.x * a.E + e] = count[e];
+  }
+}
+
+// The places of the entries of `span` workgroups of route_kernel, from all
+// workgroups' counts.
+constexpr int kPlaceThreads = 1024;
+__global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteArgs a, int span) {
+  __shared__ int first[kMaxExperts + 1];  // of each expert, then of its next entry here
+  __shared__ int before[kMaxExperts];     // entries of the workgroups in front of these
+  const int b0 = blockIdx.x * span, b1 = min(b0 + span, a.blocks);
+  for (int e = threadIdx.x; e < a.E; e += kPlaceThreads) first[e] = before[e] = 0;
+  __syncthreads();
+  // each thread one expert and every so many-th workgroup
+  int width = 64;
+  while (width < a.E) width *= 2;
+  const int e = threadIdx.x % width;
+  if (e < a.E) {
+    int all = 0, front = 0;
+    for (int b = threadIdx.x / width; b < a.blocks; b += kPlaceThreads / width) {
+      const int c = a.counts[(long long)b * a.E + e];
+      all += c;
+      front += b < b0 ? c : 0;
+    }
+    atomicAdd(&first[e], all);
+    atomicAdd(&before[e], front);
+  }
+  __syncthreads();
+  place_experts(first, first, a.E);
+  __syncthreads();
+  const int total = first[a.E];
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= a.E; i += kPlaceThreads) a.offsets[i] = first[i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.E; i += kPlaceThreads) first[i] += before[i];
+  __syncthreads();
+  const long long entries = (long long)a.T * a.topk;
+  const long long each = (long long)a.passes * a.tokens * a.topk;
+  for (int b = b0; b < b1; ++b) {
+    const long long end = min((b + 1) * each, entries);
+    for (long long i = b * each + threadIdx.x; i < end; i += kPlaceThreads) {
+      const int id = a.experts[i];
+      if (id < 0) continue;
+      const int slot = first[id] + a.slots[i];
+      a.slots[i] = slot;
+      a.rows[slot] = (int)(i / a.topk);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.E; i += kPlaceThreads) first[i] += a.counts[(long long)b * a.E + i];
+    __syncthreads();
+  }
+  for (long long i = total + (long long)blockIdx.x * kPlaceThreads + threadIdx.x; i < entries;
+       i += (long long)gridDim.x * kPlaceThreads)
+    a.rows[i] = 0;
+}
+
+template <typename Logit>
+auto pick(int E) {
+  return E <= 128 ? route_kernel<16, 8, Logit>
+                  : E <= 256 ? route_kernel<64, 4, Logit> : route_kernel<64, 16, Logit>;
+}
+
+}  // namespace
+
+hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
+  hipError_t e = launch_kernel(a.bf16 ? pick<uint16_t>(a.E) : pick<float>(a.E),
+                               dim3((unsigned)a.blocks), dim3(kThreads), 0, s, a);
+  if (e != hipSuccess || !a.offsets || a.blocks == 1) return e;
+  const int span = (a.blocks + 63) / 64;
+  int blocks = (a.blocks + span - 1) / span;
+  RouteArgs args = a;
+  int arg_span = span;
+  void* list[] = {&args, &arg_span};
+  return hipLaunchKernel(reinterpret_cast<const void*>(place_kernel), dim3((unsigned)blocks),
+                         dim3(kPlaceThreads), list, 0, s);
+}
+
+}  // namespace w8

@@ -1,33 +1,16 @@
-// Row operators of the Block_FP8 layer for any token count: the 1 x 128
-// quantizer with the gated activation in front of it, and the residual
-// update with its norms.  Both read every input once and write every output
-// once; HBM bandwidth bounds them on many rows and launch latency on few.
+// Row operators for any token count: the 1 x 128 quantizer and the per-token
+// one, each with the gated activation in front of it, and the residual update
+// with its norms.  They read every input once and write every output once; HBM
+// bandwidth bounds them on many rows and launch latency on few.
 #include <type_traits>
 
 #include "w8_block.hpp"
 #include "w8_device.hpp"
+#include "w8_route.hpp"
+#include "w8_values.hpp"
 
 namespace w8 {
 namespace {
-
-// The bits of |v|: ordered like the magnitudes for finite values, infinities
-// above them and NaN above those, so an unsigned maximum keeps a NaN where
-// fmaxf would drop it.
-__device__ __forceinline__ unsigned abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
-template <int CTRL>
-__device__ __forceinline__ unsigned dpp_move_u(unsigned v) {
-  return (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
-}
-
-// Maximum over aligned segments of 16 lanes.
-__device__ __forceinline__ unsigned seg16_umax(unsigned v) {
-  v = max(v, dpp_move_u<0xB1>(v));
-  v = max(v, dpp_move_u<0x4E>(v));
-  v = max(v, dpp_move_u<0x141>(v));
-  v = max(v, dpp_move_u<0x140>(v));
-  return v;
-}
 
 // Sum over the 64 lanes of a wavefront, in a fixed order.
 __device__ __forceinline__ float wave_sum(float v) {
@@ -41,11 +24,6 @@ __device__ __forceinline__ float wave_sum(float v) {
   const float r2 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 32));
   const float r3 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 48));
   return (r0 + r1) + (r2 + r3);
-}
-
-// fp32 -> bf16, round to nearest even; a NaN stays a NaN.
-__device__ __forceinline__ unsigned bf16_bits(float f) {
-  return abs_bits(f) > 0x7F800000u ? 0x7FC0u : (unsigned)bf16_rne(f);
 }
 
 __device__ __forceinline__ void unpack8(v4u v, float* f) {
@@ -155,36 +133,7 @@ __device__ __forceinline__ v2u encode_group(float* f, float* scale, float factor
   m = seg16_umax(m);
   const float s = act_scale<false>(__uint_as_float(m));
   *scale = m ? s * factor : 1.0f;
-  const float r = act_recip(s);
-  if (r != 0.0f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = act_quot(f[i], s, r);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = f[i] / s;
-  }
-  return v2u{e4m3_pack4(f[0], f[1], f[2], f[3]), e4m3_pack4(f[4], f[5], f[6], f[7])};
-}
-
-// g * sigmoid(g) = g / d, d = 1 + exp(-g).  exp(-g) = 2^t with t = -g log2(e)
-// taken as a rounded product and its remainder, which keeps the exponential's
-// relative error at a few 2^-24 for every g (the rounded product alone loses
-// |t| 2^-25 of it); the quotient from the reciprocal with one correction.
-__device__ __forceinline__ float silu(float g) {
-  const float hi = g * -0x1.715476p+0f;
-  const float lo = __builtin_fmaf(g, -0x1.715476p+0f, -hi) - g * 0x1.4ae0cp-26f;
-  const float e = __builtin_amdgcn_exp2f(hi);
-  const float d = 1.0f + __builtin_fmaf(e, 0x1.62e43p-1f * lo, e);
-  const float r = __builtin_amdgcn_rcpf(d);
-  const float q = g * r;
-  const float s = __builtin_fmaf(__builtin_fmaf(-q, d, g), r, q);
-  if (hi > 126.0f) {
-    // d is 2^hi to every bit and its reciprocal, below 2^-126, would come out
-    // as 0: g 2^-hi, the power with 64 more in its exponent
-    const float p = __builtin_amdgcn_exp2f(64.0f - hi);
-    return p == 0.0f ? g * 0.0f : g * __builtin_fmaf(p, -0x1.62e43p-1f * lo, p) * 0x1p-64f;
-  }
-  return s;
+  return encode_values<false>(f, s, act_recip(s));
 }
 
 // ---------------------------------------------------------------- quantize --
@@ -222,6 +171,95 @@ __global__ __launch_bounds__(kQThreads) void block_quantize_kernel(BlockQuantArg
     if (j == 0) a.sx[id] = s;
     store8_codes(a.xq + m * a.ldq + k, n, q);
   }
+}
+
+// ---------------------------------------------------------- token quantize --
+// One scale a row: s = max |v| / Qmax, or (reciprocal) times 1 / Qmax.  A row by the waves of a workgroup
+// (ONE_WAVE: four rows, a wave each), NC chunks of eight values a lane, whose
+// gated products stay in registers between the maximum and the codes; what a
+// row has beyond those is read and computed again.
+template <bool INT8, bool GATED, bool ONE_WAVE, int NC>
+__global__ __launch_bounds__(ONE_WAVE ? 256 : 1024) void token_quantize_kernel(TokenQuantArgs a) {
+  __shared__ unsigned red[16];
+  const int T = ONE_WAVE ? 64 : blockDim.x;
+  const int t = ONE_WAVE ? threadIdx.x & 63 : threadIdx.x;
+  const long long row =
+      ONE_WAVE ? (long long)blockIdx.x * 4 + (threadIdx.x >> 6) : (long long)blockIdx.x;
+  if (ONE_WAVE && row >= a.M) return;  // (no barrier with one wave per row)
+  const uint16_t* x = a.x + row * a.ldx;
+  const uint16_t* gate = GATED ? a.gate + row * a.ldg : nullptr;
+  uint8_t* q = a.xq + row * a.ldq;
+  // (K is a multiple of 8: a chunk is whole or past the end)
+  auto product = [&](v4u xv, v4u gv, float* f) {
+    unpack8(xv, f);
+    if (GATED) {
+      float g[8];
+      unpack8(gv, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= silu(g[i]);
+    }
+  };
+  auto largest = [](const float* f, unsigned m) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(f[i]));
+    return m;
+  };
+  v4u xv[NC], gv[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int k = 8 * (t + c * T);
+    xv[c] = load8_bf16(x, k, a.K);
+    gv[c] = GATED ? load8_bf16(gate, k, a.K) : v4u{0u, 0u, 0u, 0u};
+  }
+  float f[NC][8];
+  unsigned m = 0;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    if (8 * (t + c * T) >= a.K) xv[c] = gv[c] = v4u{0u, 0u, 0u, 0u};
+    product(xv[c], gv[c], f[c]);
+    m = largest(f[c], m);
+  }
+  auto rest = [&](auto&& use) {
+    if (ONE_WAVE) return;  // (rows that fit)
+    for (int k = 8 * (t + NC * T); k < a.K; k += 8 * T) {
+      float v[8];
+      product(load8_bf16(x, k, a.K), GATED ? load8_bf16(gate, k, a.K) : v4u{0u, 0u, 0u, 0u}, v);
+      use(k, v);
+    }
+  };
+  rest([&](int, const float* v) { m = largest(v, m); });
+  m = wave_umax(m);
+  if (!ONE_WAVE) {
+    if ((t & 63) == 0) red[t >> 6] = m;
+    __syncthreads();
+    for (int w = 0; w < T / 64; ++w) m = max(m, red[w]);
+  }
+  float s = act_scale<INT8>(__uint_as_float(m));
+  if (a.reciprocal && m) s = __uint_as_float(m) * (1.0f / (INT8 ? kQmaxInt8 : kQmaxE4M3));
+  const float r = act_recip(s);
+  if (t == 0) a.sx[row] = s;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int k = 8 * (t + c * T);
+    const v2u v = encode_values<INT8>(f[c], s, r);
+    if (k < a.K) *reinterpret_cast<v2u*>(q + k) = v;
+  }
+  rest([&](int k, float* v) { *reinterpret_cast<v2u*>(q + k) = encode_values<INT8>(v, s, r); });
+}
+
+template <bool INT8, bool ONE_WAVE, int NC>
+hipError_t launch_token(const TokenQuantArgs& a, hipStream_t s) {
+  const int threads = ONE_WAVE ? 256 : min((a.K + 512 * NC - 1) / (512 * NC) * 64, 1024);
+  const dim3 grid((unsigned)(ONE_WAVE ? (a.M + 3) / 4 : a.M)), block((unsigned)threads);
+  return launch_kernel(a.gate ? token_quantize_kernel<INT8, true, ONE_WAVE, NC>
+                              : token_quantize_kernel<INT8, false, ONE_WAVE, NC>,
+                       grid, block, 0, s, a);
+}
+template <bool INT8>
+hipError_t launch_token(const TokenQuantArgs& a, hipStream_t s) {
+  if (a.K <= 512) return launch_token<INT8, true, 1>(a, s);
+  if (a.K <= 8192) return launch_token<INT8, false, 1>(a, s);
+  return launch_token<INT8, false, 4>(a, s);
 }
 
 // -------------------------------------------------------------------- norm --
@@ -391,7 +429,69 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
   return launch_kernel(kernel, grid, block, 0, s, a);
 }
 
+// ----------------------------------------------------------------- combine --
+// out[t] = base[t] + sum_j weights[t, j] y[slots[t, j]], in fp32 in the order of
+// j, rounded once.  A thread takes eight columns of a token, its experts' rows
+// in batches whose loads are all in flight; `shift` lanes (a power of two) take
+// a token, or for wide rows `span` workgroups.
+constexpr int kCombineThreads = 256, kCombineBatch = 8;
+
+template <bool RAGGED>
+__global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineArgs a, int shift,
+                                                                  int span) {
+  const int lane = threadIdx.x & ((1 << shift) - 1);
+  const long long t =
+      (long long)(blockIdx.x / span) * (kCombineThreads >> shift) + (threadIdx.x >> shift);
+  const int k = 8 * (blockIdx.x % span * kCombineThreads + lane);
+  if (t >= a.T || k >= a.D) return;
+  const bool is_short = RAGGED && a.D < 8;
+  auto load = [&](const uint16_t* row) {
+    v4u v = is_short ? short8_bf16(row, k, a.D) : load8_bf16(row, k, a.D);
+    if (RAGGED && !is_short) trim8(v, k, a.D);
+    return v;
+  };
+  float sum[8] = {};
+  if (a.base) unpack8(load(a.base + t * a.ldb), sum);
+  const int* slots = a.slots + t * a.topk;
+  const float* weights = a.weights + t * a.topk;
+  for (int j0 = 0; j0 < a.topk && a.n_rows > 0; j0 += kCombineBatch) {
+    v4u v[kCombineBatch];
+    float w[kCombineBatch];
+    bool on[kCombineBatch];
+#pragma unroll
+    for (int j = 0; j < kCombineBatch; ++j) {
+      const int at = min(j0 + j, a.topk - 1);
+      const int slot = slots[at];
+      w[j] = weights[at];
+      on[j] = j0 + j < a.topk && (unsigned)slot < (unsigned)a.n_rows;
+      v[j] = load(a.y + (on[j] ? slot : 0) * a.ldy);
+    }
+#pragma unroll
+    for (int j = 0; j < kCombineBatch; ++j) {
+      float f[8];
+      unpack8(v[j], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = on[j] ? __builtin_fmaf(w[j], f[i], sum[i]) : sum[i];
+    }
+  }
+  store8_bf16(a.out + t * a.ldo + k, a.D - k, sum);
+}
+
 }  // namespace
+
+hipError_t launch_combine(const CombineArgs& a, hipStream_t s) {
+  const int chunks = (a.D + 7) / 8;
+  int shift = 3;
+  while (shift < 8 && (1 << shift) < chunks) ++shift;
+  int span = (chunks + kCombineThreads - 1) / kCombineThreads;
+  const int tokens = kCombineThreads >> shift;
+  const long long blocks = ((long long)a.T + tokens - 1) / tokens * span;
+  CombineArgs args = a;
+  void* list[] = {&args, &shift, &span};
+  return hipLaunchKernel(
+      reinterpret_cast<const void*>(a.D % 8 ? combine_kernel<true> : combine_kernel<false>),
+      dim3((unsigned)blocks), dim3(kCombineThreads), list, 0, s);
+}
 
 hipError_t launch_block_quantize(BlockQuantArgs a, hipStream_t s) {
   // id / G = umulhi(id, magic) >> shift for id < 2^31, with magic the
@@ -406,6 +506,10 @@ hipError_t launch_block_quantize(BlockQuantArgs a, hipStream_t s) {
   const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20))), block(kQThreads);
   return launch_kernel(a.gate ? block_quantize_kernel<true> : block_quantize_kernel<false>, grid,
                        block, 0, s, a);
+}
+
+hipError_t launch_token_quantize(int fmt, const TokenQuantArgs& a, hipStream_t s) {
+  return fmt == W8A8_INT8 ? launch_token<true>(a, s) : launch_token<false>(a, s);
 }
 
 hipError_t launch_residual_norm(const NormArgs& a, hipStream_t s) {

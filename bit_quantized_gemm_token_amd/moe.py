@@ -1,0 +1,198 @@
+"""The MoE layer around the grouped products (the C-ABI's w8_moe_route,
+w8_moe_combine and w8_moe_layer): the routing that makes the lists which
+moe_gemm, moe_linear and grouped_gemm take, the weighted sum of their outputs,
+and for a few tokens the experts as a whole in two launches.  Like the rest of
+the package this module only checks and marshals arguments.
+"""
+import ctypes
+
+import torch
+
+from . import _capi
+from .block import _BF16, _E_WORKSPACE, _F32, _I32, _codes, _flat, _new, _rows, _shape
+from .tokens import _new_flat, _on_device, _one_device
+
+_BLOCK = _capi.FORMATS["Block_FP8"]
+_GROUP = _capi.GROUP
+
+
+def moe_route_workspace_size(T, E, topk):
+    """Bytes of workspace moe_route needs for its lists (0 for few tokens)."""
+    n = ctypes.c_size_t(0)
+    _check(_lib.w8_moe_route_workspace_size(T, E, topk, ctypes.byref(n)))
+    return n.value
+
+
+def moe_route(logits, topk, renormalize=True, scale=1.0, lists=True, workspace=None, stream=None):
+    """Top-k routing of T tokens over E experts from the router's logits
+    (bf16 or fp32 [T, E]).
+
+    Returns (experts, weights, offsets, rows, slots), or with lists=False
+    (experts, weights):
+
+      experts  int32 [T, topk], the topk largest logits' experts in descending
+               order, ties to the lowest; -inf and NaN are never chosen, and
+               where fewer are left the choice is -1
+      weights  fp32 [T, topk]: scale times the softmax over the chosen
+               (renormalize) or over all experts; 0 for a choice of -1
+      offsets  int32 [E + 1], rows int32 [T * topk]: the entries (token,
+               choice) in order, grouped by expert, as moe_gemm, moe_linear and
+               grouped_gemm take them (rows: the token of each, 0 behind
+               offsets[E])
+      slots    int32 [T, topk]: where in rows each choice went, or -1 (for
+               moe_combine)
+
+    topk at most 32 and E, E at most 1024.  One launch for T * topk up to 256
+    entries, else two; whole numbers only, the same every time.  workspace: as
+    for block_gemm.
+    """
+    lp, ldl = _rows(logits, "logits")
+    if logits.dtype is not _F32 and logits.dtype is not _BF16:
+        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+    T, E = logits.shape
+    dev = logits.device
+    experts, ep, _ = _new(T, topk, _I32, dev, stream)
+    weights, wp, _ = _new(T, topk, _F32, dev, stream)
+    op = rp = sp = buf = None
+    if lists:
+        offsets, op = _new_flat(E + 1, _I32, dev, stream)
+        rows, rp = _new_flat(T * topk, _I32, dev, stream)
+        slots, sp, _ = _new(T, topk, _I32, dev, stream)
+    s = _handle(stream, dev)
+    if lists and T * topk > 256:
+        if workspace is None:
+            workspace = _workspace_of(dev, s)
+        buf = workspace.buf
+    index = logits.get_device()
+    for retry in (True, False):
+        status = _on_device(index, _lib.w8_moe_route, T, E, topk, lp, ldl, logits.dtype is _F32,
+                            bool(renormalize), scale, ep, wp, op, rp, sp,
+                            None if buf is None else buf.data_ptr(),
+                            0 if buf is None else buf.numel(), s)
+        if status != _E_WORKSPACE or not retry:
+            break
+        if workspace is None:
+            workspace = _workspace_of(dev, s)
+        buf = workspace.reserve(moe_route_workspace_size(T, E, topk), stream)
+    _check(status)
+    return (experts, weights, offsets, rows, slots) if lists else (experts, weights)
+
+
+def moe_combine(y, weights, slots, base=None, out=None, stream=None):
+    """Each token's sum of its experts' outputs, bf16 [T, D]:
+
+        out[t] = base[t] + sum_j weights[t, j] y[slots[t, j]]
+
+    y: bf16 [n_rows, D], one row an entry (grouped_gemm, moe_gemm); weights
+    fp32, slots int32 [T, topk] (moe_route); slots outside [0, n_rows) are left
+    out.  base: bf16 [T, D] (a shared expert's output, a residual) or None;
+    out may be base.  In fp32 in the order of the choices, rounded once.
+    """
+    yp, ldy = _rows(y, "y", _BF16)
+    n_rows, D = y.shape
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 2:
+        raise ValueError("slots must be an int32 [T, topk] tensor")
+    T, topk = slots.shape
+    sp = _flat(slots, "slots", _I32, T * topk)
+    wp = _flat(weights, "weights", _F32, T * topk)
+    bp, ldb = None, 0
+    if base is not None:
+        bp, ldb = _rows(base, "base", _BF16)
+        _shape(base, T, D, "base")
+    if out is None:
+        out, outp, ldo = _new(T, D, _BF16, y.device, stream)
+    else:
+        _shape(out, T, D, "out")
+        outp, ldo = _rows(out, "out", _BF16)
+    index = _one_device(y, weights, slots, base, out)
+    _check(_on_device(index, _lib.w8_moe_combine, T, topk, D, yp, ldy, n_rows, wp, sp, bp, ldb,
+                      outp, ldo, _handle(stream, y.device)))
+    return out
+
+
+def moe_layer_workspace_size(T, topk, D, I):
+    """Bytes of workspace moe_layer needs."""
+    n = ctypes.c_size_t(0)
+    _check(_lib.w8_moe_layer_workspace_size(T, topk, D, I, ctypes.byref(n)))
+    return n.value
+
+
+def _layer_weights(f, w, s, name):
+    """(E, N, K, pointer, ldw, stride, scales' pointer and stride, tensor) of
+    [E, N, K] codes or PackedExperts and their scales."""
+    if isinstance(w, PackedExperts):
+        if w.fmt != f:
+            raise ValueError("experts were packed for another format")
+        E, N, K, t = w.E, w.N, w.K, w.data
+        ldw, stride = 0, t.stride(0)
+    else:
+        if not isinstance(w, torch.Tensor) or not w.is_cuda:
+            raise TypeError(f"{name} must be a CUDA (HIP) tensor or PackedExperts")
+        if w.dim() != 3 or w.element_size() != 1 or w.stride(2) != 1:
+            raise ValueError(f"{name} must be [E, N, K] 1-byte codes with unit inner stride")
+        E, N, K = w.shape
+        stride, ld, _ = w.stride()
+        ldw, t = _weight_stride(ld, N, K), w
+    per = N if f != _BLOCK else -(-N // _GROUP) * -(-K // _GROUP)
+    return E, N, K, t.data_ptr(), ldw, stride, _flat(s, "the scales of " + name, _F32, E * per), per, t
+
+
+def moe_layer(fmt, xq, sx, experts, weights, w1, s1, w2, s2, y=None, workspace=None, stream=None):
+    """The experts of a few tokens (T <= 32) as a whole, bf16 [T, D]:
+
+        a = x W1_e^T             [2 I]: gate, then up
+        v = silu(a[:I]) * a[I:]  quantized as the format's activations
+        y[t] = sum_j weights[t, j] (v W2_e^T),   e = experts[t, j]
+
+    fmt: any of the three.  xq, sx: codes [T, D] and scales as the GEMMs take
+    them (quantize_act, token_quantize, residual_norm); experts int32, weights
+    fp32 [T, topk] (moe_route); experts outside [0, E) are left out, an expert
+    chosen twice counts with both weights.  w1: [E, 2 I, D], w2: [E, D, I]
+    codes or PackedExperts; s1, s2: their scales, per output channel ([E, 2 I],
+    [E, D]) or Block_FP8's per 128 x 128 block.  D and I are multiples of 16
+    (Block_FP8: of 128) up to 65536, E at most 1024, topk at most 32.
+
+    Two launches, no lists, no host sync; the hidden values stay fp32 until
+    they are quantized and the sum is fp32 in the order of the choices, so
+    results are the same every time.  workspace: as for block_gemm,
+    moe_layer_workspace_size bytes.
+    """
+    f = _fmt(fmt)
+    xp, ldq = _codes(xq, "xq")
+    T, D = xq.shape
+    sxp = _flat(sx, "sx", _F32, T * -(-D // _GROUP) if f == _BLOCK else T)
+    if not isinstance(experts, torch.Tensor) or experts.dim() != 2 or experts.shape[0] != T:
+        raise ValueError(f"experts must be an int32 [{T}, topk] tensor")
+    topk = experts.shape[1]
+    ep = _flat(experts, "experts", _I32, T * topk)
+    wp = _flat(weights, "weights", _F32, T * topk)
+    E, N1, K1, w1p, ldw1, w1s, s1p, s1s, w1t = _layer_weights(f, w1, s1, "w1")
+    E2, N2, I, w2p, ldw2, w2s, s2p, s2s, w2t = _layer_weights(f, w2, s2, "w2")
+    if E2 != E or N1 != 2 * I or K1 != D or N2 != D:
+        raise ValueError(f"w1 [{E}, {N1}, {K1}] and w2 [{E2}, {N2}, {I}] must be [E, 2 I, {D}] and "
+                         f"[E, {D}, I]")
+    if y is None:
+        y, yp, ldy = _new(T, D, _BF16, xq.device, stream)
+    else:
+        _shape(y, T, D, "y")
+        yp, ldy = _rows(y, "y", _BF16)
+    index = _one_device(xq, sx, experts, weights, w1t, s1, w2t, s2, y)
+    s = _handle(stream, xq.device)
+    if workspace is None:
+        workspace = _workspace_of(xq.device, s)
+    buf = workspace.buf
+    for retry in (True, False):
+        status = _on_device(index, _lib.w8_moe_layer, f, E, T, topk, D, I, xp, ldq, sxp, ep, wp,
+                            w1p, ldw1, w1s, s1p, s1s, w2p, ldw2, w2s, s2p, s2s, yp, ldy,
+                            None if buf is None else buf.data_ptr(),
+                            0 if buf is None else buf.numel(), s)
+        if status != _E_WORKSPACE or not retry:
+            break
+        buf = workspace.reserve(moe_layer_workspace_size(T, topk, D, I), stream)
+    _check(status)
+    return y
+
+
+# (the package's own helpers; __init__ imports this module after defining them)
+from . import (PackedExperts, _check, _fmt, _handle, _lib, _weight_stride,  # noqa: E402
+               _workspace_of)

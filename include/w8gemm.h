@@ -3,8 +3,11 @@
  *
  *     Y[M, N] = dequant(Xq)[M, K] . dequant(Wq)[N, K]^T,   1 <= M <= 32
  *
- * and, for the Block_FP8 format, the operators of a layer at any token count
- * (w8_block_gemm, w8_grouped_gemm, w8_residual_norm, w8_block_quantize).
+ * and the operators of a layer at any token count: for the Block_FP8 format
+ * w8_block_gemm, w8_grouped_gemm, w8_residual_norm and w8_block_quantize, for
+ * the other two w8_token_gemm and w8_token_quantize; the MoE routing and the
+ * combination of the experts' outputs (w8_moe_route, w8_moe_combine), and the
+ * whole MoE layer of a few tokens (w8_moe_layer).
  *
  * The method: ai-radar.it, "Helion nel backend vLLM: un solo GEMM, tuning per
  * forma e guadagni fino al 10%".
@@ -700,6 +703,119 @@ w8_status w8_grouped_gemm(int E, int T, int N, int K, const void *xq, int64_t ld
  * the offsets). */
 w8_status w8_grouped_gemm_plan(int E, int T, int N, int K, int64_t ldq, int n_rows,
                                w8_block_plan *plan);
+
+/* ------------------- FP8_Dynamic and W8A8_INT8 at any token count -- */
+/* The quantizer and the GEMM of the formats with one scale per token and per
+ * output channel outside the small-M window: any number of rows (0: nothing is
+ * computed or launched, buffers may be NULL), up to 2^22 - 1 per call.  Same
+ * allocation, ordering, capture and error rules as w8_gemm_w8a8; no
+ * configuration.  fmt is W8_FP8_DYNAMIC or W8_W8A8_INT8 (W8_BLOCK_FP8:
+ * W8_E_INVALID).                                                           */
+
+/* Codes and scales of x, or with gate != NULL of silu(gate) * x: per row
+ * s = amax / Qmax (1 for a row of zeros), codes = round-to-nearest-even(x / s),
+ * as w8_quantize_act gives them.  The gated product is fp32, not rounded before
+ * it is quantized.  One launch.
+ *   x, gate  bf16 [M, K] as for w8_block_quantize
+ *   reciprocal  0, or 1: s = amax * (1 / Qmax), the reciprocal rounded to fp32
+ *            first.  That is how torch divides by a constant on a GPU: the
+ *            codes and scales are those of amax / Qmax and x / s there, where
+ *            the division's own may lie one rounding beside them
+ *   xq       codes [M, K], row stride ldq bytes, 8-byte aligned, ldq % 8 == 0
+ *            (the GEMM needs 16)
+ *   sx       fp32 [M]
+ * 8 <= K <= 2^22, K % 8 == 0.  A row with a NaN or an infinity gets a
+ * non-finite scale, so it dequantizes to non-finite values.                */
+w8_status w8_token_quantize(w8_fmt fmt, int M, int K, const void *x, int64_t ldx,
+                            const void *gate, int64_t ldg, int reciprocal, void *xq, int64_t ldq,
+                            float *sx, w8_stream stream);
+
+/* Y[m, n] = sx[m] sw[n] sum_k Xq[m, k] Wq[n, k] for any M, arguments as for
+ * w8_block_gemm with scales sx [M] and sw [N].  W8A8_INT8's sums are exact
+ * (int32): K <= 131056, where K products of any two codes stay in range; the
+ * output is their fp32 value times sx times sw, rounded to bf16.  FP8_Dynamic's
+ * are fp32, by the fp8 matrix instructions; results are run-to-run
+ * deterministic.  ws: w8_token_gemm_workspace_size bytes.  Up to W8_MAX_M tokens
+ * on small weights run w8_gemm_w8a8's kernel (and configuration table).    */
+w8_status w8_token_gemm(w8_fmt fmt, int M, int N, int K, const void *xq, int64_t ldq,
+                        const float *sx, const void *wq, int64_t ldw, const float *sw, void *y,
+                        int64_t ldy, void *ws, size_t ws_bytes, w8_stream stream);
+/* Bytes of workspace (packed: the weight layout, 0 or 1). */
+w8_status w8_token_gemm_workspace_size(w8_fmt fmt, int M, int N, int K, int packed,
+                                       size_t *bytes);
+/* What a call runs.  Host only; no device is touched. */
+w8_status w8_token_gemm_plan(w8_fmt fmt, int M, int N, int K, int packed, w8_block_plan *plan);
+
+/* ------------------------- the MoE layer around the grouped products -- */
+/* Same allocation, ordering, capture and error rules as w8_gemm_w8a8; results
+ * are run-to-run deterministic.                                            */
+
+/* Top-k routing of T tokens (0 .. 2^22 - 1) over E experts (1 .. 1024).
+ *   logits   bf16, or with logits_fp32 == 1 fp32, [T, E], row stride ldl
+ *            elements
+ *   experts  int32 [T, topk]: the topk largest logits' experts in descending
+ *            order, ties to the lowest expert (the two zeros are one value);
+ *            -inf and NaN are never chosen, and where fewer logits are left
+ *            the choice is -1
+ *   weights  fp32 [T, topk]: scale * exp(l - l_max) / sum, the sum over the
+ *            chosen (renormalize == 1) or over all experts but -inf and NaN
+ *            (0); at l_max itself, +inf too, exp(l - l_max) is 1; 0 for a
+ *            choice of -1
+ *   offsets  int32 [E + 1], rows int32 [T * topk], slots int32 [T, topk]; or
+ *            all three NULL.  The entries (t, j) in order, grouped by expert
+ *            and in order within it: offsets[e] counts the entries of experts
+ *            below e, rows[i] is the token of entry i (0 from offsets[E] on),
+ *            slots[t, j] the place of choice j of token t (-1 for a choice of
+ *            -1).  offsets and rows are what the grouped products take.  T == 0:
+ *            the offsets, all 0, are still written.
+ *   ws       w8_moe_route_workspace_size bytes (0 up to 256 entries and
+ *            without lists), with w8_gemm_w8a8's rules
+ * 1 <= topk <= min(E, 32).  One launch for up to 256 entries or without lists,
+ * else two.                                                                */
+w8_status w8_moe_route(int T, int E, int topk, const void *logits, int64_t ldl, int logits_fp32,
+                       int renormalize, float scale, int32_t *experts, float *weights,
+                       int32_t *offsets, int32_t *rows, int32_t *slots, void *ws,
+                       size_t ws_bytes, w8_stream stream);
+w8_status w8_moe_route_workspace_size(int T, int E, int topk, size_t *bytes);
+
+/* out[t] = base[t] + sum_j weights[t, j] y[slots[t, j]] in fp32, in the order
+ * of j, rounded once.  One launch.
+ *   y        bf16 [n_rows, D] (n_rows 0: may be NULL)
+ *   weights  fp32 [T, topk];  slots  int32 [T, topk], those outside [0, n_rows)
+ *            left out
+ *   base     bf16 [T, D] or NULL (0);  out  bf16 [T, D], may be base (same
+ *            stride)
+ * 0 <= T < 2^22, 1 <= topk <= 32, 1 <= D <= 2^20; strides in elements, >= D.  */
+w8_status w8_moe_combine(int T, int topk, int D, const void *y, int64_t ldy, int n_rows,
+                         const float *weights, const int32_t *slots, const void *base,
+                         int64_t ldb, void *out, int64_t ldo, w8_stream stream);
+
+/* The experts of T tokens as a whole, T <= 32 (above: W8_E_UNSUPPORTED, use the
+ * grouped products), in any of the three formats, in two launches:
+ *   a    = dequant(xq[t]) . dequant(W1_e)^T        [2 I]: gate, then up
+ *   v    = silu(a[:I]) * a[I:], fp32, quantized as w8_quantize_act does (one
+ *          scale for the row, Block_FP8 one per 128 columns)
+ *   y[t] = sum_j weights[t, j] dequant(v) . dequant(W2_e)^T, e = experts[t, j]
+ *   xq, sx   T rows of D codes and their scales
+ *   experts  int32 [T, topk] (device); those outside [0, E) are left out, one
+ *            chosen twice by a token counts with both weights
+ *   weights  fp32 [T, topk]
+ *   w1, s1   expert e's codes [2 I, D] at w1 + e * w1_stride bytes (row-major
+ *            with row stride ldw1, or ldw1 = 0: the packed layout 1), scales at
+ *            s1 + e * s1_stride floats: [2 I], Block_FP8 [2 I / 128, D / 128]
+ *   w2, s2   likewise [D, I]
+ *   y        bf16 [T, D], row stride ldy elements
+ *   ws       w8_moe_layer_workspace_size bytes, with w8_gemm_w8a8's rules (one
+ *            workspace may serve every entry point)
+ * 1 <= E <= 1024, 1 <= topk <= 32; D and I multiples of 16 (Block_FP8: of 128)
+ * up to 65536.  An expert without tokens reads no weights.                 */
+w8_status w8_moe_layer(w8_fmt fmt, int E, int T, int topk, int D, int I, const void *xq,
+                       int64_t ldq, const float *sx, const int32_t *experts,
+                       const float *weights, const void *w1, int64_t ldw1, int64_t w1_stride,
+                       const float *s1, int64_t s1_stride, const void *w2, int64_t ldw2,
+                       int64_t w2_stride, const float *s2, int64_t s2_stride, void *y,
+                       int64_t ldy, void *ws, size_t ws_bytes, w8_stream stream);
+w8_status w8_moe_layer_workspace_size(int T, int topk, int D, int I, size_t *bytes);
 
 /* -------------------------------------------------------- measurement -- */
 /* The read floor the GEMM is measured against: one kernel launch on `stream`

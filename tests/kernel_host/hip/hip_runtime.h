@@ -148,7 +148,7 @@ inline void barrier() {
 
 // One operation of a whole wavefront: every lane puts its words in, the last
 // to arrive has them combined, every lane takes its result.
-enum Op { kMfma = 1, kReadlane, kBallot, kDpp };
+enum Op { kMfma = 1, kMfmaInt8, kReadlane, kBallot, kDpp };
 void combine(Machine::Wave& in, Machine::Wave& out);
 inline unsigned* wave_op(int op, const void* words, size_t bytes) {
   Machine& g = m();
@@ -193,6 +193,20 @@ inline void combine(Machine::Wave& in, Machine::Wave& out) {
         for (int k = 0; k < 128; ++k) s += x[k] * y[k];
         memcpy(&out.w[l][u], &s, 4);
       }
+  } else if (in.op[0] == kMfmaInt8) {  // the same map of lanes, 16 bytes each
+    static int a[16][64], b[16][64];
+    for (int l = 0; l < 64; ++l)
+      for (int i = 0; i < 16; ++i) {
+        a[l % 16][l / 16 * 16 + i] = (int8_t)(in.w[l][i / 4] >> 8 * (i % 4));
+        b[l % 16][l / 16 * 16 + i] = (int8_t)(in.w[l][4 + i / 4] >> 8 * (i % 4));
+      }
+    for (int l = 0; l < 64; ++l)
+      for (int u = 0; u < 4; ++u) {
+        const int *x = a[4 * (l / 16) + u], *y = b[l % 16];
+        int s = 0;
+        for (int k = 0; k < 64; ++k) s += x[k] * y[k];
+        out.w[l][u] = (unsigned)s;
+      }
   } else if (in.op[0] == kReadlane) {
     for (int l = 0; l < 64; ++l) out.w[l][0] = in.w[in.w[l][1]][0];
   } else if (in.op[0] == kBallot) {
@@ -225,6 +239,14 @@ inline v4f mfma(v8i a, v8i b, v4f c) {
   memcpy(w + 8, &b, 32);
   v4f r;
   memcpy(&r, wave_op(kMfma, w, 64), 16);
+  return r + c;
+}
+inline v4i mfma_int8(v4i a, v4i b, v4i c) {
+  unsigned w[8];
+  memcpy(w, &a, 16);
+  memcpy(w + 4, &b, 16);
+  v4i r;
+  memcpy(&r, wave_op(kMfmaInt8, w, 32), 16);
   return r + c;
 }
 inline int readlane(int v, int lane) {
@@ -370,7 +392,7 @@ inline unsigned emu_fetch_add(unsigned* p, unsigned v) {
 #define __builtin_amdgcn_raw_buffer_store_b128(v, r, off, s, c) emu::rsrc_store(r, off, v)
 #define __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, d, e, f, g, h, i) \
   emu::mfma(a, b, c)
-#define __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, d, e, f) (c)
+#define __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, d, e, f) emu::mfma_int8(a, b, c)
 #define __builtin_amdgcn_cvt_pk_fp8_f32(a, b, old, hi) (old)
 #define __builtin_amdgcn_readfirstlane(v) (v)
 #define __builtin_amdgcn_readlane(v, l) emu::readlane(v, l)
