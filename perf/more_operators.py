@@ -291,7 +291,9 @@ def _own(s):
     if op == "gemm":
         return w8.token_gemm(s["fmt"], s["xq"], s["sx"], s["wq"], s["sw"])
     if op == "quantize":
-        return w8.token_quantize(s["fmt"], s["x"], gate=s["gate"])
+        # (torch divides by a constant through its reciprocal on the GPU; whole numbers are equal
+        # only with scales that are rounded the same way)
+        return w8.token_quantize(s["fmt"], s["x"], gate=s["gate"], reciprocal=True)
     if op == "route":
         return w8.moe_route(s["scores"], s["topk"])
     if op == "combine":
