@@ -1,7 +1,7 @@
 // The experts of a few tokens as a whole, in two launches:
 //
 //   up    a = x W1_e^T for the tokens of expert e, gate and up halves;
-//         h = silu(a_gate) a_up in fp32, and its maxima over 16 columns
+//         h = silu(a_gate) a_up in fp32
 //   down  hq = codes of h in the format; p = hq W2_e^T;
 //         y[t] = sum_j weights[t, j] p[t, j], by the last workgroup of a column
 //         tile to arrive
@@ -26,19 +26,42 @@ constexpr int kMaxEntries = kLayerTokens * kMaxTopk;
 // The choices of a launch in LDS: which experts have tokens, and the tokens of
 // this workgroup's.
 struct Choices {
-  int ids[kMaxEntries];                // (-1: no expert of this call's)
-  unsigned set[kMaxExperts / 32];      // experts with tokens
-  int entry[kLayerTokens];          // first entry of each of the expert's tokens
+  int ids[kMaxEntries];                  // (-1: no expert of this call's)
+  unsigned set[kMaxExperts / 32];        // experts with tokens
+  int entry[kWaves][kLayerTokens];       // first entry of each of the expert's tokens
 };
 struct Expert {
-  int e;       // -1: fewer experts have tokens
+  int e;       // -1: none for this workgroup
   int tokens;  // of the expert
-  int active;  // experts with tokens
 };
 
-// The slot-th expert that has tokens, in expert order; every wave computes it.
-__device__ __forceinline__ Expert find_expert(const MoeLayerArgs& a, int slot, Choices& c) {
+// Lane t's first entry with the expert (-1: none) becomes the wave's list.
+__device__ __forceinline__ int list_tokens(int first, Choices& c) {
   const int lane = threadIdx.x & 63;
+  const unsigned long long mine = __ballot(first >= 0);
+  if (first >= 0) c.entry[threadIdx.x >> 6][__popcll(mine & ((1ull << lane) - 1))] = first;
+  return __popcll(mine);
+}
+
+// The expert of a launch's slot; every wave finds it for itself.
+//
+// Up to 64 entries, no more than experts: slot s is entry s, if it is the first
+// of its expert.  The entries lie in the lanes, and nothing waits for another
+// wave.
+__device__ __forceinline__ Expert find_among_few(const MoeLayerArgs& a, int slot, Choices& c) {
+  const int lane = threadIdx.x & 63, n = a.T * a.topk;
+  const int id = lane < n ? a.experts[lane] : -1;
+  const int e = __builtin_amdgcn_readlane(id, slot);
+  const unsigned long long same = __ballot(lane < n && id == e);
+  if ((unsigned)e >= (unsigned)a.E || __builtin_ctzll(same) != slot) return {-1, 0};
+  const unsigned long long mine =
+      lane < a.T ? same >> (lane * a.topk) & ((1ull << (a.topk - 1) << 1) - 1) : 0;
+  return {e, list_tokens(mine ? lane * a.topk + __builtin_ctzll(mine) : -1, c)};
+}
+
+// Otherwise slot s is the s-th of the experts that have tokens, from a set of
+// them in LDS (*active: how many there are).
+__device__ __forceinline__ void load_choices(const MoeLayerArgs& a, Choices& c) {
   if (threadIdx.x < kMaxExperts / 32) c.set[threadIdx.x] = 0u;
   __syncthreads();
   for (int i = threadIdx.x; i < a.T * a.topk; i += kThreads) {
@@ -48,70 +71,94 @@ __device__ __forceinline__ Expert find_expert(const MoeLayerArgs& a, int slot, C
     if (on) atomicOr(&c.set[id >> 5], 1u << (id & 31));
   }
   __syncthreads();
+}
+__device__ __forceinline__ int count_active(const Choices& c) {
+  const int lane = threadIdx.x & 63;
+  return __builtin_amdgcn_readlane(
+      wave_scan(lane < kMaxExperts / 32 ? __popc(c.set[lane]) : 0), 63);
+}
+__device__ __forceinline__ Expert find_among_all(const MoeLayerArgs& a, int slot, Choices& c) {
+  const int lane = threadIdx.x & 63;
+  load_choices(a, c);
   const unsigned word = lane < kMaxExperts / 32 ? c.set[lane] : 0u;
   const int upto = wave_scan(__popc(word));
-  Expert x{-1, 0, __builtin_amdgcn_readlane(upto, 63)};
   const unsigned long long past = __ballot(upto > slot);
-  if (past) {
-    const int l = __builtin_ctzll(past);
-    unsigned bits = __builtin_amdgcn_readlane((int)word, l);
-    for (int i = l ? __builtin_amdgcn_readlane(upto, l - 1) : 0; i < slot; ++i) bits &= bits - 1;
-    x.e = 32 * l + __builtin_ctz(bits);
-    int first = -1;
-    if (lane < a.T)
-      for (int j = a.topk - 1; j >= 0; --j)
-        if (c.ids[lane * a.topk + j] == x.e) first = lane * a.topk + j;
-    const unsigned long long mine = __ballot(first >= 0);
-    x.tokens = __popcll(mine);
-    if (threadIdx.x < 64 && first >= 0) c.entry[__popcll(mine & ((1ull << lane) - 1))] = first;
+  if (!past) return {-1, 0};
+  const int l = __builtin_ctzll(past);
+  unsigned bits = __builtin_amdgcn_readlane((int)word, l);
+  for (int i = l ? __builtin_amdgcn_readlane(upto, l - 1) : 0; i < slot; ++i) bits &= bits - 1;
+  const int e = 32 * l + __builtin_ctz(bits);
+  int first = -1;
+  if (lane < a.T)
+    for (int j = a.topk - 1; j >= 0; --j)
+      if (c.ids[lane * a.topk + j] == e) first = lane * a.topk + j;
+  return {e, list_tokens(first, c)};
+}
+__device__ __forceinline__ Expert find_expert(const MoeLayerArgs& a, int slot, Choices& c) {
+  return a.few ? find_among_few(a, slot, c) : find_among_all(a, slot, c);
+}
+
+// ids becomes, for every entry, the one whose outputs serve it: the first of its
+// token with the same expert (-1: none).
+__device__ __forceinline__ void find_outputs(const MoeLayerArgs& a, Choices& c) {
+  const int n = a.T * a.topk;
+  int at[kMaxEntries / kThreads];
+#pragma unroll
+  for (int q = 0; q < kMaxEntries / kThreads; ++q) {
+    const int i = threadIdx.x + q * kThreads;
+    at[q] = -1;
+    if (i < n && c.ids[i] >= 0) {
+      at[q] = i / a.topk * a.topk;
+      while (c.ids[at[q]] != c.ids[i]) ++at[q];
+    }
   }
   __syncthreads();
-  return x;
+#pragma unroll
+  for (int q = 0; q < kMaxEntries / kThreads; ++q)
+    if ((int)threadIdx.x + q * kThreads < n) c.ids[threadIdx.x + q * kThreads] = at[q];
+  __syncthreads();
 }
 
-// The entry whose outputs serve entry i: the first of its token with the same
-// expert.
-__device__ __forceinline__ int served_by(const Choices& c, int i, int t, int topk) {
-  int at = t * topk;
-  while (c.ids[at] != c.ids[i]) ++at;
-  return at;
-}
-
-// Accumulates the products of K-steps [la, lb) of NB blocks of 16 weight rows
-// with MB blocks of 16 token rows.  weights(j, k), tokens(b, k): operands of
-// step k, tails with zeros past K; scale(j, b, k): the Block_FP8 factor.  The
-// steps up to kfull are whole.  Stages of U steps alternate between two
-// register sets, the loads of the next in flight while one is multiplied; the
-// first may begin before la, with zeros there, so that the loop has no
-// conditions.
-template <int FMT, int NB, int MB, int U, class W, class X, class S, class WT, class XT>
-__device__ __forceinline__ void products(typename Traits<FMT>::Acc (&acc)[MB][NB], int la, int lb,
-                                         int kfull, W weights, X tokens, S scale, WT weights_tail,
-                                         XT tokens_tail) {
+// The products of NB blocks of 16 weight rows with MB blocks of 16 token rows
+// over the whole K-steps [la, lfull).  weights(j, k) and tokens(b, k) are the
+// operands of step k, wscale(j, k) and xscale(b, k) Block_FP8's factors.  R
+// steps are in flight: begin() issues the first R, run() multiplies each and
+// issues the one R steps on into the same registers.  (Loads past the last step
+// repeat it.)  EARLY: tokens come from memory, with the weights; else from LDS,
+// when they are multiplied.
+template <int FMT, int NB, int MB, int R, bool EARLY, class W, class X, class WS, class XS>
+struct Products {
   typedef typename Traits<FMT>::Frag Frag;
   typedef typename Traits<FMT>::Acc Acc;
-  constexpr bool BLOCK = FMT == BLOCK_FP8;
-  struct Stage {
-    Frag w[U][NB], x[U][MB];
-    float sc[BLOCK ? U : 1][MB][NB];
-  };
-  auto load = [&](Stage& st, int k0) {
+  static constexpr bool BLOCK = FMT == BLOCK_FP8;
+  W weights;
+  X tokens;
+  WS wscale;
+  XS xscale;
+  int la, lfull;
+  Frag w[R][NB], x[EARLY ? R : 1][MB];
+  float ws[BLOCK ? R : 1][NB], xs[BLOCK && EARLY ? R : 1][MB];
+
+  __device__ __forceinline__ Products(int la, int lfull, W w, X x, WS ws, XS xs)
+      : weights(w), tokens(x), wscale(ws), xscale(xs), la(la), lfull(lfull) {}
+  __device__ __forceinline__ void load(int u, int step) {
+    const int k = min(step, lfull - 1);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = max(k0 + u, la);
+    for (int j = 0; j < NB; ++j) w[u][j] = weights(j, k);
+    if constexpr (BLOCK) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) st.w[u][j] = weights(j, k);
+      for (int j = 0; j < NB; ++j) ws[u][j] = wscale(j, k);
+    }
+    if constexpr (EARLY) {
 #pragma unroll
-      for (int b = 0; b < MB; ++b) st.x[u][b] = tokens(b, k);
-      if constexpr (BLOCK) {
-#pragma unroll
-        for (int b = 0; b < MB; ++b)
-#pragma unroll
-          for (int j = 0; j < NB; ++j) st.sc[u][b][j] = scale(j, b, k);
+      for (int b = 0; b < MB; ++b) {
+        x[u][b] = tokens(b, k);
+        if constexpr (BLOCK) xs[u][b] = xscale(b, k);
       }
     }
-  };
-  auto multiply = [&](const Frag& w, const Frag& x, Acc& c, float sc) {
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  static __device__ __forceinline__ void multiply(Acc& c, const Frag& w, const Frag& x, float sc) {
     if constexpr (BLOCK) {
       const Acc p = mma<FMT, 1>(w, x, Acc{0, 0, 0, 0});
 #pragma unroll
@@ -119,56 +166,54 @@ __device__ __forceinline__ void products(typename Traits<FMT>::Acc (&acc)[MB][NB
     } else {
       c = mma<FMT, 1>(w, x, c);
     }
-  };
-  auto run = [&](const Stage& st, int k0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const Frag zero = {};
-        const Frag w = k0 + u < la ? zero : st.w[u][j];
-#pragma unroll
-        for (int b = 0; b < MB; ++b)
-          multiply(w, st.x[u][b], acc[b][j], BLOCK ? st.sc[u][b][j] : 0.0f);
-      }
-  };
-  const int lfull = min(lb, kfull);
-  const int ns = (max(lfull - la, 0) + U - 1) / U, k0 = lfull - ns * U;
-  Stage A, B;
-  if (ns > 0) load(A, k0);
-  if (ns > 1) load(B, k0 + U);
-  if (ns == 1) {
-    run(A, k0);
-  } else if (ns > 1) {
-    run(A, k0);
-    int s = 1;  // B holds stage s
-    for (; s + 2 <= ns - 1; s += 2) {
-      load(A, k0 + (s + 1) * U);
-      run(B, k0 + s * U);
-      load(B, k0 + (s + 2) * U);
-      run(A, k0 + (s + 1) * U);
-    }
-    if (s + 1 <= ns - 1) {
-      load(A, k0 + (s + 1) * U);
-      run(B, k0 + s * U);
-      run(A, k0 + (s + 1) * U);
-    } else {
-      run(B, k0 + s * U);
-    }
   }
-  if constexpr (!BLOCK) {  // (Block_FP8's K is whole steps)
-    if (lb > kfull && la < lb) {
-      Frag x[MB];
+  __device__ __forceinline__ void use(int u, int k, Acc (&acc)[MB][NB]) {
 #pragma unroll
-      for (int b = 0; b < MB; ++b) x[b] = tokens_tail(b);
+    for (int b = 0; b < MB; ++b) {
+      Frag xf;
+      float sc = 0.0f;
+      if constexpr (EARLY) {
+        xf = x[u][b];
+        if constexpr (BLOCK) sc = xs[u][b];
+      } else {
+        xf = tokens(b, k);
+        if constexpr (BLOCK) sc = xscale(b, k);
+      }
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const Frag w = weights_tail(j);
+      for (int j = 0; j < NB; ++j)
+        multiply(acc[b][j], w[u][j], xf, BLOCK ? sc * ws[u][j] : 0.0f);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  __device__ __forceinline__ void begin() {
+    if (la >= lfull) return;
 #pragma unroll
-        for (int b = 0; b < MB; ++b) multiply(w, x[b], acc[b][j], 0.0f);
+    for (int u = 0; u < R; ++u) load(u, la + u);
+  }
+  __device__ __forceinline__ void run(Acc (&acc)[MB][NB]) {
+    int k = la;
+    for (; k + R < lfull; k += R) {
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        use(u, k + u, acc);
+        load(u, k + R + u);
       }
     }
+#pragma unroll
+    for (int u = 0; u < R; ++u)
+      if (k + u < lfull) use(u, k + u, acc);
   }
+};
+template <int FMT, int NB, int MB, int R, bool EARLY, class W, class X, class WS, class XS>
+__device__ __forceinline__ Products<FMT, NB, MB, R, EARLY, W, X, WS, XS> products(
+    int la, int lfull, W w, X x, WS ws, XS xs) {
+  return {la, lfull, w, x, ws, xs};
+}
+
+// Steps in flight: so many 128-byte pieces of a weight row's K.
+template <int FMT>
+constexpr int steps(int pieces) {
+  return FMT == W8A8_INT8 ? 2 * pieces : pieces;
 }
 
 // The wave's first fragment (PACKED) or row of 16 weight rows from row n.
@@ -179,18 +224,41 @@ __device__ __forceinline__ const uint8_t* weight_rows(const uint8_t* w, long lon
   if (PACKED) return w + (long long)(n / 16) * ksteps * (16 * Traits<FMT>::KSTEP) + 16 * lane;
   return w + (n + (lane & 15)) * ld + 16 * (lane >> 4);
 }
+template <int FMT, bool PACKED>
+__device__ __forceinline__ typename Traits<FMT>::Frag weight_step(const uint8_t* w, int k) {
+  if constexpr (PACKED)
+    return load_packed<FMT>(w, k);
+  else
+    return load_frag<FMT>(w, k);
+}
+// Where K ends inside step k: zeros past it (packed weights hold them).
+template <int FMT, bool PACKED>
+__device__ __forceinline__ typename Traits<FMT>::Frag weight_tail(const uint8_t* w, int k, int K) {
+  if constexpr (PACKED)
+    return load_packed<FMT>(w, k);
+  else
+    return load_frag_tail<FMT>(w, k, 16 * ((threadIdx.x & 63) >> 4), K);
+}
+// One value for the whole wave: a scalar load, off the vector-memory path.
+__device__ __forceinline__ float uniform_load(const float* p) {
+  return *(const __attribute__((address_space(4))) float*)p;
+}
 
 // ---------------------------------------------------------------------- up --
 // 16 columns of h: 16 gate and 16 up rows of one expert, K split over the
 // waves, their sums joined through LDS in wave order.
+constexpr int kUpPieces = 2;
+
+template <int MB>
 struct UpLds {
   Choices c;
-  v4i part[kWaves - 1][2][2][64];
+  v4i part[kWaves - 1][MB][2][64];
 };
 
+// MB blocks of 16 tokens from the expert's t0-th on.
 template <int FMT, bool PACKED, int MB>
-__device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Expert& x,
-                                        UpLds& lds) {
+__device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Expert& x, int t0,
+                                        UpLds<MB>& lds) {
   typedef typename Traits<FMT>::Frag Frag;
   typedef typename Traits<FMT>::Acc Acc;
   constexpr int KSTEP = Traits<FMT>::KSTEP;
@@ -208,35 +276,49 @@ __device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Exp
   int entry[MB];
 #pragma unroll
   for (int b = 0; b < MB; ++b) {
-    entry[b] = lds.c.entry[min(16 * b + r, x.tokens - 1)];
+    entry[b] = lds.c.entry[wave][min(t0 + 16 * b + r, x.tokens - 1)];
     const int t = entry[b] / a.topk;
     xp[b] = a.xq + t * a.ldq + 16 * g;
     sxp[b] = a.sx + (BLOCK ? (long long)t * G : t);
   }
-  const float* swp[2] = {s1 + (BLOCK ? (long long)(n0 / kGroup) * G : n0 + 4 * g),
-                         s1 + (BLOCK ? (long long)((a.I + n0) / kGroup) * G : a.I + n0 + 4 * g)};
+  const float* swp[2] = {s1 + (BLOCK ? (long long)(n0 / kGroup) * G : n0),
+                         s1 + (BLOCK ? (long long)((a.I + n0) / kGroup) * G : a.I + n0)};
   Acc acc[MB][2];
 #pragma unroll
   for (int b = 0; b < MB; ++b)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[b][j] = Acc{0, 0, 0, 0};
-  products<FMT, 2, MB, FMT == W8A8_INT8 ? 4 : 2>(
-      acc, ksteps * wave / kWaves, ksteps * (wave + 1) / kWaves, kfull,
-      [&](int j, int k) -> Frag {
-        if constexpr (PACKED)
-          return load_packed<FMT>(wp[j], k);
-        else
-          return load_frag<FMT>(wp[j], k);
-      },
+  const int la = ksteps * wave / kWaves, lb = ksteps * (wave + 1) / kWaves;
+  auto p = products<FMT, 2, MB, steps<FMT>(kUpPieces), true>(
+      la, min(lb, kfull), [&](int j, int k) -> Frag { return weight_step<FMT, PACKED>(wp[j], k); },
       [&](int b, int k) -> Frag { return load_frag<FMT>(xp[b], k); },
-      [&](int j, int b, int k) { return sxp[b][k] * swp[j][k]; },
-      [&](int j) -> Frag {
-        if constexpr (PACKED)
-          return load_packed<FMT>(wp[j], kfull);
-        else
-          return load_frag_tail<FMT>(wp[j], kfull, 16 * g, a.D);
-      },
-      [&](int b) -> Frag { return load_frag_tail<FMT>(xp[b], kfull, 16 * g, a.D); });
+      [&](int j, int k) { return uniform_load(swp[j] + k); },
+      [&](int b, int k) { return sxp[b][k]; });
+  p.begin();
+  // the epilogue's scales, behind the first weights
+  float sx[MB], sw[2][4];
+  if constexpr (!BLOCK) {
+    if (wave == 0) {
+#pragma unroll
+      for (int b = 0; b < MB; ++b) sx[b] = *sxp[b];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sw[j][i] = swp[j][4 * g + i];
+    }
+  }
+  p.run(acc);
+  if constexpr (!BLOCK) {  // (Block_FP8's K is whole steps)
+    if (lb > kfull && la < lb) {
+#pragma unroll
+      for (int b = 0; b < MB; ++b) {
+        const Frag t = load_frag_tail<FMT>(xp[b], kfull, 16 * g, a.D);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          p.multiply(acc[b][j], weight_tail<FMT, PACKED>(wp[j], kfull, a.D), t, 0.0f);
+      }
+    }
+  }
   // the waves' sums
   if (wave > 0) {
 #pragma unroll
@@ -245,66 +327,78 @@ __device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Exp
       for (int j = 0; j < 2; ++j) lds.part[wave - 1][b][j][lane] = __builtin_bit_cast(v4i, acc[b][j]);
   }
   __syncthreads();
-  if (wave > 0) return;
+  if (wave == 0) {
 #pragma unroll
-  for (int w = 0; w < kWaves - 1; ++w)
+    for (int w = 0; w < kWaves - 1; ++w)
 #pragma unroll
-    for (int b = 0; b < MB; ++b)
+      for (int b = 0; b < MB; ++b)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        acc[b][j] += __builtin_bit_cast(Acc, lds.part[w][b][j][lane]);
-  // lane (r, g): token r of block b, columns n0 + 4 g .. + 3
+        for (int j = 0; j < 2; ++j)
+          acc[b][j] += __builtin_bit_cast(Acc, lds.part[w][b][j][lane]);
+    // lane (r, g): token r of block b, columns n0 + 4 g .. + 3
 #pragma unroll
-  for (int b = 0; b < MB; ++b) {
-    v4f h;
-    unsigned top = 0;
+    for (int b = 0; b < MB; ++b) {
+      v4f h;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float gate, up;
-      if constexpr (BLOCK) {
-        gate = acc[b][0][i];
-        up = acc[b][1][i];
-      } else {
-        gate = (float)acc[b][0][i] * sxp[b][0] * swp[0][i];
-        up = (float)acc[b][1][i] * sxp[b][0] * swp[1][i];
+      for (int i = 0; i < 4; ++i) {
+        float gate = (float)acc[b][0][i], up = (float)acc[b][1][i];
+        if constexpr (!BLOCK) {
+          gate *= sx[b] * sw[0][i];
+          up *= sx[b] * sw[1][i];
+        }
+        h[i] = silu(gate) * up;
       }
-      h[i] = silu(gate) * up;
-      top = max(top, abs_bits(h[i]));
-    }
-    top = max(top, (unsigned)__shfl_xor((int)top, 16, 64));
-    top = max(top, (unsigned)__shfl_xor((int)top, 32, 64));
-    if (16 * b + r < x.tokens) {
-      *reinterpret_cast<v4f*>(a.h + (long long)entry[b] * a.I + n0 + 4 * g) = h;
-      if (g == 0) a.hmax[(long long)entry[b] * (a.I / 16) + n0 / 16] = __uint_as_float(top);
+      if (t0 + 16 * b + r < x.tokens)
+        *reinterpret_cast<v4f*>(a.h + (long long)entry[b] * a.I + n0 + 4 * g) = h;
     }
   }
 }
 
-template <int FMT, bool PACKED>
+template <int FMT, bool PACKED, int MB>
 __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeLayerArgs a) {
-  __shared__ UpLds lds;
+  __shared__ UpLds<MB> lds;
   const Expert x = find_expert(a, blockIdx.y, lds.c);
   if (x.e < 0) return;
-  if (x.tokens <= 16)
-    up_tile<FMT, PACKED, 1>(a, blockIdx.x * 16, x, lds);
-  else
-    up_tile<FMT, PACKED, 2>(a, blockIdx.x * 16, x, lds);
+  for (int t0 = 0; t0 < x.tokens; t0 += 16 * MB) {
+    if (t0) __syncthreads();  // (the sums have been read)
+    up_tile<FMT, PACKED, MB>(a, blockIdx.x * 16, x, t0, lds);
+  }
 }
 
 // -------------------------------------------------------------------- down --
-// 64 columns of y for one expert: each wave 16 of its weight rows over the
-// whole of I, the tokens' codes from LDS, where the workgroup makes them from h
+// 64 columns of y for one expert: each wave 16 of its weight rows over the whole
+// of I, the tokens' codes from LDS, where the workgroup makes them from h
 // `chunk` columns at a time.
 constexpr int kColumns = 16 * kWaves;
+constexpr int kDownPieces = 2;
 constexpr int kPad = 16;  // bytes that move a row's codes on by four LDS banks
 
 extern __shared__ __align__(16) uint8_t codes[];
 
 struct DownLds {
   Choices c;
-  float scale[kLayerTokens];  // (one scale a token)
+  unsigned top[kLayerTokens];  // (one scale a token) the bits of the largest |h|
   int last;
 };
+
+// Eight of the expert's hidden values: those of thread i of a chunk's
+// `per` threads a token, from column c0 on; zeros past column `cols`.
+struct Hidden {
+  float f[8];
+};
+__device__ __forceinline__ Hidden load_hidden(const MoeLayerArgs& a, const int* entry, int i,
+                                              int per, int c0, int cols) {
+  Hidden v = {};
+  const int t = i / per, k = 8 * (i - t * per);
+  if (k < cols) __builtin_memcpy(v.f, a.h + (long long)entry[t] * a.I + c0 + k, 32);
+  return v;
+}
+__device__ __forceinline__ unsigned largest(const Hidden& v) {
+  unsigned m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v.f[i]));
+  return m;
+}
 
 template <int FMT, bool PACKED, int MB>
 __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const Expert& x,
@@ -316,104 +410,112 @@ __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const E
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int ksteps = (a.I + KSTEP - 1) / KSTEP, G = a.I / kGroup;
+  const int ksteps = (a.I + KSTEP - 1) / KSTEP, kfull = a.I / KSTEP, G = a.I / kGroup;
   const uint8_t* w2 = a.w2 + x.e * a.w2_stride;
   const float* s2 = a.s2 + x.e * a.s2_stride;
   // (waves past the last column repeat the last whole block, and store nothing)
   const int n = min(n0 + 16 * wave, a.D - 16);
   const uint8_t* wp = weight_rows<FMT, PACKED>(w2, a.ldw2, ksteps, n);
+  const float* swp = s2 + (BLOCK ? (long long)(n / kGroup) * G : n + 4 * g);
+  const int* entry = lds.c.entry[wave];
   const int stride = a.chunk + kPad;
   float* gscale = reinterpret_cast<float*>(codes + (long long)x.tokens * stride);  // Block_FP8's
 
-  if constexpr (!BLOCK) {  // a token's scale: its waves' maxima
-    for (int t = wave; t < x.tokens; t += kWaves) {
-      const float* m = a.hmax + (long long)lds.c.entry[t] * (a.I / 16);
-      unsigned top = 0;
-      for (int i = lane; i < a.I / 16; i += 64) top = max(top, __float_as_uint(m[i]));
-      top = wave_umax(top);
-      if (lane == 0) lds.scale[t] = act_scale<INT8>(__uint_as_float(top));
-    }
-    __syncthreads();
+  const uint8_t* xp[MB];
+  const float* sxp[MB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b) {
+    const int t = min(16 * b + r, x.tokens - 1);
+    xp[b] = codes + t * stride + 16 * g;
+    sxp[b] = gscale + t * (a.chunk / kGroup);
   }
   Acc acc[MB][1];
 #pragma unroll
   for (int b = 0; b < MB; ++b) acc[b][0] = Acc{0, 0, 0, 0};
+  float sw[4];
   for (int c0 = 0; c0 < a.I; c0 += a.chunk) {
     const int cols = min(a.chunk, a.I - c0), per = (cols + kGroup - 1) / kGroup * (kGroup / 8);
-    if (c0) __syncthreads();  // the last chunk's codes have been read
-    // eight columns a thread; zeros up to a whole step
-    for (int i = threadIdx.x; i < x.tokens * per; i += kThreads) {
-      const int t = i / per, k = 8 * (i - t * per);
-      v2u q = {0u, 0u};
-      if (k < cols) {
-        const float* h = a.h + (long long)lds.c.entry[t] * a.I + c0 + k;
-        float f[8];
-        __builtin_memcpy(f, h, 32);
-        float s;
-        if constexpr (BLOCK) {
-          const float* m = a.hmax + (long long)lds.c.entry[t] * (a.I / 16) + (c0 + k) / kGroup * 8;
-          unsigned top = 0;
+    const int kb = c0 / KSTEP, kend = (c0 + cols + KSTEP - 1) / KSTEP;
+    // a thread's first eight hidden values, then the first weights: loads
+    // return in order, so that the codes are made while the weights arrive
+    Hidden first = {};
+    if ((int)threadIdx.x < x.tokens * per)
+      first = load_hidden(a, entry, threadIdx.x, per, c0, cols);
+    auto p = products<FMT, 1, MB, steps<FMT>(kDownPieces), false>(
+        kb, min(kend, kfull), [&](int, int k) -> Frag { return weight_step<FMT, PACKED>(wp, k); },
+        [&](int b, int k) -> Frag { return load_frag<FMT>(xp[b], k - kb); },
+        [&](int, int k) { return uniform_load(swp + k); },
+        [&](int b, int k) { return sxp[b][k - kb]; });
+    p.begin();
+    if constexpr (!BLOCK) {
+      if (c0 == 0) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u) top = max(top, __float_as_uint(m[u]));
-          s = act_scale<false>(__uint_as_float(top));
-          if (k % kGroup == 0) gscale[t * (a.chunk / kGroup) + k / kGroup] = s;
-        } else {
-          s = lds.scale[t];
+        for (int i = 0; i < 4; ++i) sw[i] = swp[i];
+        // the tokens' largest values, over all of I
+        if (threadIdx.x < kLayerTokens) lds.top[threadIdx.x] = 0u;
+        __syncthreads();
+        // (a token's threads are whole groups of 16 lanes)
+        auto take = [&](int i, int each, const Hidden& v) {
+          const unsigned m = seg16_umax(largest(v));
+          if ((i & 15) == 0) atomicMax(&lds.top[i / each], m);
+        };
+        if ((int)threadIdx.x < x.tokens * per) take(threadIdx.x, per, first);
+        for (int i = threadIdx.x + kThreads; i < x.tokens * per; i += kThreads)
+          take(i, per, load_hidden(a, entry, i, per, 0, cols));
+        for (int c = a.chunk; c < a.I; c += a.chunk) {
+          const int more = min(a.chunk, a.I - c), each = (more + kGroup - 1) / kGroup * (kGroup / 8);
+          for (int i = threadIdx.x; i < x.tokens * each; i += kThreads)
+            take(i, each, load_hidden(a, entry, i, each, c, more));
         }
-        q = encode_values<INT8>(f, s, act_recip(s));
       }
-      *reinterpret_cast<v2u*>(codes + t * stride + k) = q;
+    }
+    __syncthreads();  // (and the last chunk's codes have been read)
+    for (int i = threadIdx.x; i < x.tokens * per; i += kThreads) {
+      Hidden v = i < kThreads ? first : load_hidden(a, entry, i, per, c0, cols);
+      const int t = i / per, k = 8 * (i - t * per);
+      float s;
+      if constexpr (BLOCK) {  // 16 lanes hold a group
+        const unsigned m = seg16_umax(largest(v));
+        s = act_scale<false>(__uint_as_float(m));
+        if (k % kGroup == 0) gscale[t * (a.chunk / kGroup) + k / kGroup] = s;
+      } else {
+        s = act_scale<INT8>(__uint_as_float(lds.top[t]));
+      }
+      *reinterpret_cast<v2u*>(codes + t * stride + k) = encode_values<INT8>(v.f, s, act_recip(s));
     }
     __syncthreads();
-    const uint8_t* xp[MB];
-    const float* sxp[MB];
+    p.run(acc);
+    if constexpr (!BLOCK) {
+      if (kend > kfull) {
+        const Frag w = weight_tail<FMT, PACKED>(wp, kfull, a.I);
 #pragma unroll
-    for (int b = 0; b < MB; ++b) {
-      const int t = min(16 * b + r, x.tokens - 1);
-      xp[b] = codes + t * stride + 16 * g;
-      sxp[b] = gscale + t * (a.chunk / kGroup);
+        for (int b = 0; b < MB; ++b)
+          p.multiply(acc[b][0], w, load_frag<FMT>(xp[b], kfull - kb), 0.0f);
+      }
     }
-    const float* swp = s2 + (long long)(n / kGroup) * G;
-    const int kb = c0 / KSTEP;
-    auto tokens = [&](int b, int k) -> Frag { return load_frag<FMT>(xp[b], k - kb); };
-    products<FMT, 1, MB, INT8 ? 4 : 2>(
-        acc, kb, (c0 + cols + KSTEP - 1) / KSTEP, a.I / KSTEP,
-        [&](int, int k) -> Frag {
-          if constexpr (PACKED)
-            return load_packed<FMT>(wp, k);
-          else
-            return load_frag<FMT>(wp, k);
-        },
-        tokens, [&](int, int b, int k) { return sxp[b][k - kb] * swp[k]; },
-        [&](int) -> Frag {
-          if constexpr (PACKED)
-            return load_packed<FMT>(wp, a.I / KSTEP);
-          else
-            return load_frag_tail<FMT>(wp, a.I / KSTEP, 16 * g, a.I);
-        },
-        [&](int b) -> Frag { return tokens(b, a.I / KSTEP); });
   }
   // The experts' outputs, lane (r, g): token r of block b, columns n + 4 g .. +
   // 3; written through to where the last workgroup reads them, acknowledged
   // before this one counts itself in (the split-K hand-off of the small-M GEMM).
   const __amdgpu_buffer_rsrc_t out = coherent_rsrc(a.part, a.T * a.topk * a.D * 4);
-  if (n0 + 16 * wave < a.D) {
 #pragma unroll
-    for (int b = 0; b < MB; ++b) {
-      const int t = 16 * b + r;
-      v4f p;
+  for (int b = 0; b < MB; ++b) {
+    const int t = 16 * b + r, at = min(t, x.tokens - 1);
+    float sx = 0.0f;
+    if constexpr (!BLOCK) sx = act_scale<INT8>(__uint_as_float(lds.top[at]));
+    v4f o;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (BLOCK)
-          p[i] = acc[b][0][i];
-        else
-          p[i] = (float)acc[b][0][i] * lds.scale[min(t, x.tokens - 1)] * s2[n + 4 * g + i];
-      }
-      if (t < x.tokens)
-        coherent_store16(out, (lds.c.entry[t] * a.D + n + 4 * g) * 4, __builtin_bit_cast(v4i, p));
+    for (int i = 0; i < 4; ++i) {
+      o[i] = (float)acc[b][0][i];
+      if constexpr (!BLOCK) o[i] *= sx * sw[i];
     }
+    if (t < x.tokens && n0 + 16 * wave < a.D)
+      coherent_store16(out, (entry[at] * a.D + n + 4 * g) * 4, __builtin_bit_cast(v4i, o));
   }
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  // (how many will, while the stores are on their way)
+  if (a.few) load_choices(a, lds.c);
+  const int active = count_active(lds.c);
   __builtin_amdgcn_s_waitcnt(0);
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
   __syncthreads();
@@ -423,28 +525,32 @@ __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const E
     unsigned* counter = a.counters + (long long)blockIdx.x * kCounterWords + 2;
     const unsigned before =
         __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    lds.last = before == (unsigned)x.active - 1;
+    lds.last = before == (unsigned)active - 1;
     if (lds.last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-template <int FMT, bool PACKED>
+template <int FMT, bool PACKED, int MB>
 __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLayerArgs a) {
   __shared__ DownLds lds;
   const Expert x = find_expert(a, blockIdx.y, lds.c);
   const int n0 = blockIdx.x * kColumns;
-  if (x.e < 0) {
-    if (x.active || blockIdx.y) return;  // (no token has an expert: zeros)
+  if (x.e < 0) {  // (no token has an expert: zeros)
+    if (blockIdx.y) return;
+    if (a.few) load_choices(a, lds.c);
+    if (count_active(lds.c)) return;
   } else {
-    if (x.tokens <= 16)
+    if (MB == 1 || x.tokens <= 16)
       down_tile<FMT, PACKED, 1>(a, n0, x, lds);
     else
-      down_tile<FMT, PACKED, 2>(a, n0, x, lds);
+      down_tile<FMT, PACKED, MB>(a, n0, x, lds);
     if (!lds.last) return;
   }
-  // y of the tile's columns, four a thread, in the order of the choices
+  // y of the tile's columns, four a thread, in the order of the choices; the
+  // loads of a batch are all in flight (left out: entry 0's, not used)
+  find_outputs(a, lds.c);
   const __amdgpu_buffer_rsrc_t part = coherent_rsrc(a.part, a.T * a.topk * a.D * 4);
   constexpr int kBatch = 8;
   for (int i = threadIdx.x; i < a.T * (kColumns / 4); i += kThreads) {
@@ -454,49 +560,162 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLayerArgs a) {
     for (int j0 = 0; j0 < a.topk; j0 += kBatch) {
       v4i v[kBatch];
       float w[kBatch];
+      bool on[kBatch];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const int at = t * a.topk + j0 + j;
-        const bool on = j0 + j < a.topk && lds.c.ids[at] >= 0;
-        v[j] = v4i{0, 0, 0, 0};
-        w[j] = 0.0f;
-        if (on) {
-          v[j] = coherent_load16(part, (served_by(lds.c, at, t, a.topk) * a.D + n) * 4);
-          w[j] = a.weights[at];
-        }
+        const int at = t * a.topk + min(j0 + j, a.topk - 1), from = lds.c.ids[at];
+        on[j] = j0 + j < a.topk && from >= 0;
+        v[j] = coherent_load16(part, (max(from, 0) * a.D + n) * 4);
+        w[j] = a.weights[at];
       }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         const v4f p = __builtin_bit_cast(v4f, v[j]);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) sum[u] = __builtin_fmaf(w[j], p[u], sum[u]);
+        for (int u = 0; u < 4; ++u) sum[u] = on[j] ? __builtin_fmaf(w[j], p[u], sum[u]) : sum[u];
       }
     }
-    uint16_t* y = a.y + t * a.ldy + n;
+    uint16_t y[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) y[u] = (uint16_t)bf16_bits(sum[u]);
+    __builtin_memcpy(a.y + t * a.ldy + n, y, 8);
   }
 }
 
+// Up to 16 entries: 16 columns of y for all of them, a wave an entry, so that
+// their sum needs no hand-off between workgroups (which is what a call of so
+// few bytes waits for: 1 token, 8 experts of 2048 x 768 8.0 us by the kernel
+// above).  The same values in the same order.
+constexpr int kFewEntries = 16;
+
 template <int FMT, bool PACKED>
-hipError_t launch_up(const MoeLayerArgs& a, int slots, hipStream_t s) {
-  return launch_kernel(moe_up_kernel<FMT, PACKED>, dim3((unsigned)(a.I / 16), (unsigned)slots),
+__global__ __launch_bounds__(64 * kFewEntries) void moe_down_few_kernel(MoeLayerArgs a) {
+  typedef typename Traits<FMT>::Frag Frag;
+  typedef typename Traits<FMT>::Acc Acc;
+  constexpr int KSTEP = Traits<FMT>::KSTEP;
+  constexpr bool BLOCK = FMT == BLOCK_FP8, INT8 = FMT == W8A8_INT8;
+  __shared__ float outputs[kFewEntries][16];
+  __shared__ float weights[kFewEntries];  // of the choices that count
+  const int lane = threadIdx.x & 63;
+  const int entry = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, n = blockIdx.x * 16;
+  const int e = __builtin_amdgcn_readfirstlane(a.experts[entry]);
+  const bool on = (unsigned)e < (unsigned)a.E;
+  if (on) {
+    const int ksteps = (a.I + KSTEP - 1) / KSTEP, kfull = a.I / KSTEP, G = a.I / kGroup;
+    const float* s2 = a.s2 + e * a.s2_stride;
+    const uint8_t* wp = weight_rows<FMT, PACKED>(a.w2 + e * a.w2_stride, a.ldw2, ksteps, n);
+    const float* swp = s2 + (BLOCK ? (long long)(n / kGroup) * G : n + 4 * g);
+    const float weight = a.weights[entry];
+    const int stride = a.chunk + kPad;
+    uint8_t* x = codes + entry * stride;
+    float* xs = reinterpret_cast<float*>(codes + (blockDim.x >> 6) * stride) +
+                entry * (a.chunk / kGroup);  // Block_FP8's
+    Acc acc[1][1] = {{Acc{0, 0, 0, 0}}};
+    float sw[4], sx = 0.0f;
+    for (int c0 = 0; c0 < a.I; c0 += a.chunk) {
+      const int cols = min(a.chunk, a.I - c0), per = (cols + kGroup - 1) / kGroup * (kGroup / 8);
+      const int kb = c0 / KSTEP, kend = (c0 + cols + KSTEP - 1) / KSTEP;
+      constexpr int kHeld = 2;  // pieces of eight hidden values a lane
+      Hidden first[kHeld] = {};
+#pragma unroll
+      for (int q = 0; q < kHeld; ++q)
+        if (lane + 64 * q < per) first[q] = load_hidden(a, &entry, lane + 64 * q, per, c0, cols);
+      auto p = products<FMT, 1, 1, steps<FMT>(kDownPieces), false>(
+          kb, min(kend, kfull), [&](int, int k) -> Frag { return weight_step<FMT, PACKED>(wp, k); },
+          [&](int, int k) -> Frag { return load_frag<FMT>(x + 16 * g, k - kb); },
+          [&](int, int k) { return uniform_load(swp + k); },
+          [&](int, int k) { return xs[k - kb]; });
+      p.begin();
+      if constexpr (!BLOCK) {
+        if (c0 == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sw[i] = swp[i];
+          unsigned top = max(largest(first[0]), largest(first[1]));
+          const float* h = a.h + (long long)entry * a.I;
+          for (int k = 8 * (lane + 64 * kHeld); k < a.I; k += 512) {
+            Hidden v;
+            __builtin_memcpy(v.f, h + k, 32);
+            top = max(top, largest(v));
+          }
+          sx = act_scale<INT8>(__uint_as_float(wave_umax(top)));
+        }
+      }
+      auto encode = [&](Hidden v, int i) {
+        const int k = 8 * i;
+        float s = sx;
+        if constexpr (BLOCK) {  // 16 lanes hold a group
+          s = act_scale<false>(__uint_as_float(seg16_umax(largest(v))));
+          if (k % kGroup == 0) xs[k / kGroup] = s;
+        }
+        *reinterpret_cast<v2u*>(x + k) = encode_values<INT8>(v.f, s, act_recip(s));
+      };
+      // (the wave's own LDS, which it accesses in order: the fences keep the
+      // compiler from moving reads of the codes above the writes, and the next
+      // chunk's writes above the reads)
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+#pragma unroll
+      for (int q = 0; q < kHeld; ++q)
+        if (lane + 64 * q < per) encode(first[q], lane + 64 * q);
+      for (int i = lane + 64 * kHeld; i < per; i += 64)
+        encode(load_hidden(a, &entry, i, per, c0, cols), i);
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      p.run(acc);
+      if constexpr (!BLOCK) {
+        if (kend > kfull)
+          p.multiply(acc[0][0], weight_tail<FMT, PACKED>(wp, kfull, a.I),
+                     load_frag<FMT>(x + 16 * g, kfull - kb), 0.0f);
+      }
+    }
+    // (every column of the product is the entry's)
+    if ((lane & 15) == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float o = (float)acc[0][0][i];
+        if constexpr (!BLOCK) o *= sx * sw[i];
+        outputs[entry][4 * g + i] = o;
+      }
+    }
+    if (lane == 0) weights[entry] = weight;
+  }
+  if (lane == 0 && !on) weights[entry] = 0.0f;
+  if (lane < 16 && !on) outputs[entry][lane] = 0.0f;
+  __syncthreads();
+  if ((int)threadIdx.x < 16 * a.T) {
+    const int t = threadIdx.x / 16, c = threadIdx.x % 16;
+    float sum = 0.0f;
+    for (int j = t * a.topk; j < (t + 1) * a.topk; ++j)
+      sum = __builtin_fmaf(weights[j], outputs[j][c], sum);
+    a.y[t * a.ldy + n + c] = (uint16_t)bf16_bits(sum);
+  }
+}
+
+template <int FMT, bool PACKED, int MB>
+hipError_t launch_up(const MoeLayerArgs& a, hipStream_t s) {
+  return launch_kernel(moe_up_kernel<FMT, PACKED, MB>, dim3((unsigned)(a.I / 16), (unsigned)a.slots),
                        dim3(kThreads), 0, s, a);
 }
-template <int FMT, bool PACKED>
-hipError_t launch_down(const MoeLayerArgs& a, int slots, hipStream_t s) {
-  const size_t lds = (size_t)a.T * (a.chunk + kPad + (FMT == BLOCK_FP8 ? a.chunk / kGroup * 4 : 0));
-  return launch_kernel(moe_down_kernel<FMT, PACKED>,
-                       dim3((unsigned)((a.D + kColumns - 1) / kColumns), (unsigned)slots),
+template <int FMT, bool PACKED, int MB>
+hipError_t launch_down(const MoeLayerArgs& a, hipStream_t s) {
+  const int rows = a.T * a.topk <= kFewEntries ? a.T * a.topk : a.T;
+  const size_t lds = (size_t)rows * (a.chunk + kPad + (FMT == BLOCK_FP8 ? a.chunk / kGroup * 4 : 0));
+  if (MB == 1 && a.T * a.topk <= kFewEntries)
+    return launch_kernel(moe_down_few_kernel<FMT, PACKED>, dim3((unsigned)(a.D / 16)),
+                         dim3((unsigned)(64 * a.T * a.topk)), lds, s, a);
+  return launch_kernel(moe_down_kernel<FMT, PACKED, MB>,
+                       dim3((unsigned)((a.D + kColumns - 1) / kColumns), (unsigned)a.slots),
                        dim3(kThreads), lds, s, a);
+}
+template <int FMT, int MB>
+hipError_t launch_layer(bool packed1, bool packed2, const MoeLayerArgs& a, hipStream_t s) {
+  const hipError_t e = packed1 ? launch_up<FMT, true, MB>(a, s) : launch_up<FMT, false, MB>(a, s);
+  if (e != hipSuccess) return e;
+  return packed2 ? launch_down<FMT, true, MB>(a, s) : launch_down<FMT, false, MB>(a, s);
 }
 template <int FMT>
 hipError_t launch_layer(bool packed1, bool packed2, const MoeLayerArgs& a, hipStream_t s) {
-  const int slots = a.E < a.T * a.topk ? a.E : a.T * a.topk;
-  const hipError_t e =
-      packed1 ? launch_up<FMT, true>(a, slots, s) : launch_up<FMT, false>(a, slots, s);
-  if (e != hipSuccess) return e;
-  return packed2 ? launch_down<FMT, true>(a, slots, s) : launch_down<FMT, false>(a, slots, s);
+  return a.T > 16 ? launch_layer<FMT, 2>(packed1, packed2, a, s)
+                  : launch_layer<FMT, 1>(packed1, packed2, a, s);
 }
 
 }  // namespace

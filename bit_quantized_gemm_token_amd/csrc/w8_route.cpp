@@ -59,14 +59,13 @@ size_t route_bytes(const RouteArgs& a) {
 // The layer's workspace (byte offsets): the counter region that every
 // operation keeps, then its arrays.
 struct LayerWs {
-  size_t h, hmax, part, total;
+  size_t h, part, total;
 };
 LayerWs layer_ws(int T, int topk, int D, int I) {
   const size_t n = (size_t)T * topk;
   LayerWs w;
   w.h = ws_counter_bytes(0);
-  w.hmax = w.h + round256(n * I * 4);
-  w.part = w.hmax + round256(n * (I / 16) * 4);
+  w.part = w.h + round256(n * I * 4);
   w.total = w.part + round256(n * D * 4);
   return w;
 }
@@ -109,9 +108,11 @@ w8_status check_experts(int fmt, int E, int N, int K, const void* w, int64_t ldw
 }
 
 // Columns of I whose codes a workgroup of the layer's second kernel holds in
-// LDS, beside 64 KiB less what the kernel needs itself: whole 128s.
-int layer_chunk(int T, int I) {
-  const int per_row = 56 * 1024 / T - 16;  // (codes, 16 bytes of padding, Block_FP8's scales)
+// LDS, for T tokens or up to 16 entries, in 64 KiB less what the kernel needs
+// itself: whole 128s.
+int layer_chunk(int T, int topk, int I) {
+  const int rows = T * topk <= 16 ? T * topk : T;
+  const int per_row = 56 * 1024 / rows - 16;  // (codes, 16 bytes of padding, Block_FP8's scales)
   const int most = per_row * 32 / 33 / W8_GROUP * W8_GROUP;
   return std::min(most, (I + W8_GROUP - 1) / W8_GROUP * W8_GROUP);
 }
@@ -245,7 +246,6 @@ w8_status w8_moe_layer(w8_fmt fmt_in, int E, int T, int topk, int D, int I, cons
   a.s2 = s2;
   a.y = static_cast<uint16_t*>(y);
   a.h = reinterpret_cast<float*>(p + w.h);
-  a.hmax = reinterpret_cast<float*>(p + w.hmax);
   a.part = reinterpret_cast<float*>(p + w.part);
   a.counters = static_cast<unsigned*>(ws);
   a.ldq = ldq;
@@ -261,7 +261,9 @@ w8_status w8_moe_layer(w8_fmt fmt_in, int E, int T, int topk, int D, int I, cons
   a.topk = topk;
   a.D = D;
   a.I = I;
-  a.chunk = layer_chunk(T, I);
+  a.few = T * topk <= 64 && T * topk <= E;
+  a.slots = std::min(E, T * topk);
+  a.chunk = layer_chunk(T, topk, I);
   const hipError_t e =
       launch_moe_layer(fmt, ldw1 == 0, ldw2 == 0, a, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("moe_layer launch", e));

@@ -59,13 +59,14 @@ struct MoeLayerArgs {
   const float* s2;
   uint16_t* y;          // bf16 [T, D]
   float* h;             // [T * topk, I] gated products (workspace)
-  float* hmax;          // [T * topk, I / 16] their maxima
   float* part;          // [T * topk, D] the experts' outputs
   unsigned* counters;   // arrival counters
   long long ldq, ldw1, ldw2, ldy;       // bytes; y: elements
   long long w1_stride, w2_stride;       // bytes between experts
   long long s1_stride, s2_stride;       // floats
   int E, T, topk, D, I;
+  int slots;            // of experts that a launch holds: each has tokens or ends at once
+  int few;              // a slot is an entry (at most 64), else one of the experts with tokens
   int chunk;            // of I that a workgroup of the second kernel keeps as codes
 };
 // Two launches.  packed1, packed2: the layouts of w1 and w2.

@@ -123,7 +123,8 @@ SIZES = [  # T, E, topk, D, I (Block_FP8: rounded up to whole 128s)
     (1, 1, 1, 16, 16), (1, 8, 2, 128, 128), (1, 128, 8, 256, 128), (2, 5, 3, 272, 144),
     (3, 4, 4, 80, 336), (5, 16, 2, 1040, 48), (8, 128, 8, 256, 128), (16, 4, 2, 528, 256),
     (17, 2, 1, 64, 400), (31, 3, 2, 144, 1680), (32, 2, 2, 256, 272), (32, 64, 8, 128, 64),
-    (32, 1000, 32, 32, 32), (4, 8, 2, 2048, 768), (32, 1, 1, 256, 2064), (2, 3, 2, 64, 8192)]
+    (32, 1000, 32, 32, 32), (4, 8, 2, 2048, 768), (32, 1, 1, 256, 2064), (2, 3, 2, 64, 8192),
+    (8, 3, 2, 64, 7200), (16, 2, 1, 144, 3472), (5, 9, 9, 64, 16)]
 
 
 def sized(fmt, D, I):
