@@ -20,7 +20,7 @@ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 constexpr int kMaxRows = (1 << 22) - 1;  // (as the other operators for any token count)
 constexpr int kMaxColumns = 1 << 20;     // of a combined row
 constexpr int kMaxWidth = 1 << 16;       // D and I of the layer: 32-bit offsets of its partials
-constexpr int kRouteBlocks = 2048;       // workgroups of the routing's first launch
+constexpr int kRouteBlocks = 1024;       // workgroups of the routing's first launch
 
 w8_status check_workspace(const void* ws, size_t have, size_t need) {
   if (!ws || have < need)
@@ -43,17 +43,17 @@ w8_status check_route(int T, int E, int topk) {
   return W8_OK;
 }
 
-// Passes of at most kRoutePass entries, as many to a workgroup as keep the
-// workgroups, whose counts the second launch reads, to kRouteBlocks.
+// As many passes to a workgroup as keep the workgroups, whose counts the second
+// launch reads, to kRouteBlocks.
 void plan_route(RouteArgs* a) {
-  a->tokens = kRoutePass / a->topk;
+  a->tokens = ((long long)a->T * a->topk <= kRoutePass ? kRoutePass : kRouteMany) / a->topk;
   const long long passes = ceil_div(a->T, a->tokens);
   a->passes = (int)ceil_div(passes, kRouteBlocks);
   a->blocks = (int)ceil_div(passes, a->passes);
 }
 
 size_t route_bytes(const RouteArgs& a) {
-  return a.blocks > 1 ? ws_counter_bytes(0) + (size_t)a.blocks * a.E * 4 : 0;
+  return a.blocks > 1 ? ws_counter_bytes(0) + (size_t)a.blocks * count_stride(a.E) * 4 : 0;
 }
 
 // The layer's workspace (byte offsets): the counter region that every
@@ -154,7 +154,9 @@ w8_status w8_moe_route(int T, int E, int topk, const void* logits, int64_t ldl, 
       !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(slots, 4))
     return fail(W8_E_INVALID, "every pointer must be aligned to its element type");
   RouteArgs a{logits, !logits_fp32, ldl, T, E, topk, renormalize, scale, experts, weights, offsets,
-              rows, slots, 0, 0, 0, nullptr};
+              rows, slots, 0, 0, 0, nullptr, 0};
+  const int per = logits_fp32 ? 4 : 8;  // logits of 16 bytes
+  a.wide = aligned(logits, 16) && ldl % per == 0 && E % per == 0;
   a.blocks = 1;  // (no tokens: the offsets alone)
   if (T) plan_route(&a);
   const size_t need = offsets ? route_bytes(a) : 0;

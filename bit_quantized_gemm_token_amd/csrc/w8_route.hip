@@ -5,9 +5,9 @@
 // are never chosen.  The entries (token, choice) in order, sorted by expert
 // with their order kept, are the lists: an entry's place is its expert's
 // offset, plus the entries of that expert in front of it.  Those are counted
-// within a pass of up to 256 entries, over the passes of a workgroup and, in a
-// second launch, over the workgroups: whole numbers in a fixed order, so the
-// lists are the same every time.
+// within a pass of up to kRoutePass entries, over the passes of a workgroup and,
+// in a second launch, over the workgroups: whole numbers in a fixed order, so
+// the lists are the same every time.
 #include "w8_block.hpp"
 #include "w8_device.hpp"
 #include "w8_route.hpp"
@@ -58,10 +58,10 @@ __device__ __forceinline__ float lanes_sum(float v) {
 
 // Unsigned keys in the order of the logits; 0: never chosen (-inf, NaN).  The
 // two zeros are one.
-__device__ __forceinline__ unsigned key_of(float l) {
-  if (!(l > -__builtin_inff())) return 0u;
-  const unsigned u = __float_as_uint(l == 0.0f ? 0.0f : l);
-  return u >> 31 ? ~u : u | 0x80000000u;
+__device__ __forceinline__ unsigned key_of(float l, bool there) {
+  const unsigned u = l == 0.0f ? 0u : __float_as_uint(l);
+  const unsigned key = u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
+  return (there & (l > -__builtin_inff())) ? key : 0u;
 }
 __device__ __forceinline__ float logit_of(unsigned key) {
   return __uint_as_float(key >> 31 ? key & 0x7FFFFFFFu : ~key);
@@ -95,10 +95,45 @@ __device__ __forceinline__ void place_experts(const int* count, int* at, int E) 
   }
 }
 
+// A lane's PER logits of a row from expert e0 on, as keys; wide: 16 bytes a load
+// (aligned rows, whole pieces).  Loads past the row's end repeat its last ones,
+// so that none waits for a condition.
+template <int PER, typename Logit>
+__device__ __forceinline__ void load_keys(const Logit* row, int e0, int E, bool wide,
+                                          unsigned (&key)[PER]) {
+  constexpr bool HALF = sizeof(Logit) == 2;
+  constexpr int N = 16 / sizeof(Logit);
+  static_assert(PER % N == 0, "whole loads");
+  float l[PER];
+  if (wide) {
+    v4u v[PER / N];
+#pragma unroll
+    for (int c = 0; c < PER / N; ++c)
+      v[c] = *reinterpret_cast<const v4u*>(row + min(e0 + c * N, E - N));
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const v4u& u = v[i / N];
+      l[i] = HALF ? (i & 1 ? bf16_hi(u[i % N / 2]) : bf16_lo(u[i % N / 2]))
+                  : __uint_as_float(u[HALF ? 0 : i % N]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const Logit v = row[min(e0 + i, E - 1)];
+      if constexpr (HALF)
+        l[i] = bf16_lo(v);
+      else
+        l[i] = v;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) key[i] = key_of(l[i], e0 + i < E);
+}
+
 // L lanes take a token, PER logits each (E <= L * PER).
 template <int L, int PER, typename Logit>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
-  __shared__ int ids[kRoutePass];
+  __shared__ __align__(16) int ids[kRoutePass];
   __shared__ float vals[kRoutePass];
   __shared__ float sums[kRoutePass];         // (not renormalized) of all experts, by token
   __shared__ int count[kMaxExperts + 1];     // entries of each expert in the passes so far
@@ -116,14 +151,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
     for (int t = group; t < nt; t += kThreads / L) {
       const Logit* row = static_cast<const Logit*>(a.logits) + (t0 + t) * a.ldl;
       unsigned key[PER];
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int e = i * L + sub;
-        if constexpr (sizeof(Logit) == 2)
-          key[i] = e < a.E ? key_of(bf16_lo(row[e])) : 0u;
-        else
-          key[i] = e < a.E ? key_of(row[e]) : 0u;
-      }
+      load_keys<PER>(row, sub * PER, a.E, a.wide, key);
       float top = 0.0f, all = 0.0f;
       for (int j = 0; j < a.topk; ++j) {
         unsigned best = 0;
@@ -132,7 +160,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
         best = lanes_umax<L>(best);
         unsigned e = kNone;
 #pragma unroll
-        for (int i = PER - 1; i >= 0; --i) e = key[i] == best ? (unsigned)(i * L + sub) : e;
+        for (int i = PER - 1; i >= 0; --i) e = key[i] == best ? (unsigned)(sub * PER + i) : e;
         e = lanes_umin<L>(e);
         const float l = logit_of(best);
         if (j == 0) {
@@ -144,7 +172,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
           }
         }
 #pragma unroll
-        for (int i = 0; i < PER; ++i) key[i] = (unsigned)(i * L + sub) == e ? 0u : key[i];
+        for (int i = 0; i < PER; ++i) key[i] = (unsigned)(sub * PER + i) == e ? 0u : key[i];
         if (sub == 0) {
           ids[t * a.topk + j] = best ? (int)e : -1;
           vals[t * a.topk + j] = best ? over_top(l, top) : 0.0f;
@@ -169,7 +197,12 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
       a.weights[at] = id >= 0 ? a.scale * (vals[i] / sum) : 0.0f;
       if (lists && id >= 0) {
         rank = count[id];
-        for (int b = 0; b < i; ++b) rank += ids[b] == id;
+#pragma unroll 4
+        for (int b = 0; b + 4 <= i; b += 4) {
+          const v4i v = *reinterpret_cast<const v4i*>(ids + b);
+          rank += (v[0] == id) + (v[1] == id) + (v[2] == id) + (v[3] == id);
+        }
+        for (int b = i & ~3; b < i; ++b) rank += ids[b] == id;
       }
     }
     if (!lists) {
@@ -195,57 +228,70 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
   }
   if (lists && a.blocks > 1) {
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kThreads)
-      a.counts[(long long)blockIdx.x * a.E + e] = count[e];
+    for (int e = threadIdx.x; e < count_stride(a.E); e += kThreads)
+      a.counts[(long long)blockIdx.x * count_stride(a.E) + e] = e < a.E ? count[e] : 0;
   }
 }
 
-// The places of the entries of `span` workgroups of route_kernel, from all
-// workgroups' counts.
-constexpr int kPlaceThreads = 1024;
-__global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteArgs a, int span) {
-  __shared__ int first[kMaxExperts + 1];  // of each expert, then of its next entry here
-  __shared__ int before[kMaxExperts];     // entries of the workgroups in front of these
-  const int b0 = blockIdx.x * span, b1 = min(b0 + span, a.blocks);
-  for (int e = threadIdx.x; e < a.E; e += kPlaceThreads) first[e] = before[e] = 0;
+// The places of the entries of kSpan workgroups of route_kernel, from all
+// workgroups' counts, which every workgroup here reads (64 KiB of L2 for each
+// 128 of them and 128 experts): four experts a thread, the workgroups dealt to
+// the threads.
+constexpr int kPlaceThreads = 1024, kSpan = 8;
+
+__global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteArgs a) {
+  __shared__ int first[kMaxExperts + 4];        // of each expert
+  __shared__ int before[kMaxExperts];           // entries of the workgroups in front of these
+  __shared__ int next[kSpan][kMaxExperts];      // of each of these: its first entry's place
+  const int b0 = blockIdx.x * kSpan, b1 = min(b0 + kSpan, a.blocks);
+  const int stride = count_stride(a.E), quads = stride / 4;
+  for (int e = threadIdx.x; e < stride; e += kPlaceThreads) {
+    first[e] = 0;
+    before[e] = 0;
+  }
   __syncthreads();
-  // each thread one expert and every so many-th workgroup
-  int width = 64;
-  while (width < a.E) width *= 2;
-  const int e = threadIdx.x % width;
-  if (e < a.E) {
-    int all = 0, front = 0;
-    for (int b = threadIdx.x / width; b < a.blocks; b += kPlaceThreads / width) {
-      const int c = a.counts[(long long)b * a.E + e];
+  int width = 16;  // threads that take a workgroup's counts
+  while (width < quads) width *= 2;
+  const int q = threadIdx.x % width, step = kPlaceThreads / width;
+  if (q < quads) {
+    v4i all = {0, 0, 0, 0}, front = {0, 0, 0, 0};
+#pragma unroll 8
+    for (int b = threadIdx.x / width; b < a.blocks; b += step) {
+      const v4i c = *reinterpret_cast<const v4i*>(a.counts + (long long)b * stride + 4 * q);
       all += c;
-      front += b < b0 ? c : 0;
+      if (b < b0) front += c;
+      if (b >= b0 && b < b1) *reinterpret_cast<v4i*>(&next[b - b0][4 * q]) = c;
     }
-    atomicAdd(&first[e], all);
-    atomicAdd(&before[e], front);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      atomicAdd(&first[4 * q + i], all[i]);
+      atomicAdd(&before[4 * q + i], front[i]);
+    }
   }
   __syncthreads();
   place_experts(first, first, a.E);
   __syncthreads();
   const int total = first[a.E];
+  for (int e = threadIdx.x; e < a.E; e += kPlaceThreads) {
+    int at = first[e] + before[e];
+    for (int b = 0; b < b1 - b0; ++b) {
+      const int c = next[b][e];
+      next[b][e] = at;
+      at += c;
+    }
+  }
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= a.E; i += kPlaceThreads) a.offsets[i] = first[i];
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.E; i += kPlaceThreads) first[i] += before[i];
+    for (int e = threadIdx.x; e <= a.E; e += kPlaceThreads) a.offsets[e] = first[e];
   __syncthreads();
   const long long entries = (long long)a.T * a.topk;
   const long long each = (long long)a.passes * a.tokens * a.topk;
-  for (int b = b0; b < b1; ++b) {
-    const long long end = min((b + 1) * each, entries);
-    for (long long i = b * each + threadIdx.x; i < end; i += kPlaceThreads) {
-      const int id = a.experts[i];
-      if (id < 0) continue;
-      const int slot = first[id] + a.slots[i];
-      a.slots[i] = slot;
-      a.rows[slot] = (int)(i / a.topk);
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.E; i += kPlaceThreads) first[i] += a.counts[(long long)b * a.E + i];
-    __syncthreads();
+  const long long end = min(b1 * each, entries);
+  for (long long i = b0 * each + threadIdx.x; i < end; i += kPlaceThreads) {
+    const int id = a.experts[i];
+    if (id < 0) continue;
+    const int slot = next[(int)(i / each) - b0][id] + a.slots[i];
+    a.slots[i] = slot;
+    a.rows[slot] = (int)(i / a.topk);
   }
   for (long long i = total + (long long)blockIdx.x * kPlaceThreads + threadIdx.x; i < entries;
        i += (long long)gridDim.x * kPlaceThreads)
@@ -255,22 +301,17 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteArgs a, int s
 template <typename Logit>
 auto pick(int E) {
   return E <= 128 ? route_kernel<16, 8, Logit>
-                  : E <= 256 ? route_kernel<64, 4, Logit> : route_kernel<64, 16, Logit>;
+                  : E <= 512 ? route_kernel<64, 8, Logit> : route_kernel<64, 16, Logit>;
 }
 
 }  // namespace
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
-  hipError_t e = launch_kernel(a.bf16 ? pick<uint16_t>(a.E) : pick<float>(a.E),
-                               dim3((unsigned)a.blocks), dim3(kThreads), 0, s, a);
+  const hipError_t e = launch_kernel(a.bf16 ? pick<uint16_t>(a.E) : pick<float>(a.E),
+                                     dim3((unsigned)a.blocks), dim3(kThreads), 0, s, a);
   if (e != hipSuccess || !a.offsets || a.blocks == 1) return e;
-  const int span = (a.blocks + 63) / 64;
-  int blocks = (a.blocks + span - 1) / span;
-  RouteArgs args = a;
-  int arg_span = span;
-  void* list[] = {&args, &arg_span};
-  return hipLaunchKernel(reinterpret_cast<const void*>(place_kernel), dim3((unsigned)blocks),
-                         dim3(kPlaceThreads), list, 0, s);
+  return launch_kernel(place_kernel, dim3((unsigned)((a.blocks + kSpan - 1) / kSpan)),
+                       dim3(kPlaceThreads), 0, s, a);
 }
 
 }  // namespace w8

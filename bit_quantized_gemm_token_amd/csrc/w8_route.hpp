@@ -29,9 +29,14 @@ struct RouteArgs {
   // T * topk entries in passes of `tokens` tokens (at most kRoutePass entries),
   // `passes` of them a workgroup; more than one workgroup: its experts' counts
   int tokens, passes, blocks;
-  int* counts;  // [blocks, E] (workspace)
+  int* counts;  // [blocks, count_stride(E)] (workspace)
+  int wide;     // rows load in 16-byte pieces
 };
-constexpr int kRoutePass = 256;
+// Up to 256 entries are one pass of one workgroup; more go in passes of half as
+// many, which is a token for every 16 lanes of a workgroup at top 8 (8192 tokens
+// of 128 experts, passes of 256: the first launch 12.5 us).
+constexpr int kRoutePass = 256, kRouteMany = 128;
+__host__ __device__ constexpr int count_stride(int E) { return (E + 3) / 4 * 4; }
 // One launch, or for more than one workgroup's entries two.
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
 

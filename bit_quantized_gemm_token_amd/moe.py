@@ -10,7 +10,7 @@ import torch
 
 from . import _capi
 from .block import _BF16, _E_WORKSPACE, _F32, _I32, _codes, _flat, _new, _rows, _shape
-from .tokens import _new_flat, _on_device, _one_device
+from .tokens import _current_device, _elsewhere, _new_flat, _one_device
 
 _BLOCK = _capi.FORMATS["Block_FP8"]
 _GROUP = _capi.GROUP
@@ -50,31 +50,36 @@ def moe_route(logits, topk, renormalize=True, scale=1.0, lists=True, workspace=N
     if logits.dtype is not _F32 and logits.dtype is not _BF16:
         raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
     T, E = logits.shape
-    dev = logits.device
-    experts, ep, _ = _new(T, topk, _I32, dev, stream)
-    weights, wp, _ = _new(T, topk, _F32, dev, stream)
+    dev, index, n = logits.device, logits.get_device(), T * topk
+    s = _handle(stream, dev)
     op = rp = sp = buf = None
     if lists:
-        offsets, op = _new_flat(E + 1, _I32, dev, stream)
-        rows, rp = _new_flat(T * topk, _I32, dev, stream)
-        slots, sp, _ = _new(T, topk, _I32, dev, stream)
-    s = _handle(stream, dev)
-    if lists and T * topk > 256:
-        if workspace is None:
-            workspace = _workspace_of(dev, s)
-        buf = workspace.buf
-    index = logits.get_device()
+        # one allocation for all five outputs (each costs the host more than a
+        # view does, and the call a third of its time)
+        whole, wp = _new_flat(4 * n + E + 1, _I32, dev, stream)
+        weights, experts, slots, rows, offsets = _split(whole, (n, n, n, n, E + 1))
+        weights = weights.view(_F32).view(T, topk)
+        experts, slots = experts.view(T, topk), slots.view(T, topk)
+        ep, sp, rp, op = wp + 4 * n, wp + 8 * n, wp + 12 * n, wp + 16 * n
+        if n > 256:
+            if workspace is None:
+                workspace = _workspace_of(dev, s)
+            buf = workspace.buf
+    else:
+        experts, ep, _ = _new(T, topk, _I32, dev, stream)
+        weights, wp, _ = _new(T, topk, _F32, dev, stream)
     for retry in (True, False):
-        status = _on_device(index, _lib.w8_moe_route, T, E, topk, lp, ldl, logits.dtype is _F32,
-                            bool(renormalize), scale, ep, wp, op, rp, sp,
-                            None if buf is None else buf.data_ptr(),
-                            0 if buf is None else buf.numel(), s)
+        args = (T, E, topk, lp, ldl, 1 if logits.dtype is _F32 else 0, 1 if renormalize else 0,
+                scale, ep, wp, op, rp, sp, None if buf is None else buf.data_ptr(),
+                0 if buf is None else buf.numel(), s)
+        status = _route(*args) if index == _current_device() else _elsewhere(index, _route, args)
         if status != _E_WORKSPACE or not retry:
             break
         if workspace is None:
             workspace = _workspace_of(dev, s)
         buf = workspace.reserve(moe_route_workspace_size(T, E, topk), stream)
-    _check(status)
+    if status:
+        _check(status)
     return (experts, weights, offsets, rows, slots) if lists else (experts, weights)
 
 
@@ -99,14 +104,17 @@ def moe_combine(y, weights, slots, base=None, out=None, stream=None):
     if base is not None:
         bp, ldb = _rows(base, "base", _BF16)
         _shape(base, T, D, "base")
+    index = _one_device(y, weights, slots, base, out)
+    dev = y.device
     if out is None:
-        out, outp, ldo = _new(T, D, _BF16, y.device, stream)
+        out, outp, ldo = _new(T, D, _BF16, dev, stream)
     else:
         _shape(out, T, D, "out")
         outp, ldo = _rows(out, "out", _BF16)
-    index = _one_device(y, weights, slots, base, out)
-    _check(_on_device(index, _lib.w8_moe_combine, T, topk, D, yp, ldy, n_rows, wp, sp, bp, ldb,
-                      outp, ldo, _handle(stream, y.device)))
+    args = (T, topk, D, yp, ldy, n_rows, wp, sp, bp, ldb, outp, ldo, _handle(stream, dev))
+    status = _combine(*args) if index == _current_device() else _elsewhere(index, _combine, args)
+    if status:
+        _check(status)
     return out
 
 
@@ -171,28 +179,33 @@ def moe_layer(fmt, xq, sx, experts, weights, w1, s1, w2, s2, y=None, workspace=N
     if E2 != E or N1 != 2 * I or K1 != D or N2 != D:
         raise ValueError(f"w1 [{E}, {N1}, {K1}] and w2 [{E2}, {N2}, {I}] must be [E, 2 I, {D}] and "
                          f"[E, {D}, I]")
+    index = _one_device(xq, sx, experts, weights, w1t, s1, w2t, s2, y)
+    dev = xq.device
     if y is None:
-        y, yp, ldy = _new(T, D, _BF16, xq.device, stream)
+        y, yp, ldy = _new(T, D, _BF16, dev, stream)
     else:
         _shape(y, T, D, "y")
         yp, ldy = _rows(y, "y", _BF16)
-    index = _one_device(xq, sx, experts, weights, w1t, s1, w2t, s2, y)
-    s = _handle(stream, xq.device)
+    s = _handle(stream, dev)
     if workspace is None:
-        workspace = _workspace_of(xq.device, s)
+        workspace = _workspace_of(dev, s)
     buf = workspace.buf
     for retry in (True, False):
-        status = _on_device(index, _lib.w8_moe_layer, f, E, T, topk, D, I, xp, ldq, sxp, ep, wp,
-                            w1p, ldw1, w1s, s1p, s1s, w2p, ldw2, w2s, s2p, s2s, yp, ldy,
-                            None if buf is None else buf.data_ptr(),
-                            0 if buf is None else buf.numel(), s)
+        args = (f, E, T, topk, D, I, xp, ldq, sxp, ep, wp, w1p, ldw1, w1s, s1p, s1s, w2p, ldw2,
+                w2s, s2p, s2s, yp, ldy, None if buf is None else buf.data_ptr(),
+                0 if buf is None else buf.numel(), s)
+        status = _layer(*args) if index == _current_device() else _elsewhere(index, _layer, args)
         if status != _E_WORKSPACE or not retry:
             break
         buf = workspace.reserve(moe_layer_workspace_size(T, topk, D, I), stream)
-    _check(status)
+    if status:
+        _check(status)
     return y
 
 
 # (the package's own helpers; __init__ imports this module after defining them)
 from . import (PackedExperts, _check, _fmt, _handle, _lib, _weight_stride,  # noqa: E402
                _workspace_of)
+
+_route, _combine, _layer = _lib.w8_moe_route, _lib.w8_moe_combine, _lib.w8_moe_layer
+_split = torch.unsafe_split_with_sizes

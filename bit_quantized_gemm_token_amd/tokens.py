@@ -9,8 +9,10 @@ import ctypes
 import torch
 
 from . import _capi
-from .block import (_BF16, _E_WORKSPACE, _F32, _codes, _flat, _new, _new_codes, _rows, _shape)
+from .block import (_BF16, _CODES, _E_WORKSPACE, _F32, _codes, _flat, _new, _new_codes, _rows,
+                    _shape)
 
+_I8 = torch.int8
 _INT8 = _capi.FORMATS["W8A8_INT8"]
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
     else torch.cuda.current_device
@@ -25,10 +27,8 @@ def _one_device(x, *others):
     return index
 
 
-def _on_device(index, entry, *args):
-    """entry(*args) with that device the current one, which the library launches on."""
-    if index == _current_device():
-        return entry(*args)
+def _elsewhere(index, entry, args):
+    """entry(*args) on a device that is not the current one (the library launches on that)."""
     with torch.cuda.device(index):
         return entry(*args)
 
@@ -56,18 +56,21 @@ def token_quantize(fmt, x, gate=None, reciprocal=False, xq=None, sx=None, stream
     if gate is not None:
         gp, ldg = _rows(gate, "gate", _BF16)
         _shape(gate, M, K, "gate")
+    index = _one_device(x, gate, xq, sx)
+    dev = x.device
     if xq is None:
-        xq, qp, ldq = _new_codes(M, K, x.device, stream, _codes_dtype(f))
+        xq, qp, ldq = _new_codes(M, K, dev, stream, _I8 if f == _INT8 else _CODES)
     else:
         _shape(xq, M, K, "xq")
         qp, ldq = _codes(xq, "xq")
     if sx is None:
-        sx, sp = _new_flat(M, _F32, x.device, stream)
+        sx, sp = _new_flat(M, _F32, dev, stream)
     else:
         sp = _flat(sx, "sx", _F32, M)
-    index = _one_device(x, gate, xq, sx)
-    _check(_on_device(index, _lib.w8_token_quantize, f, M, K, xp, ldx, gp, ldg,
-                      1 if reciprocal else 0, qp, ldq, sp, _handle(stream, x.device)))
+    args = (f, M, K, xp, ldx, gp, ldg, 1 if reciprocal else 0, qp, ldq, sp, _handle(stream, dev))
+    status = _quantize(*args) if index == _current_device() else _elsewhere(index, _quantize, args)
+    if status:
+        _check(status)
     return xq, sx
 
 
@@ -122,28 +125,32 @@ def token_gemm(fmt, xq, sx, wq, sw, y=None, workspace=None, stream=None):
     if wk != K:
         raise ValueError(f"K mismatch: xq {tuple(xq.shape)} vs weights {(N, wk)}")
     sxp, swp = _flat(sx, "sx", _F32, M), _flat(sw, "sw", _F32, N)
+    index = _one_device(xq, sx, wt, sw, y)
+    dev = xq.device
     if y is None:
-        y, yp, ldy = _new(M, N, _BF16, xq.device, stream)
+        y, yp, ldy = _new(M, N, _BF16, dev, stream)
     else:
         _shape(y, M, N, "y")
         yp, ldy = _rows(y, "y", _BF16)
-    index = _one_device(xq, sx, wt, sw, y)
-    s = _handle(stream, xq.device)
+    s = _handle(stream, dev)
     if workspace is None:
-        workspace = _workspace_of(xq.device, s)
+        workspace = _workspace_of(dev, s)
     # (what the workspace holds is enough for most calls, as in block_gemm)
     buf = workspace.buf
     for retry in (True, False):
-        status = _on_device(index, _lib.w8_token_gemm, f, M, N, K, xp, ldq, sxp, wp, ldw, swp, yp,
-                            ldy, None if buf is None else buf.data_ptr(),
-                            0 if buf is None else buf.numel(), s)
+        args = (f, M, N, K, xp, ldq, sxp, wp, ldw, swp, yp, ldy,
+                None if buf is None else buf.data_ptr(), 0 if buf is None else buf.numel(), s)
+        status = _gemm(*args) if index == _current_device() else _elsewhere(index, _gemm, args)
         if status != _E_WORKSPACE or not retry:
             break
         buf = workspace.reserve(token_gemm_workspace_size(f, M, N, K, packed), stream)
-    _check(status)
+    if status:
+        _check(status)
     return y
 
 
 # (the package's own helpers; __init__ imports this module after defining them)
-from . import (PackedWeight, _allocate, _check, _codes_dtype, _fmt, _handle, _layout,  # noqa: E402
-               _lib, _weight_stride, _workspace_of)
+from . import (PackedWeight, _allocate, _check, _fmt, _handle, _layout, _lib,  # noqa: E402
+               _weight_stride, _workspace_of)
+
+_quantize, _gemm = _lib.w8_token_quantize, _lib.w8_token_gemm

@@ -134,11 +134,9 @@ def test_strided_logits(w8):
 
 
 def test_more_tokens_than_workgroups_of_one_pass(w8):
-    """More than 2048 workgroups' worth of entries: several passes each."""
-    T, E, topk = 9000, 16, 32
-    topk = 16
+    """More than 1024 workgroups' worth of entries: several passes each."""
+    T, E, topk = 2048 * 16 + 5, 16, 16  # 8 tokens a pass
     g = np.random.default_rng(1)
-    T = 2048 * 16 + 5  # 16 tokens a pass: two passes a workgroup
     d, l = logits_of(g, T, E, "fp32")
     l[5::7] = -np.inf
     d = on_device(l)

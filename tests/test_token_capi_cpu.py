@@ -113,8 +113,8 @@ def test_route_workspace(lib, w8):
     assert call(lib.w8_moe_route, ROUTE, ws_bytes=need - 1) == WORKSPACE
     assert call(lib.w8_moe_route, ROUTE, ws=None) == WORKSPACE
     assert w8.moe_route_workspace_size(0, 64, 8) == 0
-    # the counts of at most 2048 workgroups, past the counter region
-    assert w8.moe_route_workspace_size((1 << 22) - 1, 1024, 32) <= (2 << 20) + 2048 * 1024 * 4
+    # the counts of at most 1024 workgroups, past the counter region
+    assert w8.moe_route_workspace_size((1 << 22) - 1, 1024, 32) <= (2 << 20) + 1024 * 1024 * 4
     with pytest.raises(w8.W8Error, match="topk"):
         w8.moe_route_workspace_size(4, 8, 9)
 
