@@ -125,40 +125,55 @@ struct Plan {
 // than tells times: for long runs of the largest tile, whose clock falls under
 // power, it is 12 to 17% under what is measured (8192 x 5120 x 8192 244 us of
 // 284 to 300).
+//
+// The token-scaled formats' steps are shorter by the additions of the groups'
+// sums; their own costs were fitted the same way to 310 shapes (both formats,
+// 14 to 8192 tokens), and on 104 others the choice was within 1.3% of the fastest
+// measured on average, 17% at worst (by Block_FP8's costs 1.4%; 48 x 4608 x 7168
+// 10.8 us on 64 x 128, K in four, where 64 x 64, K in two takes 9.5).
 struct TileCost {
   int resident;         // workgroups of a compute unit
   double step1, step2;  // us a step, one or two of them resident
   double round;         // us a round beside the steps
 };
-constexpr double kLaunch = 1.7;
-constexpr TileCost kTileCost[kBlockTiles] = {{2, 0.26, 0.50, 1.5},
-                                             {2, 0.23, 0.465, 2.0},
-                                             {2, 0.36, 0.725, 2.5},
-                                             {1, 0.47, 0.47, 3.15},
-                                             {1, 1.305, 1.305, 7.4}};
-// pieces of the largest tile
-constexpr double kHalfStep = 0.89, kQuarterStep = 0.456, kPieceRound = 3.3;
-constexpr double kWeightBytesPerUs = 4.5e6;
+struct Costs {
+  TileCost tile[kBlockTiles];
+  double launch;
+  double half_step, quarter_step, piece_round;  // pieces of the largest tile
+  double split, split_bytes;                    // K split: the hand-off, us a partial's byte
+  double weight_bytes;                          // a us
+};
+constexpr Costs kBlockCosts = {
+    {{2, 0.26, 0.50, 1.5}, {2, 0.23, 0.465, 2.0}, {2, 0.36, 0.725, 2.5}, {1, 0.47, 0.47, 3.15},
+     {1, 1.305, 1.305, 7.4}},
+    1.7, 0.89, 0.456, 3.3, 1.1, 0.38e-6, 4.5e6};
+constexpr Costs kTokenCosts = {
+    {{2, 0.208, 0.432, 1.15}, {2, 0.177, 0.418, 1.37}, {2, 0.319, 0.735, 1.85},
+     {1, 0.439, 0.439, 2.73}, {1, 1.344, 1.344, 6.69}},
+    1.67, 0.819, 0.433, 3.03, 1.33, 0.362e-6, 5.2e6};
 
-double estimate(const Plan& p, int N, int K) {
-  const TileCost& c = kTileCost[p.tile];
+double estimate(const Costs& costs, const Plan& p, int N, int K) {
+  const TileCost& c = costs.tile[p.tile];
   const BlockTile& t = block_tile(p.tile);
   const int G = groups_of(K);
   const long long tiles = p.tiles_m * p.tiles_n, n = tiles * p.split_k;
   if (p.tile == kLargeTile)
-    return kLaunch + (double)ceil_div(p.whole, kComputeUnits) * (G * c.step1 + c.round) +
-           (p.whole < tiles ? G * (p.parts == 4 ? kQuarterStep : kHalfStep) + kPieceRound : 0);
+    return costs.launch + (double)ceil_div(p.whole, kComputeUnits) * (G * c.step1 + c.round) +
+           (p.whole < tiles
+                ? G * (p.parts == 4 ? costs.quarter_step : costs.half_step) + costs.piece_round
+                : 0);
   const double steps = (double)ceil_div(G, p.split_k);
   const long long cap = (long long)kComputeUnits * c.resident;
   double loop = (double)(n / cap) * (steps * c.step2 + c.round);
   if (n % cap) loop += steps * (n % cap <= kComputeUnits ? c.step1 : c.step2) + c.round;
-  const double weights = (double)N * K / kWeightBytesPerUs;
-  double us = kLaunch + (loop > weights ? loop : weights);
-  if (p.split_k > 1) us += 1.1 + 0.38e-6 * (double)n * t.bm * t.bn * 4;
+  const double weights = (double)N * K / costs.weight_bytes;
+  double us = costs.launch + (loop > weights ? loop : weights);
+  if (p.split_k > 1) us += costs.split + costs.split_bytes * (double)n * t.bm * t.bn * 4;
   return us;
 }
 
-Plan plan_dense(int M, int N, int K) {
+Plan plan_dense(int fmt, int M, int N, int K) {
+  const Costs& costs = fmt == W8_BLOCK_FP8 ? kBlockCosts : kTokenCosts;
   Plan best{};
   double best_us = 0;
   for (int tile = 0; tile < kBlockTiles; ++tile) {
@@ -180,7 +195,7 @@ Plan plan_dense(int M, int N, int K) {
                             groups_of(K) < 2 * p.split_k || tiles * p.split_k > 2 * kComputeUnits))
         break;
       p.wgs = tile == kLargeTile ? p.whole + p.parts * (tiles - p.whole) : tiles * p.split_k;
-      const double us = estimate(p, N, K);
+      const double us = estimate(costs, p, N, K);
       if (!best.wgs || us < best_us) {
         best = p;
         best_us = us;
@@ -296,7 +311,7 @@ w8_status dense_gemm(int fmt, int M, int N, int K, const void* xq, int64_t ldq, 
   if (use_small_m(fmt, M, N, K, packed))
     return w8_gemm_w8a8((w8_fmt)fmt, M, N, K, xq, ldq, sx, wq, ldw, sw, y, ldy, nullptr, ws,
                         ws_bytes, stream);
-  const Plan p = plan_dense(M, N, K);
+  const Plan p = plan_dense(fmt, M, N, K);
   const size_t need = plan_bytes(p);
   if (need > 0) {
     if (!ws || ws_bytes < need)
@@ -406,7 +421,7 @@ w8_status w8_block_gemm_workspace_size(int M, int N, int K, int packed, size_t* 
   if (!bytes) return fail(W8_E_INVALID, "null output pointer");
   if (M && use_small_m(W8_BLOCK_FP8, M, N, K, packed))
     return w8_workspace_size(W8_BLOCK_FP8, W8_OP_GEMM, M, N, K, packed, nullptr, bytes);
-  *bytes = M ? plan_bytes(plan_dense(M, N, K)) : 0;
+  *bytes = M ? plan_bytes(plan_dense(W8_BLOCK_FP8, M, N, K)) : 0;
   return ok();
 }
 
@@ -420,7 +435,7 @@ w8_status w8_block_gemm_plan(int M, int N, int K, int packed, w8_block_plan* pla
   if (packed && K % W8_GROUP) return fail(W8_E_INVALID, "packed weights need K % 128 == 0");
   if (!plan) return fail(W8_E_INVALID, "null output pointer");
   *plan = w8_block_plan{0, 0, 1, 1, 0};
-  if (M && !use_small_m(W8_BLOCK_FP8, M, N, K, packed)) *plan = describe(plan_dense(M, N, K));
+  if (M && !use_small_m(W8_BLOCK_FP8, M, N, K, packed)) *plan = describe(plan_dense(W8_BLOCK_FP8, M, N, K));
   return ok();
 }
 
@@ -445,7 +460,7 @@ w8_status w8_token_gemm_workspace_size(w8_fmt fmt_in, int M, int N, int K, int p
   if (!bytes) return fail(W8_E_INVALID, "null output pointer");
   if (M && use_small_m(fmt, M, N, K, packed))
     return w8_workspace_size((w8_fmt)fmt, W8_OP_GEMM, M, N, K, packed, nullptr, bytes);
-  *bytes = M ? plan_bytes(plan_dense(M, N, K)) : 0;
+  *bytes = M ? plan_bytes(plan_dense(fmt, M, N, K)) : 0;
   return ok();
 }
 
@@ -458,7 +473,7 @@ w8_status w8_token_gemm_plan(w8_fmt fmt_in, int M, int N, int K, int packed, w8_
   if (packed && K % W8_GROUP) return fail(W8_E_INVALID, "packed weights need K % 128 == 0");
   if (!plan) return fail(W8_E_INVALID, "null output pointer");
   *plan = w8_block_plan{0, 0, 1, 1, 0};
-  if (M && !use_small_m(fmt, M, N, K, packed)) *plan = describe(plan_dense(M, N, K));
+  if (M && !use_small_m(fmt, M, N, K, packed)) *plan = describe(plan_dense(fmt, M, N, K));
   return ok();
 }
 

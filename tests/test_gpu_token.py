@@ -7,6 +7,7 @@ import torch
 from tests.block_cases import DEV, bf16, on_device
 from tests.token_cases import (FORMATS, QMAX, assert_codes, assert_product, bits_of, codes,
                                quantized, scales, values)
+from tests.token_plans import SHAPES
 
 pytestmark = pytest.mark.gpu
 
@@ -156,24 +157,14 @@ def tile(p):
     return p["tile_m"], p["tile_n"]
 
 
-# one token to many; K from 16 on, with and without a tail; every tile, split
-# and not, the largest with its last round whole, in halves and in quarters
-SHAPES = [(1, 16, 16, False), (1, 4608, 7168, False), (7, 130, 272, False), (32, 300, 144, False),
-          (33, 1, 16, False), (48, 256, 384, True), (100, 256, 2064, False), (36, 66, 4096, True),
-          (354, 3939, 352, False), (2075, 133, 256, True), (179, 779, 2272, False),
-          (131, 6634, 944, False), (48, 4608, 7168, False), (129, 5521, 1152, True),
-          (1551, 2087, 848, False), (394, 4750, 384, True), (202, 4210, 5376, False),
-          (66, 2051, 10112, True), (2568, 3090, 64, False), (2717, 1417, 112, False),
-          (4000, 4200, 16, False), (2568, 3090, 1040, False), (2403, 3329, 128, True),
-          (2695, 1423, 384, True), (5000, 3600, 1024, True)]
-
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("shape", SHAPES)
 def test_gemm(w8, fmt, shape):
     M, N, K, packed = shape
+    p = w8.token_gemm_plan(fmt, M, N, K, packed=packed)
+    assert (tile(p), p["split_k"], p["parts"]) == SHAPES[shape]
     c = Gemm(fmt, M, N, K)
-    print(w8.token_gemm_plan(fmt, M, N, K, packed=packed), flush=True)
     if packed:
         c.dev[2] = w8.pack_weight(fmt, c.dev[2])
     buf = torch.full((M + 2, N + 5), 7.0, dtype=torch.bfloat16, device=DEV)
@@ -186,13 +177,13 @@ def test_gemm(w8, fmt, shape):
 
 def test_every_tile_and_split_gives_the_same_int8_bits(w8):
     """Exact sums: whichever kernel runs, the first rows are the same."""
-    c = Gemm("W8A8_INT8", 4000, 4200, 2080)
+    c = Gemm("W8A8_INT8", 4000, 4200, 4128)
     xq, sx, wq, sw = c.dev
     first = w8.token_gemm("W8A8_INT8", *c.dev)[:20]
     c.check(first, np.arange(20))
     plans = set()
     for M in (20, 33, 48, 70, 100, 150, 300, 500, 700, 930, 1000, 1500, 2500, 3300):
-        p = w8.token_gemm_plan("W8A8_INT8", M, 4200, 2080)
+        p = w8.token_gemm_plan("W8A8_INT8", M, 4200, 4128)
         plans.add((tile(p), p["split_k"], p["parts"]))
         assert torch.equal(w8.token_gemm("W8A8_INT8", xq[:M], sx[:M], wq, sw)[:20], first), p
     assert len(plans) >= 6, plans

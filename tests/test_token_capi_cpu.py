@@ -36,7 +36,7 @@ def null(d):
 
 QUANT = dict(fmt=INT8, M=4, K=256, x=P, ldx=256, gate=P, ldg=256, reciprocal=0, xq=P, ldq=256, sx=P,
              stream=None)
-GEMM = dict(fmt=INT8, M=48, N=512, K=1024, xq=P, ldq=1024, sx=P, wq=P, ldw=1024, sw=P, y=P,
+GEMM = dict(fmt=INT8, M=48, N=512, K=5120, xq=P, ldq=5120, sx=P, wq=P, ldw=5120, sw=P, y=P,
             ldy=512, ws=P, ws_bytes=BIG, stream=None)
 ROUTE = dict(T=100, E=64, topk=8, logits=P, ldl=64, fp32=1, renormalize=1, scale=1.0, experts=P,
              weights=P, offsets=P, rows=P, slots=P, ws=P, ws_bytes=BIG, stream=None)
@@ -59,18 +59,18 @@ def test_quantize_refuses(lib, bad):
 
 @pytest.mark.parametrize("bad", [
     dict(fmt=BLOCK), dict(fmt=7), dict(M=-1), dict(M=1 << 22), dict(N=0), dict(N=(1 << 24) + 1),
-    dict(K=8), dict(K=1032), dict(K=(1 << 17), ldq=1 << 17, ldw=1 << 17),
+    dict(K=8), dict(K=5112), dict(K=(1 << 17), ldq=1 << 17, ldw=1 << 17),
     dict(fmt=FP8, K=(1 << 22) + 16), dict(xq=None), dict(sx=None), dict(wq=None), dict(sw=None),
-    dict(y=None), dict(xq=P + 8), dict(wq=P + 8), dict(ldq=1008), dict(ldq=1032), dict(ldw=1008),
-    dict(ldw=1032), dict(ldw=-2), dict(ldy=511), dict(sx=P + 2), dict(sw=P + 1), dict(y=P + 1),
-    dict(ldw=0, K=1008), dict(ldq=(1 << 23) + 16), dict(ldw=(1 << 23) + 16), dict(ws=P + 8)])
+    dict(y=None), dict(xq=P + 8), dict(wq=P + 8), dict(ldq=5104), dict(ldq=5128), dict(ldw=5104),
+    dict(ldw=5128), dict(ldw=-2), dict(ldy=511), dict(sx=P + 2), dict(sw=P + 1), dict(y=P + 1),
+    dict(ldw=0, K=5104), dict(ldq=(1 << 23) + 16), dict(ldw=(1 << 23) + 16), dict(ws=P + 8)])
 def test_gemm_refuses(lib, bad):
     assert call(lib.w8_token_gemm, GEMM, **bad) == INVALID
     assert lib.w8_last_error()
 
 
 def test_gemm_workspace_and_plan(lib, w8):
-    need = w8.token_gemm_workspace_size("W8A8_INT8", 48, 512, 1024)
+    need = w8.token_gemm_workspace_size("W8A8_INT8", 48, 512, 5120)
     assert need > 0
     assert call(lib.w8_token_gemm, GEMM, ws_bytes=need - 1) == WORKSPACE
     assert call(lib.w8_token_gemm, GEMM, ws=None) == WORKSPACE
@@ -85,7 +85,7 @@ def test_gemm_workspace_and_plan(lib, w8):
     for fmt in ("W8A8_INT8", "FP8_Dynamic"):
         assert w8.token_gemm_workspace_size(fmt, 8192, 8192, 8192) == 0
         assert w8.token_gemm_plan(fmt, 8192, 8192, 8192)["tile_m"] == 256
-        p = w8.token_gemm_plan(fmt, 48, 512, 1024)
+        p = w8.token_gemm_plan(fmt, 48, 512, 5120)
         assert p["split_k"] > 1 and p["workgroups"] > 0
         assert w8.token_gemm_plan(fmt, 1, 512, 1024)["tile_m"] == 0  # the small-M GEMM
     with pytest.raises(w8.W8Error, match="128"):
