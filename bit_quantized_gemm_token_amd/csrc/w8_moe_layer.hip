@@ -370,7 +370,6 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeLayerArgs a) {
 // of I, the tokens' codes from LDS, where the workgroup makes them from h
 // `chunk` columns at a time.
 constexpr int kColumns = 16 * kWaves;
-constexpr int kDownPieces = 2;
 constexpr int kPad = 16;  // bytes that move a row's codes on by four LDS banks
 
 extern __shared__ __align__(16) uint8_t codes[];
@@ -392,6 +391,19 @@ __device__ __forceinline__ Hidden load_hidden(const MoeLayerArgs& a, const int* 
   const int t = i / per, k = 8 * (i - t * per);
   if (k < cols) __builtin_memcpy(v.f, a.h + (long long)entry[t] * a.I + c0 + k, 32);
   return v;
+}
+// Two of them a thread, from piece i0 on of `count`; their loads are all in
+// flight.
+constexpr int kHeld = 2;
+__device__ __forceinline__ void load_hidden(const MoeLayerArgs& a, const int* entry, int i0,
+                                            int count, int per, int c0, int cols,
+                                            Hidden (&v)[kHeld]) {
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q) {
+    const int i = i0 + (int)threadIdx.x + q * kThreads;
+    v[q] = Hidden{};
+    if (i < count) v[q] = load_hidden(a, entry, i, per, c0, cols);
+  }
 }
 __device__ __forceinline__ unsigned largest(const Hidden& v) {
   unsigned m = 0;
@@ -436,12 +448,12 @@ __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const E
   for (int c0 = 0; c0 < a.I; c0 += a.chunk) {
     const int cols = min(a.chunk, a.I - c0), per = (cols + kGroup - 1) / kGroup * (kGroup / 8);
     const int kb = c0 / KSTEP, kend = (c0 + cols + KSTEP - 1) / KSTEP;
-    // a thread's first eight hidden values, then the first weights: loads
-    // return in order, so that the codes are made while the weights arrive
-    Hidden first = {};
-    if ((int)threadIdx.x < x.tokens * per)
-      first = load_hidden(a, entry, threadIdx.x, per, c0, cols);
-    auto p = products<FMT, 1, MB, steps<FMT>(kDownPieces), false>(
+    // a thread's first hidden values, then the first weights: loads return in
+    // order, so that the codes are made while the weights arrive
+    const int pieces = x.tokens * per;
+    Hidden held[kHeld];
+    load_hidden(a, entry, 0, pieces, per, c0, cols, held);
+    auto p = products<FMT, 1, MB, steps<FMT>(2), false>(
         kb, min(kend, kfull), [&](int, int k) -> Frag { return weight_step<FMT, PACKED>(wp, k); },
         [&](int b, int k) -> Frag { return load_frag<FMT>(xp[b], k - kb); },
         [&](int, int k) { return uniform_load(swp + k); },
@@ -455,33 +467,44 @@ __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const E
         if (threadIdx.x < kLayerTokens) lds.top[threadIdx.x] = 0u;
         __syncthreads();
         // (a token's threads are whole groups of 16 lanes)
-        auto take = [&](int i, int each, const Hidden& v) {
-          const unsigned m = seg16_umax(largest(v));
-          if ((i & 15) == 0) atomicMax(&lds.top[i / each], m);
+        auto take = [&](int i0, int count, int each, const Hidden (&v)[kHeld]) {
+#pragma unroll
+          for (int q = 0; q < kHeld; ++q) {
+            const int i = i0 + (int)threadIdx.x + q * kThreads;
+            if (i >= count) continue;
+            const unsigned m = seg16_umax(largest(v[q]));
+            if ((i & 15) == 0) atomicMax(&lds.top[i / each], m);
+          }
         };
-        if ((int)threadIdx.x < x.tokens * per) take(threadIdx.x, per, first);
-        for (int i = threadIdx.x + kThreads; i < x.tokens * per; i += kThreads)
-          take(i, per, load_hidden(a, entry, i, per, 0, cols));
-        for (int c = a.chunk; c < a.I; c += a.chunk) {
+        take(0, pieces, per, held);
+        for (int c = 0, from = kHeld * kThreads; c < a.I; c += a.chunk, from = 0) {
           const int more = min(a.chunk, a.I - c), each = (more + kGroup - 1) / kGroup * (kGroup / 8);
-          for (int i = threadIdx.x; i < x.tokens * each; i += kThreads)
-            take(i, each, load_hidden(a, entry, i, each, c, more));
+          for (int i0 = from; i0 < x.tokens * each; i0 += kHeld * kThreads) {
+            Hidden v[kHeld];
+            load_hidden(a, entry, i0, x.tokens * each, each, c, more, v);
+            take(i0, x.tokens * each, each, v);
+          }
         }
       }
     }
     __syncthreads();  // (and the last chunk's codes have been read)
-    for (int i = threadIdx.x; i < x.tokens * per; i += kThreads) {
-      Hidden v = i < kThreads ? first : load_hidden(a, entry, i, per, c0, cols);
-      const int t = i / per, k = 8 * (i - t * per);
-      float s;
-      if constexpr (BLOCK) {  // 16 lanes hold a group
-        const unsigned m = seg16_umax(largest(v));
-        s = act_scale<false>(__uint_as_float(m));
-        if (k % kGroup == 0) gscale[t * (a.chunk / kGroup) + k / kGroup] = s;
-      } else {
-        s = act_scale<INT8>(__uint_as_float(lds.top[t]));
+    for (int i0 = 0; i0 < pieces; i0 += kHeld * kThreads) {
+      if (i0) load_hidden(a, entry, i0, pieces, per, c0, cols, held);
+#pragma unroll
+      for (int q = 0; q < kHeld; ++q) {
+        const int i = i0 + (int)threadIdx.x + q * kThreads;
+        if (i >= pieces) continue;
+        const int t = i / per, k = 8 * (i - t * per);
+        float s;
+        if constexpr (BLOCK) {  // 16 lanes hold a group
+          s = act_scale<false>(__uint_as_float(seg16_umax(largest(held[q]))));
+          if (k % kGroup == 0) gscale[t * (a.chunk / kGroup) + k / kGroup] = s;
+        } else {
+          s = act_scale<INT8>(__uint_as_float(lds.top[t]));
+        }
+        *reinterpret_cast<v2u*>(codes + t * stride + k) =
+            encode_values<INT8>(held[q].f, s, act_recip(s));
       }
-      *reinterpret_cast<v2u*>(codes + t * stride + k) = encode_values<INT8>(v.f, s, act_recip(s));
     }
     __syncthreads();
     p.run(acc);
@@ -582,110 +605,147 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLayerArgs a) {
   }
 }
 
-// Up to 16 entries: 16 columns of y for all of them, a wave an entry, so that
-// their sum needs no hand-off between workgroups (which is what a call of so
-// few bytes waits for: 1 token, 8 experts of 2048 x 768 8.0 us by the kernel
-// above).  The same values in the same order.
-constexpr int kFewEntries = 16;
+// Few entries: 16 columns of y for all of them, one or several waves an entry
+// (`parts`, a power of two, of I), so that their sum needs no hand-off between
+// workgroups, which is what a call of so few bytes waits for (1 token, 8 experts
+// of 2048 x 768: 8.0 us by the kernel above).
+constexpr int kFewWaves = 16;
 
 template <int FMT, bool PACKED>
-__global__ __launch_bounds__(64 * kFewEntries) void moe_down_few_kernel(MoeLayerArgs a) {
+__global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeLayerArgs a) {
   typedef typename Traits<FMT>::Frag Frag;
   typedef typename Traits<FMT>::Acc Acc;
   constexpr int KSTEP = Traits<FMT>::KSTEP;
   constexpr bool BLOCK = FMT == BLOCK_FP8, INT8 = FMT == W8A8_INT8;
-  __shared__ float outputs[kFewEntries][16];
-  __shared__ float weights[kFewEntries];  // of the choices that count
+  __shared__ decltype(Acc{}[0] + 0) sums[kFewWaves][16];  // by wave: the 16 columns
+  __shared__ float outputs[kFewWaves][16];  // by entry
+  __shared__ unsigned tops[kFewWaves];      // (one scale a token) the bits of the largest |h|
+  __shared__ float scales[kFewWaves][16];   // by entry: of the 16 columns
+  __shared__ float weights[kFewWaves];      // by entry
+  __shared__ bool counts[kFewWaves];        // by entry: it is not left out
   const int lane = threadIdx.x & 63;
-  const int entry = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int entry = wave >> __builtin_ctz(a.parts), part = wave & (a.parts - 1);
   const int g = lane >> 4, n = blockIdx.x * 16;
   const int e = __builtin_amdgcn_readfirstlane(a.experts[entry]);
   const bool on = (unsigned)e < (unsigned)a.E;
-  if (on) {
-    const int ksteps = (a.I + KSTEP - 1) / KSTEP, kfull = a.I / KSTEP, G = a.I / kGroup;
-    const float* s2 = a.s2 + e * a.s2_stride;
-    const uint8_t* wp = weight_rows<FMT, PACKED>(a.w2 + e * a.w2_stride, a.ldw2, ksteps, n);
-    const float* swp = s2 + (BLOCK ? (long long)(n / kGroup) * G : n + 4 * g);
-    const float weight = a.weights[entry];
-    const int stride = a.chunk + kPad;
-    uint8_t* x = codes + entry * stride;
-    float* xs = reinterpret_cast<float*>(codes + (blockDim.x >> 6) * stride) +
-                entry * (a.chunk / kGroup);  // Block_FP8's
-    Acc acc[1][1] = {{Acc{0, 0, 0, 0}}};
-    float sw[4], sx = 0.0f;
-    for (int c0 = 0; c0 < a.I; c0 += a.chunk) {
-      const int cols = min(a.chunk, a.I - c0), per = (cols + kGroup - 1) / kGroup * (kGroup / 8);
-      const int kb = c0 / KSTEP, kend = (c0 + cols + KSTEP - 1) / KSTEP;
-      constexpr int kHeld = 2;  // pieces of eight hidden values a lane
-      Hidden first[kHeld] = {};
+  const float weight = a.weights[entry];
+  const int ksteps = (a.I + KSTEP - 1) / KSTEP, kfull = a.I / KSTEP, G = a.I / kGroup;
+  const float* s2 = a.s2 + (on ? e * a.s2_stride : 0);
+  const uint8_t* wp = weight_rows<FMT, PACKED>(a.w2 + (on ? e * a.w2_stride : 0), a.ldw2, ksteps, n);
+  const float* swp = s2 + (BLOCK ? (long long)(n / kGroup) * G : n + 4 * g);
+  // the wave's columns of I, in whole 128s
+  const int groups = (a.I + kGroup - 1) / kGroup;
+  const int lo = groups * part / a.parts * kGroup;
+  const int hi = on ? min(groups * (part + 1) / a.parts * kGroup, a.I) : lo;
+  const int stride = a.chunk + kPad;
+  uint8_t* x = codes + wave * stride;
+  float* xs = reinterpret_cast<float*>(codes + (blockDim.x >> 6) * stride) +
+              wave * (a.chunk / kGroup);  // Block_FP8's
+  constexpr int kLaneHeld = 2;  // pieces of eight hidden values a lane
+  auto load_held = [&](Hidden (&h)[kLaneHeld], int c0) {
+    const int cols = min(a.chunk, hi - c0), per = (cols + kGroup - 1) / kGroup * (kGroup / 8);
 #pragma unroll
-      for (int q = 0; q < kHeld; ++q)
-        if (lane + 64 * q < per) first[q] = load_hidden(a, &entry, lane + 64 * q, per, c0, cols);
-      auto p = products<FMT, 1, 1, steps<FMT>(kDownPieces), false>(
-          kb, min(kend, kfull), [&](int, int k) -> Frag { return weight_step<FMT, PACKED>(wp, k); },
-          [&](int, int k) -> Frag { return load_frag<FMT>(x + 16 * g, k - kb); },
-          [&](int, int k) { return uniform_load(swp + k); },
-          [&](int, int k) { return xs[k - kb]; });
-      p.begin();
-      if constexpr (!BLOCK) {
-        if (c0 == 0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sw[i] = swp[i];
-          unsigned top = max(largest(first[0]), largest(first[1]));
-          const float* h = a.h + (long long)entry * a.I;
-          for (int k = 8 * (lane + 64 * kHeld); k < a.I; k += 512) {
-            Hidden v;
-            __builtin_memcpy(v.f, h + k, 32);
-            top = max(top, largest(v));
-          }
-          sx = act_scale<INT8>(__uint_as_float(wave_umax(top)));
-        }
-      }
-      auto encode = [&](Hidden v, int i) {
-        const int k = 8 * i;
-        float s = sx;
-        if constexpr (BLOCK) {  // 16 lanes hold a group
-          s = act_scale<false>(__uint_as_float(seg16_umax(largest(v))));
-          if (k % kGroup == 0) xs[k / kGroup] = s;
-        }
-        *reinterpret_cast<v2u*>(x + k) = encode_values<INT8>(v.f, s, act_recip(s));
-      };
-      // (the wave's own LDS, which it accesses in order: the fences keep the
-      // compiler from moving reads of the codes above the writes, and the next
-      // chunk's writes above the reads)
-      __atomic_signal_fence(__ATOMIC_SEQ_CST);
-#pragma unroll
-      for (int q = 0; q < kHeld; ++q)
-        if (lane + 64 * q < per) encode(first[q], lane + 64 * q);
-      for (int i = lane + 64 * kHeld; i < per; i += 64)
-        encode(load_hidden(a, &entry, i, per, c0, cols), i);
-      __atomic_signal_fence(__ATOMIC_SEQ_CST);
-      p.run(acc);
-      if constexpr (!BLOCK) {
-        if (kend > kfull)
-          p.multiply(acc[0][0], weight_tail<FMT, PACKED>(wp, kfull, a.I),
-                     load_frag<FMT>(x + 16 * g, kfull - kb), 0.0f);
-      }
+    for (int q = 0; q < kLaneHeld; ++q) {
+      h[q] = Hidden{};
+      if (lane + 64 * q < per) h[q] = load_hidden(a, &entry, lane + 64 * q, per, c0, cols);
     }
-    // (every column of the product is the entry's)
-    if ((lane & 15) == 0) {
+  };
+  int kb = lo / KSTEP;  // the chunk's first step
+  auto last_step = [&](int c0) {
+    return min((min(c0 + a.chunk, hi) + KSTEP - 1) / KSTEP, kfull);
+  };
+  Hidden held[kLaneHeld];
+  load_held(held, lo);
+  auto p = products<FMT, 1, 1, steps<FMT>(2), false>(
+      kb, last_step(lo), [&](int, int k) -> Frag { return weight_step<FMT, PACKED>(wp, k); },
+      [&](int, int k) -> Frag { return load_frag<FMT>(x + 16 * g, k - kb); },
+      [&](int, int k) { return uniform_load(swp + k); }, [&](int, int k) { return xs[k - kb]; });
+  p.begin();
+  float sx = 0.0f, sw[4];
+  if constexpr (!BLOCK) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float o = (float)acc[0][0][i];
-        if constexpr (!BLOCK) o *= sx * sw[i];
-        outputs[entry][4 * g + i] = o;
-      }
+    for (int i = 0; i < 4; ++i) sw[i] = swp[i];  // (used at the end)
+    unsigned top = 0;
+#pragma unroll
+    for (int q = 0; q < kLaneHeld; ++q) top = max(top, largest(held[q]));
+    for (int k = lo + 8 * (lane + 64 * kLaneHeld); k < hi; k += 512) {
+      Hidden v;
+      __builtin_memcpy(v.f, a.h + (long long)entry * a.I + k, 32);
+      top = max(top, largest(v));
     }
-    if (lane == 0) weights[entry] = weight;
+    top = wave_umax(top);
+    if (a.parts > 1) {
+      if (lane == 0) tops[wave] = top;
+      __syncthreads();
+      for (int w = 0; w < a.parts; ++w) top = max(top, tops[entry * a.parts + w]);
+    }
+    sx = act_scale<INT8>(__uint_as_float(top));
   }
-  if (lane == 0 && !on) weights[entry] = 0.0f;
-  if (lane < 16 && !on) outputs[entry][lane] = 0.0f;
+  Acc acc[1][1] = {{Acc{0, 0, 0, 0}}};
+  for (int c0 = lo; c0 < hi; c0 += a.chunk) {
+    const int cols = min(a.chunk, hi - c0), per = (cols + kGroup - 1) / kGroup * (kGroup / 8);
+    if (c0 > lo) {
+      load_held(held, c0);
+      p.la = kb = c0 / KSTEP;
+      p.lfull = last_step(c0);
+      p.begin();
+    }
+    auto encode = [&](Hidden v, int i) {
+      const int k = 8 * i;
+      float s = sx;
+      if constexpr (BLOCK) {  // 16 lanes hold a group
+        s = act_scale<false>(__uint_as_float(seg16_umax(largest(v))));
+        if (k % kGroup == 0) xs[k / kGroup] = s;
+      }
+      *reinterpret_cast<v2u*>(x + k) = encode_values<INT8>(v.f, s, act_recip(s));
+    };
+    // (the wave's own LDS, which it accesses in order: the fences keep the
+    // compiler from moving reads of the codes above the writes, and the next
+    // chunk's writes above the reads)
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+#pragma unroll
+    for (int q = 0; q < kLaneHeld; ++q)
+      if (lane + 64 * q < per) encode(held[q], lane + 64 * q);
+    for (int i = lane + 64 * kLaneHeld; i < per; i += 64)
+      encode(load_hidden(a, &entry, i, per, c0, cols), i);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    p.run(acc);
+    if constexpr (!BLOCK) {
+      if (c0 + cols > kfull * KSTEP)
+        p.multiply(acc[0][0], weight_tail<FMT, PACKED>(wp, kfull, a.I),
+                   load_frag<FMT>(x + 16 * g, kfull - kb), 0.0f);
+    }
+  }
+  // (every column of the product is the entry's)
+  const int entries = a.T * a.topk;
+  if ((lane & 15) == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (!BLOCK) scales[entry][4 * g + i] = sx * sw[i];
+      sums[wave][4 * g + i] = acc[0][0][i];
+    }
+  }
+  if (lane == 0) {
+    weights[entry] = weight;
+    counts[entry] = on;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < 16 * entries) {
+    const int i = threadIdx.x / 16, c = threadIdx.x % 16;
+    auto v = sums[i * a.parts][c];
+    for (int w = 1; w < a.parts; ++w) v += sums[i * a.parts + w][c];
+    float o = (float)v;
+    if constexpr (!BLOCK) o *= scales[i][c];
+    outputs[i][c] = o;
+  }
   __syncthreads();
   if ((int)threadIdx.x < 16 * a.T) {
     const int t = threadIdx.x / 16, c = threadIdx.x % 16;
     float sum = 0.0f;
+#pragma unroll 4
     for (int j = t * a.topk; j < (t + 1) * a.topk; ++j)
-      sum = __builtin_fmaf(weights[j], outputs[j][c], sum);
+      sum = counts[j] ? __builtin_fmaf(weights[j], outputs[j][c], sum) : sum;
     a.y[t * a.ldy + n + c] = (uint16_t)bf16_bits(sum);
   }
 }
@@ -697,14 +757,15 @@ hipError_t launch_up(const MoeLayerArgs& a, hipStream_t s) {
 }
 template <int FMT, bool PACKED, int MB>
 hipError_t launch_down(const MoeLayerArgs& a, hipStream_t s) {
-  const int rows = a.T * a.topk <= kFewEntries ? a.T * a.topk : a.T;
-  const size_t lds = (size_t)rows * (a.chunk + kPad + (FMT == BLOCK_FP8 ? a.chunk / kGroup * 4 : 0));
-  if (MB == 1 && a.T * a.topk <= kFewEntries)
+  const size_t row = a.chunk + kPad + (FMT == BLOCK_FP8 ? a.chunk / kGroup * 4 : 0);
+  if (MB == 1 && a.parts) {
+    const int waves = a.T * a.topk * a.parts;
     return launch_kernel(moe_down_few_kernel<FMT, PACKED>, dim3((unsigned)(a.D / 16)),
-                         dim3((unsigned)(64 * a.T * a.topk)), lds, s, a);
+                         dim3((unsigned)(64 * waves)), waves * row, s, a);
+  }
+  const int tiles = (a.D + kColumns - 1) / kColumns;
   return launch_kernel(moe_down_kernel<FMT, PACKED, MB>,
-                       dim3((unsigned)((a.D + kColumns - 1) / kColumns), (unsigned)a.slots),
-                       dim3(kThreads), lds, s, a);
+                       dim3((unsigned)tiles, (unsigned)a.slots), dim3(kThreads), a.T * row, s, a);
 }
 template <int FMT, int MB>
 hipError_t launch_layer(bool packed1, bool packed2, const MoeLayerArgs& a, hipStream_t s) {

@@ -107,11 +107,23 @@ w8_status check_experts(int fmt, int E, int N, int K, const void* w, int64_t ldw
   return W8_OK;
 }
 
+// Up to 16 entries whose experts are hardly ever the same (one token's never
+// are; otherwise each reads its expert's weights) take the second kernel for few
+// entries, with as many waves an entry as 16 leave, of 1024 columns of I at
+// least (2 experts of 4096 x 4096: one wave 31.6 us, two 25.8, four 25.1; 8 of
+// 2048 x 768: 14.6 and 16.4).  0: the other kernel.
+int layer_parts(int E, int T, int topk, int I) {
+  const int n = T * topk;
+  if (n > 16 || (T > 1 && 4 * n > E)) return 0;
+  int parts = 1;
+  while (2 * parts * n <= 16 && I >= 2048 * parts) parts *= 2;
+  return parts;
+}
+
 // Columns of I whose codes a workgroup of the layer's second kernel holds in
-// LDS, for T tokens or up to 16 entries, in 64 KiB less what the kernel needs
-// itself: whole 128s.
-int layer_chunk(int T, int topk, int I) {
-  const int rows = T * topk <= 16 ? T * topk : T;
+// LDS for each of `rows` rows, in 64 KiB less what the kernel needs itself:
+// whole 128s.
+int layer_chunk(int rows, int I) {
   const int per_row = 56 * 1024 / rows - 16;  // (codes, 16 bytes of padding, Block_FP8's scales)
   const int most = per_row * 32 / 33 / W8_GROUP * W8_GROUP;
   return std::min(most, (I + W8_GROUP - 1) / W8_GROUP * W8_GROUP);
@@ -265,7 +277,9 @@ w8_status w8_moe_layer(w8_fmt fmt_in, int E, int T, int topk, int D, int I, cons
   a.I = I;
   a.few = T * topk <= 64 && T * topk <= E;
   a.slots = std::min(E, T * topk);
-  a.chunk = layer_chunk(T, topk, I);
+  a.parts = layer_parts(E, T, topk, I);
+  a.chunk = a.parts ? layer_chunk(T * topk * a.parts, (I + a.parts - 1) / a.parts + W8_GROUP)
+                    : layer_chunk(T, I);
   const hipError_t e =
       launch_moe_layer(fmt, ldw1 == 0, ldw2 == 0, a, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("moe_layer launch", e));

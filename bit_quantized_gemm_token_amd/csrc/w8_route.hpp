@@ -72,7 +72,8 @@ struct MoeLayerArgs {
   int E, T, topk, D, I;
   int slots;            // of experts that a launch holds: each has tokens or ends at once
   int few;              // a slot is an entry (at most 64), else one of the experts with tokens
-  int chunk;            // of I that a workgroup of the second kernel keeps as codes
+  int parts;            // > 0: few entries, so many waves each for the second product
+  int chunk;            // of I that a workgroup of the second kernel (parts: a wave) keeps as codes
 };
 // Two launches.  packed1, packed2: the layouts of w1 and w2.
 hipError_t launch_moe_layer(int fmt, bool packed1, bool packed2, const MoeLayerArgs& a,
