@@ -242,6 +242,6 @@ def load():
     lib.w8_moe_layer_workspace_size.restype = st
     lib.w8_moe_layer.argtypes = [c_int, c_int, c_int, c_int, c_int, c_int, vp, i64, f32p, vp, f32p,
                                  vp, i64, i64, f32p, i64, vp, i64, i64, f32p, i64, vp, i64, vp,
-                                 ctypes.c_size_t, vp]
+                                 i64, vp, ctypes.c_size_t, vp]
     lib.w8_moe_layer.restype = st
     return lib

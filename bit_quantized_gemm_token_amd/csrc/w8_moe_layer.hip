@@ -3,8 +3,8 @@
 //   up    a = x W1_e^T for the tokens of expert e, gate and up halves;
 //         h = silu(a_gate) a_up in fp32
 //   down  hq = codes of h in the format; p = hq W2_e^T;
-//         y[t] = sum_j weights[t, j] p[t, j], by the last workgroup of a column
-//         tile to arrive
+//         y[t] = base[t] + sum_j weights[t, j] p[t, j], by the last workgroup of
+//         a column tile to arrive
 //
 // The weights' bytes are nearly all that a launch moves, so every workgroup
 // streams its own piece of one expert's weights into MFMA registers, as the
@@ -560,7 +560,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLayerArgs a) {
   __shared__ DownLds lds;
   const Expert x = find_expert(a, blockIdx.y, lds.c);
   const int n0 = blockIdx.x * kColumns;
-  if (x.e < 0) {  // (no token has an expert: zeros)
+  if (x.e < 0) {  // (no token has an expert: the base alone)
     if (blockIdx.y) return;
     if (a.few) load_choices(a, lds.c);
     if (count_active(lds.c)) return;
@@ -580,6 +580,12 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLayerArgs a) {
     const int t = i / (kColumns / 4), n = n0 + 4 * (i % (kColumns / 4));
     if (n >= a.D) continue;
     v4f sum = {0, 0, 0, 0};
+    if (a.base) {
+      uint16_t b[4];
+      __builtin_memcpy(b, a.base + t * a.ldb + n, 8);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sum[u] = bf16_lo(b[u]);
+    }
     for (int j0 = 0; j0 < a.topk; j0 += kBatch) {
       v4i v[kBatch];
       float w[kBatch];
@@ -742,7 +748,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeLayerAr
   __syncthreads();
   if ((int)threadIdx.x < 16 * a.T) {
     const int t = threadIdx.x / 16, c = threadIdx.x % 16;
-    float sum = 0.0f;
+    float sum = a.base ? bf16_lo(a.base[t * a.ldb + n + c]) : 0.0f;
 #pragma unroll 4
     for (int j = t * a.topk; j < (t + 1) * a.topk; ++j)
       sum = counts[j] ? __builtin_fmaf(weights[j], outputs[j][c], sum) : sum;

@@ -227,8 +227,8 @@ w8_status w8_moe_layer(w8_fmt fmt_in, int E, int T, int topk, int D, int I, cons
                        int64_t ldq, const float* sx, const int32_t* experts, const float* weights,
                        const void* w1, int64_t ldw1, int64_t w1_stride, const float* s1,
                        int64_t s1_stride, const void* w2, int64_t ldw2, int64_t w2_stride,
-                       const float* s2, int64_t s2_stride, void* y, int64_t ldy, void* ws,
-                       size_t ws_bytes, w8_stream stream) {
+                       const float* s2, int64_t s2_stride, const void* base, int64_t ldb, void* y,
+                       int64_t ldy, void* ws, size_t ws_bytes, w8_stream stream) {
   const int fmt = raw_enum(fmt_in);
   w8_status st = check_layer(fmt, E, T, topk, D, I);
   if (st) return st;
@@ -236,8 +236,10 @@ w8_status w8_moe_layer(w8_fmt fmt_in, int E, int T, int topk, int D, int I, cons
   if (!xq || !sx || !experts || !weights || !y) return fail(W8_E_INVALID, "null device pointer");
   if (!aligned(xq, 16) || ldq < D || ldq % 16)
     return fail(W8_E_INVALID, "xq must be 16-byte aligned with ldq >= D and ldq % 16 == 0");
-  if (ldy < D) return fail(W8_E_INVALID, "output leading dimension must be >= D");
-  if (!aligned(sx, 4) || !aligned(experts, 4) || !aligned(weights, 4) || !aligned(y, 2))
+  if (ldy < D || (base && ldb < D))
+    return fail(W8_E_INVALID, "the output's and the base's leading dimensions must be >= D");
+  if (!aligned(sx, 4) || !aligned(experts, 4) || !aligned(weights, 4) || !aligned(base, 2) ||
+      !aligned(y, 2))
     return fail(W8_E_INVALID, "every pointer must be aligned to its element type");
   st = check_experts(fmt, E, 2 * I, D, w1, ldw1, w1_stride, s1, s1_stride);
   if (st) return st;
@@ -258,6 +260,8 @@ w8_status w8_moe_layer(w8_fmt fmt_in, int E, int T, int topk, int D, int I, cons
   a.s1 = s1;
   a.w2 = static_cast<const uint8_t*>(w2);
   a.s2 = s2;
+  a.base = static_cast<const uint16_t*>(base);
+  a.ldb = ldb;
   a.y = static_cast<uint16_t*>(y);
   a.h = reinterpret_cast<float*>(p + w.h);
   a.part = reinterpret_cast<float*>(p + w.part);

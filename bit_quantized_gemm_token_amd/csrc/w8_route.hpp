@@ -62,11 +62,12 @@ struct MoeLayerArgs {
   const float* s1;
   const uint8_t* w2;    // expert 0's [D, I]
   const float* s2;
+  const uint16_t* base; // bf16 [T, D], or null
   uint16_t* y;          // bf16 [T, D]
   float* h;             // [T * topk, I] gated products (workspace)
   float* part;          // [T * topk, D] the experts' outputs
   unsigned* counters;   // arrival counters
-  long long ldq, ldw1, ldw2, ldy;       // bytes; y: elements
+  long long ldq, ldw1, ldw2, ldb, ldy;  // bytes; base, y: elements
   long long w1_stride, w2_stride;       // bytes between experts
   long long s1_stride, s2_stride;       // floats
   int E, T, topk, D, I;

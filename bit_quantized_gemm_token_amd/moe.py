@@ -145,12 +145,13 @@ def _layer_weights(f, w, s, name):
     return E, N, K, t.data_ptr(), ldw, stride, _flat(s, "the scales of " + name, _F32, E * per), per, t
 
 
-def moe_layer(fmt, xq, sx, experts, weights, w1, s1, w2, s2, y=None, workspace=None, stream=None):
+def moe_layer(fmt, xq, sx, experts, weights, w1, s1, w2, s2, base=None, y=None, workspace=None,
+              stream=None):
     """The experts of a few tokens (T <= 32) as a whole, bf16 [T, D]:
 
         a = x W1_e^T             [2 I]: gate, then up
         v = silu(a[:I]) * a[I:]  quantized as the format's activations
-        y[t] = sum_j weights[t, j] (v W2_e^T),   e = experts[t, j]
+        y[t] = base[t] + sum_j weights[t, j] (v W2_e^T),   e = experts[t, j]
 
     fmt: any of the three.  xq, sx: codes [T, D] and scales as the GEMMs take
     them (quantize_act, token_quantize, residual_norm); experts int32, weights
@@ -158,7 +159,8 @@ def moe_layer(fmt, xq, sx, experts, weights, w1, s1, w2, s2, y=None, workspace=N
     chosen twice counts with both weights.  w1: [E, 2 I, D], w2: [E, D, I]
     codes or PackedExperts; s1, s2: their scales, per output channel ([E, 2 I],
     [E, D]) or Block_FP8's per 128 x 128 block.  D and I are multiples of 16
-    (Block_FP8: of 128) up to 65536, E at most 1024, topk at most 32.
+    (Block_FP8: of 128) up to 65536, E at most 1024, topk at most 32.  base:
+    bf16 [T, D] (a shared expert's output, a residual) or None; y may be base.
 
     Two launches, no lists, no host sync; the hidden values stay fp32 until
     they are quantized and the sum is fp32 in the order of the choices, so
@@ -179,7 +181,11 @@ def moe_layer(fmt, xq, sx, experts, weights, w1, s1, w2, s2, y=None, workspace=N
     if E2 != E or N1 != 2 * I or K1 != D or N2 != D:
         raise ValueError(f"w1 [{E}, {N1}, {K1}] and w2 [{E2}, {N2}, {I}] must be [E, 2 I, {D}] and "
                          f"[E, {D}, I]")
-    index = _one_device(xq, sx, experts, weights, w1t, s1, w2t, s2, y)
+    bp, ldb = None, 0
+    if base is not None:
+        bp, ldb = _rows(base, "base", _BF16)
+        _shape(base, T, D, "base")
+    index = _one_device(xq, sx, experts, weights, w1t, s1, w2t, s2, base, y)
     dev = xq.device
     if y is None:
         y, yp, ldy = _new(T, D, _BF16, dev, stream)
@@ -192,7 +198,7 @@ def moe_layer(fmt, xq, sx, experts, weights, w1, s1, w2, s2, y=None, workspace=N
     buf = workspace.buf
     for retry in (True, False):
         args = (f, E, T, topk, D, I, xp, ldq, sxp, ep, wp, w1p, ldw1, w1s, s1p, s1s, w2p, ldw2,
-                w2s, s2p, s2s, yp, ldy, None if buf is None else buf.data_ptr(),
+                w2s, s2p, s2s, bp, ldb, yp, ldy, None if buf is None else buf.data_ptr(),
                 0 if buf is None else buf.numel(), s)
         status = _layer(*args) if index == _current_device() else _elsewhere(index, _layer, args)
         if status != _E_WORKSPACE or not retry:

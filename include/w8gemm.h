@@ -795,7 +795,8 @@ w8_status w8_moe_combine(int T, int topk, int D, const void *y, int64_t ldy, int
  *   a    = dequant(xq[t]) . dequant(W1_e)^T        [2 I]: gate, then up
  *   v    = silu(a[:I]) * a[I:], fp32, quantized as w8_quantize_act does (one
  *          scale for the row, Block_FP8 one per 128 columns)
- *   y[t] = sum_j weights[t, j] dequant(v) . dequant(W2_e)^T, e = experts[t, j]
+ *   y[t] = base[t] + sum_j weights[t, j] dequant(v) . dequant(W2_e)^T, with
+ *          e = experts[t, j], in the order of j, rounded once
  *   xq, sx   T rows of D codes and their scales
  *   experts  int32 [T, topk] (device); those outside [0, E) are left out, one
  *            chosen twice by a token counts with both weights
@@ -804,7 +805,9 @@ w8_status w8_moe_combine(int T, int topk, int D, const void *y, int64_t ldy, int
  *            with row stride ldw1, or ldw1 = 0: the packed layout 1), scales at
  *            s1 + e * s1_stride floats: [2 I], Block_FP8 [2 I / 128, D / 128]
  *   w2, s2   likewise [D, I]
- *   y        bf16 [T, D], row stride ldy elements
+ *   base     bf16 [T, D], row stride ldb elements (a shared expert's output, a
+ *            residual), or NULL: 0
+ *   y        bf16 [T, D], row stride ldy elements; may be base (same stride)
  *   ws       w8_moe_layer_workspace_size bytes, with w8_gemm_w8a8's rules (one
  *            workspace may serve every entry point)
  * 1 <= E <= 1024, 1 <= topk <= 32; D and I multiples of 16 (Block_FP8: of 128)
@@ -813,8 +816,9 @@ w8_status w8_moe_layer(w8_fmt fmt, int E, int T, int topk, int D, int I, const v
                        int64_t ldq, const float *sx, const int32_t *experts,
                        const float *weights, const void *w1, int64_t ldw1, int64_t w1_stride,
                        const float *s1, int64_t s1_stride, const void *w2, int64_t ldw2,
-                       int64_t w2_stride, const float *s2, int64_t s2_stride, void *y,
-                       int64_t ldy, void *ws, size_t ws_bytes, w8_stream stream);
+                       int64_t w2_stride, const float *s2, int64_t s2_stride, const void *base,
+                       int64_t ldb, void *y, int64_t ldy, void *ws, size_t ws_bytes,
+                       w8_stream stream);
 w8_status w8_moe_layer_workspace_size(int T, int topk, int D, int I, size_t *bytes);
 
 /* -------------------------------------------------------- measurement -- */

@@ -177,6 +177,32 @@ def test_choices_left_out_and_repeated(w8, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T", [1, 7, 20])
+def test_base(w8, fmt, T):
+    """Added before the one rounding, in place too; a token without an expert
+    keeps it."""
+    c = Layer(fmt, T, 5, 2, 256, 128)
+    c.experts[T // 2] = -1
+    a = c.args(w8)
+    y, room = c.expected()
+    g = np.random.default_rng(T)
+    buf = torch.from_numpy(g.standard_normal((T, 259)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    base = buf[:, 1:257]
+    want = y + base.double().cpu().numpy()
+    got = w8.moe_layer(*a, base=base)
+    # (the bound holds a rounding of y; here it is the sum that is rounded)
+    room = room + 1.01 * 2.0 ** -8 * np.abs(want)
+    assert (np.abs(got.double().cpu().numpy() - want) <= room).all()
+    assert torch.equal(got[T // 2], base[T // 2])
+    before = buf.clone()
+    assert w8.moe_layer(*a, base=base, y=base) is base
+    assert torch.equal(base, got) and torch.equal(buf[:, 0], before[:, 0])
+    assert torch.equal(buf[:, 257:], before[:, 257:])
+    c = Layer(fmt, T, 5, 2, 256, 128, experts=np.full((T, 2), -1))
+    assert torch.equal(w8.moe_layer(*c.args(w8), base=before[:, 1:257]), before[:, 1:257])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_experts_without_tokens_are_not_read(w8, fmt):
     """Their codes and scales may hold anything."""
     c = Layer(fmt, 4, 8, 2, 256, 128, experts=[[1, 6], [6, 1], [1, -1], [6, 6]])

@@ -44,7 +44,8 @@ COMBINE = dict(T=10, topk=8, D=100, y=P, ldy=100, n_rows=80, weights=P, slots=P,
                out=P, ldo=100, stream=None)
 LAYER = dict(fmt=BLOCK, E=4, T=8, topk=2, D=256, I=128, xq=P, ldq=256, sx=P, experts=P, weights=P,
              w1=P, ldw1=256, w1_stride=256 * 256, s1=P, s1_stride=4, w2=P, ldw2=128,
-             w2_stride=256 * 128, s2=P, s2_stride=2, y=P, ldy=256, ws=P, ws_bytes=BIG, stream=None)
+             w2_stride=256 * 128, s2=P, s2_stride=2, base=P, ldb=256, y=P, ldy=256, ws=P, ws_bytes=BIG,
+             stream=None)
 
 
 @pytest.mark.parametrize("bad", [
@@ -136,6 +137,7 @@ def test_combine_refuses(lib, bad):
     dict(fmt=INT8, D=264, ldq=272), dict(fmt=FP8, I=136), dict(xq=None), dict(sx=None),
     dict(experts=None), dict(weights=None), dict(w1=None), dict(s1=None), dict(w2=None),
     dict(s2=None), dict(y=None), dict(xq=P + 8), dict(ldq=240), dict(ldq=264), dict(ldy=255),
+    dict(ldb=255), dict(base=P + 1),
     dict(sx=P + 2), dict(experts=P + 2), dict(weights=P + 1), dict(y=P + 1), dict(w1=P + 8),
     dict(w2=P + 8), dict(s1=P + 2), dict(s2=P + 2), dict(ldw1=240), dict(ldw1=264), dict(ldw1=-2),
     dict(ldw2=112), dict(ldw2=136), dict(w1_stride=256 * 256 - 16), dict(w1_stride=256 * 256 + 8),
@@ -216,6 +218,8 @@ def test_binding_refuses_shapes_types_and_devices(w8, fake):
         layer(w2=fake(E, I, D).transpose(1, 2))
     with pytest.raises(ValueError, match="y must be"):
         layer(y=fake(T, D + 1, dtype=BF16))
+    with pytest.raises(ValueError, match="base must be"):
+        layer(base=fake(T + 1, D, dtype=BF16))
     with pytest.raises(ValueError, match="must be on"):
         layer(s2=fake(E, D, dtype=F32, device="cuda:1"))
     with pytest.raises(ValueError, match="must be on"):
