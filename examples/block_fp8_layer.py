@@ -5,12 +5,15 @@ residual stream back to it, on the library's operators:
                    and the norm's codes and scales, in one pass
   block_gemm       the shared expert's projections
   block_quantize   silu(gate) * up straight to codes and scales
+  moe_route        each token's experts and weights, and the experts' lists
   grouped_gemm     the routed experts' projections over ragged lists of rows
+  moe_combine      each token's weighted sum of its experts' outputs
+  moe_layer        the last three steps as two launches, for up to 32 tokens
 
     python examples/block_fp8_layer.py [--tokens 1,48,1024] [--hidden 2048] ...
 
 builds random weights, runs the block at each token count and prints the time
-per call of the whole block (routing in plain torch included).
+per call of the whole block (the router's product, in plain torch, included).
 """
 import argparse
 import os
@@ -41,6 +44,8 @@ class MoeBlock:
             return w8.quantize_weight(FMT, randn(n, k) / k ** 0.5)
 
         self.hidden, self.width, self.experts, self.topk = hidden, width, experts, topk
+        # (moe_layer takes Block_FP8 widths of whole groups)
+        self.whole = hidden % w8.GROUP == 0 and width % w8.GROUP == 0
         self.post_norm = (1 + 0.1 * randn(hidden)).to(torch.bfloat16)
         self.norm = (1 + 0.1 * randn(hidden)).to(torch.bfloat16)
         self.router = randn(experts, hidden) / hidden ** 0.5
@@ -60,16 +65,9 @@ class MoeBlock:
         """Top-k routing: entries grouped by expert.  Returns the offsets [E + 1],
         the token row of each entry, each token's weights [T, topk] and where
         its entries went [T, topk]."""
-        weight, expert = torch.softmax(z.float() @ self.router.t(), dim=1).topk(self.topk, dim=1)
-        expert = expert.reshape(-1)
-        order = expert.argsort(stable=True)
-        counts = torch.zeros(self.experts, dtype=torch.int32, device=z.device)
-        counts.scatter_add_(0, expert, torch.ones_like(expert, dtype=torch.int32))
-        offsets = torch.zeros(self.experts + 1, dtype=torch.int32, device=z.device)
-        offsets[1:] = counts.cumsum(0)
-        place = torch.empty_like(order)
-        place[order] = torch.arange(len(order), device=z.device)
-        return offsets, (order // self.topk).to(torch.int32), weight, place.view(-1, self.topk)
+        _, weight, offsets, rows, place = w8.moe_route(z.float() @ self.router.t(), self.topk,
+                                                       renormalize=False)
+        return offsets, rows, weight, place
 
     def expert_mlp(self, xq, sx, offsets, rows):
         both = w8.grouped_gemm(xq, sx, offsets, *self.up, rows=rows)
@@ -88,10 +86,15 @@ class MoeBlock:
         residual, xq, sx, z = w8.residual_norm(branch, residual, self.norm,
                                                post_weight=self.post_norm, quantize=True,
                                                with_z=True)
+        shared = self.shared_mlp(xq, sx)
+        if self.whole and len(z) <= w8.MAX_M:
+            expert, weight = w8.moe_route(z.float() @ self.router.t(), self.topk,
+                                          renormalize=False, lists=False)
+            return w8.moe_layer(FMT, xq, sx, expert, weight, *self.up, *self.down,
+                                base=shared), residual
         offsets, rows, weight, place = self.route(z)
-        routed = self.expert_mlp(xq, sx, offsets, rows)[place]  # [T, topk, hidden]
-        out = self.shared_mlp(xq, sx).float() + (routed.float() * weight[:, :, None]).sum(1)
-        return out.to(torch.bfloat16), residual
+        routed = self.expert_mlp(xq, sx, offsets, rows)
+        return w8.moe_combine(routed, weight, place, base=shared), residual
 
 
 def main():
