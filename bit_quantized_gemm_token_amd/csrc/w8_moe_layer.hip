@@ -632,9 +632,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeLayerAr
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int entry = wave >> __builtin_ctz(a.parts), part = wave & (a.parts - 1);
-  const int g = lane >> 4, n = blockIdx.x * 16;
-  const int e = __builtin_amdgcn_readfirstlane(a.experts[entry]);
+  const int g = lane >> 4, n = blockIdx.x * 16, entries = a.T * a.topk;
+  const int id = lane < entries ? a.experts[lane] : -1;
+  const int e = __builtin_amdgcn_readlane(id, entry);
   const bool on = (unsigned)e < (unsigned)a.E;
+  // the hidden values of an expert that the token has chosen before are there
+  const int first = entry / a.topk * a.topk;
+  const int from = first + __builtin_ctzll(__ballot(lane < entries && id == e) >> first);
   const float weight = a.weights[entry];
   const int ksteps = (a.I + KSTEP - 1) / KSTEP, kfull = a.I / KSTEP, G = a.I / kGroup;
   const float* s2 = a.s2 + (on ? e * a.s2_stride : 0);
@@ -654,7 +658,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeLayerAr
 #pragma unroll
     for (int q = 0; q < kLaneHeld; ++q) {
       h[q] = Hidden{};
-      if (lane + 64 * q < per) h[q] = load_hidden(a, &entry, lane + 64 * q, per, c0, cols);
+      if (lane + 64 * q < per) h[q] = load_hidden(a, &from, lane + 64 * q, per, c0, cols);
     }
   };
   int kb = lo / KSTEP;  // the chunk's first step
@@ -677,7 +681,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeLayerAr
     for (int q = 0; q < kLaneHeld; ++q) top = max(top, largest(held[q]));
     for (int k = lo + 8 * (lane + 64 * kLaneHeld); k < hi; k += 512) {
       Hidden v;
-      __builtin_memcpy(v.f, a.h + (long long)entry * a.I + k, 32);
+      __builtin_memcpy(v.f, a.h + (long long)from * a.I + k, 32);
       top = max(top, largest(v));
     }
     top = wave_umax(top);
@@ -714,7 +718,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeLayerAr
     for (int q = 0; q < kLaneHeld; ++q)
       if (lane + 64 * q < per) encode(held[q], lane + 64 * q);
     for (int i = lane + 64 * kLaneHeld; i < per; i += 64)
-      encode(load_hidden(a, &entry, i, per, c0, cols), i);
+      encode(load_hidden(a, &from, i, per, c0, cols), i);
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     p.run(acc);
     if constexpr (!BLOCK) {
@@ -724,7 +728,6 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeLayerAr
     }
   }
   // (every column of the product is the entry's)
-  const int entries = a.T * a.topk;
   if ((lane & 15) == 0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -107,8 +107,8 @@ w8_status check_experts(int fmt, int E, int N, int K, const void* w, int64_t ldw
   return W8_OK;
 }
 
-// Up to 16 entries whose experts are hardly ever the same (one token's never
-// are; otherwise each reads its expert's weights) take the second kernel for few
+// Up to 16 entries whose experts are hardly ever the same (one token's, as a
+// rule; each entry reads its expert's weights) take the second kernel for few
 // entries, with as many waves an entry as 16 leave, of 1024 columns of I at
 // least (2 experts of 4096 x 4096: one wave 31.6 us, two 25.8, four 25.1; 8 of
 // 2048 x 768: 14.6 and 16.4).  0: the other kernel.

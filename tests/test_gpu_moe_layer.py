@@ -177,6 +177,22 @@ def test_choices_left_out_and_repeated(w8, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("E,I,experts", [
+    (4, 128, [[2, 2]]), (8, 128, [[3, 1, 3, -1, 1]]), (64, 256, [[7, 9, 7], [9, 7, 9]]),
+    (3, 4224, [[1, 0, 1]]), (50, 128, [[5, 5, 5, 5], [5, 6, 5, 6], [9, 9, 50, 9]]),
+    (64, 128, [[8, 8, 3, 3], [3, 8, 8, 3], [1, 2, 2, 1], [2, 2, 2, 2], [0, 0, 1, 0]])])
+def test_an_expert_twice_among_few(w8, fmt, E, I, experts):
+    """In a workspace of NaN, so that what no kernel has written shows."""
+    c = Layer(fmt, len(experts), E, len(experts[0]), 256, I, experts=experts)
+    size = w8.moe_layer_workspace_size(c.T, c.topk, c.D, c.I)
+    ws = w8.Workspace(DEV, size)
+    arrays = c.T * c.topk * 4 * (c.I + c.D)  # (behind the counters)
+    assert arrays % 256 == 0
+    ws.buf[size - arrays:size].fill_(255)
+    c.check(w8.moe_layer(*c.args(w8), workspace=ws))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T", [1, 7, 20])
 def test_base(w8, fmt, T):
     """Added before the one rounding, in place too; a token without an expert
