@@ -107,14 +107,17 @@ w8_status check_experts(int fmt, int E, int N, int K, const void* w, int64_t ldw
   return W8_OK;
 }
 
-// Up to 16 entries whose experts are hardly ever the same (one token's, as a
-// rule; each entry reads its expert's weights) take the second kernel for few
-// entries, with as many waves an entry as 16 leave, of 1024 columns of I at
-// least (2 experts of 4096 x 4096: one wave 31.6 us, two 25.8, four 25.1; 8 of
-// 2048 x 768: 14.6 and 16.4).  0: the other kernel.
-int layer_parts(int E, int T, int topk, int I) {
+// Up to 8 entries, and up to 16 of one token's, take the second kernel for few
+// entries, which reads an expert's weights for each entry that has chosen it
+// (2048 x 768, E experts: 1 token, 8 of 128 14.4 us, 16.1 by the other kernel; 16
+// of 64 20.4 and 22.0; 2 tokens, 4 of 8 13.8 and 15.0; 8 tokens, 2 of 8 16.5 and
+// 15.8; 4 tokens, 4 of 32, of 4096 x 2048 60.2 and 58.8), with as many waves an
+// entry as 16 leave, of 1024 columns of I at least (2 experts of 4096 x 4096: one
+// wave 30.1 us, two 24.5, four 23.6; 4096 x 1024 12.6, 12.7 and 12.9).  0: the
+// other kernel.
+int layer_parts(int T, int topk, int I) {
   const int n = T * topk;
-  if (n > 16 || (T > 1 && 4 * n > E)) return 0;
+  if (n > (T == 1 ? 16 : 8)) return 0;
   int parts = 1;
   while (2 * parts * n <= 16 && I >= 2048 * parts) parts *= 2;
   return parts;
@@ -281,7 +284,7 @@ w8_status w8_moe_layer(w8_fmt fmt_in, int E, int T, int topk, int D, int I, cons
   a.I = I;
   a.few = T * topk <= 64 && T * topk <= E;
   a.slots = std::min(E, T * topk);
-  a.parts = layer_parts(E, T, topk, I);
+  a.parts = layer_parts(T, topk, I);
   a.chunk = a.parts ? layer_chunk(T * topk * a.parts, (I + a.parts - 1) / a.parts + W8_GROUP)
                     : layer_chunk(T, I);
   const hipError_t e =

@@ -174,10 +174,13 @@ __global__ __launch_bounds__(kQThreads) void block_quantize_kernel(BlockQuantArg
 }
 
 // ---------------------------------------------------------- token quantize --
-// One scale a row: s = max |v| / Qmax, or (reciprocal) times 1 / Qmax.  A row by the waves of a workgroup
-// (ONE_WAVE: four rows, a wave each), NC chunks of eight values a lane, whose
-// gated products stay in registers between the maximum and the codes; what a
-// row has beyond those is read and computed again.
+// One scale a row: s = max |v| / Qmax, or (reciprocal) times 1 / Qmax.  A row by
+// the waves of a workgroup (ONE_WAVE: four rows, a wave each), NC chunks of eight
+// values a lane, whose gated products stay in registers between the maximum and
+// the codes; what a row has beyond those is read and computed again.  Every value
+// is read once, so HBM bounds it on many rows (8192 x 8192 gated: 335 MB in 59.6
+// us, 5.6 TB/s) and the launch with one chain of load, maximum and store on few
+// (48 x 7168: 2.9 us).
 template <bool INT8, bool GATED, bool ONE_WAVE, int NC>
 __global__ __launch_bounds__(ONE_WAVE ? 256 : 1024) void token_quantize_kernel(TokenQuantArgs a) {
   __shared__ unsigned red[16];
@@ -255,11 +258,22 @@ hipError_t launch_token(const TokenQuantArgs& a, hipStream_t s) {
                               : token_quantize_kernel<INT8, false, ONE_WAVE, NC>,
                        grid, block, 0, s, a);
 }
+// A wave holds 512 values of a row with one chunk a lane.  Rows that need no more
+// take one wave each (131072 x 128: 27.2 us, a workgroup each 31.0; 131072 x 512
+// 36.5 and 36.1).  Longer rows take one chunk a lane where the launch is short
+// (64 x 7168 gated: 3.8 us, two chunks 4.1), and two where several rows share a
+// compute unit and hide each other's wait for the maximum, of 2^21 values on
+// (8192 x 8192: 32.2 us, one chunk 39.9; 512 x 2048 2.7 and 2.5) or gated, where
+// registers are what runs out, on long rows alone (8192 x 8192 59.6 and 67.0; 32768
+// x 1536 49.1 and 44.9; 512 x 7168 6.9 and 6.5).  Four keep the longest rows in
+// registers (4096 x 24576 gated: 94 us, two chunks 109; 4096 x 18432 85 and 74).
 template <bool INT8>
 hipError_t launch_token(const TokenQuantArgs& a, hipStream_t s) {
   if (a.K <= 512) return launch_token<INT8, true, 1>(a, s);
-  if (a.K <= 8192) return launch_token<INT8, false, 1>(a, s);
-  return launch_token<INT8, false, 4>(a, s);
+  if (a.K > 20480) return launch_token<INT8, false, 4>(a, s);
+  const bool many = a.gate ? a.K > 4096 && a.M >= 1024 : (long long)a.M * a.K >= 1 << 21;
+  if (a.K > 8192 || many) return launch_token<INT8, false, 2>(a, s);
+  return launch_token<INT8, false, 1>(a, s);
 }
 
 // -------------------------------------------------------------------- norm --

@@ -126,7 +126,7 @@ SIZES = [  # T, E, topk, D, I (Block_FP8: rounded up to whole 128s)
     (32, 1000, 32, 32, 32), (4, 8, 2, 2048, 768), (32, 1, 1, 256, 2064), (2, 3, 2, 64, 8192),
     (8, 3, 2, 64, 7200), (16, 2, 1, 144, 3472), (5, 9, 9, 64, 16), (1, 40, 16, 64, 3600),
     (1, 8, 1, 272, 9008), (1, 2, 2, 1024, 4096), (2, 64, 8, 144, 1552), (4, 64, 3, 64, 528),
-    (1, 5, 5, 80, 50000)]
+    (1, 5, 5, 80, 50000), (4, 2, 2, 272, 2064), (8, 3, 1, 64, 128), (2, 4, 4, 144, 4208)]
 
 
 def sized(fmt, D, I):

@@ -29,7 +29,7 @@ def code_bytes(q):
 # ----------------------------------------------------------------- quantize --
 SIZES = [(1, 8), (1, 128), (3, 136), (5, 512), (6, 520), (33, 768), (5, 2048), (300, 1040),
          (1, 7168), (2, 8192), (3, 8200), (1, 16384), (2, 32768), (2, 40008), (1, 100000),
-         (4100, 264)]
+         (4100, 264), (1050, 2056), (1024, 4104), (1, 16392), (3, 20480)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
