@@ -1,6 +1,8 @@
-// Tiled Block_FP8 GEMM for any token count, dense and per expert.
+// Tiled GEMM for any token count: Block_FP8, dense and per expert, and the formats
+// of one scale per token and output channel, dense.
 //
 //   Y[m, n] = sum_g sx[m, g] sw[n / 128, g] sum_{k in group g} Xq[m, k] Wq[n, k]
+//   Y[m, n] = sx[m] sw[n] sum_k Xq[m, k] Wq[n, k]
 //
 // A workgroup computes BM tokens x BN weight rows.  K advances by one 128-wide
 // scale group per step.  Each step's codes (and the tokens' scales) go from
@@ -15,6 +17,12 @@
 // results), so about 1% of the bf16 outputs lie one step beside the rounded
 // exact one; the fp32 sum over the groups adds nothing to that.
 //
+// With one scale per token and channel the MFMAs add into the accumulators
+// themselves (W8A8_INT8: int32, exact), the scales are two products an element
+// before the one rounding to bf16, and a K-step still is 128 codes, the last one
+// with zeros past K.  The scales of a tile go to LDS once, behind the first
+// stages' loads.
+//
 // Measured, and what bounds it: 8192 x 5120 x 8192 284 to 300 us, 2.3 to 2.4
 // PFLOP/s, by power (0.555 M clocks at 1.7 .. 2.0 GHz) and the direct-to-LDS
 // loads beside the MFMAs; 4096 x 5120 x 2048 46 us, 1.87 PFLOP/s, by the start
@@ -23,6 +31,10 @@
 // the hand-off of split K and the start; 128 experts, top 8, of 1536 x 2048: 8
 // tokens 33.5 us, 4.9 TB/s, by the weights' bytes; 4096 tokens 158 to 182 us
 // (0.333 M clocks at 1.85 .. 2.1 GHz), 1.3 PFLOP/s, as the dense tiles.
+// One scale per token and channel: 8192 x 5120 x 8192 in int8 253 to 300 us, 2.3
+// to 2.7 POP/s, by power too (0.52 M clocks, the MFMAs busy in 63% of them); 48 x
+// 4608 x 7168 9.6 us by the weights, the hand-off and the start; 333 x 897 x 1040
+// 5.5 us by the start and one chain of nine steps.
 #include <atomic>
 #include <climits>
 #include <type_traits>

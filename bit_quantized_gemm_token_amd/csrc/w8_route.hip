@@ -8,6 +8,14 @@
 // within a pass of up to kRoutePass entries, over the passes of a workgroup and,
 // in a second launch, over the workgroups: whole numbers in a fixed order, so
 // the lists are the same every time.
+//
+// A row of logits is a few hundred bytes and stays in the registers of 16 or 64
+// lanes; each choice is a maximum over them, its place a minimum, so a token is a
+// chain of topk reductions and the chains of many tokens hide each other.
+// Measured: 8 tokens of 128 experts, top 8, 5.6 us in one launch, all latency;
+// 8192 tokens 8.0 us by the chains' instructions (the bytes, 2.6 MB, take 1 us)
+// and 6.8 us for the places, by the counts of 1024 workgroups and the latency of
+// reading, adding and writing one after the other.
 #include "w8_block.hpp"
 #include "w8_device.hpp"
 #include "w8_route.hpp"
