@@ -43,10 +43,25 @@ w8_status check_route(int T, int E, int topk) {
   return W8_OK;
 }
 
-// As many passes to a workgroup as keep the workgroups, whose counts the second
-// launch reads, to kRouteBlocks.
+// One workgroup takes up to kRoutePass entries, unless its tokens come to several
+// rounds of many choices, which cost more than the second launch (about 0.3 us a
+// choice; 128 tokens of 300 experts, top 2, 8 rounds 18.0 us, by two launches XX).
+// Otherwise a workgroup's pass is r rounds of its threads: they cost r topk choices,
+// and half as many workgroups, whose counts the second launch reads, half of 0.012
+// us each (239 tokens of 256 experts, top 6: passes of 21 tokens 20.8 us, of 16
+// 10.9; 261 of 8, top 1: 128 11.7, 16 7.3), with as many passes as keep the
+// workgroups to kRouteBlocks.
 void plan_route(RouteArgs* a) {
-  a->tokens = ((long long)a->T * a->topk <= kRoutePass ? kRoutePass : kRouteMany) / a->topk;
+  const int lanes = route_lanes(a->T, a->E);
+  const long long rounds = ceil_div((long long)a->T * lanes, kRouteWide);
+  if ((long long)a->T * a->topk <= kRoutePass && (rounds - 1) * a->topk <= 8) {
+    a->tokens = a->T;
+  } else {
+    const int round = kRouteThreads / lanes;
+    int r = 1;
+    while ((long long)(r + 1) * (r + 1) * round * a->topk * 25 <= a->T) ++r;
+    a->tokens = std::min(r * round, kRouteMany / a->topk);
+  }
   const long long passes = ceil_div(a->T, a->tokens);
   a->passes = (int)ceil_div(passes, kRouteBlocks);
   a->blocks = (int)ceil_div(passes, a->passes);

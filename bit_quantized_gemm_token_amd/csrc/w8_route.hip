@@ -24,30 +24,12 @@
 namespace w8 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kNone = 0x7FFFFFFF;
+constexpr int kThreads = kRouteThreads;
 
-__device__ __forceinline__ unsigned seg16_umin(unsigned v) {
-  v = min(v, dpp_move_u<0xB1>(v));
-  v = min(v, dpp_move_u<0x4E>(v));
-  v = min(v, dpp_move_u<0x141>(v));
-  v = min(v, dpp_move_u<0x140>(v));
-  return v;
-}
 // Over the L lanes (16 or 64) that share a token.
 template <int L>
 __device__ __forceinline__ unsigned lanes_umax(unsigned v) {
   return L == 16 ? seg16_umax(v) : wave_umax(v);
-}
-template <int L>
-__device__ __forceinline__ unsigned lanes_umin(unsigned v) {
-  v = seg16_umin(v);
-  if (L == 16) return v;
-  const unsigned r0 = __builtin_amdgcn_readlane((int)v, 0);
-  const unsigned r1 = __builtin_amdgcn_readlane((int)v, 16);
-  const unsigned r2 = __builtin_amdgcn_readlane((int)v, 32);
-  const unsigned r3 = __builtin_amdgcn_readlane((int)v, 48);
-  return min(min(r0, r1), min(r2, r3));
 }
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
@@ -65,14 +47,17 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 
 // Unsigned keys in the order of the logits; 0: never chosen (-inf, NaN).  The
-// two zeros are one.
+// two zeros are one.  A bf16 logit's key leaves 16 bits free, which hold the
+// expert, the lower the larger: such keys are all different.
 __device__ __forceinline__ unsigned key_of(float l, bool there) {
   const unsigned u = l == 0.0f ? 0u : __float_as_uint(l);
   const unsigned key = u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
   return (there & (l > -__builtin_inff())) ? key : 0u;
 }
+template <bool HALF>
 __device__ __forceinline__ float logit_of(unsigned key) {
-  return __uint_as_float(key >> 31 ? key & 0x7FFFFFFFu : ~key);
+  const unsigned u = key >> 31 ? key & 0x7FFFFFFFu : ~key;
+  return __uint_as_float(HALF ? u & 0xFFFF0000u : u);
 }
 
 // exp(l - top), 1 at the top itself (where that is +inf too)
@@ -135,70 +120,93 @@ __device__ __forceinline__ void load_keys(const Logit* row, int e0, int E, bool 
     }
   }
 #pragma unroll
-  for (int i = 0; i < PER; ++i) key[i] = key_of(l[i], e0 + i < E);
+  for (int i = 0; i < PER; ++i) {
+    key[i] = key_of(l[i], e0 + i < E);
+    if (HALF) key[i] = key[i] ? (key[i] & 0xFFFF0000u) | (0xFFFFu - (e0 + i)) : 0u;
+  }
 }
 
-// L lanes take a token, PER logits each (E <= L * PER).
-template <int L, int PER, typename Logit>
-__global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
+// L lanes take a token, PER logits each (E <= L * PER).  A choice is the largest
+// key, over a lane's and then over the lanes; where keys can be equal, the first
+// lane that holds it gives up its first.  Exponentials wait for the entries'
+// turn, a thread each.
+template <int THREADS, int L, int PER, typename Logit>
+__global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs a) {
+  constexpr bool HALF = sizeof(Logit) == 2;
   __shared__ __align__(16) int ids[kRoutePass];
+  __shared__ unsigned best_keys[kRoutePass];
   __shared__ float vals[kRoutePass];
   __shared__ float sums[kRoutePass];         // (not renormalized) of all experts, by token
   __shared__ int count[kMaxExperts + 1];     // entries of each expert in the passes so far
   const int sub = threadIdx.x % L, group = threadIdx.x / L;
   const bool lists = a.offsets != nullptr;
   if (a.T == 0) {  // (lists of nothing)
-    for (int e = threadIdx.x; e <= a.E; e += kThreads) a.offsets[e] = 0;
+    for (int e = threadIdx.x; e <= a.E; e += THREADS) a.offsets[e] = 0;
     return;
   }
-  for (int e = threadIdx.x; e < a.E; e += kThreads) count[e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += THREADS) count[e] = 0;
   for (int pass = 0; pass < a.passes; ++pass) {
     const long long t0 = ((long long)blockIdx.x * a.passes + pass) * a.tokens;
     if (t0 >= a.T) break;
     const int nt = (int)min((long long)a.tokens, a.T - t0);
-    for (int t = group; t < nt; t += kThreads / L) {
+    for (int t = group; t < nt; t += THREADS / L) {
       const Logit* row = static_cast<const Logit*>(a.logits) + (t0 + t) * a.ldl;
       unsigned key[PER];
       load_keys<PER>(row, sub * PER, a.E, a.wide, key);
-      float top = 0.0f, all = 0.0f;
       for (int j = 0; j < a.topk; ++j) {
-        unsigned best = 0;
+        unsigned mine = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) best = max(best, key[i]);
-        best = lanes_umax<L>(best);
-        unsigned e = kNone;
+        for (int i = 0; i < PER; ++i) mine = max(mine, key[i]);
+        const unsigned best = lanes_umax<L>(mine);
+        if (j == 0 && !a.renormalize) {
+          const float top = logit_of<HALF>(best);
+          float all = 0.0f;
 #pragma unroll
-        for (int i = PER - 1; i >= 0; --i) e = key[i] == best ? (unsigned)(sub * PER + i) : e;
-        e = lanes_umin<L>(e);
-        const float l = logit_of(best);
-        if (j == 0) {
-          top = l;
-          if (!a.renormalize) {
+          for (int i = 0; i < PER; ++i)
+            all += key[i] ? over_top(logit_of<HALF>(key[i]), top) : 0.0f;
+          all = lanes_sum<L>(all);
+          if (sub == 0) sums[t] = all;
+        }
+        if constexpr (HALF) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) all += key[i] ? over_top(logit_of(key[i]), top) : 0.0f;
-            all = lanes_sum<L>(all);
+          for (int i = 0; i < PER; ++i) key[i] = key[i] == best ? 0u : key[i];
+          if (sub == 0) best_keys[t * a.topk + j] = best;
+        } else {
+          // the first of the equals: lanes hold the experts in order
+          unsigned long long at = __ballot(mine == best);
+          if (L == 16) at = at >> (threadIdx.x & 48) & 0xFFFFu;
+          const bool owner = sub == __builtin_ctzll(at);
+          int e = PER;
+#pragma unroll
+          for (int i = PER - 1; i >= 0; --i) e = key[i] == best ? i : e;
+          e = owner ? e : PER;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) key[i] = i == e ? 0u : key[i];
+          if (owner) {
+            ids[t * a.topk + j] = best ? sub * PER + e : -1;
+            best_keys[t * a.topk + j] = best;
           }
         }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) key[i] = (unsigned)(sub * PER + i) == e ? 0u : key[i];
-        if (sub == 0) {
-          ids[t * a.topk + j] = best ? (int)e : -1;
-          vals[t * a.topk + j] = best ? over_top(l, top) : 0.0f;
-        }
       }
-      if (sub == 0) sums[t] = all;
     }
     __syncthreads();
     // an entry a thread
     const int n = nt * a.topk, i = threadIdx.x;
+    const int t = i / a.topk;
     const long long at = t0 * a.topk + i;
     int id = -1, rank = 0;
     if (i < n) {
-      const int t = i / a.topk;
-      float sum = sums[t];
+      const unsigned best = best_keys[i];
+      vals[i] = best ? over_top(logit_of<HALF>(best), logit_of<HALF>(best_keys[t * a.topk])) : 0.0f;
+      if (HALF) ids[i] = best ? (int)(0xFFFFu - (best & 0xFFFFu)) : -1;
+    }
+    __syncthreads();
+    if (i < n) {
+      float sum = 0.0f;
       if (a.renormalize) {
-        sum = 0.0f;
         for (int j = 0; j < a.topk; ++j) sum += vals[t * a.topk + j];
+      } else {
+        sum = sums[t];
       }
       id = ids[i];
       a.experts[at] = id;
@@ -227,7 +235,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
     // (one workgroup has one pass)
     place_experts(count, count, a.E);
     __syncthreads();
-    for (int e = threadIdx.x; e <= a.E; e += kThreads) a.offsets[e] = count[e];
+    for (int e = threadIdx.x; e <= a.E; e += THREADS) a.offsets[e] = count[e];
     if (i < n) {
       a.slots[at] = id >= 0 ? count[id] + rank : -1;
       if (id >= 0) a.rows[count[id] + rank] = i / a.topk;
@@ -236,7 +244,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
   }
   if (lists && a.blocks > 1) {
     __syncthreads();
-    for (int e = threadIdx.x; e < count_stride(a.E); e += kThreads)
+    for (int e = threadIdx.x; e < count_stride(a.E); e += THREADS)
       a.counts[(long long)blockIdx.x * count_stride(a.E) + e] = e < a.E ? count[e] : 0;
   }
 }
@@ -306,17 +314,24 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteArgs a) {
     a.rows[i] = 0;
 }
 
+template <int THREADS, typename Logit>
+auto pick(const RouteArgs& a) {
+  if (route_lanes(a.T, a.E) == 16)
+    return a.E <= 128 ? route_kernel<THREADS, 16, 8, Logit> : route_kernel<THREADS, 16, 16, Logit>;
+  return a.E <= 512 ? route_kernel<THREADS, 64, 8, Logit> : route_kernel<THREADS, 64, 16, Logit>;
+}
 template <typename Logit>
-auto pick(int E) {
-  return E <= 128 ? route_kernel<16, 8, Logit>
-                  : E <= 512 ? route_kernel<64, 8, Logit> : route_kernel<64, 16, Logit>;
+hipError_t launch_first(const RouteArgs& a, hipStream_t s) {
+  // (a single workgroup takes as many tokens at once as it can)
+  const bool wide = a.blocks == 1 && (long long)a.T * route_lanes(a.T, a.E) > kThreads;
+  return launch_kernel(wide ? pick<kRouteWide, Logit>(a) : pick<kThreads, Logit>(a),
+                       dim3((unsigned)a.blocks), dim3(wide ? kRouteWide : kThreads), 0, s, a);
 }
 
 }  // namespace
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
-  const hipError_t e = launch_kernel(a.bf16 ? pick<uint16_t>(a.E) : pick<float>(a.E),
-                                     dim3((unsigned)a.blocks), dim3(kThreads), 0, s, a);
+  const hipError_t e = a.bf16 ? launch_first<uint16_t>(a, s) : launch_first<float>(a, s);
   if (e != hipSuccess || !a.offsets || a.blocks == 1) return e;
   return launch_kernel(place_kernel, dim3((unsigned)((a.blocks + kSpan - 1) / kSpan)),
                        dim3(kPlaceThreads), 0, s, a);

@@ -32,10 +32,16 @@ struct RouteArgs {
   int* counts;  // [blocks, count_stride(E)] (workspace)
   int wide;     // rows load in 16-byte pieces
 };
-// Up to 256 entries are one pass of one workgroup; more go in passes of half as
-// many, which is a token for every 16 lanes of a workgroup at top 8 (8192 tokens
-// of 128 experts, passes of 256: the first launch 12.5 us).
+// Few entries are one pass of one workgroup (of kRouteWide threads where there are
+// tokens for them); more go in passes of at most kRouteMany.
 constexpr int kRoutePass = 256, kRouteMany = 128;
+constexpr int kRouteThreads = 256, kRouteWide = 1024;
+// Lanes that share a token: 16 hold up to 256 logits, 64 more.  Between 128 and
+// 256 a choice takes 64 less time and 16 less work (256 experts, top 8: 1 token 5.4
+// us and 7.1, 4096 tokens 17.7 and 14.5).
+__host__ __device__ constexpr int route_lanes(int T, int E) {
+  return E <= 128 || (E <= 256 && T > 16) ? 16 : 64;
+}
 __host__ __device__ constexpr int count_stride(int E) { return (E + 3) / 4 * 4; }
 // One launch, or for more than one workgroup's entries two.
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);

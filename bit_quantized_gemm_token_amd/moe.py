@@ -43,7 +43,7 @@ def moe_route(logits, topk, renormalize=True, scale=1.0, lists=True, workspace=N
                moe_combine)
 
     topk at most 32 and E, E at most 1024.  One launch for T * topk up to 256
-    entries, else two; whole numbers only, the same every time.  workspace: as
+    entries (fewer above 256 experts), else two; whole numbers only, the same every time.  workspace: as
     for block_gemm.
     """
     lp, ldl = _rows(logits, "logits")
@@ -61,7 +61,7 @@ def moe_route(logits, topk, renormalize=True, scale=1.0, lists=True, workspace=N
         weights = weights.view(_F32).view(T, topk)
         experts, slots = experts.view(T, topk), slots.view(T, topk)
         ep, sp, rp, op = wp + 4 * n, wp + 8 * n, wp + 12 * n, wp + 16 * n
-        if n > 256:
+        if n > 256 or (E > 256 and T > 16):  # (the calls that may take two launches)
             if workspace is None:
                 workspace = _workspace_of(dev, s)
             buf = workspace.buf

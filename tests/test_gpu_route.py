@@ -71,7 +71,8 @@ def logits_of(g, T, E, dtype, spread=2.0):
     (1, 1, 1), (1, 8, 2), (1, 128, 8), (3, 5, 5), (8, 128, 8), (32, 128, 8), (33, 128, 8),
     (64, 60, 4), (65, 60, 4), (100, 64, 6), (42, 64, 6), (43, 64, 6), (257, 16, 1), (16, 1024, 32),
     (8, 1000, 32), (9, 1000, 31), (300, 200, 7), (1000, 129, 8), (5000, 128, 8), (3000, 256, 2),
-    (20000, 8, 2), (40, 1024, 1)])
+    (20000, 8, 2), (40, 1024, 1), (16, 256, 8), (17, 256, 8), (32, 250, 8), (200, 256, 1),
+    (24, 300, 8), (42, 1000, 6), (128, 300, 2), (239, 256, 6), (2100, 200, 1)])
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_route(w8, T, E, topk, dtype):
     print(f"[case] T={T} E={E} topk={topk} {dtype}", flush=True)
