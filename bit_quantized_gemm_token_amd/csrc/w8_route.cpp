@@ -44,13 +44,14 @@ w8_status check_route(int T, int E, int topk) {
 }
 
 // One workgroup takes up to kRoutePass entries, unless its tokens come to several
-// rounds of many choices, which cost more than the second launch (about 0.3 us a
-// choice; 128 tokens of 300 experts, top 2, 8 rounds 18.0 us, by two launches XX).
-// Otherwise a workgroup's pass is r rounds of its threads: they cost r topk choices,
-// and half as many workgroups, whose counts the second launch reads, half of 0.012
-// us each (239 tokens of 256 experts, top 6: passes of 21 tokens 20.8 us, of 16
-// 10.9; 261 of 8, top 1: 128 11.7, 16 7.3), with as many passes as keep the
-// workgroups to kRouteBlocks.
+// rounds of many choices, which cost more than the second launch (128 tokens of 300
+// experts, top 2, 8 rounds 15.3 us, by two launches 9.0; 42 of 1000, top 6, 3 rounds
+// 18.3 and 12.2; 24 of 300, top 8, 2 rounds 9.0 both; 64 of 300, top 1, 4 rounds 7.3
+// and 8.0).  Otherwise a workgroup's pass is r rounds of its threads, which take
+// longer by r - 1 times topk choices, and the second launch has fewer workgroups'
+// counts to read: about 25 of them cost a choice's time (239 tokens of 256 experts,
+// top 6: passes of 21 tokens 20.8 us, of 16 10.9; 261 of 8, top 1: of 128 11.7, of 16
+// 7.3), with as many passes as keep the workgroups to kRouteBlocks.
 void plan_route(RouteArgs* a) {
   const int lanes = route_lanes(a->T, a->E);
   const long long rounds = ceil_div((long long)a->T * lanes, kRouteWide);

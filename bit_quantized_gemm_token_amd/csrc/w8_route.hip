@@ -12,10 +12,11 @@
 // A row of logits is a few hundred bytes and stays in the registers of 16 or 64
 // lanes; each choice is a maximum over them, its place a minimum, so a token is a
 // chain of topk reductions and the chains of many tokens hide each other.
-// Measured: 8 tokens of 128 experts, top 8, 5.6 us in one launch, all latency;
-// 8192 tokens 8.0 us by the chains' instructions (the bytes, 2.6 MB, take 1 us)
-// and 6.8 us for the places, by the counts of 1024 workgroups and the latency of
-// reading, adding and writing one after the other.
+// Measured: 8 tokens of 128 experts, top 8, 4.8 us in one launch, 32 tokens 4.9,
+// all latency (with 1 of 16 experts 3.3); 8192 tokens 5.7 us by the same chain (the
+// bytes, 3.1 MB, take 1 us) and 6.7 us for the places, by the 256 KiB of counts that
+// each workgroup reads and the latency of reading, adding and writing one after
+// the other.
 #include "w8_block.hpp"
 #include "w8_device.hpp"
 #include "w8_route.hpp"
@@ -211,23 +212,29 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs a) {
       id = ids[i];
       a.experts[at] = id;
       a.weights[at] = id >= 0 ? a.scale * (vals[i] / sum) : 0.0f;
-      if (lists && id >= 0) {
-        rank = count[id];
-#pragma unroll 4
-        for (int b = 0; b + 4 <= i; b += 4) {
-          const v4i v = *reinterpret_cast<const v4i*>(ids + b);
-          rank += (v[0] == id) + (v[1] == id) + (v[2] == id) + (v[3] == id);
-        }
-        for (int b = i & ~3; b < i; ++b) rank += ids[b] == id;
-      }
     }
     if (!lists) {
       __syncthreads();
       continue;
     }
-    __syncthreads();
-    if (id >= 0) atomicAdd(&count[id], 1);
-    __syncthreads();
+    // An entry's rank is the number of entries of its expert in front of it: those
+    // of its wave by comparing the expert's bits over the lanes, and what the waves
+    // in front, which take their turns, have added to the expert's count.
+    unsigned long long same = __ballot(id >= 0);
+    for (int bit = 1; bit < a.E; bit *= 2) {
+      const unsigned long long set = __ballot((id & bit) != 0);
+      same &= id & bit ? set : ~set;
+    }
+    const int before =
+        __builtin_amdgcn_mbcnt_hi((unsigned)(same >> 32),
+                                  __builtin_amdgcn_mbcnt_lo((unsigned)same, 0u));
+    for (int w = 0; w < n; w += 64) {
+      if ((int)threadIdx.x >> 6 == w >> 6 && id >= 0) {
+        rank = count[id] + before;
+        if (before == 0) count[id] = rank + __popcll(same);
+      }
+      __syncthreads();
+    }
     if (a.blocks > 1) {
       if (i < n) a.slots[at] = id >= 0 ? rank : -1;
       continue;
@@ -260,6 +267,15 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteArgs a) {
   __shared__ int before[kMaxExperts];           // entries of the workgroups in front of these
   __shared__ int next[kSpan][kMaxExperts];      // of each of these: its first entry's place
   const int b0 = blockIdx.x * kSpan, b1 = min(b0 + kSpan, a.blocks);
+  const long long entries = (long long)a.T * a.topk;
+  const long long each = (long long)a.passes * a.tokens * a.topk;
+  const long long begin = b0 * each + threadIdx.x, end = min(b1 * each, entries);
+  // (a thread's first entry, long before it is needed)
+  int id = -1, rank = 0;
+  if (begin < end) {
+    id = a.experts[begin];
+    rank = a.slots[begin];
+  }
   const int stride = count_stride(a.E), quads = stride / 4;
   for (int e = threadIdx.x; e < stride; e += kPlaceThreads) {
     first[e] = 0;
@@ -299,13 +315,13 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(RouteArgs a) {
   if (blockIdx.x == 0)
     for (int e = threadIdx.x; e <= a.E; e += kPlaceThreads) a.offsets[e] = first[e];
   __syncthreads();
-  const long long entries = (long long)a.T * a.topk;
-  const long long each = (long long)a.passes * a.tokens * a.topk;
-  const long long end = min(b1 * each, entries);
-  for (long long i = b0 * each + threadIdx.x; i < end; i += kPlaceThreads) {
-    const int id = a.experts[i];
+  for (long long i = begin; i < end; i += kPlaceThreads) {
+    if (i != begin) {
+      id = a.experts[i];
+      rank = a.slots[i];
+    }
     if (id < 0) continue;
-    const int slot = next[(int)(i / each) - b0][id] + a.slots[i];
+    const int slot = next[(int)(i / each) - b0][id] + rank;
     a.slots[i] = slot;
     a.rows[slot] = (int)(i / a.topk);
   }

@@ -768,10 +768,10 @@ w8_status w8_token_gemm_plan(w8_fmt fmt, int M, int N, int K, int packed, w8_blo
  *            slots[t, j] the place of choice j of token t (-1 for a choice of
  *            -1).  offsets and rows are what the grouped products take.  T == 0:
  *            the offsets, all 0, are still written.
- *   ws       w8_moe_route_workspace_size bytes (0 up to 256 entries and
- *            without lists), with w8_gemm_w8a8's rules
- * 1 <= topk <= min(E, 32).  One launch for up to 256 entries or without lists,
- * else two.                                                                */
+ *   ws       w8_moe_route_workspace_size bytes (0 where one launch does; not
+ *            used without lists), with w8_gemm_w8a8's rules
+ * 1 <= topk <= min(E, 32).  One launch without lists and for up to 256 entries
+ * (above 256 experts fewer), else two.                                     */
 w8_status w8_moe_route(int T, int E, int topk, const void *logits, int64_t ldl, int logits_fp32,
                        int renormalize, float scale, int32_t *experts, float *weights,
                        int32_t *offsets, int32_t *rows, int32_t *slots, void *ws,
