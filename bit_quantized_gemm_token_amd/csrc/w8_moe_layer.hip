@@ -261,16 +261,17 @@ __device__ __forceinline__ float uniform_load(const float* p) {
 // fewer workgroups).
 constexpr int kUpPieces = 2;
 
-template <int MB>
+template <int MB, int KW>
 struct UpLds {
   Choices c;
-  v4i part[kWaves - 1][MB][2][64];
+  v4i part[KW > 1 ? KW - 1 : 1][KW > 1 ? MB : 1][2][64];
 };
 
-// MB blocks of 16 tokens from the expert's t0-th on.
-template <int FMT, bool PACKED, int MB>
+// MB blocks of 16 tokens from the expert's t0-th on; KW waves share a block of
+// columns, wave kw a part of its K.
+template <int FMT, bool PACKED, int MB, int KW>
 __device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Expert& x, int t0,
-                                        UpLds<MB>& lds) {
+                                        UpLds<MB, KW>& lds) {
   typedef typename Traits<FMT>::Frag Frag;
   typedef typename Traits<FMT>::Acc Acc;
   constexpr int KSTEP = Traits<FMT>::KSTEP;
@@ -300,7 +301,8 @@ __device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Exp
   for (int b = 0; b < MB; ++b)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[b][j] = Acc{0, 0, 0, 0};
-  const int la = ksteps * wave / kWaves, lb = ksteps * (wave + 1) / kWaves;
+  const int kw = KW > 1 ? wave : 0;
+  const int la = ksteps * kw / KW, lb = ksteps * (kw + 1) / KW;
   auto p = products<FMT, 2, MB, steps<FMT>(kUpPieces), true>(
       la, min(lb, kfull), [&](int j, int k) -> Frag { return weight_step<FMT, PACKED>(wp[j], k); },
       [&](int b, int k) -> Frag { return load_frag<FMT>(xp[b], k); },
@@ -310,7 +312,7 @@ __device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Exp
   // the epilogue's scales, behind the first weights
   float sx[MB], sw[2][4];
   if constexpr (!BLOCK) {
-    if (wave == 0) {
+    if (kw == 0) {
 #pragma unroll
       for (int b = 0; b < MB; ++b) sx[b] = *sxp[b];
 #pragma unroll
@@ -332,16 +334,19 @@ __device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Exp
     }
   }
   // the waves' sums
-  if (wave > 0) {
+  if constexpr (KW > 1) {
+    if (kw > 0) {
 #pragma unroll
-    for (int b = 0; b < MB; ++b)
+      for (int b = 0; b < MB; ++b)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) lds.part[wave - 1][b][j][lane] = __builtin_bit_cast(v4i, acc[b][j]);
+        for (int j = 0; j < 2; ++j)
+          lds.part[kw - 1][b][j][lane] = __builtin_bit_cast(v4i, acc[b][j]);
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  if (wave == 0) {
+  if (kw == 0) {
 #pragma unroll
-    for (int w = 0; w < kWaves - 1; ++w)
+    for (int w = 0; w < KW - 1; ++w)
 #pragma unroll
       for (int b = 0; b < MB; ++b)
 #pragma unroll
@@ -366,14 +371,17 @@ __device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Exp
   }
 }
 
-template <int FMT, bool PACKED, int MB>
+template <int FMT, bool PACKED, int MB, int KW>
 __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeLayerArgs a) {
-  __shared__ UpLds<MB> lds;
+  __shared__ UpLds<MB, KW> lds;
   const Expert x = find_expert(a, blockIdx.y, lds.c);
   if (x.e < 0) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = KW > 1 ? blockIdx.x * 16 : (blockIdx.x * kWaves + wave) * 16;
+  if (n0 >= a.I) return;  // (a wave by itself, KW == 1)
   for (int t0 = 0; t0 < x.tokens; t0 += 16 * MB) {
-    if (t0) __syncthreads();  // (the sums have been read)
-    up_tile<FMT, PACKED, MB>(a, blockIdx.x * 16, x, t0, lds);
+    if (KW > 1 && t0) __syncthreads();  // (the sums have been read)
+    up_tile<FMT, PACKED, MB, KW>(a, n0, x, t0, lds);
   }
 }
 
@@ -447,6 +455,11 @@ __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const E
   const int stride = a.chunk + kPad;
   float* gscale = reinterpret_cast<float*>(codes + (long long)x.tokens * stride);  // Block_FP8's
 
+  // the workgroup's columns of I, in whole 128s
+  const int groups = (a.I + kGroup - 1) / kGroup;
+  const int lo = groups * (int)blockIdx.z / a.splits * kGroup;
+  const int hi = min(groups * ((int)blockIdx.z + 1) / a.splits * kGroup, a.I);
+
   const uint8_t* xp[MB];
   const float* sxp[MB];
 #pragma unroll
@@ -459,8 +472,8 @@ __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const E
 #pragma unroll
   for (int b = 0; b < MB; ++b) acc[b][0] = Acc{0, 0, 0, 0};
   float sw[4];
-  for (int c0 = 0; c0 < a.I; c0 += a.chunk) {
-    const int cols = min(a.chunk, a.I - c0), per = (cols + kGroup - 1) / kGroup * (kGroup / 8);
+  for (int c0 = lo; c0 < hi; c0 += a.chunk) {
+    const int cols = min(a.chunk, hi - c0), per = (cols + kGroup - 1) / kGroup * (kGroup / 8);
     const int kb = c0 / KSTEP, kend = (c0 + cols + KSTEP - 1) / KSTEP;
     // a thread's first hidden values, then the first weights: loads return in
     // order, so that the codes are made while the weights arrive
@@ -474,7 +487,7 @@ __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const E
         [&](int b, int k) { return sxp[b][k - kb]; });
     p.begin();
     if constexpr (!BLOCK) {
-      if (c0 == 0) {
+      if (c0 == lo) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) sw[i] = swp[i];
         // the tokens' largest values, over all of I
@@ -491,9 +504,10 @@ __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const E
           }
         };
         take(0, pieces, per, held);
-        for (int c = 0, from = kHeld * kThreads; c < a.I; c += a.chunk, from = 0) {
+        for (int c = 0; c < a.I; c += a.chunk) {
           const int more = min(a.chunk, a.I - c), each = (more + kGroup - 1) / kGroup * (kGroup / 8);
-          for (int i0 = from; i0 < x.tokens * each; i0 += kHeld * kThreads) {
+          // (those that are held are the first chunk's start, if I is not split)
+          for (int i0 = c == 0 && a.splits == 1 ? kHeld * kThreads : 0; i0 < x.tokens * each; i0 += kHeld * kThreads) {
             Hidden v[kHeld];
             load_hidden(a, entry, i0, x.tokens * each, each, c, more, v);
             take(i0, x.tokens * each, each, v);
@@ -534,7 +548,8 @@ __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const E
   // The experts' outputs, lane (r, g): token r of block b, columns n + 4 g .. +
   // 3; written through to where the last workgroup reads them, acknowledged
   // before this one counts itself in (the split-K hand-off of the small-M GEMM).
-  const __amdgpu_buffer_rsrc_t out = coherent_rsrc(a.part, a.T * a.topk * a.D * 4);
+  const int n_entries = a.T * a.topk;
+  const __amdgpu_buffer_rsrc_t out = coherent_rsrc(a.part, a.splits * n_entries * a.D * 4);
 #pragma unroll
   for (int b = 0; b < MB; ++b) {
     const int t = 16 * b + r, at = min(t, x.tokens - 1);
@@ -547,12 +562,13 @@ __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const E
       if constexpr (!BLOCK) o[i] *= sx * sw[i];
     }
     if (t < x.tokens && n0 + 16 * wave < a.D)
-      coherent_store16(out, (entry[at] * a.D + n + 4 * g) * 4, __builtin_bit_cast(v4i, o));
+      coherent_store16(out, ((blockIdx.z * n_entries + entry[at]) * a.D + n + 4 * g) * 4,
+                       __builtin_bit_cast(v4i, o));
   }
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
   // (how many will, while the stores are on their way)
   if (a.few) load_choices(a, lds.c);
-  const int active = count_active(lds.c);
+  const int active = count_active(lds.c) * a.splits;
   __builtin_amdgcn_s_waitcnt(0);
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
   __syncthreads();
@@ -575,7 +591,7 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLayerArgs a) {
   const Expert x = find_expert(a, blockIdx.y, lds.c);
   const int n0 = blockIdx.x * kColumns;
   if (x.e < 0) {  // (no token has an expert: the base alone)
-    if (blockIdx.y) return;
+    if (blockIdx.y || blockIdx.z) return;
     if (a.few) load_choices(a, lds.c);
     if (count_active(lds.c)) return;
   } else {
@@ -588,7 +604,8 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLayerArgs a) {
   // y of the tile's columns, four a thread, in the order of the choices; the
   // loads of a batch are all in flight (left out: entry 0's, not used)
   find_outputs(a, lds.c);
-  const __amdgpu_buffer_rsrc_t part = coherent_rsrc(a.part, a.T * a.topk * a.D * 4);
+  const int n_entries = a.T * a.topk;
+  const __amdgpu_buffer_rsrc_t part = coherent_rsrc(a.part, a.splits * n_entries * a.D * 4);
   constexpr int kBatch = 8;
   for (int i = threadIdx.x; i < a.T * (kColumns / 4); i += kThreads) {
     const int t = i / (kColumns / 4), n = n0 + 4 * (i % (kColumns / 4));
@@ -603,19 +620,31 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLayerArgs a) {
     for (int j0 = 0; j0 < a.topk; j0 += kBatch) {
       v4i v[kBatch];
       float w[kBatch];
+      int from[kBatch];
       bool on[kBatch];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const int at = t * a.topk + min(j0 + j, a.topk - 1), from = lds.c.ids[at];
-        on[j] = j0 + j < a.topk && from >= 0;
-        v[j] = coherent_load16(part, (max(from, 0) * a.D + n) * 4);
+        const int at = t * a.topk + min(j0 + j, a.topk - 1), id = lds.c.ids[at];
+        on[j] = j0 + j < a.topk && id >= 0;
+        from[j] = max(id, 0);
+        v[j] = coherent_load16(part, (from[j] * a.D + n) * 4);
         w[j] = a.weights[at];
+      }
+      v4f p[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) p[j] = __builtin_bit_cast(v4f, v[j]);
+      for (int z = 1; z < a.splits; ++z) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          v[j] = coherent_load16(part, ((z * n_entries + from[j]) * a.D + n) * 4);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) p[j] += __builtin_bit_cast(v4f, v[j]);
       }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const v4f p = __builtin_bit_cast(v4f, v[j]);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) sum[u] = on[j] ? __builtin_fmaf(w[j], p[u], sum[u]) : sum[u];
+        for (int u = 0; u < 4; ++u)
+          sum[u] = on[j] ? __builtin_fmaf(w[j], p[j][u], sum[u]) : sum[u];
       }
     }
     uint16_t y[4];
@@ -775,8 +804,16 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_down_few_kernel(MoeLayerAr
 
 template <int FMT, bool PACKED, int MB>
 hipError_t launch_up(const MoeLayerArgs& a, hipStream_t s) {
-  return launch_kernel(moe_up_kernel<FMT, PACKED, MB>, dim3((unsigned)(a.I / 16), (unsigned)a.slots),
-                       dim3(kThreads), 0, s, a);
+  // Short K leaves four waves a step or two each: where there are columns enough
+  // for every compute unit, a wave takes all of it (64 experts, top 8, I = 1024, 8
+  // tokens: D = 512 27.9 us and 22.9, 768 32.1 and 29.7, 1024 35.2 and 37.1; 1 token,
+  // D = 768: 12.9 and 13.6).
+  const int blocks = (a.I / 16 + kWaves - 1) / kWaves;
+  if (a.D <= 768 && (long long)blocks * a.slots >= kComputeUnits)
+    return launch_kernel(moe_up_kernel<FMT, PACKED, MB, 1>,
+                         dim3((unsigned)blocks, (unsigned)a.slots), dim3(kThreads), 0, s, a);
+  return launch_kernel(moe_up_kernel<FMT, PACKED, MB, kWaves>,
+                       dim3((unsigned)(a.I / 16), (unsigned)a.slots), dim3(kThreads), 0, s, a);
 }
 template <int FMT, bool PACKED, int MB>
 hipError_t launch_down(const MoeLayerArgs& a, hipStream_t s) {
@@ -788,7 +825,8 @@ hipError_t launch_down(const MoeLayerArgs& a, hipStream_t s) {
   }
   const int tiles = (a.D + kColumns - 1) / kColumns;
   return launch_kernel(moe_down_kernel<FMT, PACKED, MB>,
-                       dim3((unsigned)tiles, (unsigned)a.slots), dim3(kThreads), a.T * row, s, a);
+                       dim3((unsigned)tiles, (unsigned)a.slots, (unsigned)a.splits),
+                       dim3(kThreads), a.T * row, s, a);
 }
 template <int FMT, int MB>
 hipError_t launch_layer(bool packed1, bool packed2, const MoeLayerArgs& a, hipStream_t s) {

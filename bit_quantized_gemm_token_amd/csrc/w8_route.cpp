@@ -77,12 +77,24 @@ size_t route_bytes(const RouteArgs& a) {
 struct LayerWs {
   size_t h, part, total;
 };
+// Parts of I that workgroups of the layer's second kernel share where its columns
+// and experts leave compute units without two of them (32 tokens, 2 of 8 experts of
+// 1024 x 2048: whole 37.2 us, in two 32.0; 12 tokens, 4 of 16 of 256 x 4096 33.8, in
+// two 28.6, in four 26.6; 8 tokens, 2 of 16 of 1024 x 1024 15.1 and 15.6, which is why
+// a part has 1024 columns at least).
+int layer_splits(int slots, int D, int I) {
+  const int tiles = (int)ceil_div(D, 64);
+  int splits = 1;
+  while (splits < 4 && (long long)tiles * slots * 2 * splits <= 512 && I >= 2048 * splits) splits *= 2;
+  return splits;
+}
 LayerWs layer_ws(int T, int topk, int D, int I) {
   const size_t n = (size_t)T * topk;
   LayerWs w;
   w.h = ws_counter_bytes(0);
   w.part = w.h + round256(n * I * 4);
-  w.total = w.part + round256(n * D * 4);
+  // (as many splits as one expert would take: E is not known here)
+  w.total = w.part + round256(n * D * 4 * layer_splits(1, D, I));
   return w;
 }
 
@@ -123,17 +135,17 @@ w8_status check_experts(int fmt, int E, int N, int K, const void* w, int64_t ldw
   return W8_OK;
 }
 
-// Up to 8 entries, and up to 16 of one token's, take the second kernel for few
-// entries, which reads an expert's weights for each entry that has chosen it
-// (2048 x 768, E experts: 1 token, 8 of 128 14.4 us, 16.1 by the other kernel; 16
-// of 64 20.4 and 22.0; 2 tokens, 4 of 8 13.8 and 15.0; 8 tokens, 2 of 8 16.5 and
-// 15.8; 4 tokens, 4 of 32, of 4096 x 2048 60.2 and 58.8), with as many waves an
-// entry as 16 leave, of 1024 columns of I at least (2 experts of 4096 x 4096: one
-// wave 30.1 us, two 24.5, four 23.6; 4096 x 1024 12.6, 12.7 and 12.9).  0: the
-// other kernel.
+// Up to 4 entries, and on short I up to 8 and up to 16 of one token's, take the
+// second kernel for few entries, which reads an expert's weights for each entry that
+// has chosen it and keeps one workgroup busy for 16 columns of all of them (2048 x
+// 768, E experts: 1 token, 8 of 128 14.4 us, 16.1 by the other kernel; 2 tokens, 4 of
+// 8 13.8 and 15.0; 8 tokens, 2 of 8 16.5 and 15.8; 1 token of 2048 x 4096: 2 of 8
+// 25.1 and 27.4, 8 of 60 of 928 x 3360 31.0 and 23.3), with as many waves an entry as
+// 16 leave, of 1024 columns of I at least (2 experts of 4096 x 4096: one wave 30.1 us,
+// two 24.5, four 23.6; 4096 x 1024 12.6, 12.7 and 12.9).  0: the other kernel.
 int layer_parts(int T, int topk, int I) {
   const int n = T * topk;
-  if (n > (T == 1 ? 16 : 8)) return 0;
+  if (n > (I > 1024 ? 4 : T == 1 ? 16 : 8)) return 0;
   int parts = 1;
   while (2 * parts * n <= 16 && I >= 2048 * parts) parts *= 2;
   return parts;
@@ -301,8 +313,10 @@ w8_status w8_moe_layer(w8_fmt fmt_in, int E, int T, int topk, int D, int I, cons
   a.few = T * topk <= 64 && T * topk <= E;
   a.slots = std::min(E, T * topk);
   a.parts = layer_parts(T, topk, I);
-  a.chunk = a.parts ? layer_chunk(T * topk * a.parts, (I + a.parts - 1) / a.parts + W8_GROUP)
-                    : layer_chunk(T, I);
+  a.splits = a.parts ? 1 : layer_splits(a.slots, D, I);
+  const int each = a.parts ? a.parts : a.splits;
+  a.chunk = layer_chunk(a.parts ? T * topk * a.parts : T,
+                        each > 1 ? (I + each - 1) / each + W8_GROUP : I);
   const hipError_t e =
       launch_moe_layer(fmt, ldw1 == 0, ldw2 == 0, a, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(W8_E_HIP, hip_msg("moe_layer launch", e));

@@ -71,7 +71,7 @@ struct MoeLayerArgs {
   const uint16_t* base; // bf16 [T, D], or null
   uint16_t* y;          // bf16 [T, D]
   float* h;             // [T * topk, I] gated products (workspace)
-  float* part;          // [T * topk, D] the experts' outputs
+  float* part;          // [splits, T * topk, D] the experts' outputs
   unsigned* counters;   // arrival counters
   long long ldq, ldw1, ldw2, ldb, ldy;  // bytes; base, y: elements
   long long w1_stride, w2_stride;       // bytes between experts
@@ -80,6 +80,7 @@ struct MoeLayerArgs {
   int slots;            // of experts that a launch holds: each has tokens or ends at once
   int few;              // a slot is an entry (at most 64), else one of the experts with tokens
   int parts;            // > 0: few entries, so many waves each for the second product
+  int splits;           // parts of I that workgroups of the second kernel share
   int chunk;            // of I that a workgroup of the second kernel (parts: a wave) keeps as codes
 };
 // Two launches.  packed1, packed2: the layouts of w1 and w2.

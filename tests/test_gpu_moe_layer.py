@@ -126,7 +126,10 @@ SIZES = [  # T, E, topk, D, I (Block_FP8: rounded up to whole 128s)
     (32, 1000, 32, 32, 32), (4, 8, 2, 2048, 768), (32, 1, 1, 256, 2064), (2, 3, 2, 64, 8192),
     (8, 3, 2, 64, 7200), (16, 2, 1, 144, 3472), (5, 9, 9, 64, 16), (1, 40, 16, 64, 3600),
     (1, 8, 1, 272, 9008), (1, 2, 2, 1024, 4096), (2, 64, 8, 144, 1552), (4, 64, 3, 64, 528),
-    (1, 5, 5, 80, 50000), (4, 2, 2, 272, 2064), (8, 3, 1, 64, 128), (2, 4, 4, 144, 4208)]
+    (1, 5, 5, 80, 50000), (4, 2, 2, 272, 2064), (8, 3, 1, 64, 128), (2, 4, 4, 144, 4208),
+    # the second projection in parts, the first by whole waves
+    (1, 8, 8, 144, 3360), (6, 4, 2, 80, 4112), (5, 3, 3, 64, 2064), (32, 2, 1, 64, 8208),
+    (8, 60, 6, 128, 512), (20, 64, 8, 144, 336), (3, 2, 2, 64, 9008)]
 
 
 def sized(fmt, D, I):
@@ -151,7 +154,7 @@ def test_layer(w8, fmt, T, E, topk, D, I):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("packed", [(True, False), (False, True), (True, True)])
-@pytest.mark.parametrize("T,D,I", [(3, 256, 128), (20, 272, 400)])
+@pytest.mark.parametrize("T,D,I", [(3, 256, 128), (20, 272, 400), (20, 144, 2752), (5, 80, 4112)])
 def test_packed_weights(w8, fmt, packed, T, D, I):
     """Either layout of either weight: the same bits."""
     c = Layer(fmt, T, 6, 2, *sized(fmt, D, I))
