@@ -50,6 +50,8 @@ def moe_route(logits, topk, renormalize=True, scale=1.0, lists=True, workspace=N
     if logits.dtype is not _F32 and logits.dtype is not _BF16:
         raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
     T, E = logits.shape
+    if topk < 1:
+        moe_route_workspace_size(T, E, topk)  # (raises)
     dev, index, n = logits.device, logits.get_device(), T * topk
     s = _handle(stream, dev)
     op = rp = sp = buf = None

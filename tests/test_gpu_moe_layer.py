@@ -301,8 +301,10 @@ def test_workspace_shared_with_the_other_operators(w8, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-def test_capture_streams_and_overlap(w8, fmt):
-    c = Layer(fmt, 8, 16, 4, 512, 256)
+@pytest.mark.parametrize("T,E,topk,D,I", [(8, 16, 4, 512, 256), (6, 4, 2, 128, 4224),
+                                          (2, 16, 4, 256, 384)])
+def test_capture_streams_and_overlap(w8, fmt, T, E, topk, D, I):
+    c = Layer(fmt, T, E, topk, D, I)
     a = c.args(w8)
     want = w8.moe_layer(*a)
     c.check(want)
@@ -311,7 +313,7 @@ def test_capture_streams_and_overlap(w8, fmt):
     got = [w8.moe_layer(*a, y=torch.empty_like(want), stream=st) for _ in range(10) for st in streams]
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for y in got)
-    y, ws = torch.empty_like(want), w8.Workspace(DEV, w8.moe_layer_workspace_size(8, 4, 512, 256))
+    y, ws = torch.empty_like(want), w8.Workspace(DEV, w8.moe_layer_workspace_size(T, topk, D, I))
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):

@@ -114,6 +114,10 @@ def test_route_workspace(lib, w8):
     assert call(lib.w8_moe_route, ROUTE, ws_bytes=need - 1) == WORKSPACE
     assert call(lib.w8_moe_route, ROUTE, ws=None) == WORKSPACE
     assert w8.moe_route_workspace_size(0, 64, 8) == 0
+    # several rounds of choices in one workgroup take two launches
+    assert w8.moe_route_workspace_size(16, 1000, 8) == 0
+    assert w8.moe_route_workspace_size(42, 1000, 6) > 0
+    assert w8.moe_route_workspace_size(85, 256, 3) == w8.moe_route_workspace_size(256, 8, 1) == 0
     # the counts of at most 1024 workgroups, past the counter region
     assert w8.moe_route_workspace_size((1 << 22) - 1, 1024, 32) <= (2 << 20) + 1024 * 1024 * 4
     with pytest.raises(w8.W8Error, match="topk"):
@@ -236,6 +240,9 @@ def test_binding_refuses_shapes_types_and_devices(w8, fake):
         w8.token_quantize("W8A8_INT8", fake(T, D, dtype=BF16), gate=fake(T, D + 8, dtype=BF16))
     with pytest.raises(TypeError, match="logits"):
         w8.moe_route(fake(T, E, dtype=torch.float16), k)
+    for topk in (0, -1):
+        with pytest.raises(w8.W8Error, match="topk"):
+            w8.moe_route(fake(T, E, dtype=F32), topk)
     with pytest.raises(ValueError, match="slots"):
         w8.moe_combine(fake(16, D, dtype=BF16), weights, fake(T * k, dtype=I32))
     with pytest.raises(ValueError, match="base"):
