@@ -84,9 +84,9 @@ def _new(rows, cols, dtype, device, stream):
     return t, t.data_ptr(), cols
 
 
-def _new_codes(M, K, device, stream, dtype=_CODES):
+def _new_codes(M, K, device, stream):
     """Codes [M, K] whose row stride the GEMMs take (a multiple of 16)."""
-    t, p, ld = _new(M, (K + 15) // 16 * 16, dtype, device, stream)
+    t, p, ld = _new(M, (K + 15) // 16 * 16, _CODES, device, stream)
     return (t if ld == K else t[:, :K]), p, ld
 
 

@@ -104,6 +104,14 @@ def test_quantize_edges(w8, fmt):
     assert q.shape == (0, 64) and s.shape == (0,)
     q, s = w8.token_quantize(fmt, torch.zeros(2, 256, dtype=torch.bfloat16, device=DEV))
     assert (q.view(torch.uint8) == 0).all() and (s == 1).all()
+    # rows that the GEMMs take, on whole lines where they are long
+    for K, ld in ((8, 16), (504, 512), (496, 496), (512, 512), (520, 640), (7248, 7296)):
+        x, v = bf16(np.random.default_rng(K).standard_normal((3, K)))
+        q, s = w8.token_quantize(fmt, x)
+        assert q.stride() == (ld, 1)
+        np.testing.assert_array_equal(code_bytes(q), quantized(fmt, v)[0])
+        q, s = w8.token_quantize(fmt, x, stream=torch.cuda.current_stream())
+        assert q.stride() == (ld, 1)
     # from a wider buffer into a wider buffer: the columns beside stay
     for K in (256, 1040, 9000):
         both, v = bf16(np.random.default_rng(0).standard_normal((5, K + 24)))
