@@ -1,7 +1,8 @@
-// The experts of a few tokens as a whole, in two launches:
+// The experts of a few tokens as a whole, in two launches or three:
 //
 //   up    a = x W1_e^T for the tokens of expert e, gate and up halves;
 //         h = silu(a_gate) a_up in fp32
+//         (codes of h in the format, where many tiles would make them again)
 //   down  hq = codes of h in the format; p = hq W2_e^T;
 //         y[t] = base[t] + sum_j weights[t, j] p[t, j], by the last workgroup of
 //         a column tile to arrive
@@ -388,9 +389,9 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeLayerArgs a) {
 // -------------------------------------------------------------------- down --
 // 64 columns of y for one expert: each wave 16 of its weight rows over the whole
 // of I, the tokens' codes from LDS, where the workgroup makes them from h
-// `chunk` columns at a time.  Two steps are in flight (as above, two, three, four
-// and six: 8 tokens 22.4, 22.8, 25.6 and 22.6 us, 32 tokens 42.9, 42.8, 48.0 and
-// 43.9).
+// `chunk` columns at a time, or from memory, if they are there.  Two steps are in
+// flight (as above, two, three, four and six: 8 tokens 22.4, 22.8, 25.6 and 22.6 us,
+// 32 tokens 42.9, 42.8, 48.0 and 43.9).
 constexpr int kColumns = 16 * kWaves;
 constexpr int kPad = 16;  // bytes that move a row's codes on by four LDS banks
 
@@ -434,7 +435,8 @@ __device__ __forceinline__ unsigned largest(const Hidden& v) {
   return m;
 }
 
-template <int FMT, bool PACKED, int MB>
+// CODED: moe_encode_kernel has made the tokens' codes.
+template <int FMT, bool PACKED, int MB, bool CODED>
 __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const Expert& x,
                                           DownLds& lds) {
   typedef typename Traits<FMT>::Frag Frag;
@@ -472,7 +474,35 @@ __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const E
 #pragma unroll
   for (int b = 0; b < MB; ++b) acc[b][0] = Acc{0, 0, 0, 0};
   float sw[4];
-  for (int c0 = lo; c0 < hi; c0 += a.chunk) {
+  if constexpr (CODED) {
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+      const int e = entry[min(16 * b + r, x.tokens - 1)];
+      xp[b] = a.hq + (long long)e * a.ldh + 16 * g;
+      sxp[b] = a.hs + (BLOCK ? (long long)e * G : e);
+    }
+    const int la = lo / KSTEP, lb = (hi + KSTEP - 1) / KSTEP;
+    auto p = products<FMT, 1, MB, steps<FMT>(2), true>(
+        la, min(lb, kfull), [&](int, int k) -> Frag { return weight_step<FMT, PACKED>(wp, k); },
+        [&](int b, int k) -> Frag { return load_frag<FMT>(xp[b], k); },
+        [&](int, int k) { return uniform_load(swp + k); },
+        [&](int b, int k) { return sxp[b][k]; });
+    p.begin();
+    if constexpr (!BLOCK) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sw[i] = swp[i];
+    }
+    p.run(acc);
+    if constexpr (!BLOCK) {
+      if (lb > kfull) {
+        const Frag w = weight_tail<FMT, PACKED>(wp, kfull, a.I);
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+          p.multiply(acc[b][0], w, load_frag_tail<FMT>(xp[b], kfull, 16 * g, a.I), 0.0f);
+      }
+    }
+  }
+  for (int c0 = lo; !CODED && c0 < hi; c0 += a.chunk) {
     const int cols = min(a.chunk, hi - c0), per = (cols + kGroup - 1) / kGroup * (kGroup / 8);
     const int kb = c0 / KSTEP, kend = (c0 + cols + KSTEP - 1) / KSTEP;
     // a thread's first hidden values, then the first weights: loads return in
@@ -554,7 +584,8 @@ __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const E
   for (int b = 0; b < MB; ++b) {
     const int t = 16 * b + r, at = min(t, x.tokens - 1);
     float sx = 0.0f;
-    if constexpr (!BLOCK) sx = act_scale<INT8>(__uint_as_float(lds.top[at]));
+    if constexpr (!BLOCK)
+      sx = CODED ? a.hs[entry[at]] : act_scale<INT8>(__uint_as_float(lds.top[at]));
     v4f o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -585,28 +616,13 @@ __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const E
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-template <int FMT, bool PACKED, int MB>
-__global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLayerArgs a) {
-  __shared__ DownLds lds;
-  const Expert x = find_expert(a, blockIdx.y, lds.c);
-  const int n0 = blockIdx.x * kColumns;
-  if (x.e < 0) {  // (no token has an expert: the base alone)
-    if (blockIdx.y || blockIdx.z) return;
-    if (a.few) load_choices(a, lds.c);
-    if (count_active(lds.c)) return;
-  } else {
-    if (MB == 1 || x.tokens <= 16)
-      down_tile<FMT, PACKED, 1>(a, n0, x, lds);
-    else
-      down_tile<FMT, PACKED, MB>(a, n0, x, lds);
-    if (!lds.last) return;
-  }
-  // y of the tile's columns, four a thread, in the order of the choices; the
-  // loads of a batch are all in flight (left out: entry 0's, not used)
-  find_outputs(a, lds.c);
+// y of a tile's columns, four a thread, in the order of the choices, an output's
+// parts (SPLIT: of I) first; the loads of a batch are all in flight (left out: entry
+// 0's, not used).
+template <int BATCH, bool SPLIT>
+__device__ __forceinline__ void sum_outputs(const MoeLayerArgs& a, int n0, const Choices& c) {
   const int n_entries = a.T * a.topk;
   const __amdgpu_buffer_rsrc_t part = coherent_rsrc(a.part, a.splits * n_entries * a.D * 4);
-  constexpr int kBatch = 8;
   for (int i = threadIdx.x; i < a.T * (kColumns / 4); i += kThreads) {
     const int t = i / (kColumns / 4), n = n0 + 4 * (i % (kColumns / 4));
     if (n >= a.D) continue;
@@ -617,31 +633,31 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLayerArgs a) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) sum[u] = bf16_lo(b[u]);
     }
-    for (int j0 = 0; j0 < a.topk; j0 += kBatch) {
-      v4i v[kBatch];
-      float w[kBatch];
-      int from[kBatch];
-      bool on[kBatch];
+    for (int j0 = 0; j0 < a.topk; j0 += BATCH) {
+      v4i v[BATCH];
+      float w[BATCH];
+      int from[BATCH];
+      bool on[BATCH];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int at = t * a.topk + min(j0 + j, a.topk - 1), id = lds.c.ids[at];
+      for (int j = 0; j < BATCH; ++j) {
+        const int at = t * a.topk + min(j0 + j, a.topk - 1), id = c.ids[at];
         on[j] = j0 + j < a.topk && id >= 0;
         from[j] = max(id, 0);
         v[j] = coherent_load16(part, (from[j] * a.D + n) * 4);
         w[j] = a.weights[at];
       }
-      v4f p[kBatch];
+      v4f p[BATCH];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) p[j] = __builtin_bit_cast(v4f, v[j]);
-      for (int z = 1; z < a.splits; ++z) {
+      for (int j = 0; j < BATCH; ++j) p[j] = __builtin_bit_cast(v4f, v[j]);
+      for (int z = 1; SPLIT && z < a.splits; ++z) {
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
+        for (int j = 0; j < BATCH; ++j)
           v[j] = coherent_load16(part, ((z * n_entries + from[j]) * a.D + n) * 4);
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) p[j] += __builtin_bit_cast(v4f, v[j]);
+        for (int j = 0; j < BATCH; ++j) p[j] += __builtin_bit_cast(v4f, v[j]);
       }
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
+      for (int j = 0; j < BATCH; ++j) {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           sum[u] = on[j] ? __builtin_fmaf(w[j], p[j][u], sum[u]) : sum[u];
@@ -651,6 +667,87 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLayerArgs a) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) y[u] = (uint16_t)bf16_bits(sum[u]);
     __builtin_memcpy(a.y + t * a.ldy + n, y, 8);
+  }
+}
+
+template <int FMT, bool PACKED, int MB, bool CODED>
+__global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLayerArgs a) {
+  __shared__ DownLds lds;
+  const Expert x = find_expert(a, blockIdx.y, lds.c);
+  const int n0 = blockIdx.x * kColumns;
+  if (x.e < 0) {  // (no token has an expert: the base alone)
+    if (blockIdx.y || blockIdx.z) return;
+    if (a.few) load_choices(a, lds.c);
+    if (count_active(lds.c)) return;
+  } else {
+    if (MB == 1 || x.tokens <= 16)
+      down_tile<FMT, PACKED, 1, CODED>(a, n0, x, lds);
+    else
+      down_tile<FMT, PACKED, MB, CODED>(a, n0, x, lds);
+    if (!lds.last) return;
+  }
+  find_outputs(a, lds.c);
+  if (a.splits == 1)
+    sum_outputs<8, false>(a, n0, lds.c);
+  else
+    sum_outputs<4, true>(a, n0, lds.c);
+}
+
+// The codes and scales of an entry's hidden values, a workgroup each, with as many
+// threads as take them at once (64 entries of 14336: 4.8 us, by 256 threads 9.0).
+constexpr int kEncodeThreads = 1024;
+
+template <int FMT>
+__global__ __launch_bounds__(kEncodeThreads) void moe_encode_kernel(MoeLayerArgs a) {
+  constexpr bool BLOCK = FMT == BLOCK_FP8, INT8 = FMT == W8A8_INT8;
+  __shared__ unsigned tops[kEncodeThreads / 64];
+  const int entry = blockIdx.x, id = a.experts[entry], threads = blockDim.x;
+  // (of an expert that the token has chosen before nothing is there; nobody asks)
+  if ((unsigned)id >= (unsigned)a.E) return;
+  const int per = (a.I + kGroup - 1) / kGroup * (kGroup / 8);
+  uint8_t* q = a.hq + (long long)entry * a.ldh;
+  constexpr int N = 2;  // pieces of eight values in flight, the first two kept
+  auto load = [&](int i0, Hidden (&v)[N]) {
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int i = i0 + (int)threadIdx.x + u * threads;
+      v[u] = Hidden{};
+      if (i < per) v[u] = load_hidden(a, &entry, i, per, 0, a.I);
+    }
+  };
+  Hidden held[N];
+  load(0, held);
+  float s = 0.0f;
+  if constexpr (!BLOCK) {
+    unsigned top = 0;
+#pragma unroll
+    for (int u = 0; u < N; ++u) top = max(top, largest(held[u]));
+    for (int i0 = N * threads; i0 < per; i0 += N * threads) {
+      Hidden v[N];
+      load(i0, v);
+#pragma unroll
+      for (int u = 0; u < N; ++u) top = max(top, largest(v[u]));
+    }
+    top = wave_umax(top);
+    if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+    __syncthreads();
+    for (int w = 0; w < threads / 64; ++w) top = max(top, tops[w]);
+    s = act_scale<INT8>(__uint_as_float(top));
+    if (threadIdx.x == 0) a.hs[entry] = s;
+  }
+  for (int i0 = 0; i0 < per; i0 += N * threads) {
+    if (i0) load(i0, held);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int i = i0 + (int)threadIdx.x + u * threads;
+      if (i >= per) continue;
+      if constexpr (BLOCK) {  // 16 lanes hold a group
+        s = act_scale<false>(__uint_as_float(seg16_umax(largest(held[u]))));
+        if ((i & 15) == 0) a.hs[(long long)entry * (a.I / kGroup) + i / 16] = s;
+      }
+      if (8 * i < a.I)
+        *reinterpret_cast<v2u*>(q + 8 * i) = encode_values<INT8>(held[u].f, s, act_recip(s));
+    }
   }
 }
 
@@ -823,10 +920,16 @@ hipError_t launch_down(const MoeLayerArgs& a, hipStream_t s) {
     return launch_kernel(moe_down_few_kernel<FMT, PACKED>, dim3((unsigned)(a.D / 16)),
                          dim3((unsigned)(64 * waves)), waves * row, s, a);
   }
-  const int tiles = (a.D + kColumns - 1) / kColumns;
-  return launch_kernel(moe_down_kernel<FMT, PACKED, MB>,
-                       dim3((unsigned)tiles, (unsigned)a.slots, (unsigned)a.splits),
-                       dim3(kThreads), a.T * row, s, a);
+  const dim3 grid((unsigned)((a.D + kColumns - 1) / kColumns), (unsigned)a.slots,
+                  (unsigned)a.splits);
+  if (!a.hq)
+    return launch_kernel(moe_down_kernel<FMT, PACKED, MB, false>, grid, dim3(kThreads), a.T * row,
+                         s, a);
+  const int pieces = (a.I + 7) / 8, threads = min((pieces + 63) / 64 * 64, kEncodeThreads);
+  const hipError_t e = launch_kernel(moe_encode_kernel<FMT>, dim3((unsigned)(a.T * a.topk)),
+                                     dim3((unsigned)threads), 0, s, a);
+  if (e != hipSuccess) return e;
+  return launch_kernel(moe_down_kernel<FMT, PACKED, MB, true>, grid, dim3(kThreads), 0, s, a);
 }
 template <int FMT, int MB>
 hipError_t launch_layer(bool packed1, bool packed2, const MoeLayerArgs& a, hipStream_t s) {

@@ -75,8 +75,16 @@ size_t route_bytes(const RouteArgs& a) {
 // The layer's workspace (byte offsets): the counter region that every
 // operation keeps, then its arrays.
 struct LayerWs {
-  size_t h, part, total;
+  size_t h, hq, hs, part, total;
 };
+// Whether a launch of its own makes the codes of the hidden values, which otherwise
+// every column tile makes again for its expert's tokens: by the values that a tile
+// has to make, if the entries spread over the experts (32 tokens, 2 of 8 experts of
+// 4096 x 14336, 114688 values: 273 us, 349 by the tiles; 4 of 16 of 4096 x 2048, 16384:
+// 87 and 103; 2 of 16 of 2048 x 1024, 4096: 30.3 and 30.1; 16 tokens, 2 of 16 of 2048 x
+// 2048, 4096: 41.6 and 40.7).
+bool codes_apart(int n, int slots, int I) { return (long long)n * I >= 12288LL * slots; }
+
 // Parts of I that workgroups of the layer's second kernel share where its columns
 // and experts leave compute units without two of them (32 tokens, 2 of 8 experts of
 // 1024 x 2048: whole 37.2 us, in two 32.0; 12 tokens, 4 of 16 of 256 x 4096 33.8, in
@@ -88,11 +96,15 @@ int layer_splits(int slots, int D, int I) {
   while (splits < 4 && (long long)tiles * slots * 2 * splits <= 512 && I >= 2048 * splits) splits *= 2;
   return splits;
 }
+// Bytes of an entry's codes: whole lines.
+size_t coded_stride(int I) { return round256(I); }
 LayerWs layer_ws(int T, int topk, int D, int I) {
   const size_t n = (size_t)T * topk;
   LayerWs w;
   w.h = ws_counter_bytes(0);
-  w.part = w.h + round256(n * I * 4);
+  w.hq = w.h + round256(n * I * 4);
+  w.hs = w.hq + n * coded_stride(I);
+  w.part = w.hs + round256(n * ceil_div(I, W8_GROUP) * 4);
   // (as many splits as one expert would take: E is not known here)
   w.total = w.part + round256(n * D * 4 * layer_splits(1, D, I));
   return w;
@@ -314,6 +326,11 @@ w8_status w8_moe_layer(w8_fmt fmt_in, int E, int T, int topk, int D, int I, cons
   a.slots = std::min(E, T * topk);
   a.parts = layer_parts(T, topk, I);
   a.splits = a.parts ? 1 : layer_splits(a.slots, D, I);
+  if (!a.parts && codes_apart(T * topk, a.slots, I)) {
+    a.hq = reinterpret_cast<uint8_t*>(p + w.hq);
+    a.hs = reinterpret_cast<float*>(p + w.hs);
+    a.ldh = (long long)coded_stride(I);
+  }
   const int each = a.parts ? a.parts : a.splits;
   a.chunk = layer_chunk(a.parts ? T * topk * a.parts : T,
                         each > 1 ? (I + each - 1) / each + W8_GROUP : I);

@@ -71,6 +71,9 @@ struct MoeLayerArgs {
   const uint16_t* base; // bf16 [T, D], or null
   uint16_t* y;          // bf16 [T, D]
   float* h;             // [T * topk, I] gated products (workspace)
+  uint8_t* hq;          // codes of h [T * topk, I], row stride ldh bytes, or null: made where used
+  float* hs;            // and their scales [T * topk] (Block_FP8: [T * topk, I / 128])
+  long long ldh;
   float* part;          // [splits, T * topk, D] the experts' outputs
   unsigned* counters;   // arrival counters
   long long ldq, ldw1, ldw2, ldb, ldy;  // bytes; base, y: elements
@@ -83,7 +86,7 @@ struct MoeLayerArgs {
   int splits;           // parts of I that workgroups of the second kernel share
   int chunk;            // of I that a workgroup of the second kernel (parts: a wave) keeps as codes
 };
-// Two launches.  packed1, packed2: the layouts of w1 and w2.
+// Two launches, or three with hq.  packed1, packed2: the layouts of w1 and w2.
 hipError_t launch_moe_layer(int fmt, bool packed1, bool packed2, const MoeLayerArgs& a,
                             hipStream_t s);
 

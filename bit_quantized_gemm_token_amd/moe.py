@@ -1,7 +1,7 @@
 """The MoE layer around the grouped products (the C-ABI's w8_moe_route,
 w8_moe_combine and w8_moe_layer): the routing that makes the lists which
 moe_gemm, moe_linear and grouped_gemm take, the weighted sum of their outputs,
-and for a few tokens the experts as a whole in two launches.  Like the rest of
+and for a few tokens the experts as a whole in two launches or three.  Like the rest of
 the package this module only checks and marshals arguments.
 """
 import ctypes
@@ -165,7 +165,7 @@ def moe_layer(fmt, xq, sx, experts, weights, w1, s1, w2, s2, base=None, y=None, 
     (Block_FP8: of 128) up to 65536, E at most 1024, topk at most 32.  base:
     bf16 [T, D] (a shared expert's output, a residual) or None; y may be base.
 
-    Two launches, no lists, no host sync; the hidden values stay fp32 until
+    Two launches (three where many tokens share an expert), no lists, no host sync; the hidden values stay fp32 until
     they are quantized and the sum is fp32 in the order of the choices, so
     results are the same every time.  workspace: as for block_gemm,
     moe_layer_workspace_size bytes.

@@ -8,7 +8,7 @@ residual stream back to it, on the library's operators:
   moe_route        each token's experts and weights, and the experts' lists
   grouped_gemm     the routed experts' projections over ragged lists of rows
   moe_combine      each token's weighted sum of its experts' outputs
-  moe_layer        the last three steps as two launches, for up to 32 tokens
+  moe_layer        the last three steps in one call, for up to 32 tokens
 
     python examples/block_fp8_layer.py [--tokens 1,48,1024] [--hidden 2048] ...
 

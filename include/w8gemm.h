@@ -791,7 +791,7 @@ w8_status w8_moe_combine(int T, int topk, int D, const void *y, int64_t ldy, int
                          int64_t ldb, void *out, int64_t ldo, w8_stream stream);
 
 /* The experts of T tokens as a whole, T <= 32 (above: W8_E_UNSUPPORTED, use the
- * grouped products), in any of the three formats, in two launches:
+ * grouped products), in any of the three formats, in two or three launches:
  *   a    = dequant(xq[t]) . dequant(W1_e)^T        [2 I]: gate, then up
  *   v    = silu(a[:I]) * a[I:], fp32, quantized as w8_quantize_act does (one
  *          scale for the row, Block_FP8 one per 128 columns)

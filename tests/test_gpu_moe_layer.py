@@ -129,7 +129,9 @@ SIZES = [  # T, E, topk, D, I (Block_FP8: rounded up to whole 128s)
     (1, 5, 5, 80, 50000), (4, 2, 2, 272, 2064), (8, 3, 1, 64, 128), (2, 4, 4, 144, 4208),
     # the second projection in parts, the first by whole waves
     (1, 8, 8, 144, 3360), (6, 4, 2, 80, 4112), (5, 3, 3, 64, 2064), (32, 2, 1, 64, 8208),
-    (8, 60, 6, 128, 512), (20, 64, 8, 144, 336), (3, 2, 2, 64, 9008)]
+    (8, 60, 6, 128, 512), (20, 64, 8, 144, 336), (3, 2, 2, 64, 9008),
+    # the hidden codes by a launch of their own; by the tiles, in chunks
+    (32, 2, 2, 64, 400), (20, 2, 1, 80, 2064), (6, 1, 1, 64, 2064), (32, 40, 1, 64, 3968)]
 
 
 def sized(fmt, D, I):
@@ -177,13 +179,19 @@ def test_choices_left_out_and_repeated(w8, fmt):
     assert (y == 0).all()
     c = Layer(fmt, 32, E, 1, 256, 128, experts=np.full((32, 1), 4))
     c.check(w8.moe_layer(*c.args(w8)))
+    # with the hidden codes made once
+    experts = [[0, 3, 0], [-1, -1, -1], [2, 2, 2], [-1, 4, -7], [6, 1, 1 << 30], [5, 0, 5]] * 5
+    c = Layer(fmt, 30, E, 3, 128, 1152, experts=experts)
+    c.check(w8.moe_layer(*c.args(w8)))
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("E,I,experts", [
     (4, 128, [[2, 2]]), (8, 128, [[3, 1, 3, -1, 1]]), (64, 256, [[7, 9, 7], [9, 7, 9]]),
     (3, 4224, [[1, 0, 1]]), (50, 128, [[5, 5, 5, 5], [5, 6, 5, 6], [9, 9, 50, 9]]),
-    (64, 128, [[8, 8, 3, 3], [3, 8, 8, 3], [1, 2, 2, 1], [2, 2, 2, 2], [0, 0, 1, 0]])])
+    (64, 128, [[8, 8, 3, 3], [3, 8, 8, 3], [1, 2, 2, 1], [2, 2, 2, 2], [0, 0, 1, 0]]),
+    (4, 1664, [[1, 1, 0], [2, 0, 2], [0, 0, 0], [3, 1, 3], [1, 0, 1], [2, 2, 2], [0, 1, -1],
+               [9, 1, 1], [1, 0, 2], [3, 2, 3]])])
 def test_an_expert_twice_among_few(w8, fmt, E, I, experts):
     """In a workspace of NaN, so that what no kernel has written shows."""
     c = Layer(fmt, len(experts), E, len(experts[0]), 256, I, experts=experts)
@@ -302,7 +310,8 @@ def test_workspace_shared_with_the_other_operators(w8, fmt):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T,E,topk,D,I", [(8, 16, 4, 512, 256), (6, 4, 2, 128, 4224),
-                                          (2, 16, 4, 256, 384)])
+                                          (2, 16, 4, 256, 384), (24, 16, 2, 128, 4096),
+                                          (24, 4, 2, 128, 1152)])
 def test_capture_streams_and_overlap(w8, fmt, T, E, topk, D, I):
     c = Layer(fmt, T, E, topk, D, I)
     a = c.args(w8)
