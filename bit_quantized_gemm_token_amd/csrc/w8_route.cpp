@@ -80,16 +80,16 @@ struct LayerWs {
 // Whether a launch of its own makes the codes of the hidden values, which otherwise
 // every column tile makes again for its expert's tokens: by the values that a tile
 // has to make, if the entries spread over the experts (32 tokens, 2 of 8 experts of
-// 4096 x 14336, 114688 values: 273 us, 349 by the tiles; 4 of 16 of 4096 x 2048, 16384:
+// 4096 x 14336, 114688 values: 270 us, 349 by the tiles; 4 of 16 of 4096 x 2048, 16384:
 // 87 and 103; 2 of 16 of 2048 x 1024, 4096: 30.3 and 30.1; 16 tokens, 2 of 16 of 2048 x
 // 2048, 4096: 41.6 and 40.7).
 bool codes_apart(int n, int slots, int I) { return (long long)n * I >= 12288LL * slots; }
 
 // Parts of I that workgroups of the layer's second kernel share where its columns
 // and experts leave compute units without two of them (32 tokens, 2 of 8 experts of
-// 1024 x 2048: whole 37.2 us, in two 32.0; 12 tokens, 4 of 16 of 256 x 4096 33.8, in
-// two 28.6, in four 26.6; 8 tokens, 2 of 16 of 1024 x 1024 15.1 and 15.6, which is why
-// a part has 1024 columns at least).
+// 1024 x 2048: in two 23.4 us, whole 27.3; 12 tokens, 4 of 16 of 256 x 4096, in four
+// 21.0 and 28.6; 16 tokens, 2 of 60 of 384 x 4096, in two 37.7 and 42.9; 8 tokens, 2 of
+// 16 of 1024 x 1024 15.6 and 15.1, which is why a part has 1024 columns at least).
 int layer_splits(int slots, int D, int I) {
   const int tiles = (int)ceil_div(D, 64);
   int splits = 1;
