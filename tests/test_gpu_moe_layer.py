@@ -138,6 +138,14 @@ def sized(fmt, D, I):
     return (D, I) if fmt != "Block_FP8" else (groups(D) * GROUP, groups(I) * GROUP)
 
 
+def workspace_of_nan(w8, c):
+    """NaN behind the counters (the smallest layer's are followed by four arrays of
+    256 bytes), so that what is read without having been written shows."""
+    ws = w8.Workspace(DEV, w8.moe_layer_workspace_size(c.T, c.topk, c.D, c.I))
+    ws.buf[w8.moe_layer_workspace_size(1, 1, 16, 16) - 4 * 256:].fill_(255)
+    return ws
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T,E,topk,D,I", SIZES)
 def test_layer(w8, fmt, T, E, topk, D, I):
@@ -150,8 +158,10 @@ def test_layer(w8, fmt, T, E, topk, D, I):
     c.check(y)
     assert (buf[:, 0] == 7).all() and (buf[:, 1 + c.D:] == 7).all()
     assert (buf[0] == 7).all() and (buf[T + 1] == 7).all()
+    ws = workspace_of_nan(w8, c)
     for _ in range(2):
         assert torch.equal(w8.moe_layer(*args), y)
+        assert torch.equal(w8.moe_layer(*args, workspace=ws), y)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -182,7 +192,7 @@ def test_choices_left_out_and_repeated(w8, fmt):
     # with the hidden codes made once
     experts = [[0, 3, 0], [-1, -1, -1], [2, 2, 2], [-1, 4, -7], [6, 1, 1 << 30], [5, 0, 5]] * 5
     c = Layer(fmt, 30, E, 3, 128, 1152, experts=experts)
-    c.check(w8.moe_layer(*c.args(w8)))
+    c.check(w8.moe_layer(*c.args(w8), workspace=workspace_of_nan(w8, c)))
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -193,14 +203,8 @@ def test_choices_left_out_and_repeated(w8, fmt):
     (4, 1664, [[1, 1, 0], [2, 0, 2], [0, 0, 0], [3, 1, 3], [1, 0, 1], [2, 2, 2], [0, 1, -1],
                [9, 1, 1], [1, 0, 2], [3, 2, 3]])])
 def test_an_expert_twice_among_few(w8, fmt, E, I, experts):
-    """In a workspace of NaN, so that what no kernel has written shows."""
     c = Layer(fmt, len(experts), E, len(experts[0]), 256, I, experts=experts)
-    size = w8.moe_layer_workspace_size(c.T, c.topk, c.D, c.I)
-    ws = w8.Workspace(DEV, size)
-    arrays = c.T * c.topk * 4 * (c.I + c.D)  # (behind the counters)
-    assert arrays % 256 == 0
-    ws.buf[size - arrays:size].fill_(255)
-    c.check(w8.moe_layer(*c.args(w8), workspace=ws))
+    c.check(w8.moe_layer(*c.args(w8), workspace=workspace_of_nan(w8, c)))
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
