@@ -265,14 +265,14 @@ constexpr int kUpPieces = 2;
 template <int MB, int KW>
 struct UpLds {
   Choices c;
-  v4i part[KW > 1 ? KW - 1 : 1][KW > 1 ? MB : 1][2][64];
+  v4i part[KW > 1 ? (KW - 1) * MB * 2 : 1][64];
 };
 
 // MB blocks of 16 tokens from the expert's t0-th on; KW waves share a block of
 // columns, wave kw a part of its K.
 template <int FMT, bool PACKED, int MB, int KW>
 __device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Expert& x, int t0,
-                                        UpLds<MB, KW>& lds) {
+                                        const Choices& c, v4i (*part)[64]) {
   typedef typename Traits<FMT>::Frag Frag;
   typedef typename Traits<FMT>::Acc Acc;
   constexpr int KSTEP = Traits<FMT>::KSTEP;
@@ -290,7 +290,7 @@ __device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Exp
   int entry[MB];
 #pragma unroll
   for (int b = 0; b < MB; ++b) {
-    entry[b] = lds.c.entry[wave][min(t0 + 16 * b + r, x.tokens - 1)];
+    entry[b] = c.entry[wave][min(t0 + 16 * b + r, x.tokens - 1)];
     const int t = entry[b] / a.topk;
     xp[b] = a.xq + t * a.ldq + 16 * g;
     sxp[b] = a.sx + (BLOCK ? (long long)t * G : t);
@@ -341,7 +341,7 @@ __device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Exp
       for (int b = 0; b < MB; ++b)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          lds.part[kw - 1][b][j][lane] = __builtin_bit_cast(v4i, acc[b][j]);
+          part[((kw - 1) * MB + b) * 2 + j][lane] = __builtin_bit_cast(v4i, acc[b][j]);
     }
     __syncthreads();
   }
@@ -352,7 +352,7 @@ __device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Exp
       for (int b = 0; b < MB; ++b)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          acc[b][j] += __builtin_bit_cast(Acc, lds.part[w][b][j][lane]);
+          acc[b][j] += __builtin_bit_cast(Acc, part[(w * MB + b) * 2 + j][lane]);
     // lane (r, g): token r of block b, columns n0 + 4 g .. + 3
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
@@ -382,7 +382,10 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeLayerArgs a) {
   if (n0 >= a.I) return;  // (a wave by itself, KW == 1)
   for (int t0 = 0; t0 < x.tokens; t0 += 16 * MB) {
     if (KW > 1 && t0) __syncthreads();  // (the sums have been read)
-    up_tile<FMT, PACKED, MB, KW>(a, n0, x, t0, lds);
+    if (MB == 1 || x.tokens <= 16)
+      up_tile<FMT, PACKED, 1, KW>(a, n0, x, t0, lds.c, lds.part);
+    else
+      up_tile<FMT, PACKED, MB, KW>(a, n0, x, t0, lds.c, lds.part);
   }
 }
 
@@ -939,8 +942,8 @@ hipError_t launch_layer(bool packed1, bool packed2, const MoeLayerArgs& a, hipSt
 }
 // Experts of more than 16 tokens multiply two blocks of them by one weight (32
 // tokens, 8 of 8 experts of 2048 x 768: 32.9 us, a block at a time 35.8); the
-// registers cost the others a little (32 tokens, 2 of 8 of 4096 x 4096: 103.2 and
-// 101.4), so only calls that can have such experts take it.
+// registers cost the others a little, so only calls that can have such experts take
+// it.
 template <int FMT>
 hipError_t launch_layer(bool packed1, bool packed2, const MoeLayerArgs& a, hipStream_t s) {
   return a.T > 16 ? launch_layer<FMT, 2>(packed1, packed2, a, s)
