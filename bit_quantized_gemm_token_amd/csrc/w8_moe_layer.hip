@@ -941,9 +941,9 @@ hipError_t launch_layer(bool packed1, bool packed2, const MoeLayerArgs& a, hipSt
   return packed2 ? launch_down<FMT, true, MB>(a, s) : launch_down<FMT, false, MB>(a, s);
 }
 // Experts of more than 16 tokens multiply two blocks of them by one weight (32
-// tokens, 8 of 8 experts of 2048 x 768: 32.9 us, a block at a time 35.8); the
-// registers cost the others a little, so only calls that can have such experts take
-// it.
+// tokens, 8 of 8 experts of 2048 x 4096: 72 us, a block at a time in the first kernel
+// alone 80); calls without such experts are as fast either way (32 tokens, 2 of 8 of
+// 4096 x 4096: 90.9), and calls that cannot have any need no registers for them.
 template <int FMT>
 hipError_t launch_layer(bool packed1, bool packed2, const MoeLayerArgs& a, hipStream_t s) {
   return a.T > 16 ? launch_layer<FMT, 2>(packed1, packed2, a, s)
