@@ -17,8 +17,8 @@
 // Measured with 128 experts, top 8, of 2048 x 768 (the weights of the experts
 // that are chosen, and their rate): 1 token 14.6 us (38 MB: up 8.0, down 6.6, two
 // chains of choices, weights and sums that few workgroups run once); 8 tokens 57
-// us (240 MB; up 34, 4.7 TB/s, down 22, 3.6); 32 tokens 110 us (530 MB; up 67, 5.3
-// TB/s, down 43, 4.1), by the weights' bytes.  Of down's time 3.5 to 5 us are the
+// us (240 MB; up 34, 4.7 TB/s, down 22, 3.6); 32 tokens 99 us (530 MB; up 61, 5.8
+// TB/s, down 41, 4.3), by the weights' bytes.  Of down's time 3.5 to 5 us are the
 // hand-off of the outputs to the workgroup that sums them, about what a launch of
 // its own would take for that.
 #include "w8_block.hpp"
