@@ -86,6 +86,14 @@ def moe_route(logits, topk, renormalize=True, scale=1.0, lists=True, workspace=N
     return (experts, weights, offsets, rows, slots) if lists else (experts, weights)
 
 
+def _weights_of(weights, T, topk):
+    """Pointer of the choices' weights: contiguous fp32 [T, topk].  (As many elements
+    in another order, [topk, T] say, are other weights.)"""
+    p = _flat(weights, "weights", _F32, T * topk)
+    _shape(weights, T, topk, "weights")
+    return p
+
+
 def moe_combine(y, weights, slots, base=None, out=None, stream=None):
     """Each token's sum of its experts' outputs, bf16 [T, D]:
 
@@ -102,7 +110,7 @@ def moe_combine(y, weights, slots, base=None, out=None, stream=None):
         raise ValueError("slots must be an int32 [T, topk] tensor")
     T, topk = slots.shape
     sp = _flat(slots, "slots", _I32, T * topk)
-    wp = _flat(weights, "weights", _F32, T * topk)
+    wp = _weights_of(weights, T, topk)
     bp, ldb = None, 0
     if base is not None:
         bp, ldb = _rows(base, "base", _BF16)
@@ -178,7 +186,7 @@ def moe_layer(fmt, xq, sx, experts, weights, w1, s1, w2, s2, base=None, y=None, 
         raise ValueError(f"experts must be an int32 [{T}, topk] tensor")
     topk = experts.shape[1]
     ep = _flat(experts, "experts", _I32, T * topk)
-    wp = _flat(weights, "weights", _F32, T * topk)
+    wp = _weights_of(weights, T, topk)
     E, N1, K1, w1p, ldw1, w1s, s1p, s1s, w1t = _layer_weights(f, w1, s1, "w1")
     E2, N2, I, w2p, ldw2, w2s, s2p, s2s, w2t = _layer_weights(f, w2, s2, "w2")
     if E2 != E or N1 != 2 * I or K1 != D or N2 != D:
