@@ -129,6 +129,18 @@ def moe_combine(y, weights, slots, base=None, out=None, stream=None):
     return out
 
 
+def _scales(s, name, shape):
+    """Pointer of contiguous fp32 scales: of that shape, or in another number of
+    dimensions."""
+    n = 1
+    for size in shape:
+        n *= size
+    p = _flat(s, name, _F32, n)
+    if s.dim() == len(shape) and s.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {tuple(s.shape)}")
+    return p
+
+
 def moe_layer_workspace_size(T, topk, D, I):
     """Bytes of workspace moe_layer needs."""
     n = ctypes.c_size_t(0)
@@ -152,8 +164,9 @@ def _layer_weights(f, w, s, name):
         E, N, K = w.shape
         stride, ld, _ = w.stride()
         ldw, t = _weight_stride(ld, N, K), w
-    per = N if f != _BLOCK else -(-N // _GROUP) * -(-K // _GROUP)
-    return E, N, K, t.data_ptr(), ldw, stride, _flat(s, "the scales of " + name, _F32, E * per), per, t
+    per = (N,) if f != _BLOCK else (-(-N // _GROUP), -(-K // _GROUP))
+    sp = _scales(s, "the scales of " + name, (E, *per))
+    return E, N, K, t.data_ptr(), ldw, stride, sp, per[0] * per[-1] if f == _BLOCK else N, t
 
 
 def moe_layer(fmt, xq, sx, experts, weights, w1, s1, w2, s2, base=None, y=None, workspace=None,
@@ -181,7 +194,7 @@ def moe_layer(fmt, xq, sx, experts, weights, w1, s1, w2, s2, base=None, y=None, 
     f = _fmt(fmt)
     xp, ldq = _codes(xq, "xq")
     T, D = xq.shape
-    sxp = _flat(sx, "sx", _F32, T * -(-D // _GROUP) if f == _BLOCK else T)
+    sxp = _scales(sx, "sx", (T, -(-D // _GROUP)) if f == _BLOCK else (T,))
     if not isinstance(experts, torch.Tensor) or experts.dim() != 2 or experts.shape[0] != T:
         raise ValueError(f"experts must be an int32 [{T}, topk] tensor")
     topk = experts.shape[1]

@@ -36,3 +36,22 @@ def test_weights_of_the_choices_in_another_order(w8, fake, shape):
         w8.moe_layer("W8A8_INT8", fake(T, D), fake(T, dtype=F32), choices, weights,
                      fake(E, 2 * I, D), fake(E, 2 * I, dtype=F32), fake(E, D, I),
                      fake(E, D, dtype=F32))
+
+
+def test_scales_of_blocks_in_another_order(w8, fake, monkeypatch):
+    """Block_FP8's scales as they lie behind a transposed or permuted tensor: as many
+    elements, of other blocks.  Flat ones are taken as they lie."""
+    G, H = D // 128, I // 128
+    a = dict(xq=fake(T, D), sx=fake(T, G, dtype=F32), experts=fake(T, K, dtype=I32),
+             weights=fake(T, K, dtype=F32), w1=fake(E, 2 * I, D), s1=fake(E, 2 * H, G, dtype=F32),
+             w2=fake(E, D, I), s2=fake(E, G, H, dtype=F32))
+    for name, what, shape in (("sx", "sx", (G, T)), ("s1", "scales of w1", (E, G, 2 * H)),
+                              ("s1", "scales of w1", (2 * H, E, G)), ("s2", "scales of w2", (E, H, G))):
+        with pytest.raises(ValueError, match=what + " must be"):
+            w8.moe_layer("Block_FP8", **{**a, name: fake(*shape, dtype=F32)})
+    monkeypatch.setattr(w8.moe, "_current_device", lambda: 0)
+    # (past these checks: pointers without memory are what the library refuses)
+    for s in ({}, dict(sx=fake(T * G, dtype=F32), s1=fake(E * 2 * H * G, dtype=F32))):
+        with pytest.raises(w8.W8Error, match="null device pointer"):
+            w8.moe_layer("Block_FP8", **{**a, **s}, y=fake(T, D, dtype=BF16),
+                         workspace=w8.Workspace("cuda:0"), stream=0)
