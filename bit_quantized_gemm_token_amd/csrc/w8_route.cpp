@@ -139,7 +139,8 @@ w8_status check_experts(int fmt, int E, int N, int K, const void* w, int64_t ldw
     return fail(W8_E_INVALID, "ldw must be >= K and a multiple of 16 (row-major) or 0 (packed)");
   const int64_t one = ldw == 0 ? (int64_t)packed_weight_bytes(fmt, N, K, 1)
                                : (int64_t)(N - 1) * ldw + K;
-  if (w_stride % 16 || (E > 1 && w_stride < one))
+  // (of a single expert the strides are never used, and torch lets them be anything)
+  if (E > 1 && (w_stride % 16 || w_stride < one))
     return fail(W8_E_INVALID, "the experts' stride must be a multiple of 16 that holds one's codes");
   const int64_t scales = fmt == W8_BLOCK_FP8 ? (int64_t)(N / W8_GROUP) * (K / W8_GROUP) : N;
   if (E > 1 && s_stride < scales)

@@ -55,3 +55,21 @@ def test_scales_of_blocks_in_another_order(w8, fake, monkeypatch):
         with pytest.raises(w8.W8Error, match="null device pointer"):
             w8.moe_layer("Block_FP8", **{**a, **s}, y=fake(T, D, dtype=BF16),
                          workspace=w8.Workspace("cuda:0"), stream=0)
+
+
+def test_a_single_expert_may_have_any_stride(w8):
+    """No address holds it.  (The call ends at the workspace that it does not have.)"""
+    p = 0x1000
+
+    def status(E, **kw):
+        a = dict(fmt=1, E=E, T=T, topk=1, D=D, I=I, xq=p, ldq=D, sx=p, experts=p, weights=p, w1=p,
+                 ldw1=D, w1_stride=2 * I * D, s1=p, s1_stride=2 * I, w2=p, ldw2=I, w2_stride=D * I,
+                 s2=p, s2_stride=D, base=None, ldb=0, y=p, ldy=D, ws=None, ws_bytes=0, stream=None)
+        assert set(kw) <= set(a)
+        return w8._lib.w8_moe_layer(*{**a, **kw}.values())
+
+    invalid, workspace = 1, 3
+    for kw in (dict(w1_stride=1), dict(w2_stride=0), dict(w1_stride=-7, s1_stride=0),
+               dict(w2_stride=8, s2_stride=1), dict(ldw1=0, w1_stride=1)):
+        assert status(1, **kw) == workspace
+        assert status(2, **kw) == invalid
