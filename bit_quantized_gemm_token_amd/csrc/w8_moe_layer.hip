@@ -268,10 +268,10 @@ struct UpLds {
   v4i part[KW > 1 ? (KW - 1) * MB * 2 : 1][64];
 };
 
-// MB blocks of 16 tokens from the expert's t0-th on; KW waves share a block of
+// MB blocks of 16 tokens, all that the expert has; KW waves share a block of
 // columns, wave kw a part of its K.
 template <int FMT, bool PACKED, int MB, int KW>
-__device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Expert& x, int t0,
+__device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Expert& x,
                                         const Choices& c, v4i (*part)[64]) {
   typedef typename Traits<FMT>::Frag Frag;
   typedef typename Traits<FMT>::Acc Acc;
@@ -290,7 +290,7 @@ __device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Exp
   int entry[MB];
 #pragma unroll
   for (int b = 0; b < MB; ++b) {
-    entry[b] = c.entry[wave][min(t0 + 16 * b + r, x.tokens - 1)];
+    entry[b] = c.entry[wave][min(16 * b + r, x.tokens - 1)];
     const int t = entry[b] / a.topk;
     xp[b] = a.xq + t * a.ldq + 16 * g;
     sxp[b] = a.sx + (BLOCK ? (long long)t * G : t);
@@ -366,7 +366,7 @@ __device__ __forceinline__ void up_tile(const MoeLayerArgs& a, int n0, const Exp
         }
         h[i] = silu(gate) * up;
       }
-      if (t0 + 16 * b + r < x.tokens)
+      if (16 * b + r < x.tokens)
         *reinterpret_cast<v4f*>(a.h + (long long)entry[b] * a.I + n0 + 4 * g) = h;
     }
   }
@@ -380,13 +380,10 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeLayerArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = KW > 1 ? blockIdx.x * 16 : (blockIdx.x * kWaves + wave) * 16;
   if (n0 >= a.I) return;  // (a wave by itself, KW == 1)
-  for (int t0 = 0; t0 < x.tokens; t0 += 16 * MB) {
-    if (KW > 1 && t0) __syncthreads();  // (the sums have been read)
-    if (MB == 1 || x.tokens <= 16)
-      up_tile<FMT, PACKED, 1, KW>(a, n0, x, t0, lds.c, lds.part);
-    else
-      up_tile<FMT, PACKED, MB, KW>(a, n0, x, t0, lds.c, lds.part);
-  }
+  if (MB == 1 || x.tokens <= 16)
+    up_tile<FMT, PACKED, 1, KW>(a, n0, x, lds.c, lds.part);
+  else
+    up_tile<FMT, PACKED, MB, KW>(a, n0, x, lds.c, lds.part);
 }
 
 // -------------------------------------------------------------------- down --
@@ -946,6 +943,7 @@ hipError_t launch_layer(bool packed1, bool packed2, const MoeLayerArgs& a, hipSt
 // 4096 x 4096: 90.9), and calls that cannot have any need no registers for them.
 template <int FMT>
 hipError_t launch_layer(bool packed1, bool packed2, const MoeLayerArgs& a, hipStream_t s) {
+  static_assert(kLayerTokens <= 32, "both kernels take all of an expert's tokens in two blocks");
   return a.T > 16 ? launch_layer<FMT, 2>(packed1, packed2, a, s)
                   : launch_layer<FMT, 1>(packed1, packed2, a, s);
 }
