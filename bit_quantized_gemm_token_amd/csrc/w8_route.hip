@@ -229,10 +229,12 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs a) {
         __builtin_amdgcn_mbcnt_hi((unsigned)(same >> 32),
                                   __builtin_amdgcn_mbcnt_lo((unsigned)same, 0u));
     for (int w = 0; w < n; w += 64) {
-      if ((int)threadIdx.x >> 6 == w >> 6 && id >= 0) {
-        rank = count[id] + before;
-        if (before == 0) count[id] = rank + __popcll(same);
-      }
+      // (the wave's lanes read a count before one of them adds to it: the fence keeps
+      // the compiler from moving the write up)
+      const bool turn = (int)threadIdx.x >> 6 == w >> 6 && id >= 0;
+      if (turn) rank = count[id] + before;
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      if (turn && before == 0) count[id] = rank + __popcll(same);
       __syncthreads();
     }
     if (a.blocks > 1) {

@@ -9,6 +9,9 @@
 // between two barriers one wavefront runs as far ahead of the others as the
 // program lets it, which is the order that shows a missing barrier.
 //
+// A launch through hipLaunchKernel is taken and does nothing, unless the program
+// has set a thunk that calls its kernels: then every workgroup of the grid runs.
+//
 // Direct-to-LDS loads (w8_lds.hpp beside this file) are checked against the
 // buffers the program registered, and land either at once or only when a wait
 // asks for them: the two ends of what the memory may do.
@@ -43,14 +46,15 @@ struct dim3 {
   unsigned x, y, z;
   dim3(unsigned x = 1, unsigned y = 1, unsigned z = 1) : x(x), y(y), z(z) {}
 };
-// (a launch through the library's own launchers is taken and does nothing)
+hipError_t emu_launch(const void* kernel, dim3 grid, dim3 block, void** args, size_t lds);
 inline hipError_t hipGetDevice(int* device) {
   *device = 0;
   return hipSuccess;
 }
 inline hipError_t hipFuncSetAttribute(const void*, int, int) { return hipSuccess; }
-inline hipError_t hipLaunchKernel(const void*, dim3, dim3, void**, size_t, hipStream_t) {
-  return hipSuccess;
+inline hipError_t hipLaunchKernel(const void* kernel, dim3 grid, dim3 block, void** args,
+                                  size_t lds, hipStream_t) {
+  return emu_launch(kernel, grid, block, args, lds);
 }
 
 namespace emu {
@@ -62,6 +66,7 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 struct Options {
   bool descending = false;  // wavefronts are tried from the last to the first
   bool late = false;        // direct-to-LDS loads land only when waited for
+  bool partial = false;     // DPP moves and ballots may have some lanes only
 };
 
 struct Range {
@@ -90,6 +95,9 @@ struct Machine {
   ucontext_t home;
   int current = -1;
   unsigned block = 0, grid = 0;
+  dim3 at{0, 0, 0}, grid_size, block_size;  // of a launch by thunk
+  void (*thunk)(const void* kernel, void** args) = nullptr;
+  uint8_t* (*dynamic_lds)(size_t bytes) = nullptr;
   const std::function<void()>* body = nullptr;
   uint8_t* lds = nullptr;
   size_t lds_bytes = 0;
@@ -148,8 +156,10 @@ inline void barrier() {
 
 // One operation of a whole wavefront: every lane puts its words in, the last
 // to arrive has them combined, every lane takes its result.
-enum Op { kMfma = 1, kMfmaInt8, kReadlane, kBallot, kDpp };
-void combine(Machine::Wave& in, Machine::Wave& out);
+// With Options::partial the lanes of a DPP move or a ballot may be some of the
+// wavefront's: the others are at a barrier, at a later operation or have ended.
+enum Op { kMfma = 1, kMfmaInt8, kReadlane, kBallot, kDpp, kSync };
+void combine(Machine::Wave& in, Machine::Wave& out, unsigned long long lanes);
 inline unsigned* wave_op(int op, const void* words, size_t bytes) {
   Machine& g = m();
   const int w = g.current / 64, l = g.current % 64;
@@ -174,10 +184,13 @@ inline float e4m3(uint8_t c) {
   return table[c];
 }
 
-inline void combine(Machine::Wave& in, Machine::Wave& out) {
+inline void combine(Machine::Wave& in, Machine::Wave& out, unsigned long long lanes) {
+  const int op = in.op[__builtin_ctzll(lanes)];
   for (int l = 1; l < 64; ++l)
-    if (in.op[l] != in.op[0]) return halt("lanes of one wavefront at different operations");
-  if (in.op[0] == kMfma) {
+    if (lanes >> l & 1 && in.op[l] != op)
+      return halt("lanes of one wavefront at different operations");
+  if (op == kSync) {
+  } else if (op == kMfma) {
     // lane l: row (first operand) or column (second) l % 16, one slice of K
     // by l / 16; result: column l % 16, rows 4 (l / 16) .. + 3
     static float a[16][128], b[16][128];
@@ -193,7 +206,7 @@ inline void combine(Machine::Wave& in, Machine::Wave& out) {
         for (int k = 0; k < 128; ++k) s += x[k] * y[k];
         memcpy(&out.w[l][u], &s, 4);
       }
-  } else if (in.op[0] == kMfmaInt8) {  // the same map of lanes, 16 bytes each
+  } else if (op == kMfmaInt8) {  // the same map of lanes, 16 bytes each
     static int a[16][64], b[16][64];
     for (int l = 0; l < 64; ++l)
       for (int i = 0; i < 16; ++i) {
@@ -207,17 +220,25 @@ inline void combine(Machine::Wave& in, Machine::Wave& out) {
         for (int k = 0; k < 64; ++k) s += x[k] * y[k];
         out.w[l][u] = (unsigned)s;
       }
-  } else if (in.op[0] == kReadlane) {
+  } else if (op == kReadlane) {
     for (int l = 0; l < 64; ++l) out.w[l][0] = in.w[in.w[l][1]][0];
-  } else if (in.op[0] == kBallot) {
+  } else if (op == kBallot) {
     unsigned long long v = 0;
-    for (int l = 0; l < 64; ++l) v |= (unsigned long long)(in.w[l][0] != 0) << l;
+    for (int l = 0; l < 64; ++l)
+      if (lanes >> l & 1) v |= (unsigned long long)(in.w[l][0] != 0) << l;
     for (int l = 0; l < 64; ++l) memcpy(out.w[l], &v, 8);
   } else {  // DPP: words old, source, control, row mask
     for (int l = 0; l < 64; ++l) {
+      if (!(lanes >> l & 1)) continue;
       const unsigned ctrl = in.w[l][2];
       int from = -1;
-      if (ctrl > 0x110 && ctrl < 0x120) {  // row_shr
+      if (ctrl < 0x100) {  // quad_perm
+        from = l / 4 * 4 + (ctrl >> 2 * (l % 4) & 3);
+      } else if (ctrl == 0x140) {  // row_mirror
+        from = l ^ 15;
+      } else if (ctrl == 0x141) {  // row_half_mirror
+        from = l ^ 7;
+      } else if (ctrl > 0x110 && ctrl < 0x120) {  // row_shr
         const int n = ctrl - 0x110;
         if (l % 16 >= n) from = l - n;
       } else if (ctrl == 0x142) {  // row_bcast:15
@@ -227,7 +248,7 @@ inline void combine(Machine::Wave& in, Machine::Wave& out) {
       } else {
         return halt("a DPP control that is not known here");
       }
-      const bool on = from >= 0 && (in.w[l][3] >> l / 16 & 1);
+      const bool on = from >= 0 && lanes >> from & 1 && (in.w[l][3] >> l / 16 & 1);
       out.w[l][0] = on ? in.w[from][1] : in.w[l][0];
     }
   }
@@ -283,6 +304,21 @@ inline void rsrc_store(Rsrc r, int off, v4i v) {
     memcpy(r.p + off, &v, 16);
 }
 
+// The lanes of a wavefront that run an operation now, of those that wait at one
+// (0: it cannot be run).
+inline unsigned long long runnable(const Machine::Wave& in, unsigned long long waiting) {
+  bool same = waiting == ~0ull;
+  for (int l = 1; l < 64 && same; ++l) same = in.op[l] == in.op[0];
+  if (same || !m().opt.partial) return waiting == ~0ull ? waiting : 0;
+  for (int op : {kDpp, kBallot}) {
+    unsigned long long lanes = 0;
+    for (int l = 0; l < 64; ++l)
+      if (waiting >> l & 1 && in.op[l] == op) lanes |= 1ull << l;
+    if (lanes) return lanes;
+  }
+  return 0;
+}
+
 inline void entry() {
   (*m().body)();
   m().fibers[m().current].done = true;
@@ -312,27 +348,30 @@ inline void run_block(unsigned block, unsigned grid, int threads,
     f.ctx.uc_link = nullptr;
     makecontext(&f.ctx, entry, 0);
   }
-  memset(g.lds, 0x7F, g.lds_bytes);
+  if (g.lds_bytes) memset(g.lds, 0x7F, g.lds_bytes);
   while (!g.stop) {
     bool ran = false;
     int alive = 0;
     for (int i = 0; i < waves && !ran; ++i) {
       const int w = g.opt.descending ? waves - 1 - i : i;
-      int waiting = 0, live = 0;
+      int live = 0;
+      unsigned long long waiting = 0;
       for (int l = 0; l < 64; ++l) {
         Fiber& f = g.fibers[64 * w + l];
         if (f.done) continue;
         ++live;
-        if (f.at_wave) ++waiting;
+        if (f.at_wave) waiting |= 1ull << l;
         if (f.at_wave || f.at_barrier) continue;
         g.current = 64 * w + l;
         swapcontext(&g.home, &f.ctx);
         ran = true;
       }
       if (!ran && waiting) {
-        if (waiting != 64) return halt("an operation of the whole wavefront with some lanes only");
-        combine(g.in[w], g.out[w]);
-        for (int l = 0; l < 64; ++l) g.fibers[64 * w + l].at_wave = false;
+        const unsigned long long lanes = runnable(g.in[w], waiting);
+        if (!lanes) return halt("an operation of the whole wavefront with some lanes only");
+        combine(g.in[w], g.out[w], lanes);
+        for (int l = 0; l < 64; ++l)
+          if (lanes >> l & 1) g.fibers[64 * w + l].at_wave = false;
         ran = true;
       }
       alive += live;
@@ -348,6 +387,7 @@ inline void run_block(unsigned block, unsigned grid, int threads,
     if (!g.fibers[i].loads.empty()) return fault("a workgroup ends with loads in flight");
 }
 
+// The thread index's, the block's and the grid's words.
 struct ThreadIdx {
   struct X {
     operator unsigned() const { return (unsigned)m().current; }
@@ -357,10 +397,21 @@ struct BlockIdx {
   struct X {
     operator unsigned() const { return m().block; }
   } x;
+  struct Y {
+    operator unsigned() const { return m().at.y; }
+  } y;
+  struct Z {
+    operator unsigned() const { return m().at.z; }
+  } z;
 };
 struct GridDim {
   struct X {
     operator unsigned() const { return m().grid; }
+  } x;
+};
+struct BlockDim {
+  struct X {
+    operator unsigned() const { return m().block_size.x; }
   } x;
 };
 }  // namespace emu
@@ -368,6 +419,30 @@ struct GridDim {
 static emu::ThreadIdx threadIdx;
 static emu::BlockIdx blockIdx;
 static emu::GridDim gridDim;
+static emu::BlockDim blockDim;
+
+// Every workgroup of a launch, from the first to the last or back.
+inline hipError_t emu_launch(const void* kernel, dim3 grid, dim3 block, void** args, size_t lds) {
+  emu::Machine& g = emu::m();
+  if (!g.thunk) return hipSuccess;
+  if (!grid.x || !grid.y || !grid.z || !block.x || block.x % 64 || block.x > 1024 || lds > 65536) {
+    emu::halt("a launch that cannot be");
+    return hipErrorInvalidValue;
+  }
+  g.grid_size = grid;
+  g.block_size = block;
+  g.lds = lds ? g.dynamic_lds(lds) : nullptr;
+  g.lds_bytes = lds;
+  const std::function<void()> body = [&] { g.thunk(kernel, args); };
+  const unsigned long long n = (unsigned long long)grid.x * grid.y * grid.z;
+  for (unsigned long long i = 0; i < n && !g.stop; ++i) {
+    const unsigned long long b = g.opt.descending ? n - 1 - i : i;
+    g.at.y = (unsigned)(b / grid.x % grid.y);
+    g.at.z = (unsigned)(b / grid.x / grid.y);
+    emu::run_block((unsigned)(b % grid.x), grid.x, (int)block.x, body);
+  }
+  return hipSuccess;
+}
 
 inline void __syncthreads() { emu::barrier(); }
 inline unsigned long long __ballot(bool on) { return emu::ballot(on); }
