@@ -21,6 +21,8 @@
 // TB/s, down 41, 4.3), by the weights' bytes.  Of down's time 3.5 to 5 us are the
 // hand-off of the outputs to the workgroup that sums them, about what a launch of
 // its own would take for that.
+#include <type_traits>
+
 #include "w8_block.hpp"
 #include "w8_gemm.hpp"
 #include "w8_route.hpp"
@@ -581,23 +583,33 @@ __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const E
   // The experts' outputs, lane (r, g): token r of block b, columns n + 4 g .. +
   // 3; written through to where the last workgroup reads them, acknowledged
   // before this one counts itself in (the split-K hand-off of the small-M GEMM).
+  // int8's parts of I stay whole numbers, so that their sum is exact, and the
+  // first part's workgroup leaves their scales behind the parts (whoever adds
+  // them would read the experts' scales late).
+  const bool whole = INT8 && a.splits > 1;
   const int n_entries = a.T * a.topk;
-  const __amdgpu_buffer_rsrc_t out = coherent_rsrc(a.part, a.splits * n_entries * a.D * 4);
+  const __amdgpu_buffer_rsrc_t out = coherent_rsrc(a.part, (a.splits + whole) * n_entries * a.D * 4);
 #pragma unroll
   for (int b = 0; b < MB; ++b) {
     const int t = 16 * b + r, at = min(t, x.tokens - 1);
     float sx = 0.0f;
     if constexpr (!BLOCK)
       sx = CODED ? a.hs[entry[at]] : act_scale<INT8>(__uint_as_float(lds.top[at]));
-    v4f o;
+    v4f o, scale;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       o[i] = (float)acc[b][0][i];
-      if constexpr (!BLOCK) o[i] *= sx * sw[i];
+      if constexpr (!BLOCK) {
+        scale[i] = sx * sw[i];
+        o[i] *= scale[i];
+      }
     }
-    if (t < x.tokens && n0 + 16 * wave < a.D)
-      coherent_store16(out, ((blockIdx.z * n_entries + entry[at]) * a.D + n + 4 * g) * 4,
-                       __builtin_bit_cast(v4i, o));
+    if (t >= x.tokens || n0 + 16 * wave >= a.D) continue;
+    const int to = entry[at] * a.D + n + 4 * g;
+    coherent_store16(out, ((int)blockIdx.z * n_entries * a.D + to) * 4,
+                     whole ? __builtin_bit_cast(v4i, acc[b][0]) : __builtin_bit_cast(v4i, o));
+    if (whole && blockIdx.z == 0)
+      coherent_store16(out, (a.splits * n_entries * a.D + to) * 4, __builtin_bit_cast(v4i, scale));
   }
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
   // (how many will, while the stores are on their way)
@@ -620,12 +632,13 @@ __device__ __forceinline__ void down_tile(const MoeLayerArgs& a, int n0, const E
 }
 
 // y of a tile's columns, four a thread, in the order of the choices, an output's
-// parts (SPLIT: of I) first; the loads of a batch are all in flight (left out: entry
-// 0's, not used).
-template <int BATCH, bool SPLIT>
+// parts (SPLIT: of I; WHOLE: whole numbers, whose scales lie behind them) first; the
+// loads of a batch are all in flight (left out: entry 0's, not used).
+template <int BATCH, bool SPLIT, bool WHOLE>
 __device__ __forceinline__ void sum_outputs(const MoeLayerArgs& a, int n0, const Choices& c) {
   const int n_entries = a.T * a.topk;
-  const __amdgpu_buffer_rsrc_t part = coherent_rsrc(a.part, a.splits * n_entries * a.D * 4);
+  const __amdgpu_buffer_rsrc_t part =
+      coherent_rsrc(a.part, (a.splits + WHOLE) * n_entries * a.D * 4);
   for (int i = threadIdx.x; i < a.T * (kColumns / 4); i += kThreads) {
     const int t = i / (kColumns / 4), n = n0 + 4 * (i % (kColumns / 4));
     if (n >= a.D) continue;
@@ -649,15 +662,33 @@ __device__ __forceinline__ void sum_outputs(const MoeLayerArgs& a, int n0, const
         v[j] = coherent_load16(part, (from[j] * a.D + n) * 4);
         w[j] = a.weights[at];
       }
-      v4f p[BATCH];
+      typedef std::conditional_t<WHOLE, v4i, v4f> Part;
+      Part q[BATCH];
+      v4i scale[WHOLE ? BATCH : 1];
+      if constexpr (WHOLE) {
 #pragma unroll
-      for (int j = 0; j < BATCH; ++j) p[j] = __builtin_bit_cast(v4f, v[j]);
+        for (int j = 0; j < BATCH; ++j)
+          scale[j] = coherent_load16(part, ((a.splits * n_entries + from[j]) * a.D + n) * 4);
+      }
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) q[j] = __builtin_bit_cast(Part, v[j]);
       for (int z = 1; SPLIT && z < a.splits; ++z) {
 #pragma unroll
         for (int j = 0; j < BATCH; ++j)
           v[j] = coherent_load16(part, ((z * n_entries + from[j]) * a.D + n) * 4);
 #pragma unroll
-        for (int j = 0; j < BATCH; ++j) p[j] += __builtin_bit_cast(v4f, v[j]);
+        for (int j = 0; j < BATCH; ++j) q[j] += __builtin_bit_cast(Part, v[j]);
+      }
+      v4f p[BATCH];
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {
+        if constexpr (WHOLE) {
+          const v4f f = __builtin_bit_cast(v4f, scale[j]);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) p[j][u] = (float)q[j][u] * f[u];
+        } else {
+          p[j] = q[j];
+        }
       }
 #pragma unroll
       for (int j = 0; j < BATCH; ++j) {
@@ -691,9 +722,9 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeLayerArgs a) {
   }
   find_outputs(a, lds.c);
   if (a.splits == 1)
-    sum_outputs<8, false>(a, n0, lds.c);
+    sum_outputs<8, false, false>(a, n0, lds.c);
   else
-    sum_outputs<4, true>(a, n0, lds.c);
+    sum_outputs<4, true, FMT == W8A8_INT8>(a, n0, lds.c);
 }
 
 // The codes and scales of an entry's hidden values, a workgroup each, with as many

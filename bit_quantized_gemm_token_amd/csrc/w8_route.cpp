@@ -105,8 +105,10 @@ LayerWs layer_ws(int T, int topk, int D, int I) {
   w.hq = w.h + round256(n * I * 4);
   w.hs = w.hq + n * coded_stride(I);
   w.part = w.hs + round256(n * ceil_div(I, W8_GROUP) * 4);
-  // (as many splits as one expert would take: E is not known here)
-  w.total = w.part + round256(n * D * 4 * layer_splits(1, D, I));
+  // (as many splits as one expert would take, and int8's scales: neither E nor the
+  // format is known here)
+  const int splits = layer_splits(1, D, I);
+  w.total = w.part + round256(n * D * 4 * (splits > 1 ? splits + 1 : 1));
   return w;
 }
 

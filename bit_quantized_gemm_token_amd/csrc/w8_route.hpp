@@ -74,7 +74,8 @@ struct MoeLayerArgs {
   uint8_t* hq;          // codes of h [T * topk, I], row stride ldh bytes, or null: made where used
   float* hs;            // and their scales [T * topk] (Block_FP8: [T * topk, I / 128])
   long long ldh;
-  float* part;          // [splits, T * topk, D] the experts' outputs
+  float* part;          // [splits, T * topk, D] the experts' outputs (W8A8_INT8 in parts: the
+                        // sums as int32, and behind them [T * topk, D] their scales)
   unsigned* counters;   // arrival counters
   long long ldq, ldw1, ldw2, ldb, ldy;  // bytes; base, y: elements
   long long w1_stride, w2_stride;       // bytes between experts
