@@ -1,8 +1,8 @@
 // What the kernels of w8_route.hip, w8_moe_layer.hip and w8_rows.hip need of the
 // device language beside hip/hip_runtime.h, included in front of them.  LDS
 // variables are one for all threads (static); the accesses of a wavefront to its
-// own LDS are in order, which the kernels rely on behind a signal fence: there
-// its lanes wait for each other.
+// own LDS are in order, which the kernels rely on behind a signal fence or a wave
+// barrier: there its lanes wait for each other.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -51,6 +51,7 @@ inline unsigned lanes_below(unsigned half, unsigned mask, unsigned base) {
 #define __builtin_amdgcn_mbcnt_lo(mask, base) emu::lanes_below(0, mask, base)
 #define __builtin_amdgcn_mbcnt_hi(mask, base) emu::lanes_below(1, mask, base)
 #define __atomic_signal_fence(order) emu::wave_sync()
+#define __builtin_amdgcn_wave_barrier() emu::wave_sync()
 #define __hip_atomic_store(p, v, order, scope) ((void)(*(p) = (v)))
 #define __hip_atomic_load(p, order, scope) (*(p))
 #define atomicAdd(p, v) emu::atomic_add(p, v)
