@@ -208,14 +208,25 @@ Plan plan_dense(int fmt, int M, int N, int K) {
 // Up to W8_MAX_M tokens the small-M GEMM, whose waves stream the weights into
 // registers, has the shorter start, and the tiles, whose loads do not wait for
 // registers, the higher rate: the larger the weights and M, the better for the
-// tiles (on its untuned configurations 1 x 2048 x 2048 4.1 us, tiles 5.2; 16 x
+// tiles (Block_FP8, on its untuned configurations: 1 x 2048 x 2048 4.1 us, tiles 5.2; 16 x
 // 4096 x 4096 7.9 and 7.7; 24 x 4096 x 4096 9.7 and 7.8; 24 x 896 x 512 3.5 and
 // 4.0; 1 x 4608 x 7168 12.5 and 9.8; 16 x 5120 x 8192 19.0 and 11.7).  Packed
 // weights, which it reads in whole lines, move the border (1 x 5120 x 8192 10.8
-// and 12.2; 8 x 5120 x 8192 12.4 and 11.7).  It needs whole groups.
+// and 12.2; 8 x 5120 x 8192 12.4 and 11.7).  Block_FP8's needs whole groups.
 bool use_small_m(int fmt, int M, int N, int K, bool packed) {
-  if (M > W8_MAX_M || (fmt == W8_BLOCK_FP8 && K % W8_GROUP)) return false;
+  if (M > W8_MAX_M) return false;
   const long long weights = (long long)N * K;
+  // The token-scaled formats, both ways on 16 shapes of 0.5 M to 64 M weights and 14
+  // token counts in both formats, with weights from memory and from the caches: this
+  // rule is 0.0 to 3.1% and 0.2 to 0.7% over the faster of the two on average (by
+  // layout and up to or above 16 tokens); Block_FP8's 1.9 to 6.2% and 0.2 to 3.2%;
+  // the tiles alone 6 to 42% and 3 to 25%.  Around its borders, from memory, this
+  // kernel and the tiles: 24 x 4096 x 2048 in int8 6.0 and 6.4 us, packed 5.3 and 6.4;
+  // 24 x 1792 x 5120 9.4 and 7.6; 8 x 4608 x 7168 10.9 and 10.5, packed 9.3 and 10.3;
+  // 16 x 5120 x 8192 packed 13.2 and 16.1.
+  if (fmt != W8_BLOCK_FP8)
+    return M > W8_MAX_M / 2 ? weights <= 8 << 20 : weights < 24 << 20 || packed;
+  if (K % W8_GROUP) return false;
   if (M > W8_MAX_M / 2) return weights < 1 << 22;
   return weights < 24 << 20 || (packed && M < 8);
 }
