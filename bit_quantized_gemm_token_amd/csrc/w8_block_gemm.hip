@@ -14,11 +14,13 @@
 // as acc += partial * (sx * sw), one fp32 FMA per element per group.  The
 // instruction itself rounds a group's sum: by 2^-16 of the result in the root
 // mean square, unbiased, at most 2^-16 of the sum of |products| (measured, 2^17
-// results), so about 1% of the bf16 outputs lie one step beside the rounded
-// exact one; the fp32 sum over the groups adds nothing to that.
+// results, codes of normal values; of positive ones 2^-15.7, of codes whose every
+// exponent is as likely 2^-13.4), so about 1% of the bf16 outputs lie one step
+// beside the rounded exact one; the fp32 sum over the groups adds nothing to that.
 //
 // With one scale per token and channel the MFMAs add into the accumulators
-// themselves (W8A8_INT8: int32, exact), the scales are two products an element
+// themselves (W8A8_INT8: int32, exact; FP8_Dynamic: as exact as an fp32 sum of the
+// steps, 1 to 128 of them 1.4e-5 to 1.55e-5 of the result either way), the scales are two products an element
 // before the one rounding to bf16, and a K-step still is 128 codes, the last one
 // with zeros past K.  The scales of a tile go to LDS once, behind the first
 // stages' loads.

@@ -173,6 +173,11 @@ struct Products {
     }
     __builtin_amdgcn_sched_barrier(0);
   }
+  // FP8_Dynamic's running sum stays in the instruction's accumulator, which keeps it
+  // as exactly as an fp32 sum of the steps would (codes of normal values, 1 to 128
+  // steps: 1.4e-5 to 1.55e-5 of the result in the root mean square either way).  That
+  // error is the instruction's rounding of a step's products among each other, and
+  // the forms of 32 codes an instruction have the same.
   static __device__ __forceinline__ void multiply(Acc& c, const Frag& w, const Frag& x, float sc) {
     if constexpr (BLOCK) {
       const Acc p = mma<FMT, 1>(w, x, Acc{0, 0, 0, 0});
