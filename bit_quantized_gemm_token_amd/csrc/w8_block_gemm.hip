@@ -33,10 +33,12 @@
 // the hand-off of split K and the start; 128 experts, top 8, of 1536 x 2048: 8
 // tokens 33.5 us, 4.9 TB/s, by the weights' bytes; 4096 tokens 158 to 182 us
 // (0.333 M clocks at 1.85 .. 2.1 GHz), 1.3 PFLOP/s, as the dense tiles.
-// One scale per token and channel: 8192 x 5120 x 8192 in int8 253 to 300 us, 2.3
-// to 2.7 POP/s, by power too (0.52 M clocks, the MFMAs busy in 63% of them); 48 x
-// 4608 x 7168 9.6 us by the weights, the hand-off and the start; 333 x 897 x 1040
-// 5.5 us by the start and one chain of nine steps.
+// One scale per token and channel: 8192 x 5120 x 8192 in int8 253 to 356 us over
+// two traces, their medians 293 and 305 (a loop of calls 257 to 265, 2.6 POP/s), by
+// power too (0.52 M clocks at 1.5 .. 2.05 GHz, the MFMAs busy in 63% of them), in fp8
+// 263 to 279, median 271 (2.5 PFLOP/s); 4096 x 5120 x 2048 42.4 and 41.0 us; 48 x 4608
+// x 7168 9.5 us by the weights, the hand-off and the start; 333 x 897 x 1040 5.7 us
+// by the start and one chain of nine steps.
 #include <atomic>
 #include <climits>
 #include <type_traits>

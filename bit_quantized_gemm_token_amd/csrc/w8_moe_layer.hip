@@ -14,13 +14,14 @@
 // finds for itself from the T x topk choices, so a launch needs no lists and
 // reads no weights of an expert without tokens.
 //
-// Measured with 128 experts, top 8, of 2048 x 768 (the weights of the experts
-// that are chosen, and their rate): 1 token 14.6 us (38 MB: up 8.0, down 6.6, two
-// chains of choices, weights and sums that few workgroups run once); 8 tokens 57
-// us (240 MB; up 34, 4.7 TB/s, down 22, 3.6); 32 tokens 99 us (530 MB; up 61, 5.8
-// TB/s, down 41, 4.3), by the weights' bytes.  Of down's time 3.5 to 5 us are the
-// hand-off of the outputs to the workgroup that sums them, about what a launch of
-// its own would take for that.
+// Measured with 128 experts, top 8, of 2048 x 768, row-major (a call among others,
+// and the kernels' medians in a trace, where they do not overlap; the weights of the
+// experts that are chosen, and their rate): 1 token in Block_FP8 14.4 us (38 MB: up
+// 8.8, down 7.4, two chains of choices, weights and sums that few workgroups run
+// once); 8 tokens in int8 53.6 us (244 MB; up 36.8, 4.4 TB/s, down 24.4, 3.3); 32
+// tokens in fp8 97.9 us (527 MB; up 67.9, 5.2 TB/s, down 42.8, 4.1), by the weights'
+// bytes.  Of down's time 3.5 to 5 us are the hand-off of the outputs to the workgroup
+// that sums them, about what a launch of its own would take for that.
 #include <type_traits>
 
 #include "w8_block.hpp"
@@ -267,10 +268,11 @@ __device__ __forceinline__ float uniform_load(const float* p) {
 // ---------------------------------------------------------------------- up --
 // 16 columns of h: 16 gate and 16 up rows of one expert, K split over the
 // waves, their sums joined through LDS in wave order.  So 128 bytes of 64 rows a
-// step are in flight a workgroup, two steps deep, and five workgroups share a
-// compute unit (8 tokens as above, one to four steps deep: 35.7, 35.0, 43.6 and
-// 35.7 us; 32 tokens 65.4, 66.5, 85.0 and 80.6, where registers leave room for
-// fewer workgroups).
+// step are in flight a workgroup, two steps deep, and five workgroups or six (72 to
+// 86 registers) share a compute unit, four (97 to 110) where experts may have more
+// than 16 tokens (calls of 8 tokens in int8 as above, one to four steps deep: 64.5,
+// 62.8, 69.3 and 62.7 us; 1 token 14.5, 14.7, 16.6 and 14.9; 32 tokens in fp8 105.5,
+// 105.4, 118.8 and 116.7, where registers leave room for three workgroups and two).
 constexpr int kUpPieces = 2;
 
 template <int MB, int KW>
@@ -401,8 +403,8 @@ __global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeLayerArgs a) {
 // 64 columns of y for one expert: each wave 16 of its weight rows over the whole
 // of I, the tokens' codes from LDS, where the workgroup makes them from h
 // `chunk` columns at a time, or from memory, if they are there.  Two steps are in
-// flight (as above, two, three, four and six: 8 tokens 22.4, 22.8, 25.6 and 22.6 us,
-// 32 tokens 42.9, 42.8, 48.0 and 43.9).
+// flight (calls as above, two, three, four and six: 8 tokens 62.8, 62.9, 64.3 and 62.8
+// us, 32 tokens 105.4, 105.8, 110.4 and 106.8).
 constexpr int kColumns = 16 * kWaves;
 constexpr int kPad = 16;  // bytes that move a row's codes on by four LDS banks
 
@@ -945,8 +947,9 @@ template <int FMT, bool PACKED, int MB>
 hipError_t launch_up(const MoeLayerArgs& a, hipStream_t s) {
   // Short K leaves four waves a step or two each: where there are columns enough
   // for every compute unit, a wave takes all of it (64 experts, top 8, I = 1024, 8
-  // tokens: D = 512 27.9 us and 22.9, 768 32.1 and 29.7, 1024 35.2 and 37.1; 1 token,
-  // D = 768: 12.9 and 13.6).
+  // tokens in Block_FP8: D = 512 27.5 us and 22.9, 768 31.5 and 30.8, 1024 34.7 and
+  // 37.6; in int8 28.0 and 23.5, 34.3 and 35.1, 38.2 and 42.3; 1 token, D = 768: 13.5
+  // and 13.6).
   const int blocks = (a.I / 16 + kWaves - 1) / kWaves;
   if (a.D <= 768 && (long long)blocks * a.slots >= kComputeUnits)
     return launch_kernel(moe_up_kernel<FMT, PACKED, MB, 1>,

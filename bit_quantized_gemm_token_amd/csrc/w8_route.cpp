@@ -1,7 +1,7 @@
 // C-ABI of the MoE operators around the grouped products: the routing, the
 // combination of the experts' outputs and the whole layer of a few tokens.
-// Argument checks first, then one or two kernel launches; nothing here
-// allocates, frees or synchronizes.
+// Argument checks first, then one launch or two, of the layer two or three; nothing
+// here allocates, frees or synchronizes.
 #include <algorithm>
 #include <cstdint>
 #include <string>

@@ -10,13 +10,15 @@
 // the lists are the same every time.
 //
 // A row of logits is a few hundred bytes and stays in the registers of 16 or 64
-// lanes; each choice is a maximum over them, its place a minimum, so a token is a
-// chain of topk reductions and the chains of many tokens hide each other.
-// Measured: 8 tokens of 128 experts, top 8, 4.8 us in one launch, 32 tokens 4.9,
-// all latency (with 1 of 16 experts 3.3); 8192 tokens 5.7 us by the same chain (the
-// bytes, 3.1 MB, take 1 us) and 6.7 us for the places, by the 256 KiB of counts that
-// each workgroup reads and the latency of reading, adding and writing one after
-// the other.
+// lanes as ordered keys.  Each choice is their maximum; a bf16 logit's key names its
+// expert, an fp32 logit's is found again by a ballot, whose first lane holds the
+// lowest.  So a token is a chain of topk reductions, and the chains of many tokens
+// hide each other.
+// Measured (medians of a trace): 8 tokens of 128 experts, top 8, 4.8 us in one
+// launch, 32 tokens 5.4, all latency (with 1 of 16 experts 3.3); 8192 tokens 5.8 us by
+// the same chain (the bytes, 3.1 MB, take 1 us) and 6.9 us for the places, by the 256
+// KiB of counts that each workgroup reads and the latency of reading, adding and
+// writing one after the other.
 #include "w8_block.hpp"
 #include "w8_device.hpp"
 #include "w8_route.hpp"

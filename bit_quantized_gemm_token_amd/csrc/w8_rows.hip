@@ -178,9 +178,9 @@ __global__ __launch_bounds__(kQThreads) void block_quantize_kernel(BlockQuantArg
 // the waves of a workgroup (ONE_WAVE: four rows, a wave each), NC chunks of eight
 // values a lane, whose gated products stay in registers between the maximum and
 // the codes; what a row has beyond those is read and computed again.  Every value
-// is read once, so HBM bounds it on many rows (8192 x 8192 gated: 335 MB in 59.6
+// is read once, so HBM bounds it on many rows (8192 x 8192 gated: 335 MB in 59.7
 // us, 5.6 TB/s) and the launch with one chain of load, maximum and store on few
-// (48 x 7168: 2.9 us).
+// (48 x 7168: 3.4 us, the median of a trace, 3.2 the fastest).
 template <bool INT8, bool GATED, bool ONE_WAVE, int NC>
 __global__ __launch_bounds__(ONE_WAVE ? 256 : 1024) void token_quantize_kernel(TokenQuantArgs a) {
   __shared__ unsigned red[16];

@@ -43,8 +43,10 @@ def moe_route(logits, topk, renormalize=True, scale=1.0, lists=True, workspace=N
                moe_combine)
 
     topk at most 32 and E, E at most 1024.  One launch for T * topk up to 256
-    entries (fewer above 256 experts), else two; whole numbers only, the same every time.  workspace: as
-    for block_gemm.
+    entries (fewer above 256 experts), else two; whole numbers only, the same
+    every time.  experts, weights and slots are parts of one allocation, offsets
+    and rows of another: one that is kept keeps its allocation.  workspace: as for
+    block_gemm.
     """
     lp, ldl = _rows(logits, "logits")
     if logits.dtype is not _F32 and logits.dtype is not _BF16:
@@ -186,10 +188,12 @@ def moe_layer(fmt, xq, sx, experts, weights, w1, s1, w2, s2, base=None, y=None, 
     (Block_FP8: of 128) up to 65536, E at most 1024, topk at most 32.  base:
     bf16 [T, D] (a shared expert's output, a residual) or None; y may be base.
 
-    Two launches (three where many tokens share an expert), no lists, no host sync; the hidden values stay fp32 until
-    they are quantized and the sum is fp32 in the order of the choices, so
-    results are the same every time.  workspace: as for block_gemm,
-    moe_layer_workspace_size bytes.
+    Two launches (three where many tokens share an expert), no lists, no host
+    sync; the hidden values stay fp32 until they are quantized (by a division, as
+    token_quantize without reciprocal) and the sum is fp32 in the order of the
+    choices, so results are the same every time.  W8A8_INT8's products are exact
+    whole numbers, scaled once: a token's outputs are the same bits whoever else
+    is in the call.  workspace: as for block_gemm, moe_layer_workspace_size bytes.
     """
     f = _fmt(fmt)
     xp, ldq = _codes(xq, "xq")

@@ -811,7 +811,10 @@ w8_status w8_moe_combine(int T, int topk, int D, const void *y, int64_t ldy, int
  *   ws       w8_moe_layer_workspace_size bytes, with w8_gemm_w8a8's rules (one
  *            workspace may serve every entry point)
  * 1 <= E <= 1024, 1 <= topk <= 32; D and I multiples of 16 (Block_FP8: of 128)
- * up to 65536.  An expert without tokens reads no weights.                 */
+ * up to 65536.  An expert without tokens reads no weights.  With E == 1 the
+ * experts' strides are not used.  W8A8_INT8's products are exact int32 sums,
+ * scaled once, so a token's outputs do not depend on the others of the call
+ * (the other formats': by the order of fp32 sums).                         */
 w8_status w8_moe_layer(w8_fmt fmt, int E, int T, int topk, int D, int I, const void *xq,
                        int64_t ldq, const float *sx, const int32_t *experts,
                        const float *weights, const void *w1, int64_t ldw1, int64_t w1_stride,
