@@ -14,8 +14,8 @@
 // expert, an fp32 logit's is found again by a ballot, whose first lane holds the
 // lowest.  So a token is a chain of topk reductions, and the chains of many tokens
 // hide each other.
-// Measured (medians of a trace): 8 tokens of 128 experts, top 8, 4.8 us in one
-// launch, 32 tokens 5.4, all latency (with 1 of 16 experts 3.3); 8192 tokens 5.8 us by
+// Measured (medians of a trace): 8 tokens of 128 experts, top 8, 4.6 us in one
+// launch, 32 tokens 5.4, all latency (1 token, 1 of 16 experts 3.1); 8192 tokens 5.8 us by
 // the same chain (the bytes, 3.1 MB, take 1 us) and 6.9 us for the places, by the 256
 // KiB of counts that each workgroup reads and the latency of reading, adding and
 // writing one after the other.
