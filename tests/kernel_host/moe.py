@@ -48,8 +48,8 @@ def build(folder):
 class Buffers:
     """The arrays of one call, each in pages of its own."""
 
-    def __init__(self, lib, at_end):
-        self.lib, self.at_end, self.of = lib, at_end, {}
+    def __init__(self, lib, at_end, short=None):
+        self.lib, self.at_end, self.short, self.of = lib, at_end, short, {}
         lib.emu_free_all()
         lib.emu_lds_at_end(int(at_end))
 
@@ -60,8 +60,10 @@ class Buffers:
 
     def put(self, name, v):
         v = np.ascontiguousarray(v)
-        p = self.new(name, v.nbytes)
-        ctypes.memmove(p, v.ctypes.data, v.nbytes)
+        # (short: the name of an array whose last element, or 16 codes, are not there)
+        nbytes = v.nbytes - (0 if name != self.short else 16 if v.itemsize == 1 else v.itemsize)
+        p = self.new(name, nbytes)
+        ctypes.memmove(p, v.ctypes.data, nbytes)
         return p
 
     def rows(self, name, v, ld):
@@ -94,13 +96,13 @@ def status(lib, rc):
 
 
 def layer(lib, fmt, xq, sx, experts, weights, w1, s1, w2, s2, base=None, packed=(False, False),
-          pack=None, descending=False, at_end=True, pad=16, ws=None):
+          pack=None, descending=False, at_end=True, pad=16, short=None):
     """(y's bf16 bits [T, D], what was wrong or None) of one call; codes in rows
     `pad` bytes apart, the workspace NaN behind its counters."""
     T, D = xq.shape
     E, _, I = w2.shape
     topk = experts.shape[1]
-    b = Buffers(lib, at_end)
+    b = Buffers(lib, at_end, short)
 
     def codes(name, w, is_packed):
         if is_packed:

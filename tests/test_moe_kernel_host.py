@@ -170,6 +170,19 @@ def test_an_access_outside_is_seen(lib):
         assert rc == 3 and "access at x" in lib.emu_text().decode()
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,I", [(1, 144), (9, 272), (32, 800)])
+def test_every_array_of_the_layer_is_read_to_its_end(lib, fmt, T, I):
+    """An array that is an element short is one that a kernel reads past."""
+    D, I = sized(fmt, 80, I)
+    c = Layer(fmt, T, 2, 2, D, I, experts=[[0, 1]] * T)
+    base = bf16_bits(np.ones((T, D)))
+    for name in ("xq", "sx", "experts", "weights", "w1", "s1", "w2", "s2", "base"):
+        _, wrong = host.layer(lib, fmt, c.xq, c.sx, c.experts, c.weights, c.w1, c.s1, c.w2, c.s2,
+                              base=base, short=name)
+        assert wrong and f"access at {name} " in wrong, (name, wrong)
+
+
 def test_a_refusal_is_a_refusal(lib):
     c = Layer("W8A8_INT8", 2, 2, 1, 32, 32)
     y, wrong = host.layer(lib, c.fmt, c.xq, c.sx, c.experts, c.weights, c.w1, c.s1, c.w2, c.s2, pad=8)

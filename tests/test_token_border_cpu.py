@@ -36,6 +36,6 @@ def test_block_fp8_keeps_its_own(w8, M, N, K):
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_every_packed_size_has_a_plan_and_a_workspace(w8, fmt):
     for M in (1, 7, 8, 16, 17, 32):
-        for N, K in ((1, 128), (17, 131008 // 128 * 128), (1 << 24, 128), (70001, 8192), (300000, 1024)):
+        for N, K in ((1, 128), (17, 130944), (1 << 24, 128), (70001, 8192), (300000, 1024)):
             w8.token_gemm_plan(fmt, M, N, K, packed=True)
             assert w8.token_gemm_workspace_size(fmt, M, N, K, packed=True) >= 0
